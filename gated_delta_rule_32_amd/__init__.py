@@ -528,3 +528,17 @@ def recurrent_kda(q, k, v, g, beta, A_log=None, dt_bias=None, scale=None, initia
     if checkpoint_every_n_tokens:
         return o, final, state_checkpoints
     return o, final
+
+
+# The operators of a linear-attention layer beside KDA (at the end: the module
+# uses the names above)
+from . import layers as _layers  # noqa: E402
+from .layers import (  # noqa: E402,F401
+    GATE_SIGMOID, GATE_SILU, DecayAttentionTrainingContext, KdaDecayProblem, KdaGNormProblem, KdaQkNormProblem,
+    decay_attention, decay_attention_training_backward, decay_attention_training_forward, gated_norm_backward,
+    gated_norm_forward, kda_decay_bwd, kda_decay_bwd_workspace_bytes, kda_decay_fwd, kda_decay_fwd_workspace_bytes,
+    kda_decay_infer, kda_decay_infer_workspace_bytes, kda_gnorm_bwd, kda_gnorm_bwd_workspace_bytes, kda_gnorm_fwd,
+    kda_qknorm_bwd, kda_qknorm_bwd_workspace_bytes, kda_qknorm_fwd, qk_norm_rope_backward, qk_norm_rope_forward,
+    rotary_table)
+
+EXPORTED += _layers.EXPORTED

@@ -36,6 +36,9 @@ SOURCES = [
     "kda_bwd.hip",
     "kda_infer.hip",
     "kda_noalloc.hip",
+    "kda_layers.cpp",
+    "kda_decay.hip",
+    "kda_rownorm.hip",
 ]
 
 FLAGS = [

@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "../../include/libkda.h"
+#include "kda_host.h"
 #include "kda_kernels.h"
 
 namespace {
@@ -27,6 +28,10 @@ namespace {
 constexpr int D = 128;  // head dimension
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace kda_host {
 
 kda_status fail(kda_status s, const char* fmt, ...) {
     char buf[512];
@@ -41,6 +46,15 @@ kda_status fail(kda_status s, const char* fmt, ...) {
 kda_status hip_fail(hipError_t e, const char* what) {
     return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace kda_host
+
+namespace {
+
+using kda_host::check_overlap;
+using kda_host::fail;
+using kda_host::hip_fail;
+using kda_host::Span;
 
 constexpr int64_t kStateElems = (int64_t)D * D;
 constexpr int kDefaultCk = 256;
@@ -98,7 +112,8 @@ int auto_route(const Prob& p) {
     return 1;
 }
 
-kda_status validate(const kda_problem* p, Prob& out) {
+// kda_problem's checks except the limit on a sequence's elements.
+kda_status validate_shape(const kda_problem* p, Prob& out) {
     if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
     if (p->B < 1 || p->T < 1 || p->Hqk < 1 || p->Hv < 1 || p->N < 1)
         return fail(KDA_ERR_SHAPE, "B, T, Hqk, Hv and N must be >= 1 (got %d %d %d %d %d)",
@@ -173,12 +188,18 @@ kda_status validate(const kda_problem* p, Prob& out) {
         out.total_segs += (L + ck - 1) / ck;
         out.total_chunks += ((L + kChunk - 1) / kChunk + 1) & ~(int64_t)1;
     }
-    // kernels address a sequence's rows with 32-bit element offsets
+    out.route = p->route == 0 ? auto_route(out) : p->route;
+    return KDA_OK;
+}
+
+kda_status validate(const kda_problem* p, Prob& out) {
+    kda_status s = validate_shape(p, out);
+    if (s != KDA_OK) return s;
+    // the KDA kernels address a sequence's rows with 32-bit element offsets
     for (int64_t L : out.len)
         if (L * (int64_t)p->Hv * D >= ((int64_t)1 << 31))
             return fail(KDA_ERR_SHAPE, "a sequence of %lld tokens x %d heads x 128 exceeds 2^31 elements",
                         (long long)L, p->Hv);
-    out.route = p->route == 0 ? auto_route(out) : p->route;
     return KDA_OK;
 }
 
@@ -497,13 +518,11 @@ size_t ctx_bytes_for(const Prob& p) {
     return 256 + tape_bytes(p);
 }
 
-struct Span {
-    const void* p;
-    size_t n;
-    const char* name;
-};
+}  // namespace
 
-bool overlaps(const Span& a, const Span& b) {
+namespace kda_host {
+
+static bool overlaps(const Span& a, const Span& b) {
     if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
     const char* a0 = (const char*)a.p;
     const char* b0 = (const char*)b.p;
@@ -521,6 +540,10 @@ kda_status check_overlap(const std::vector<Span>& outs, const std::vector<Span>&
     }
     return KDA_OK;
 }
+
+}  // namespace kda_host
+
+namespace {
 
 std::vector<Span> input_spans(const Prob& p, const void* q, const void* k, const void* v,
                               const void* g, const void* beta, const float* A_log,
@@ -554,6 +577,64 @@ kda::FwdArgs make_fwd_args(const Prob& p, const kda::DevPlan& plan, const void* 
 }
 
 }  // namespace
+
+namespace kda_host {
+
+static Prob seq_prob(const Seqs& s, int B, int T, bool packed, int segment) {
+    Prob p{};
+    p.B = B; p.T = T; p.Hqk = s.Hqk; p.Hv = s.Hv; p.N = s.N; p.G = s.G;
+    p.packed = packed;
+    p.ck = segment;
+    p.schedule = KDA_SCHEDULE_LONGEST_FIRST;
+    p.len = s.len;
+    p.start = s.start;
+    p.tokens = s.tokens;
+    p.num_tasks = (int64_t)s.N * s.Hv;
+    for (int64_t L : p.len) p.total_segs += (L + segment - 1) / segment;
+    return p;
+}
+
+kda_status check_seqs(int B, int T, int Hqk, int Hv, int N, const int64_t* cu, const int64_t* cu_host,
+                      Seqs& out) {
+    kda_problem q{};
+    q.B = B; q.T = T; q.Hqk = Hqk; q.Hv = Hv; q.N = N;
+    q.cu_seqlens = cu;
+    q.cu_seqlens_host = cu_host;
+    q.lower_bound = -5.0f;
+    q.route = KDA_ROUTE_ROWSPLIT;
+    Prob p;
+    kda_status s = validate_shape(&q, p);
+    if (s != KDA_OK) return s;
+    out.N = p.N; out.Hqk = p.Hqk; out.Hv = p.Hv; out.G = p.G;
+    out.tokens = p.tokens;
+    out.max_len = p.max_len;
+    out.len = std::move(p.len);
+    out.start = std::move(p.start);
+    return KDA_OK;
+}
+
+struct SeqPlan::Hold {
+    PlanLease lease;
+};
+
+kda_status get_seq_plan(const Seqs& s, int B, int T, bool packed, int segment, hipStream_t stream,
+                        SeqPlan& out) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    const Prob p = seq_prob(s, B, T, packed, segment);
+    auto hold = std::make_shared<SeqPlan::Hold>();
+    kda_status st = get_plan(p, stream, dev, hold->lease);
+    if (st != KDA_OK) return st;
+    const PlanEntry* ent = hold->lease.ent;
+    out.dev = dev_plan(ent);
+    out.seg = (const int32_t*)((const char*)ent->dev + ent->lay.off_seg);
+    out.total_segs = p.total_segs;
+    out.hold = std::move(hold);
+    return KDA_OK;
+}
+
+}  // namespace kda_host
 
 extern "C" {
 

@@ -1,0 +1,557 @@
+// Linear attention with a constant decay per head: training forward and
+// backward, prefill, and the token-serial form for decode.
+//
+//     S_t = e^l S_{t-1} + v_t k_t^T   (S[v][k], FP32),      o_t = s S_t q_t
+//
+// with one log-decay l <= 0 per value head.  Its adjoint is
+//     dS_t = s do_t q_t^T + e^l dS_{t+1},   dq_t = s S_t^T do_t,
+//     dk_t = dS_t^T v_t,   dv_t = dS_t k_t,   dS_0 = e^l dS_1,
+// so o, dq, dk and dv are one causal form over rows a, b, c (128 channels):
+//     y_i = sum_{j<=i} e^{l(i-j)} (a_i.b_j) c_j + e^{l(i+shift)} a_i X
+// with (a, b, c) = (q, k, v) and (do, v, k) forward in time (X the initial
+// state, shift 1), and (v, do, q) and (k, q, do) backward in time (X the
+// final state's adjoint, shift 0).  One kernel computes all four.
+#include "kda_chunk.hpp"
+#include "kda_common.hpp"
+#include "kda_layers.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int SC = 64;            // tokens per chunk
+constexpr int SC_THREADS = 512;
+constexpr int STATE = D * D;
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+struct Item {
+    int64_t tok0;     // first token (flattened)
+    int len;          // tokens
+    int n, h;
+    int64_t seg;      // segment number among all segments (segmented maps)
+};
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    const unsigned lo = __builtin_amdgcn_readfirstlane((int)(unsigned)x);
+    const int hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return ((int64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ double uniform(double x) {
+    return __builtin_bit_cast(double, uniform64(__builtin_bit_cast(int64_t, x)));
+}
+
+__device__ __forceinline__ Item find_item(const ItemMap& m, int64_t i) {
+    Item it;
+    const int64_t r = i / m.Hv;
+    const int lead = (int)r;   // sequence, or place in the segment list
+    it.h = (int)(i - r * m.Hv);
+    it.seg = 0;
+    int j = 0;
+    if (m.task == nullptr) {
+        it.n = lead;
+        if (m.seg_len > 0) {
+            const int per = (m.len + m.seg_len - 1) / m.seg_len;
+            it.n = lead / per;
+            j = lead - it.n * per;
+            it.seg = lead;
+        }
+        it.tok0 = (int64_t)it.n * m.len;
+        it.len = m.len;
+    } else if (m.seg_len > 0) {
+        it.n = m.seg[2 * lead];
+        j = m.seg[2 * lead + 1];
+        it.seg = m.tape_off[it.n] + it.n + j;
+        it.tok0 = m.seq_start[it.n];
+        it.len = m.seq_len[it.n];
+    } else {
+        const int code = m.task[i];
+        it.n = code / m.Hv;
+        it.h = code - it.n * m.Hv;
+        it.tok0 = m.seq_start[it.n];
+        it.len = m.seq_len[it.n];
+    }
+    if (m.seg_len > 0) {
+        it.tok0 += (int64_t)j * m.seg_len;
+        it.len = min(m.seg_len, it.len - j * m.seg_len);
+    }
+    // the same for the whole workgroup: keep it in scalar registers
+    it.n = __builtin_amdgcn_readfirstlane(it.n);
+    it.h = __builtin_amdgcn_readfirstlane(it.h);
+    it.len = __builtin_amdgcn_readfirstlane(it.len);
+    it.tok0 = uniform64(it.tok0);
+    it.seg = uniform64(it.seg);
+    return it;
+}
+
+// l in base 2, kept finite so that 0 * l is 0 for l = -inf (a NaN stays one).
+__device__ __forceinline__ float log2_decay(float l) {
+    const float x = l * LOG2E;
+    return x < -1e30f ? -1e30f : x;
+}
+__device__ __forceinline__ double decay_power(float l, int n) {  // e^{l n}, n >= 0
+    return n == 0 ? 1.0 : exp((double)l * n);
+}
+
+// e^{l n} as a factor that is applied over and over: rounded to FP32 it would
+// be off the same way every time, so `corr` carries the quotient of the true
+// power to the product of the factors given out, and that product stays within
+// half a step of the true power however many there are.
+struct Power {
+    double lam, inv, corr;
+    __device__ __forceinline__ Power(float l, int n) {
+        lam = uniform(decay_power(l, n));
+        inv = uniform(lam > 1e-30 ? 1.0 / lam : 0.0);
+        corr = 1.0;
+    }
+    __device__ __forceinline__ float next() {
+        const double want = lam * corr;
+        const float f = (float)want;
+        corr = inv != 0.0 ? 1.0 + (want - (double)f) * inv : 1.0;
+        return f;
+    }
+};
+
+// LDS rows of 128 channels are 16 blocks of 8 channels; block b of row r is
+// stored at block b ^ swz(r).  Rows 4g + r' then spread the 16 (r', b mod 4)
+// of a transposing read over all 16 places, and 16 rows the same block.
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+
+// Transposing read: the 16 lanes of group gq address 4 rows x 4 pieces of 4
+// channels, and lane m receives the 4 rows of channel m of those 16.
+__device__ __forceinline__ bf16x4 tr_read(const bf16* p) {
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)p));
+}
+
+// A load or store at a uniform address plus a 32-bit lane offset: the address
+// is pinned to scalar registers, where it would otherwise be kept as one
+// 64-bit vector per row.
+template <class T>
+__device__ __forceinline__ __attribute__((address_space(1))) T* row_ptr(const void* base, unsigned off) {
+    uint64_t b = (uint64_t)base;
+    asm volatile("" : "+s"(b));
+    return (__attribute__((address_space(1))) T*)((__attribute__((address_space(1))) char*)b + off);
+}
+
+// Takes the leading 8 significant bits of every element off x and returns
+// them as BF16 (the remainder is exact).
+__device__ __forceinline__ bf16x4 take_high(f32x4& x) {
+    const u32x4 u = __builtin_bit_cast(u32x4, x) & 0xffff0000u;
+    x -= __builtin_bit_cast(f32x4, u);
+    return __builtin_bit_cast(bf16x4, u32x2{__builtin_amdgcn_perm(u[1], u[0], 0x07060302u),
+                                            __builtin_amdgcn_perm(u[3], u[2], 0x07060302u)});
+}
+
+// x, as a value the compiler cannot know to be the same in every loop round:
+// products of it are formed where they are used instead of being kept in
+// registers over the loop.
+__device__ __forceinline__ float fresh(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+}  // namespace
+
+// One workgroup (8 waves) per item; wave w owns the state's output channels
+// 16w .. 16w+15 as MFMA accumulators: tile t holds S^T[k][v] with
+//     k = 32(t/2) + 8gq + 4(t%2) + e,   v = 16w + n
+// (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
+// rounded to BF16, the operand of S a over channels 32p + 8gq .. +7.  Per
+// chunk of 64 tokens:
+//     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)}; two tiles at
+//           most per wave, through LDS to the others)
+//     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
+//     S^T = e^{64 l} S^T + B^T (C u),   u_j = e^{l(64-shift-j)}
+// Two operands are rounded to BF16: P, and S where it meets a (each about as
+// large an error as the output's own rounding).  The FP32 products C u go in
+// as BF16 pieces of 8 significant bits each: all three, the exact product,
+// where the state is an output; the first two where it is only read back
+// rounded to BF16.  The state itself stays in FP32 registers.  A chunk's rows are fetched into registers while
+// the previous chunk is computed.  `reverse` walks the tokens downwards and
+// only shifts the exponents.
+template <bool kOut>
+__global__ __launch_bounds__(SC_THREADS, 4) void decay_scan_kernel(ScanArgs A) {
+    // one LDS block (elements): B rows, C rows, A rows, P^T tiles
+    constexpr int LB = 0, LC = SC * D, LA = 2 * SC * D, LP = 3 * SC * D;
+    __shared__ __align__(16) bf16 lds[kOut ? LP + 16 * 256 : LA];
+
+    const int tid = threadIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, gq = lane >> 4, n16 = lane & 15;
+    const int idx = xcd_order(blockIdx.x, (int)gridDim.x, A.share);
+    const ScanRole R = A.role[idx % A.roles];
+    const Item it = find_item(A.map, idx / A.roles);
+    const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
+    if (slot < 0 || slot >= A.slots) return;
+    const int64_t sidx = R.s_by_seg ? it.seg : slot;
+    const int Hv = A.map.Hv;
+    const int64_t soff = (sidx * Hv + it.h) * (int64_t)STATE;
+    const bool rev = R.reverse != 0;
+    const float l = A.log_decay[it.h];
+    const float l2 = log2_decay(l);
+    const int shift = rev ? 0 : 1;
+    const float scale = A.scale;
+    const float y_state = rev ? 1.0f : scale;     // scale of the state's part of y
+    const float s_add = rev ? scale : 1.0f;       // scale of what the state takes up
+
+    // This thread's loads: 16 bytes of rows tid/16 and tid/16 + 32 of the
+    // chunk.  A row is a uniform base (scalar registers) plus a 32-bit lane
+    // offset; walking down, the base is the group's lowest row.  Rows behind
+    // the last token are not read and count as zero.
+    const int lr = tid >> 4, lc = (tid & 15) * 8;
+    const int64_t first = rev ? it.tok0 + it.len - 1 : it.tok0;
+    const int64_t dir = rev ? -1 : 1;
+    const unsigned lrow = rev ? 31 - lr : lr;
+    const int64_t sa = R.sa * 2, sb = R.sb * 2, sc = R.sc * 2;   // bytes per token
+    const unsigned oa = lrow * (unsigned)sa + lc * 2, ob = lrow * (unsigned)sb + lc * 2,
+                   oc = lrow * (unsigned)sc + lc * 2;
+    const int64_t row0 = first - (rev ? 31 : 0);
+    const char* pa = kOut ? (const char*)(R.a + (it.h / R.ga) * D) + row0 * sa : nullptr;
+    const char* pb = (const char*)(R.b + (it.h / R.gb) * D) + row0 * sb;
+    const char* pc = (const char*)(R.c + (it.h / R.gc) * D) + row0 * sc;
+    const int64_t ga = 32 * dir * sa, gb = 32 * dir * sb, gc = 32 * dir * sc;
+
+    u32x4 xa[2], xb[2], xc[2];
+    auto fetch = [&](int t0) __attribute__((always_inline)) {
+        if (it.len - t0 >= SC) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
+                xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
+                xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                xa[i] = xb[i] = xc[i] = u32x4{0u, 0u, 0u, 0u};
+                if (t0 + lr + 32 * i < it.len) {
+                    if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
+                    xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
+                    xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
+                }
+            }
+        }
+        pa += 2 * ga;
+        pb += 2 * gb;
+        pc += 2 * gc;
+    };
+    fetch(0);
+
+    // state
+    f32x4 S[8];
+    const int vrow = 16 * w + n16;
+    const float* s_in = R.s_in;
+    if (s_in == nullptr) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) S[t] = zero4();
+    } else if (!R.s_in_t) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            S[t] = *(const f32x4*)(s_in + soff + vrow * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1));
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[t][e] = s_in[soff + (32 * (t >> 1) + 8 * gq + 4 * (t & 1) + e) * D + vrow];
+    }
+
+    // Powers of e^l, constant over the item's full chunks; each is a product
+    // of factors <= 1, so none overflows.  This wave's P^T tiles are token
+    // rows j = 16tj .. and columns i = 16(tj + odd) .. and 32 further on.
+    //     P^T at i - j = 16d + n - 4gq - e:   pf[0][e] (d = odd), pf[1][e] (d = odd + 2)
+    //     Y column i = 16ti + n:              y0 step[ti]
+    //     C row j = 16tj + r, r = 4gq + e:    u0[e] step[3-tj]
+    const int tj0 = w & 3, odd = w >> 2;
+    float pf[2][4], u0[4], step[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        step[d] = __int_as_float(__builtin_amdgcn_readfirstlane(
+            __float_as_int(__builtin_amdgcn_exp2f(l2 * (float)(16 * d)))));
+    const float y0 = y_state * __builtin_amdgcn_exp2f(l2 * (float)(n16 + shift));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int gap = 16 * odd + n16 - 4 * gq - e;
+        pf[0][e] = scale * __builtin_amdgcn_exp2f(l2 * (float)max(gap, 0));
+        pf[1][e] = scale * __builtin_amdgcn_exp2f(l2 * (float)(gap + 32));
+        u0[e] = s_add * __builtin_amdgcn_exp2f(l2 * (float)(16 - shift - 4 * gq - e));
+    }
+    Power chunk_decay(l, SC);   // the state's factor per chunk
+    float* const s_out = R.s_out;
+    const bool exact = s_out != nullptr;
+    // LDS addresses (elements)
+    const int st_off = lr * D + (((lc >> 3) ^ swz(lr)) << 3);        // + 32i rows: swz is the same
+    int rd[4], tr[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        rd[p] = n16 * D + (((4 * p + gq) ^ swz(n16)) << 3);          // + 16*ti*D
+        tr[p] = (4 * gq + (n16 >> 2)) * D + (((4 * p + (n16 & 3)) ^ swz(4 * gq + (n16 >> 2))) << 3);
+    }
+    // channels 16w + 4a of row 4gq + n/4 (a = n%4): this wave's C columns
+    const int trc = (4 * gq + (n16 >> 2)) * D +
+                    (((2 * w + ((n16 & 3) >> 1)) ^ swz(4 * gq + (n16 >> 2))) << 3) + 4 * (n16 & 1);
+    // output rows of 16 tokens: a uniform base and a 32-bit lane offset
+    const bool y_f32 = R.y_f32 != 0;
+    const int64_t sy = (int64_t)Hv * D * (y_f32 ? 4 : 2), gy = 16 * dir * sy;
+    char* py = (char*)R.y + ((first - (rev ? 15 : 0)) * Hv + it.h) * D * (y_f32 ? 4 : 2);
+    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * w + 4 * gq) * (y_f32 ? 4 : 2);
+
+    auto chunk = [&](int t0, auto tail_c) __attribute__((always_inline)) {
+        constexpr bool kTail = decltype(tail_c)::value;
+        const int rem = kTail ? it.len - t0 : SC;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (kOut) *(u32x4*)(lds + LA + st_off + 32 * i * D) = xa[i];
+            *(u32x4*)(lds + LB + st_off + 32 * i * D) = xb[i];
+            *(u32x4*)(lds + LC + st_off + 32 * i * D) = xc[i];
+        }
+        __syncthreads();
+        if (!kTail && t0 + SC < it.len) fetch(t0 + SC);
+        const float fs = kTail ? (float)decay_power(l, rem) : chunk_decay.next();
+
+        f32x4 y[4];
+        if (kOut) {
+            // this wave's P^T tiles
+            int tj = tj0;
+            asm volatile("" : "+s"(tj));   // as fresh(): the tiles' addresses are formed per chunk
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int ti = tj + odd + 2 * x;
+                if (ti < 4) {
+                    f32x4 acc = zero4();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        acc = mma32(*(const bf16x8*)(lds + LB + rd[p] + 16 * tj * D),
+                                    *(const bf16x8*)(lds + LA + rd[p] + 16 * ti * D), acc);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
+                        const bool seen = (x > 0) | (odd > 0) | (n16 >= 4 * gq + e);
+                        acc[e] = seen ? acc[e] * pf[x][e] : 0.0f;
+                    }
+                    *(bf16x4*)(lds + LP + (ti * 4 + tj) * 256 + lane * 4) = to_bf4(acc);
+                }
+            }
+            // the state's part of y, 32 channels at a time
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) y[ti] = zero4();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const bf16x8 sp = cat8(to_bf4(S[2 * p]), to_bf4(S[2 * p + 1]));
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti)
+                    y[ti] = mma32(sp, *(const bf16x8*)(lds + LA + rd[p] + 16 * ti * D), y[ti]);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                const float f = fresh(y0) * step[ti];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[ti][e] *= f;
+            }
+            __syncthreads();
+        }
+        // C columns of this wave
+        bf16x4 cf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cf[j] = tr_read(lds + LC + trc + 16 * j * D);
+        if (kOut) {
+            const bf16x4 none = to_bf4(zero4());
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+#pragma unroll
+                for (int j = 0; j <= ti; j += 2) {
+                    const bf16x4 p0 = *(const bf16x4*)(lds + LP + (ti * 4 + j) * 256 + lane * 4);
+                    if (j + 1 <= ti)
+                        y[ti] = mma32(cat8(cf[j], cf[j + 1]),
+                                      cat8(p0, *(const bf16x4*)(lds + LP + (ti * 4 + j + 1) * 256 + lane * 4)), y[ti]);
+                    else
+                        y[ti] = mma32(cat8(cf[j], none), cat8(p0, none), y[ti]);
+                }
+                const int row = 16 * ti + n16;
+                if (!kTail || row < rem) {
+                    if (y_f32)
+                        *row_ptr<f32x4>(py + ti * gy, oy) = y[ti];
+                    else
+                        *row_ptr<bf16x4>(py + ti * gy, oy) = to_bf4(y[ti]);
+                }
+            }
+        }
+        py += 4 * gy;
+        // state update
+        bf16x8 c1[2], c2[2], c3[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            bf16x4 x1[2], x2[2], x3[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                f32x4 c = from_bf4(cf[2 * j + g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(
+                                                l2 * (float)max(rem - shift - 32 * j - 16 * g - 4 * gq - e, 0))
+                                  : fresh(u0[e]) * step[3 - 2 * j - g];
+                x1[g] = take_high(c);
+                x2[g] = take_high(c);
+                x3[g] = to_bf4(c);
+            }
+            c1[j] = cat8(x1[0], x1[1]);
+            c2[j] = cat8(x2[0], x2[1]);
+            c3[j] = cat8(x3[0], x3[1]);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            bf16x8 bt[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                bt[j] = cat8(tr_read(lds + LB + tr[t >> 1] + 32 * j * D + 4 * (t & 1)),
+                             tr_read(lds + LB + tr[t >> 1] + (32 * j + 16) * D + 4 * (t & 1)));
+            f32x4 acc;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = S[t][e] * fs;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c1[j], acc);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c2[j], acc);
+            if (exact) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c3[j], acc);
+            }
+            S[t] = acc;
+        }
+        if (!kTail) __syncthreads();
+    };
+    int t0 = 0;
+    for (; t0 + SC <= it.len; t0 += SC) chunk(t0, std::false_type{});
+    if (t0 < it.len) chunk(t0, std::true_type{});
+
+    if (s_out != nullptr) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            *(f32x4*)(s_out + soff + vrow * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1)) = S[t];
+    }
+}
+
+hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
+    const int64_t blocks = a.map.items * a.roles;
+    if (states_only)
+        hipLaunchKernelGGL(decay_scan_kernel<false>, dim3((unsigned)blocks), dim3(SC_THREADS), 0, s, a);
+    else
+        hipLaunchKernelGGL(decay_scan_kernel<true>, dim3((unsigned)blocks), dim3(SC_THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
+// Chains the segments of each (sequence, value head): with R_j the own sum of
+// segment j (its state from zero), the state before it in walking order is
+// X_{j+1} = R_j + e^{l len_j} X_j.  Element by element: one thread per four
+// elements, the next segment's sums fetched a step ahead.
+__global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
+    const ItemMap& m = A.map;
+    const int64_t task = blockIdx.x >> 4;   // 16 blocks of 1024 elements per state
+    const int n = (int)(task / m.Hv), h = (int)(task - (int64_t)n * m.Hv);
+    const int e = (int)(blockIdx.x & 15) * 1024 + threadIdx.x * 4;
+    const int64_t slot = A.slot != nullptr ? A.slot[n] : n;
+    if (slot < 0 || slot >= A.slots) return;
+    const int64_t at = (slot * m.Hv + h) * (int64_t)STATE + e;
+    const int len = m.task != nullptr ? m.seq_len[n] : m.len;
+    const int segs = (len + m.seg_len - 1) / m.seg_len;
+    const int64_t base = m.task != nullptr ? m.tape_off[n] + n : (int64_t)n * segs;
+    const float l = A.log_decay[h];
+    Power full(l, m.seg_len);
+    const float f_last = (float)decay_power(l, len - (segs - 1) * m.seg_len);
+    f32x4 x = A.s_in != nullptr ? *(const f32x4*)(A.s_in + at) : zero4();
+    const int64_t step = (int64_t)m.Hv * STATE;
+    float* p = A.seg + (base * m.Hv + h) * STATE + e;
+    auto place = [&](int i) __attribute__((always_inline)) { return A.reverse ? segs - 1 - i : i; };
+    f32x4 next = *(const f32x4*)(p + place(0) * step);
+    for (int i = 0; i < segs; ++i) {
+        const int j = place(i);
+        const f32x4 r = next;
+        next = *(const f32x4*)(p + place(min(i + 1, segs - 1)) * step);
+        *(f32x4*)(p + j * step) = x;
+        x = r + x * (j == segs - 1 ? f_last : full.next());
+    }
+    if (A.s_out != nullptr) *(f32x4*)(A.s_out + at) = x;
+}
+
+hipError_t launch_decay_chain(const ChainArgs& a, hipStream_t s) {
+    const int64_t blocks = (int64_t)a.map.N * a.map.Hv * 16;
+    hipLaunchKernelGGL(decay_chain_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Token-serial form on the FP32 state pool (decode, and sequences of a few
+// tokens).  A workgroup takes 32 of the 128 state rows of one (sequence,
+// value head): a half wave holds a row (4 channels a lane), each wave 4 pairs
+// of rows, so every load and store moves 1 KiB of contiguous state, and o is
+// a sum over the half wave.  No LDS, no barrier; everything FP32.
+__global__ __launch_bounds__(256) void decay_token_kernel(TokenArgs A) {
+    const Item it = find_item(A.map, blockIdx.x >> 2);
+    const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
+    if (slot < 0 || slot >= A.slots) return;
+    const int Hv = A.map.Hv;
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int ch = (lane & 31) * 4;
+    const int row0 = (blockIdx.x & 3) * 32 + (tid >> 6) * 2 + half;   // + 8j
+    float* S = A.pool + (slot * Hv + it.h) * (int64_t)STATE + ch;
+    f32x4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = *(const f32x4*)(S + (row0 + 8 * j) * D);
+    const float f = (float)decay_power(A.log_decay[it.h], 1);
+    const int hq = it.h / A.G;
+    const bf16* q = (const bf16*)A.q + it.tok0 * A.sq + hq * D + ch;
+    const bf16* k = (const bf16*)A.k + it.tok0 * A.sk + hq * D + ch;
+    const bf16* v = (const bf16*)A.v + it.tok0 * A.sv + it.h * D + row0;
+    bf16* o = (bf16*)A.o + (it.tok0 * Hv + it.h) * D + row0;
+    for (int t = 0; t < it.len; ++t) {
+        const f32x4 qf = from_bf4(*(const bf16x4*)(q + t * A.sq));
+        const f32x4 kf = from_bf4(*(const bf16x4*)(k + t * A.sk));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float vj = (float)v[t * A.sv + 8 * j];
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[j][e] = x[j][e] * f + vj * kf[e];
+                sum += x[j][e] * qf[e];
+            }
+            sum = row16_sum(sum);
+            sum += __shfl_xor(sum, 16, 64);
+            if ((lane & 31) == 0) o[(int64_t)t * Hv * D + 8 * j] = (bf16)(A.scale * sum);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *(f32x4*)(S + (row0 + 8 * j) * D) = x[j];
+}
+
+hipError_t launch_decay_token(const TokenArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(decay_token_kernel, dim3((unsigned)(a.map.items * 4)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Sum over the G value heads of a q/k head, in head order, FP32 to BF16: 8
+// channels per thread.
+__global__ __launch_bounds__(256) void decay_group_sum_kernel(const float* src0, const float* src1, bf16* dst0,
+                                                              bf16* dst1, int64_t vecs, int G) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (token, q/k head, 8 channels)
+    if (i >= vecs) return;
+    const int64_t row = i >> 4;
+    const int c = (int)(i & 15) * 8;
+    const float* src = (blockIdx.y ? src1 : src0) + row * G * D + c;
+    f32x4 a = zero4(), b = zero4();
+    for (int g = 0; g < G; ++g) {
+        a += *(const f32x4*)(src + g * D);
+        b += *(const f32x4*)(src + g * D + 4);
+    }
+    *(bf16x8*)((blockIdx.y ? dst1 : dst0) + row * D + c) = cat8(to_bf4(a), to_bf4(b));
+}
+
+hipError_t launch_decay_group_sum(const float* src0, const float* src1, bf16_t* dst0, bf16_t* dst1,
+                                  int64_t tokens, int Hqk, int G, hipStream_t s) {
+    const int64_t vecs = tokens * Hqk * (D / 8);
+    hipLaunchKernelGGL(decay_group_sum_kernel, dim3((unsigned)((vecs + 255) / 256), 2), dim3(256), 0, s, src0, src1,
+                       (bf16*)dst0, (bf16*)dst1, vecs, G);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -1,0 +1,709 @@
+// C ABI of the linear-attention layer operators: argument checks, workspace
+// layout and launches of kda_decay_* (linear attention with a constant decay
+// per head), kda_qknorm_* (query/key norm and rotary rotation) and
+// kda_gnorm_* (gated norm of the heads' outputs).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <vector>
+
+#include "../../include/libkda.h"
+#include "kda_host.h"
+#include "kda_layers.h"
+
+namespace {
+
+using kda_host::check_overlap;
+using kda_host::fail;
+using kda_host::hip_fail;
+using kda_host::SeqPlan;
+using kda_host::Seqs;
+using kda_host::Span;
+
+constexpr int D = 128;
+constexpr int64_t kState = (int64_t)D * D;
+// Largest token stride (elements): the kernels add up to 31 of them in 32 bits.
+constexpr int64_t kMaxStride = (int64_t)1 << 25;
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Runs an entry point's body; an exception (host memory) becomes a status.
+template <class F>
+kda_status guarded(F f) {
+    try {
+        return f();
+    } catch (const std::exception& e) {
+        return fail(KDA_ERR_HIP, "host error: %s", e.what());
+    }
+}
+
+// 0 means dense rows.
+kda_status check_stride(int64_t& stride, int heads, const char* name) {
+    if (stride == 0) stride = (int64_t)heads * D;
+    if (stride < (int64_t)heads * D || stride > kMaxStride || stride % 8 != 0)
+        return fail(KDA_ERR_SHAPE, "%s token stride must be a multiple of 8 in [%d, %lld] (got %lld)", name, heads * D,
+                    (long long)kMaxStride, (long long)stride);
+    return KDA_OK;
+}
+
+kda_status check_align(const void* p, const char* name) {
+    if (((uintptr_t)p & 15) != 0) return fail(KDA_ERR_SHAPE, "%s must be 16-byte aligned", name);
+    return KDA_OK;
+}
+kda_status check_align(std::initializer_list<std::pair<const void*, const char*>> ps) {
+    for (const auto& p : ps) {
+        kda_status s = check_align(p.first, p.second);
+        if (s != KDA_OK) return s;
+    }
+    return KDA_OK;
+}
+
+// Bytes from a strided operand's first element to behind its last.
+size_t strided_bytes(int64_t tokens, int64_t stride, int heads) {
+    return (size_t)((tokens - 1) * stride + (int64_t)heads * D) * 2;
+}
+
+// ---------------------------------------------------------------------------
+// linear attention with a constant decay per head
+// ---------------------------------------------------------------------------
+struct Decay {
+    Seqs s;
+    int B = 0, T = 0;
+    bool packed = false;
+    float scale = 0;
+    int64_t sq = 0, sk = 0, sv = 0;
+    int segment = 0;       // the caller's choice; 0: automatic
+};
+
+kda_status check_decay(const kda_decay_problem* p, Decay& d) {
+    if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
+    kda_status s = kda_host::check_seqs(p->B, p->T, p->Hqk, p->Hv, p->N, p->cu_seqlens, p->cu_seqlens_host, d.s);
+    if (s != KDA_OK) return s;
+    d.B = p->B;
+    d.T = p->T;
+    d.packed = p->cu_seqlens != nullptr;
+    d.scale = p->scale == 0.0f ? 1.0f / std::sqrt(128.0f) : p->scale;
+    if (!(d.scale > 0.0f) || !std::isfinite(d.scale))
+        return fail(KDA_ERR_SCALE, "scale must be 0 or finite and positive (got %g)", (double)p->scale);
+    d.sq = p->q_stride;
+    d.sk = p->k_stride;
+    d.sv = p->v_stride;
+    if ((s = check_stride(d.sq, p->Hqk, "q")) != KDA_OK || (s = check_stride(d.sk, p->Hqk, "k")) != KDA_OK ||
+        (s = check_stride(d.sv, p->Hv, "v")) != KDA_OK)
+        return s;
+    if ((int64_t)p->Hv * D > kMaxStride) return fail(KDA_ERR_SHAPE, "too many value heads (%d)", p->Hv);
+    if (p->segment < 0 || p->segment % 64 != 0)
+        return fail(KDA_ERR_ROUTE, "segment must be 0 or a positive multiple of 64 (got %d)", p->segment);
+    d.segment = p->segment;
+    return KDA_OK;
+}
+
+int64_t total_segs(const Decay& d, int seg) {
+    int64_t n = 0;
+    for (int64_t len : d.s.len) n += (len + seg - 1) / seg;
+    return n;
+}
+
+// Tokens per segment of a scan over `roles` forms, or 0 for whole sequences.
+// A whole-sequence scan runs one workgroup per (form, sequence, value head)
+// and two fit a compute unit, so with fewer than 512 of them the card is not
+// full; cutting the sequences into segments costs another pass over two of
+// the three operands and 192 KiB of FP32 state traffic per segment and head.
+int auto_segment(const Decay& d, int roles) {
+    if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
+    const int64_t tasks = (int64_t)d.s.N * d.s.Hv * roles;
+    if (tasks >= 512 || d.s.max_len <= 256) return 0;
+    int64_t seg = (d.s.tokens * d.s.Hv * roles / 768 + 63) / 64 * 64;
+    seg = std::max<int64_t>(seg, 256);
+    return d.s.max_len > seg ? (int)seg : 0;
+}
+
+struct DecayWs {
+    size_t seg_f = 0, seg_r = 0, part_q = 0, part_k = 0, total = 0;
+};
+DecayWs decay_ws(const Decay& d, int seg, bool backward) {
+    DecayWs w;
+    size_t off = 0;
+    const size_t states = seg ? (size_t)total_segs(d, seg) * d.s.Hv * kState * sizeof(float) : 0;
+    w.seg_f = off;
+    off = align256(off + states);
+    if (backward) {
+        w.seg_r = off;
+        off = align256(off + states);
+        const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * sizeof(float) : 0;
+        w.part_q = off;
+        off = align256(off + part);
+        w.part_k = off;
+        off = align256(off + part);
+    }
+    w.total = off;
+    return w;
+}
+
+// The item map of a call and its hold on the device schedule (packed calls).
+kda_status make_map(const Decay& d, int seg, hipStream_t stream, SeqPlan& plan, kda::ItemMap& m) {
+    m = kda::ItemMap{};
+    m.N = d.s.N;
+    m.Hv = d.s.Hv;
+    m.len = d.T;
+    m.seg_len = seg;
+    m.items = (seg ? total_segs(d, seg) : (int64_t)d.s.N) * d.s.Hv;
+    if (d.packed) {
+        kda_status s = kda_host::get_seq_plan(d.s, d.B, d.T, d.packed, seg ? seg : 256, stream, plan);
+        if (s != KDA_OK) return s;
+        m.task = plan.dev.task;
+        m.seg = plan.seg;
+        m.seq_start = plan.dev.seq_start;
+        m.seq_len = plan.dev.seq_len;
+        m.tape_off = plan.dev.tape_off;
+    }
+    return KDA_OK;
+}
+
+kda_status check_grid(int64_t blocks) {
+    if (blocks > (int64_t)INT32_MAX) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks");
+    return KDA_OK;
+}
+
+// o's form over whole sequences or segments; the states come from `s_in` and
+// go to `s_out`, both by slot.
+kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const void* q, const void* k, const void* v,
+                       const float* log_decay, const float* s_in, float* s_out, const int32_t* slot, int64_t slots,
+                       void* o, char* ws, hipStream_t stream) {
+    kda::ScanArgs a{};
+    a.map = m;
+    a.roles = 1;
+    a.share = d.s.G;
+    a.log_decay = log_decay;
+    a.scale = d.scale;
+    a.slot = slot;
+    a.slots = slots;
+    kda::ScanRole& r = a.role[0];
+    r.a = (const kda::bf16_t*)q; r.sa = d.sq; r.ga = d.s.G;
+    r.b = (const kda::bf16_t*)k; r.sb = d.sk; r.gb = d.s.G;
+    r.c = (const kda::bf16_t*)v; r.sc = d.sv; r.gc = 1;
+    r.y = o;
+    r.s_in = s_in;
+    r.s_out = s_out;
+    hipError_t e;
+    if (seg != 0) {
+        float* states = (float*)ws;
+        kda::ScanArgs b = a;
+        b.role[0].s_in = nullptr;
+        b.role[0].s_out = states;
+        b.role[0].s_by_seg = 1;
+        e = kda::launch_decay_scan(b, true, stream);
+        if (e != hipSuccess) return hip_fail(e, "segment state launch");
+        kda::ChainArgs c{};
+        c.map = m;
+        c.log_decay = log_decay;
+        c.seg = states;
+        c.s_in = s_in;
+        c.s_out = s_out;
+        c.slot = slot;
+        c.slots = slots;
+        e = kda::launch_decay_chain(c, stream);
+        if (e != hipSuccess) return hip_fail(e, "segment chain launch");
+        r.s_in = states;
+        r.s_out = nullptr;
+        r.s_by_seg = 1;
+    }
+    e = kda::launch_decay_scan(a, false, stream);
+    if (e != hipSuccess) return hip_fail(e, "decay scan launch");
+    return KDA_OK;
+}
+
+// Longest sequence that the token-serial kernel takes in kda_decay_infer.
+constexpr int64_t kTokenSerialMax = 8;
+
+kda_status check_ws(const void* ws, size_t bytes, size_t need) {
+    if (need == 0) return KDA_OK;
+    if (ws == nullptr) return fail(KDA_ERR_NULL_ARG, "workspace is NULL (needs %zu bytes)", need);
+    if (bytes < need) return fail(KDA_ERR_WORKSPACE_SIZE, "workspace has %zu bytes, needs %zu", bytes, need);
+    return check_align(ws, "workspace");
+}
+
+bool token_serial(const Decay& d) { return d.s.max_len <= kTokenSerialMax; }
+
+// ---------------------------------------------------------------------------
+// row norms
+// ---------------------------------------------------------------------------
+kda_status check_qknorm(const kda_qknorm_problem* p, kda::QkNormArgs& a) {
+    if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
+    if (p->B < 1 || p->T < 1 || p->Hq < 1 || p->Hk < 1)
+        return fail(KDA_ERR_SHAPE, "B, T, Hq and Hk must be >= 1 (got %d %d %d %d)", p->B, p->T, p->Hq, p->Hk);
+    if ((int64_t)p->Hq + p->Hk > kMaxStride / D)
+        return fail(KDA_ERR_SHAPE, "too many heads (%d + %d)", p->Hq, p->Hk);
+    if (p->rot_dim < 8 || p->rot_dim > D || p->rot_dim % 8 != 0)
+        return fail(KDA_ERR_SHAPE, "rot_dim must be a multiple of 8 in [8, 128] (got %d)", p->rot_dim);
+    if (p->interleaved != 0 && p->interleaved != 1)
+        return fail(KDA_ERR_SHAPE, "interleaved must be 0 or 1 (got %d)", p->interleaved);
+    if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
+        return fail(KDA_ERR_SHAPE, "eps must be finite and positive (got %g)", (double)p->eps);
+    if (p->table_rows < 1 || p->table_rows > ((int64_t)1 << 40))
+        return fail(KDA_ERR_SHAPE, "table_rows out of range (%lld)", (long long)p->table_rows);
+    a.tokens = (int64_t)p->B * p->T;
+    a.T = p->T;
+    a.Hq = p->Hq;
+    a.Hk = p->Hk;
+    a.rot = p->rot_dim;
+    a.interleaved = p->interleaved;
+    a.eps = p->eps;
+    a.rows = p->table_rows;
+    a.sq = p->q_stride;
+    a.sk = p->k_stride;
+    kda_status s;
+    if ((s = check_stride(a.sq, p->Hq, "q")) != KDA_OK || (s = check_stride(a.sk, p->Hk, "k")) != KDA_OK) return s;
+    return KDA_OK;
+}
+kda_status qknorm_inputs(const kda_qknorm_problem* p, kda::QkNormArgs& a, const void* q, const void* k,
+                         const float* wq, const float* wk, const float* cos, const float* sin,
+                         const int64_t* positions, std::vector<Span>& ins) {
+    if (!q || !k || !wq || !wk || !cos || !sin)
+        return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_qknorm is NULL");
+    if (positions == nullptr && p->table_rows < p->T)
+        return fail(KDA_ERR_SHAPE, "without positions the table needs T=%d rows (has %lld)", p->T,
+                    (long long)p->table_rows);
+    kda_status s = check_align({{q, "q"}, {k, "k"}, {cos, "cos"}, {sin, "sin"}});
+    if (s != KDA_OK) return s;
+    a.q = (const kda::bf16_t*)q;
+    a.k = (const kda::bf16_t*)k;
+    a.wq = wq;
+    a.wk = wk;
+    a.cos = cos;
+    a.sin = sin;
+    a.positions = positions;
+    const size_t table = (size_t)a.rows * (a.rot / 2) * 4;
+    ins = {{q, strided_bytes(a.tokens, a.sq, a.Hq), "q"}, {k, strided_bytes(a.tokens, a.sk, a.Hk), "k"},
+           {wq, D * 4, "q_weight"}, {wk, D * 4, "k_weight"}, {cos, table, "cos"}, {sin, table, "sin"},
+           {positions, positions ? (size_t)a.tokens * 8 : 0, "positions"}};
+    return KDA_OK;
+}
+size_t qknorm_ws(const kda::QkNormArgs& a) {
+    return (size_t)kda::rownorm_blocks(a.tokens * (a.Hq + a.Hk)) * 2 * D * sizeof(float);
+}
+
+kda_status check_gnorm(const kda_gnorm_problem* p, kda::GNormArgs& a) {
+    if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
+    if (p->B < 1 || p->T < 1 || p->H < 1)
+        return fail(KDA_ERR_SHAPE, "B, T and H must be >= 1 (got %d %d %d)", p->B, p->T, p->H);
+    if (p->activation != KDA_GATE_SIGMOID && p->activation != KDA_GATE_SILU)
+        return fail(KDA_ERR_SHAPE, "unknown activation %d", p->activation);
+    if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
+        return fail(KDA_ERR_SHAPE, "eps must be finite and positive (got %g)", (double)p->eps);
+    a.tokens = (int64_t)p->B * p->T;
+    a.H = p->H;
+    a.silu = p->activation == KDA_GATE_SILU;
+    a.eps = p->eps;
+    a.sx = p->x_stride;
+    a.sg = p->gate_stride;
+    kda_status s;
+    if ((s = check_stride(a.sx, p->H, "x")) != KDA_OK || (s = check_stride(a.sg, p->H, "gate")) != KDA_OK) return s;
+    return KDA_OK;
+}
+size_t gnorm_ws(const kda::GNormArgs& a) {
+    return (size_t)kda::rownorm_blocks(a.tokens * a.H) * D * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_decay_fwd_workspace_bytes(const kda_decay_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = decay_ws(d, auto_segment(d, 1), false).total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_decay_bwd_workspace_bytes(const kda_decay_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = decay_ws(d, auto_segment(d, 3), true).total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_decay_fwd(const kda_decay_problem* pp, const void* q, const void* k, const void* v,
+                         const float* log_decay, const float* initial_state, void* o, float* final_state,
+                         void* workspace, size_t workspace_bytes, void* stream_) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !log_decay || !o)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_decay_fwd is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {initial_state, "initial_state"}, {o, "o"},
+                         {final_state, "final_state"}});
+        if (s != KDA_OK) return s;
+        const int seg = auto_segment(d, 1);
+        const size_t need = decay_ws(d, seg, false).total;
+        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
+        const std::vector<Span> ins = {
+            {q, strided_bytes(d.s.tokens, d.sq, d.s.Hqk), "q"}, {k, strided_bytes(d.s.tokens, d.sk, d.s.Hqk), "k"},
+            {v, strided_bytes(d.s.tokens, d.sv, d.s.Hv), "v"}, {log_decay, (size_t)d.s.Hv * 4, "log_decay"},
+            {initial_state, initial_state ? st : 0, "initial_state"},
+            {pp->cu_seqlens, d.packed ? (size_t)(d.s.N + 1) * 8 : 0, "cu_seqlens"}};
+        s = check_overlap({{o, (size_t)d.s.tokens * d.s.Hv * D * 2, "o"},
+                           {final_state, final_state ? st : 0, "final_state"},
+                           {workspace, need, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::ItemMap m;
+        if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
+        if ((s = check_grid(std::max(m.items, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
+        return run_forward(d, seg, m, q, k, v, log_decay, initial_state, final_state, nullptr, d.s.N, o,
+                           (char*)workspace, stream);
+    });
+}
+
+kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void* k, const void* v,
+                         const float* log_decay, const float* initial_state, const void* d_o,
+                         const float* dfinal_state, void* dq, void* dk, void* dv, float* dinitial_state,
+                         void* workspace, size_t workspace_bytes, void* stream_) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_decay_bwd is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {initial_state, "initial_state"}, {d_o, "do"},
+                         {dfinal_state, "dfinal_state"}, {dq, "dq"}, {dk, "dk"}, {dv, "dv"},
+                         {dinitial_state, "dinitial_state"}});
+        if (s != KDA_OK) return s;
+        const int seg = auto_segment(d, 3);
+        const DecayWs wl = decay_ws(d, seg, true);
+        if ((s = check_ws(workspace, workspace_bytes, wl.total)) != KDA_OK) return s;
+        const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
+        const size_t tq = (size_t)d.s.tokens * d.s.Hqk * D * 2, tv = (size_t)d.s.tokens * d.s.Hv * D * 2;
+        const std::vector<Span> ins = {
+            {q, strided_bytes(d.s.tokens, d.sq, d.s.Hqk), "q"}, {k, strided_bytes(d.s.tokens, d.sk, d.s.Hqk), "k"},
+            {v, strided_bytes(d.s.tokens, d.sv, d.s.Hv), "v"}, {log_decay, (size_t)d.s.Hv * 4, "log_decay"},
+            {initial_state, initial_state ? st : 0, "initial_state"}, {d_o, tv, "do"},
+            {dfinal_state, dfinal_state ? st : 0, "dfinal_state"},
+            {pp->cu_seqlens, d.packed ? (size_t)(d.s.N + 1) * 8 : 0, "cu_seqlens"}};
+        s = check_overlap({{dq, tq, "dq"}, {dk, tq, "dk"}, {dv, tv, "dv"},
+                           {dinitial_state, dinitial_state ? st : 0, "dinitial_state"},
+                           {workspace, wl.total, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::ItemMap m;
+        if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
+        if ((s = check_grid(std::max(3 * m.items, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
+        if ((s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
+
+        char* ws = (char*)workspace;
+        const int G = d.s.G;
+        const int64_t sdo = (int64_t)d.s.Hv * D;
+        kda::ScanArgs a{};
+        a.map = m;
+        a.roles = 3;
+        a.share = 3 * G;
+        a.log_decay = log_decay;
+        a.scale = d.scale;
+        a.slots = d.s.N;
+        auto q_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)q; st_ = d.sq; g = G; };
+        auto k_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)k; st_ = d.sk; g = G; };
+        auto v_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)v; st_ = d.sv; g = 1; };
+        auto o_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)d_o; st_ = sdo; g = 1; };
+        // dq: (do, v, k) forward in time, the state read transposed
+        kda::ScanRole& rq = a.role[0];
+        o_op(rq.a, rq.sa, rq.ga); v_op(rq.b, rq.sb, rq.gb); k_op(rq.c, rq.sc, rq.gc);
+        rq.y = G > 1 ? (void*)(ws + wl.part_q) : dq;
+        rq.y_f32 = G > 1;
+        rq.s_in = initial_state;
+        rq.s_in_t = 1;
+        // dk: (v, do, q) backward in time
+        kda::ScanRole& rk = a.role[1];
+        v_op(rk.a, rk.sa, rk.ga); o_op(rk.b, rk.sb, rk.gb); q_op(rk.c, rk.sc, rk.gc);
+        rk.y = G > 1 ? (void*)(ws + wl.part_k) : dk;
+        rk.y_f32 = G > 1;
+        rk.reverse = 1;
+        rk.s_in = dfinal_state;
+        rk.s_in_t = 1;
+        // dv: (k, q, do) backward in time; its state ends as dinitial_state
+        kda::ScanRole& rv = a.role[2];
+        k_op(rv.a, rv.sa, rv.ga); q_op(rv.b, rv.sb, rv.gb); o_op(rv.c, rv.sc, rv.gc);
+        rv.y = dv;
+        rv.reverse = 1;
+        rv.s_in = dfinal_state;
+        rv.s_out = dinitial_state;
+
+        hipError_t e;
+        if (seg != 0) {
+            float* fwd = (float*)(ws + wl.seg_f);
+            float* bwd = (float*)(ws + wl.seg_r);
+            kda::ScanArgs b = a;
+            b.roles = 2;
+            b.share = 2 * G;
+            // the segments' own sums: of v k^T forward, of do q^T backward in time
+            kda::ScanRole& f = b.role[0];
+            f = kda::ScanRole{};
+            k_op(f.b, f.sb, f.gb); v_op(f.c, f.sc, f.gc);
+            f.ga = 1;
+            f.s_out = fwd;
+            f.s_by_seg = 1;
+            kda::ScanRole& r = b.role[1];
+            r = kda::ScanRole{};
+            q_op(r.b, r.sb, r.gb); o_op(r.c, r.sc, r.gc);
+            r.ga = 1;
+            r.reverse = 1;
+            r.s_out = bwd;
+            r.s_by_seg = 1;
+            e = kda::launch_decay_scan(b, true, stream);
+            if (e != hipSuccess) return hip_fail(e, "segment state launch");
+            kda::ChainArgs c{};
+            c.map = m;
+            c.log_decay = log_decay;
+            c.slots = d.s.N;
+            c.seg = fwd;
+            c.s_in = initial_state;
+            e = kda::launch_decay_chain(c, stream);
+            if (e != hipSuccess) return hip_fail(e, "segment chain launch");
+            c.seg = bwd;
+            c.s_in = dfinal_state;
+            c.s_out = dinitial_state;
+            c.reverse = 1;
+            e = kda::launch_decay_chain(c, stream);
+            if (e != hipSuccess) return hip_fail(e, "segment chain launch");
+            rq.s_in = fwd;
+            rk.s_in = rv.s_in = bwd;
+            rv.s_out = nullptr;
+            rq.s_by_seg = rk.s_by_seg = rv.s_by_seg = 1;
+        }
+        e = kda::launch_decay_scan(a, false, stream);
+        if (e != hipSuccess) return hip_fail(e, "decay adjoint launch");
+        if (G > 1) {
+            e = kda::launch_decay_group_sum((const float*)(ws + wl.part_q), (const float*)(ws + wl.part_k),
+                                            (kda::bf16_t*)dq, (kda::bf16_t*)dk, d.s.tokens, d.s.Hqk, G, stream);
+            if (e != hipSuccess) return hip_fail(e, "group sum launch");
+        }
+        return KDA_OK;
+    });
+}
+
+kda_status kda_decay_infer_workspace_bytes(const kda_decay_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = token_serial(d) ? 0 : decay_ws(d, auto_segment(d, 1), false).total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_decay_infer(const kda_decay_problem* pp, const void* q, const void* k, const void* v,
+                           const float* log_decay, float* state_pool, int64_t pool_slots,
+                           const int32_t* state_indices, const int32_t* state_indices_host, void* o,
+                           void* workspace, size_t workspace_bytes, void* stream_) {
+    return guarded([&]() -> kda_status {
+        Decay d;
+        kda_status s = check_decay(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !log_decay || !state_pool || !o)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_decay_infer is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {state_pool, "state_pool"}, {o, "o"}});
+        if (s != KDA_OK) return s;
+        if (pool_slots < 1 || pool_slots > ((int64_t)1 << 40) / ((int64_t)d.s.Hv * kState))
+            return fail(KDA_ERR_SHAPE, "pool_slots out of range (%lld)", (long long)pool_slots);
+        if ((state_indices == nullptr) != (state_indices_host == nullptr))
+            return fail(KDA_ERR_NULL_ARG, "state_indices and state_indices_host go together");
+        if (state_indices_host != nullptr) {
+            std::vector<int32_t> sorted(state_indices_host, state_indices_host + d.s.N);
+            for (int i = 0; i < d.s.N; ++i)
+                if (sorted[i] < 0 || sorted[i] >= pool_slots)
+                    return fail(KDA_ERR_SHAPE, "state_indices[%d] = %d is outside the pool", i, sorted[i]);
+            std::sort(sorted.begin(), sorted.end());
+            for (int i = 1; i < d.s.N; ++i)
+                if (sorted[i] == sorted[i - 1])
+                    return fail(KDA_ERR_SHAPE, "pool slot %d is named twice", sorted[i]);
+        } else if (pool_slots < d.s.N) {
+            return fail(KDA_ERR_SHAPE, "without state_indices the pool needs N=%d slots (has %lld)", d.s.N,
+                        (long long)pool_slots);
+        }
+        const bool serial = token_serial(d);
+        const int seg = serial ? 0 : auto_segment(d, 1);
+        const size_t need = serial ? 0 : decay_ws(d, seg, false).total;
+        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const std::vector<Span> ins = {
+            {q, strided_bytes(d.s.tokens, d.sq, d.s.Hqk), "q"}, {k, strided_bytes(d.s.tokens, d.sk, d.s.Hqk), "k"},
+            {v, strided_bytes(d.s.tokens, d.sv, d.s.Hv), "v"}, {log_decay, (size_t)d.s.Hv * 4, "log_decay"},
+            {pp->cu_seqlens, d.packed ? (size_t)(d.s.N + 1) * 8 : 0, "cu_seqlens"},
+            {state_indices, state_indices ? (size_t)d.s.N * 4 : 0, "state_indices"}};
+        s = check_overlap({{o, (size_t)d.s.tokens * d.s.Hv * D * 2, "o"},
+                           {state_pool, (size_t)pool_slots * d.s.Hv * kState * 4, "state_pool"},
+                           {workspace, need, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::ItemMap m;
+        if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
+        if ((s = check_grid(std::max(m.items * 4, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
+        if (!serial)
+            return run_forward(d, seg, m, q, k, v, log_decay, state_pool, state_pool, state_indices, pool_slots, o,
+                               (char*)workspace, stream);
+        kda::TokenArgs t{};
+        t.map = m;
+        t.q = (const kda::bf16_t*)q; t.sq = d.sq;
+        t.k = (const kda::bf16_t*)k; t.sk = d.sk;
+        t.v = (const kda::bf16_t*)v; t.sv = d.sv;
+        t.G = d.s.G;
+        t.o = (kda::bf16_t*)o;
+        t.log_decay = log_decay;
+        t.scale = d.scale;
+        t.pool = state_pool;
+        t.slot = state_indices;
+        t.slots = pool_slots;
+        hipError_t e = kda::launch_decay_token(t, stream);
+        if (e != hipSuccess) return hip_fail(e, "decay decode launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_qknorm_fwd(const kda_qknorm_problem* pp, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const float* cos, const float* sin, const int64_t* positions,
+                          void* q_out, void* k_out, void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::QkNormArgs a{};
+        kda_status s = check_qknorm(pp, a);
+        if (s != KDA_OK) return s;
+        std::vector<Span> ins;
+        if ((s = qknorm_inputs(pp, a, q, k, q_weight, k_weight, cos, sin, positions, ins)) != KDA_OK) return s;
+        if (!q_out || !k_out) return fail(KDA_ERR_NULL_ARG, "an output of kda_qknorm_fwd is NULL");
+        if ((s = check_align({{q_out, "q_out"}, {k_out, "k_out"}})) != KDA_OK) return s;
+        s = check_overlap({{q_out, (size_t)a.tokens * a.Hq * D * 2, "q_out"},
+                           {k_out, (size_t)a.tokens * a.Hk * D * 2, "k_out"}}, ins);
+        if (s != KDA_OK) return s;
+        a.yq = (kda::bf16_t*)q_out;
+        a.yk = (kda::bf16_t*)k_out;
+        hipError_t e = kda::launch_qknorm_fwd(a, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "query/key norm launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_qknorm_bwd_workspace_bytes(const kda_qknorm_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        kda::QkNormArgs a{};
+        kda_status s = check_qknorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = qknorm_ws(a);
+        return KDA_OK;
+    });
+}
+
+kda_status kda_qknorm_bwd(const kda_qknorm_problem* pp, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const float* cos, const float* sin, const int64_t* positions,
+                          const void* dq_out, const void* dk_out, void* dq, void* dk, float* dq_weight,
+                          float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::QkNormArgs a{};
+        kda_status s = check_qknorm(pp, a);
+        if (s != KDA_OK) return s;
+        std::vector<Span> ins;
+        if ((s = qknorm_inputs(pp, a, q, k, q_weight, k_weight, cos, sin, positions, ins)) != KDA_OK) return s;
+        if (!dq_out || !dk_out || !dq || !dk || !dq_weight || !dk_weight)
+            return fail(KDA_ERR_NULL_ARG, "a gradient argument of kda_qknorm_bwd is NULL");
+        if ((s = check_align({{dq_out, "dq_out"}, {dk_out, "dk_out"}, {dq, "dq"}, {dk, "dk"}})) != KDA_OK) return s;
+        const size_t need = qknorm_ws(a);
+        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const size_t tq = (size_t)a.tokens * a.Hq * D * 2, tk = (size_t)a.tokens * a.Hk * D * 2;
+        ins.push_back({dq_out, tq, "dq_out"});
+        ins.push_back({dk_out, tk, "dk_out"});
+        s = check_overlap({{dq, tq, "dq"}, {dk, tk, "dk"}, {dq_weight, D * 4, "dq_weight"},
+                           {dk_weight, D * 4, "dk_weight"}, {workspace, need, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        a.dyq = (const kda::bf16_t*)dq_out;
+        a.dyk = (const kda::bf16_t*)dk_out;
+        a.dq = (kda::bf16_t*)dq;
+        a.dk = (kda::bf16_t*)dk;
+        a.dwq = dq_weight;
+        a.dwk = dk_weight;
+        a.part = (float*)workspace;
+        hipError_t e = kda::launch_qknorm_bwd(a, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "query/key norm backward launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_gnorm_fwd(const kda_gnorm_problem* pp, const void* x, const void* gate, const float* weight, void* y,
+                         void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::GNormArgs a{};
+        kda_status s = check_gnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (!x || !gate || !weight || !y) return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_gnorm_fwd is NULL");
+        if ((s = check_align({{x, "x"}, {gate, "gate"}, {y, "y"}})) != KDA_OK) return s;
+        s = check_overlap({{y, (size_t)a.tokens * a.H * D * 2, "y"}},
+                          {{x, strided_bytes(a.tokens, a.sx, a.H), "x"},
+                           {gate, strided_bytes(a.tokens, a.sg, a.H), "gate"}, {weight, D * 4, "weight"}});
+        if (s != KDA_OK) return s;
+        a.x = (const kda::bf16_t*)x;
+        a.g = (const kda::bf16_t*)gate;
+        a.w = weight;
+        a.y = (kda::bf16_t*)y;
+        hipError_t e = kda::launch_gnorm_fwd(a, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "gated norm launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_gnorm_bwd_workspace_bytes(const kda_gnorm_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        kda::GNormArgs a{};
+        kda_status s = check_gnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = gnorm_ws(a);
+        return KDA_OK;
+    });
+}
+
+kda_status kda_gnorm_bwd(const kda_gnorm_problem* pp, const void* x, const void* gate, const float* weight,
+                         const void* dy, void* dx, void* dgate, float* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::GNormArgs a{};
+        kda_status s = check_gnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (!x || !gate || !weight || !dy || !dx || !dgate || !dweight)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_gnorm_bwd is NULL");
+        if ((s = check_align({{x, "x"}, {gate, "gate"}, {dy, "dy"}, {dx, "dx"}, {dgate, "dgate"}})) != KDA_OK) return s;
+        const size_t need = gnorm_ws(a);
+        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const size_t row = (size_t)a.tokens * a.H * D * 2;
+        s = check_overlap({{dx, row, "dx"}, {dgate, row, "dgate"}, {dweight, D * 4, "dweight"},
+                           {workspace, need, "workspace"}},
+                          {{x, strided_bytes(a.tokens, a.sx, a.H), "x"},
+                           {gate, strided_bytes(a.tokens, a.sg, a.H), "gate"}, {weight, D * 4, "weight"},
+                           {dy, row, "dy"}});
+        if (s != KDA_OK) return s;
+        a.x = (const kda::bf16_t*)x;
+        a.g = (const kda::bf16_t*)gate;
+        a.w = weight;
+        a.dy = (const kda::bf16_t*)dy;
+        a.dx = (kda::bf16_t*)dx;
+        a.dg = (kda::bf16_t*)dgate;
+        a.dw = dweight;
+        a.part = (float*)workspace;
+        hipError_t e = kda::launch_gnorm_bwd(a, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "gated norm backward launch");
+        return KDA_OK;
+    });
+}
+
+}  // extern "C"

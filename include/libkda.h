@@ -362,6 +362,124 @@ kda_status kda_infer(const kda_infer_problem* p,
                      const void* beta, const float* A_log, const float* dt_bias,
                      void* state_pool, void* o, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a linear-attention layer beside KDA: linear attention with a
+ * constant decay per head, the query/key norm with rotary rotation in front
+ * of it, and the gated norm of the heads' outputs behind it.  Rows of 128
+ * channels as above.  The same rules hold for ownership, errors, streams and
+ * stream capture, with two additions:
+ *   - Token strides.  The operands named here (q, k, v, x, gate) may be slices
+ *     of a wider row, such as one fused projection's output: `*_stride` is
+ *     the distance of two tokens in elements (0: dense), a multiple of 8, with
+ *     heads and channels dense inside the token and batch rows T strides
+ *     apart.  Outputs and adjoints are dense.  Tensors are 16-byte aligned.
+ *   - Schedules.  Only packed calls (cu_seqlens) of kda_decay_* use the cached
+ *     schedule; every other call may be captured at once.  A workspace is used
+ *     by one call at a time: graphs or streams that may overlap need their own.
+ * Inputs are read once; values at tokens behind a sequence's end, and in other
+ * sequences, are never read for it.  Finite inputs are expected: a NaN or an
+ * infinity in a token's row may reach every output of that sequence and head
+ * from its 16-token tile on, also at earlier tokens of the tile.
+ * ------------------------------------------------------------------------- */
+
+/* Linear attention with a constant decay per value head.  For every sequence
+ * and value head h, with the q/k head h / (Hv/Hqk), an FP32 value-first state
+ * S[v][k] starts at initial_state and, token by token,
+ *     S <- exp(log_decay[h]) S + v k^T,      o = scale S q .
+ * log_decay (FP32 [Hv], device) is a constant of the layer and must be <= 0
+ * (minus infinity forgets every earlier token); it is not checked and has no
+ * gradient.  All sums and the states are FP32. */
+typedef struct {
+    int32_t B, T, Hqk, Hv, N;        /* as in kda_problem */
+    const int64_t* cu_seqlens;       /* device INT64 [N+1], or NULL for fixed layout */
+    const int64_t* cu_seqlens_host;  /* host mirror, NULL iff cu_seqlens is NULL */
+    float scale;                     /* 0 selects 1/sqrt(128); else finite and positive */
+    int32_t segment;                 /* tokens per segment when the sequences are split to fill the
+                                        card: 0 automatic, else a multiple of 64 (for testing) */
+    int64_t q_stride, k_stride, v_stride;  /* token strides in elements; 0: dense */
+} kda_decay_problem;
+
+/* Workspace bytes (0 when none is needed; the workspace may then be NULL). */
+kda_status kda_decay_fwd_workspace_bytes(const kda_decay_problem* p, size_t* bytes);
+kda_status kda_decay_bwd_workspace_bytes(const kda_decay_problem* p, size_t* bytes);
+kda_status kda_decay_infer_workspace_bytes(const kda_decay_problem* p, size_t* bytes);
+
+/* Training forward.  q, k BF16 [B][T][Hqk][128], v, o BF16 [B][T][Hv][128],
+ * states FP32 [N][Hv][128][128].  initial_state NULL starts from zero;
+ * final_state may be NULL.  Nothing is saved for the backward, which reads
+ * the inputs again. */
+kda_status kda_decay_fwd(const kda_decay_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, const float* initial_state, void* o, float* final_state,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Training backward: the gradients of <do, o> + <dfinal_state, S_final>.
+ * dfinal_state NULL counts as zero; dinitial_state may be NULL.  dq and dk
+ * sum over the value heads that share a q/k head, in head order. */
+kda_status kda_decay_bwd(const kda_decay_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, const float* initial_state, const void* d_o,
+                         const float* dfinal_state, void* dq, void* dk, void* dv, float* dinitial_state,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode (sequences of a few tokens, token by token) and prefill (longer
+ * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated
+ * in place: sequence n reads and writes slot state_indices[n] (slot n when
+ * NULL); other slots are not touched.  The indices must be distinct and in
+ * range, checked on the host mirror (given iff state_indices is).  A slot
+ * that the device copy places outside the pool (a replayed graph's inactive
+ * sequence, say -1) is skipped, and its rows of o are left as they were. */
+kda_status kda_decay_infer(const kda_decay_problem* p, const void* q, const void* k, const void* v,
+                           const float* log_decay, float* state_pool, int64_t pool_slots,
+                           const int32_t* state_indices, const int32_t* state_indices_host, void* o,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norm and rotation of queries and keys, per head:
+ *     n = w x / sqrt(mean(x^2) + eps),       y = R(position) n
+ * where R turns the first rot_dim channels (a multiple of 8) by the angles of
+ * the position's row of cos and sin (FP32 [table_rows][rot_dim/2]): pair p is
+ * channels p and p + rot_dim/2, or 2p and 2p+1 when interleaved.  q BF16
+ * [B][T][Hq][128], k BF16 [B][T][Hk][128], weights FP32 [128].  positions:
+ * device INT64 [B][T], or NULL for the token's index in its row.  A position
+ * outside the table makes its token's outputs (and, in the backward, the
+ * weight gradients) NaN. */
+typedef struct {
+    int32_t B, T, Hq, Hk;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float eps;
+    int64_t table_rows;
+    int64_t q_stride, k_stride;
+} kda_qknorm_problem;
+
+kda_status kda_qknorm_fwd(const kda_qknorm_problem* p, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const float* cos, const float* sin, const int64_t* positions,
+                          void* q_out, void* k_out, void* stream);
+kda_status kda_qknorm_bwd_workspace_bytes(const kda_qknorm_problem* p, size_t* bytes);
+/* From the forward's inputs and the adjoints of its outputs.  The weight
+ * gradients sum over all tokens and heads in a fixed order. */
+kda_status kda_qknorm_bwd(const kda_qknorm_problem* p, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const float* cos, const float* sin, const int64_t* positions,
+                          const void* dq_out, const void* dk_out, void* dq, void* dk, float* dq_weight,
+                          float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated norm of the heads' outputs:  y = w x / sqrt(mean(x^2) + eps) act(gate)
+ * with act the sigmoid or g sigmoid(g).  x, gate, y BF16 [B][T][H][128],
+ * weight FP32 [128]. */
+#define KDA_GATE_SIGMOID 0
+#define KDA_GATE_SILU 1
+typedef struct {
+    int32_t B, T, H;
+    int32_t activation;   /* KDA_GATE_SIGMOID or KDA_GATE_SILU */
+    float eps;
+    int64_t x_stride, gate_stride;
+} kda_gnorm_problem;
+
+kda_status kda_gnorm_fwd(const kda_gnorm_problem* p, const void* x, const void* gate, const float* weight, void* y,
+                         void* stream);
+kda_status kda_gnorm_bwd_workspace_bytes(const kda_gnorm_problem* p, size_t* bytes);
+kda_status kda_gnorm_bwd(const kda_gnorm_problem* p, const void* x, const void* gate, const float* weight,
+                         const void* dy, void* dx, void* dgate, float* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
