@@ -19,8 +19,12 @@ namespace kda {
 
 namespace {
 
-constexpr int SC = 64;            // tokens per chunk
-constexpr int SC_THREADS = 512;
+constexpr int SC = 32;            // tokens per chunk
+constexpr int NU = 2;             // 16-channel tiles of the output per wave
+constexpr int SC_WAVES = 8 / NU;
+constexpr int SC_THREADS = 64 * SC_WAVES;
+constexpr int SC_ROWS = SC_THREADS / 16;   // rows that one load instruction of the workgroup covers
+constexpr int SC_LOADS = SC / SC_ROWS;
 constexpr int STATE = D * D;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -114,9 +118,10 @@ struct Power {
 };
 
 // LDS rows of 128 channels are 16 blocks of 8 channels; block b of row r is
-// stored at block b ^ swz(r).  Rows 4g + r' then spread the 16 (r', b mod 4)
-// of a transposing read over all 16 places, and 16 rows the same block.
-__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+// stored at block b ^ swz(r).  The 16 rows of a tile then hold one block in 16
+// places, and a transposing read (4 rows of each of 4 groups, two blocks a
+// row) covers all 64 banks with every 32 lanes.
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 1) & 2) | ((r >> 3) & 1); }
 
 // Transposing read: the 16 lanes of group gq address 4 rows x 4 pieces of 4
 // channels, and lane m receives the 4 rows of channel m of those 16.
@@ -154,28 +159,32 @@ __device__ __forceinline__ float fresh(float x) {
 
 }  // namespace
 
-// One workgroup (8 waves) per item; wave w owns the state's output channels
-// 16w .. 16w+15 as MFMA accumulators: tile t holds S^T[k][v] with
-//     k = 32(t/2) + 8gq + 4(t%2) + e,   v = 16w + n
+// One workgroup (4 waves) per item; wave w owns the state's output channels
+// 32w .. 32w+31 as MFMA accumulators: tile (t, u) holds S^T[k][v] with
+//     k = 16t + 4gq + e,   v = 32w + 16u + n
 // (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
-// rounded to BF16, the operand of S a over channels 32p + 8gq .. +7.  Per
-// chunk of 64 tokens:
-//     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)}; two tiles at
-//           most per wave, through LDS to the others)
+// rounded to BF16, the operand of S a over channels 32p .. 32p+31.  Per chunk
+// of 32 tokens:
+//     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
-//     S^T = e^{64 l} S^T + B^T (C u),   u_j = e^{l(64-shift-j)}
+//     S^T = e^{32 l} S^T + B^T (C u),   u_j = e^{l(32-shift-j)}
 // Two operands are rounded to BF16: P, and S where it meets a (each about as
 // large an error as the output's own rounding).  The FP32 products C u go in
 // as BF16 pieces of 8 significant bits each: all three, the exact product,
 // where the state is an output; the first two where it is only read back
-// rounded to BF16.  The state itself stays in FP32 registers.  A chunk's rows are fetched into registers while
-// the previous chunk is computed.  `reverse` walks the tokens downwards and
-// only shifts the exponents.
+// rounded to BF16.  The state itself stays in FP32 registers.
+//
+// The chunks run as a pipeline: while chunk c's y and state are formed, three
+// of the waves form the P^T tiles of chunk c+1, and the rows of chunk c+2 are
+// on their way into registers, from where they go to chunk c's LDS buffer.
+// Two buffers and at most 168 registers let three workgroups share a compute
+// unit.  `reverse` walks the tokens downwards and only shifts the exponents.
 template <bool kOut>
-__global__ __launch_bounds__(SC_THREADS, 4) void decay_scan_kernel(ScanArgs A) {
-    // one LDS block (elements): B rows, C rows, A rows, P^T tiles
-    constexpr int LB = 0, LC = SC * D, LA = 2 * SC * D, LP = 3 * SC * D;
-    __shared__ __align__(16) bf16 lds[kOut ? LP + 16 * 256 : LA];
+__global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
+    // one LDS block (elements): two buffers of B rows, C rows, A rows; two of P^T tiles
+    constexpr int LB = 0, LC = SC * D, LA = 2 * SC * D, LBUF = (kOut ? 3 : 2) * SC * D;
+    constexpr int LP = 2 * LBUF, LPBUF = 3 * 256;
+    __shared__ __align__(16) bf16 lds[LP + (kOut ? 2 * LPBUF : 0)];
 
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -196,239 +205,265 @@ __global__ __launch_bounds__(SC_THREADS, 4) void decay_scan_kernel(ScanArgs A) {
     const float y_state = rev ? 1.0f : scale;     // scale of the state's part of y
     const float s_add = rev ? scale : 1.0f;       // scale of what the state takes up
 
-    // This thread's loads: 16 bytes of rows tid/16 and tid/16 + 32 of the
-    // chunk.  A row is a uniform base (scalar registers) plus a 32-bit lane
-    // offset; walking down, the base is the group's lowest row.  Rows behind
-    // the last token are not read and count as zero.
+    // This thread's loads: 16 bytes of rows tid/16 (+ SC_ROWS i) of a chunk.
+    // A row is a uniform base (scalar registers) plus a 32-bit lane offset;
+    // walking down, the base is the group's lowest row.  Rows behind the last
+    // token are not read and count as zero.
     const int lr = tid >> 4, lc = (tid & 15) * 8;
     const int64_t first = rev ? it.tok0 + it.len - 1 : it.tok0;
     const int64_t dir = rev ? -1 : 1;
-    const unsigned lrow = rev ? 31 - lr : lr;
+    const unsigned lrow = rev ? SC_ROWS - 1 - lr : lr;
     const int64_t sa = R.sa * 2, sb = R.sb * 2, sc = R.sc * 2;   // bytes per token
     const unsigned oa = lrow * (unsigned)sa + lc * 2, ob = lrow * (unsigned)sb + lc * 2,
                    oc = lrow * (unsigned)sc + lc * 2;
-    const int64_t row0 = first - (rev ? 31 : 0);
+    const int64_t row0 = first - (rev ? SC_ROWS - 1 : 0);
     const char* pa = kOut ? (const char*)(R.a + (it.h / R.ga) * D) + row0 * sa : nullptr;
     const char* pb = (const char*)(R.b + (it.h / R.gb) * D) + row0 * sb;
     const char* pc = (const char*)(R.c + (it.h / R.gc) * D) + row0 * sc;
-    const int64_t ga = 32 * dir * sa, gb = 32 * dir * sb, gc = 32 * dir * sc;
+    const int64_t ga = SC_ROWS * dir * sa, gb = SC_ROWS * dir * sb, gc = SC_ROWS * dir * sc;
 
-    u32x4 xa[2], xb[2], xc[2];
+    u32x4 xa[SC_LOADS], xb[SC_LOADS], xc[SC_LOADS];
     auto fetch = [&](int t0) __attribute__((always_inline)) {
         if (it.len - t0 >= SC) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < SC_LOADS; ++i) {
                 if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
                 xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
                 xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < SC_LOADS; ++i) {
                 xa[i] = xb[i] = xc[i] = u32x4{0u, 0u, 0u, 0u};
-                if (t0 + lr + 32 * i < it.len) {
+                if (t0 + lr + SC_ROWS * i < it.len) {
                     if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
                     xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
                     xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
                 }
             }
         }
-        pa += 2 * ga;
-        pb += 2 * gb;
-        pc += 2 * gc;
+        pa += SC_LOADS * ga;
+        pb += SC_LOADS * gb;
+        pc += SC_LOADS * gc;
+    };
+    const int st_off = lr * D + (((lc >> 3) ^ swz(lr)) << 3);
+    auto stage = [&](int buf) __attribute__((always_inline)) {   // (rows 16 apart share their swz)
+#pragma unroll
+        for (int i = 0; i < SC_LOADS; ++i) {
+            if (kOut) *(u32x4*)(lds + buf + LA + st_off + SC_ROWS * i * D) = xa[i];
+            *(u32x4*)(lds + buf + LB + st_off + SC_ROWS * i * D) = xb[i];
+            *(u32x4*)(lds + buf + LC + st_off + SC_ROWS * i * D) = xc[i];
+        }
     };
     fetch(0);
 
     // state
-    f32x4 S[8];
-    const int vrow = 16 * w + n16;
+    f32x4 S[8][NU];
+    const int vrow = 16 * NU * w + n16;   // + 16u
     const float* s_in = R.s_in;
     if (s_in == nullptr) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) S[t] = zero4();
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) S[t][u] = zero4();
     } else if (!R.s_in_t) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-            S[t] = *(const f32x4*)(s_in + soff + vrow * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1));
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                S[t][u] = *(const f32x4*)(s_in + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq);
     } else {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                S[t][e] = s_in[soff + (32 * (t >> 1) + 8 * gq + 4 * (t & 1) + e) * D + vrow];
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    S[t][u][e] = s_in[soff + (16 * t + 4 * gq + e) * D + vrow + 16 * u];
     }
 
     // Powers of e^l, constant over the item's full chunks; each is a product
-    // of factors <= 1, so none overflows.  This wave's P^T tiles are token
-    // rows j = 16tj .. and columns i = 16(tj + odd) .. and 32 further on.
-    //     P^T at i - j = 16d + n - 4gq - e:   pf[0][e] (d = odd), pf[1][e] (d = odd + 2)
-    //     Y column i = 16ti + n:              y0 step[ti]
-    //     C row j = 16tj + r, r = 4gq + e:    u0[e] step[3-tj]
-    const int tj0 = w & 3, odd = w >> 2;
-    float pf[2][4], u0[4], step[4];
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-        step[d] = __int_as_float(__builtin_amdgcn_readfirstlane(
-            __float_as_int(__builtin_amdgcn_exp2f(l2 * (float)(16 * d)))));
+    // of factors <= 1, so none overflows.  P^T tiles: wave 0 (i, j) = (0, 0),
+    // wave 1 (1, 1), wave 2 (1, 0).
+    //     P^T at i - j = 16d + n - 4gq - e:   pf[e] (d = 1 in wave 2, else 0)
+    //     Y column i = 16ti + n:              y0 (times far for ti = 1)
+    //     C row j = 16tj + r, r = 4gq + e:    u0[e] (times far for tj = 0)
+    const float far = __int_as_float(__builtin_amdgcn_readfirstlane(
+        __float_as_int(__builtin_amdgcn_exp2f(l2 * 16.0f))));
     const float y0 = y_state * __builtin_amdgcn_exp2f(l2 * (float)(n16 + shift));
+    float pf[4], u0[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int gap = 16 * odd + n16 - 4 * gq - e;
-        pf[0][e] = scale * __builtin_amdgcn_exp2f(l2 * (float)max(gap, 0));
-        pf[1][e] = scale * __builtin_amdgcn_exp2f(l2 * (float)(gap + 32));
+        pf[e] = scale * __builtin_amdgcn_exp2f(l2 * (float)max((w == 2 ? 16 : 0) + n16 - 4 * gq - e, 0));
         u0[e] = s_add * __builtin_amdgcn_exp2f(l2 * (float)(16 - shift - 4 * gq - e));
     }
     Power chunk_decay(l, SC);   // the state's factor per chunk
     float* const s_out = R.s_out;
     const bool exact = s_out != nullptr;
-    // LDS addresses (elements)
-    const int st_off = lr * D + (((lc >> 3) ^ swz(lr)) << 3);        // + 32i rows: swz is the same
-    int rd[4], tr[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        rd[p] = n16 * D + (((4 * p + gq) ^ swz(n16)) << 3);          // + 16*ti*D
-        tr[p] = (4 * gq + (n16 >> 2)) * D + (((4 * p + (n16 & 3)) ^ swz(4 * gq + (n16 >> 2))) << 3);
-    }
-    // channels 16w + 4a of row 4gq + n/4 (a = n%4): this wave's C columns
-    const int trc = (4 * gq + (n16 >> 2)) * D +
-                    (((2 * w + ((n16 & 3) >> 1)) ^ swz(4 * gq + (n16 >> 2))) << 3) + 4 * (n16 & 1);
+
+    // LDS addresses (elements), for p, t = 0 and in the low bits, where xors of
+    // 32p and 16t give the others (buffers are multiples of 4096): 4 channels
+    // (32p + 4gq) of row n, 8 channels (32p + 8gq) of row n, and for the
+    // transposing reads channels 16t + 4a of row 4gq + n/4 (a = n%4)
+    const int rd = n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1);
+    const int r8 = n16 * D + ((gq ^ swz(n16)) << 3);
+    const int trow = 4 * gq + (n16 >> 2);
+    const int tr = trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1);
+    const int trc = tr ^ (16 * NU * w);                 // this wave's C columns
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const bool y_f32 = R.y_f32 != 0;
     const int64_t sy = (int64_t)Hv * D * (y_f32 ? 4 : 2), gy = 16 * dir * sy;
     char* py = (char*)R.y + ((first - (rev ? 15 : 0)) * Hv + it.h) * D * (y_f32 ? 4 : 2);
-    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * w + 4 * gq) * (y_f32 ? 4 : 2);
+    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * w + 4 * gq) * (y_f32 ? 4 : 2);
 
-    auto chunk = [&](int t0, auto tail_c) __attribute__((always_inline)) {
+    // this wave's P^T tile of the chunk in buffer `buf`
+    auto form_p = [&](int buf, int pbuf) __attribute__((always_inline)) {
+        if (w < 3) {
+            const int jrow = w == 1 ? 16 * D : 0, irow = w == 0 ? 0 : 16 * D;
+            f32x4 acc = zero4();
+            const int at = buf + r8;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                acc = mma32(*(const bf16x8*)(lds + LB + (at ^ (32 * p)) + jrow),
+                            *(const bf16x8*)(lds + LA + (at ^ (32 * p)) + irow), acc);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
+                const bool seen = (w == 2) | (n16 >= 4 * gq + e);
+                acc[e] = seen ? acc[e] * pf[e] : 0.0f;
+            }
+            *(bf16x4*)(lds + LP + pbuf + w * 256 + lane * 4) = to_bf4(acc);
+        }
+    };
+
+    auto chunk = [&](int t0, int buf, int pbuf, auto tail_c) __attribute__((always_inline)) {
         constexpr bool kTail = decltype(tail_c)::value;
         const int rem = kTail ? it.len - t0 : SC;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (kOut) *(u32x4*)(lds + LA + st_off + 32 * i * D) = xa[i];
-            *(u32x4*)(lds + LB + st_off + 32 * i * D) = xb[i];
-            *(u32x4*)(lds + LC + st_off + 32 * i * D) = xc[i];
-        }
-        __syncthreads();
-        if (!kTail && t0 + SC < it.len) fetch(t0 + SC);
         const float fs = kTail ? (float)decay_power(l, rem) : chunk_decay.next();
-
-        f32x4 y[4];
+        // C columns of this wave
+        bf16x4 cf[2][NU];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (16 * u)) + 16 * j * D);
         if (kOut) {
-            // this wave's P^T tiles
-            int tj = tj0;
-            asm volatile("" : "+s"(tj));   // as fresh(): the tiles' addresses are formed per chunk
+            f32x4 y[2][NU];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int ti = tj + odd + 2 * x;
-                if (ti < 4) {
-                    f32x4 acc = zero4();
+            for (int ti = 0; ti < 2; ++ti)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        acc = mma32(*(const bf16x8*)(lds + LB + rd[p] + 16 * tj * D),
-                                    *(const bf16x8*)(lds + LA + rd[p] + 16 * ti * D), acc);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
-                        const bool seen = (x > 0) | (odd > 0) | (n16 >= 4 * gq + e);
-                        acc[e] = seen ? acc[e] * pf[x][e] : 0.0f;
-                    }
-                    *(bf16x4*)(lds + LP + (ti * 4 + tj) * 256 + lane * 4) = to_bf4(acc);
-                }
-            }
-            // the state's part of y, 32 channels at a time
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) y[ti] = zero4();
+                for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const bf16x8 sp = cat8(to_bf4(S[2 * p]), to_bf4(S[2 * p + 1]));
+                bf16x8 av[2];
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti)
-                    y[ti] = mma32(sp, *(const bf16x8*)(lds + LA + rd[p] + 16 * ti * D), y[ti]);
+                for (int ti = 0; ti < 2; ++ti)
+                    av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p)) + 16 * ti * D),
+                                  *(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p + 16)) + 16 * ti * D));
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
+                }
             }
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
-                const float f = fresh(y0) * step[ti];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[ti][e] *= f;
-            }
-            __syncthreads();
-        }
-        // C columns of this wave
-        bf16x4 cf[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cf[j] = tr_read(lds + LC + trc + 16 * j * D);
-        if (kOut) {
             const bf16x4 none = to_bf4(zero4());
+            const bf16x4 p00 = *(const bf16x4*)(lds + LP + pbuf + lane * 4);
+            const bf16x4 p11 = *(const bf16x4*)(lds + LP + pbuf + 256 + lane * 4);
+            const bf16x4 p10 = *(const bf16x4*)(lds + LP + pbuf + 512 + lane * 4);
+            const float f[2] = {y0, fresh(y0) * far};
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
+            for (int u = 0; u < NU; ++u) {
 #pragma unroll
-                for (int j = 0; j <= ti; j += 2) {
-                    const bf16x4 p0 = *(const bf16x4*)(lds + LP + (ti * 4 + j) * 256 + lane * 4);
-                    if (j + 1 <= ti)
-                        y[ti] = mma32(cat8(cf[j], cf[j + 1]),
-                                      cat8(p0, *(const bf16x4*)(lds + LP + (ti * 4 + j + 1) * 256 + lane * 4)), y[ti]);
-                    else
-                        y[ti] = mma32(cat8(cf[j], none), cat8(p0, none), y[ti]);
-                }
-                const int row = 16 * ti + n16;
-                if (!kTail || row < rem) {
-                    if (y_f32)
-                        *row_ptr<f32x4>(py + ti * gy, oy) = y[ti];
-                    else
-                        *row_ptr<bf16x4>(py + ti * gy, oy) = to_bf4(y[ti]);
+                for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[ti][u][e] *= f[ti];
+                y[0][u] = mma32(cat8(cf[0][u], none), cat8(p00, none), y[0][u]);
+                y[1][u] = mma32(cat8(cf[0][u], cf[1][u]), cat8(p10, p11), y[1][u]);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti) {
+                if (!kTail || 16 * ti + n16 < rem) {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) {
+                        if (y_f32)
+                            *row_ptr<f32x4>(py + ti * gy + 64 * u, oy) = y[ti][u];
+                        else
+                            *row_ptr<bf16x4>(py + ti * gy + 32 * u, oy) = to_bf4(y[ti][u]);
+                    }
                 }
             }
+            py += 2 * gy;
         }
-        py += 4 * gy;
         // state update
-        bf16x8 c1[2], c2[2], c3[2];
+        bf16x8 c1[NU], c2[NU], c3[NU];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int u = 0; u < NU; ++u) {
             bf16x4 x1[2], x2[2], x3[2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                f32x4 c = from_bf4(cf[2 * j + g]);
+            for (int j = 0; j < 2; ++j) {
+                f32x4 c = from_bf4(cf[j][u]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(
-                                                l2 * (float)max(rem - shift - 32 * j - 16 * g - 4 * gq - e, 0))
-                                  : fresh(u0[e]) * step[3 - 2 * j - g];
-                x1[g] = take_high(c);
-                x2[g] = take_high(c);
-                x3[g] = to_bf4(c);
+                    c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
+                            : j == 0 ? fresh(u0[e]) * far : u0[e];
+                x1[j] = take_high(c);
+                x2[j] = take_high(c);
+                x3[j] = to_bf4(c);
             }
-            c1[j] = cat8(x1[0], x1[1]);
-            c2[j] = cat8(x2[0], x2[1]);
-            c3[j] = cat8(x3[0], x3[1]);
+            c1[u] = cat8(x1[0], x1[1]);
+            c2[u] = cat8(x2[0], x2[1]);
+            c3[u] = cat8(x3[0], x3[1]);
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            bf16x8 bt[2];
+            const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (16 * t))),
+                                   tr_read(lds + LB + ((buf + tr) ^ (16 * t)) + 16 * D));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                bt[j] = cat8(tr_read(lds + LB + tr[t >> 1] + 32 * j * D + 4 * (t & 1)),
-                             tr_read(lds + LB + tr[t >> 1] + (32 * j + 16) * D + 4 * (t & 1)));
-            f32x4 acc;
+            for (int u = 0; u < NU; ++u) {
+                f32x4 acc;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = S[t][e] * fs;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c1[j], acc);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c2[j], acc);
-            if (exact) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc = mma32(bt[j], c3[j], acc);
+                for (int e = 0; e < 4; ++e) acc[e] = S[t][u][e] * fs;
+                acc = mma32(bt, c1[u], acc);
+                acc = mma32(bt, c2[u], acc);
+                if (exact) acc = mma32(bt, c3[u], acc);
+                S[t][u] = acc;
             }
-            S[t] = acc;
         }
-        if (!kTail) __syncthreads();
     };
-    int t0 = 0;
-    for (; t0 + SC <= it.len; t0 += SC) chunk(t0, std::false_type{});
-    if (t0 < it.len) chunk(t0, std::true_type{});
+    // the first two chunks' rows and the first one's P
+    stage(0);
+    if (SC < it.len) {
+        fetch(SC);
+        stage(LBUF);
+    }
+    __syncthreads();
+    if (kOut) {
+        form_p(0, 0);
+        __syncthreads();
+    }
+    int t0 = 0, buf = 0, pbuf = 0;
+    while (t0 + SC <= it.len) {
+        const int next = LBUF - buf;
+        const bool more = t0 + 2 * SC < it.len;
+        if (more) fetch(t0 + 2 * SC);
+        if (kOut && t0 + SC < it.len) form_p(next, LPBUF - pbuf);
+        chunk(t0, buf, pbuf, std::false_type{});
+        __syncthreads();
+        if (more) {
+            stage(buf);
+            __syncthreads();
+        }
+        t0 += SC;
+        buf = next;
+        pbuf = LPBUF - pbuf;
+    }
+    if (t0 < it.len) chunk(t0, buf, pbuf, std::true_type{});
 
     if (s_out != nullptr) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-            *(f32x4*)(s_out + soff + vrow * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1)) = S[t];
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                *(f32x4*)(s_out + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq) = S[t][u];
     }
 }
 

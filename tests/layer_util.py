@@ -8,8 +8,13 @@ rounding is off.
     as an operand, and the result.  Their errors are independent with standard
     deviation at most u/sqrt(3) of what they round, and the parts that P and
     the state feed add up to the result, so the error's norm is about
-    u sqrt(2/3) = 0.82 u of the result's; the bar is u.  One element is the sum
-    of many such errors: u |ref| + 8 u sqrt(2/3) times its row's RMS.
+    u sqrt(2/3) = 0.82 u of the result's; the bar is u.  One element: its own
+    rounding, u |ref|, and a sum of many errors.  The state's are those of
+    s sum_k S[v][k] q_k, of variance u^2/3 s^2 sum_k S[v][k]^2 q_k^2, and S^2
+    is about E, the same recurrence over squares (E <- e^{2l} E + v^2 k^2):
+    what a row's terms weigh does not shrink where the terms cancel.  Those of
+    P are as large.  So the bar is u |ref| + 8 u sqrt(2/3) sqrt(energy), with
+    energy = s^2 sum_k E[v][k] q_k^2: the definition at squared inputs.
   - An FP32 state adds up exact products over a chunk of 64 tokens in FP32:
     2^-24 for each of 64 sums, 2^-18 of the sum of absolute values.
 """
@@ -19,7 +24,7 @@ import numpy as np
 import torch
 
 U = 2.0 ** -8
-ROW = 8 * U * (2.0 / 3.0) ** 0.5
+ELEMENT = 8 * U * (2.0 / 3.0) ** 0.5
 STATE = 2.0 ** -18
 
 
@@ -31,14 +36,13 @@ def f64(t):
     return t.detach().float().cpu().numpy().astype(np.float64)
 
 
-def check_scanned(name, got, ref):
+def check_scanned(name, got, ref, energy):
     got = f64(got)
     assert np.isfinite(got).all(), f"{name}: not finite"
     err = np.abs(got - ref)
     norm = np.linalg.norm(ref)
     rel = np.linalg.norm(err) / norm if norm else np.linalg.norm(err)
-    rms = np.sqrt((ref * ref).mean(-1, keepdims=True))
-    worst = (err / np.maximum(U * np.abs(ref) + ROW * rms, 1e-30)).max()
+    worst = (err / np.maximum(U * np.abs(ref) + ELEMENT * np.sqrt(energy), 1e-30)).max()
     print(f"{name:14s} rel {rel:.2e} (bar {U:.2e})  elementwise {worst:.2f} of the bar", flush=True)
     assert rel <= U and worst <= 1.0, name
 

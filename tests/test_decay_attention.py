@@ -61,6 +61,15 @@ class Inp:
         return lo.decay_forward(lu.f64(self.q), lu.f64(self.k), lu.f64(self.v), lu.f64(self.l), lu.f64(s0),
                                 self.lengths, self.packed, scale)
 
+    def energies(self, scale=SCALE):
+        """Of o, dq, dk and dv: the definitions at squared inputs."""
+        s0 = self.s0 if self.s0 is not None else self.zeros()
+        ds = self.ds if self.ds is not None else self.zeros()
+        q, k, v, s0, do, ds = (lu.f64(x) ** 2 for x in (self.q, self.k, self.v, s0, self.do, ds))
+        l = 2 * lu.f64(self.l)
+        o = lo.decay_forward(q, k, v, l, s0, self.lengths, self.packed, scale ** 2)[0]
+        return (o,) + lo.decay_backward(q, k, v, l, s0, do, ds, self.lengths, self.packed, scale ** 2)[:3]
+
     def gradients(self, scale=SCALE):
         s0 = self.s0 if self.s0 is not None else self.zeros()
         ds = self.ds if self.ds is not None else self.zeros()
@@ -85,10 +94,11 @@ def check_train(inp, got, scale=SCALE):
     o, final, major, mfinal = inp.reference(scale)
     (dq, dk, dv, dinit), minit = inp.gradients(scale)
     lu.check_bars("o, majorant", got[0], o, lu.U * np.abs(o) + 2 * lu.U * major)
-    lu.check_scanned("o", got[0], o)
+    energies = inp.energies(scale)
+    lu.check_scanned("o", got[0], o, energies[0])
     lu.check_state("final_state", got[1], final, mfinal)
-    for name, x, ref in zip(("dq", "dk", "dv"), got[2:5], (dq, dk, dv)):
-        lu.check_scanned(name, x, ref)
+    for name, x, ref, energy in zip(("dq", "dk", "dv"), got[2:5], (dq, dk, dv), energies[1:]):
+        lu.check_scanned(name, x, ref, energy)
     lu.check_state("dinitial_state", got[5], dinit, minit)
 
 
@@ -165,7 +175,7 @@ def test_segments_agree_with_whole_sequences():
     a, b = train(inp, 0), train(inp, 64)
     _, _, _, mfinal = inp.reference()
     assert (np.abs(lu.f64(a[1]) - lu.f64(b[1])) <= 2 * lu.STATE * mfinal).all()
-    lu.check_scanned("o of segments", b[0], inp.reference()[0])
+    lu.check_scanned("o of segments", b[0], inp.reference()[0], inp.energies()[0])
 
 
 @pytest.mark.parametrize("l", [-1e-5, -1.7e-4, -0.0039])
@@ -249,7 +259,7 @@ def test_pool(lengths, packed, segment):
     pool = pool0.cuda()
     out = pool_call(inp, pool, slots, segment=segment)
     o, final, major, mfinal = inp.reference()
-    lu.check_scanned("o", out, o)
+    lu.check_scanned("o", out, o, inp.energies()[0])
     lu.check_state("pool", pool[slots], final, mfinal)
     rest = [i for i in range(len(lengths) + 3) if i not in slots]
     assert torch.equal(pool[rest].cpu(), pool0[rest])
@@ -261,11 +271,11 @@ def test_pool_without_indices_and_new_pool():
     pool = inp.s0.cuda()
     out = pool_call(inp, pool, None)
     o, final, _, mfinal = inp.reference()
-    lu.check_scanned("o", out, o)
+    lu.check_scanned("o", out, o, inp.energies()[0])
     lu.check_state("pool", pool, final, mfinal)
     inp.s0 = None
     out, new = kda.decay_attention(inp.dev(inp.q), inp.dev(inp.k), inp.dev(inp.v), inp.dev(inp.l))
-    lu.check_scanned("o from zero", out, inp.reference()[0])
+    lu.check_scanned("o from zero", out, inp.reference()[0], inp.energies()[0])
     lu.check_state("new pool", new, inp.reference()[1], inp.reference()[3])
 
 
@@ -280,7 +290,7 @@ def test_prefill_then_decode_equals_one_prefill():
         part = Inp([b - a], False, 1, 2)
         part.q, part.k, part.v = (x[:, a:b].contiguous() for x in (inp.q, inp.k, inp.v))
         outs.append(pool_call(part, pool, None))
-    lu.check_scanned("o", torch.cat(outs, 1), o)
+    lu.check_scanned("o", torch.cat(outs, 1), o, inp.energies()[0])
     # 13 more steps, each with a rounding of the factor and of the sum
     lu.check_bars("pool", pool, final, (lu.STATE + 26 * 2.0 ** -24) * mfinal)
 
