@@ -159,8 +159,41 @@ __device__ __forceinline__ float fresh(float x) {
 
 }  // namespace
 
-// One workgroup (4 waves) per item; wave w owns the state's output channels
-// 32w .. 32w+31 as MFMA accumulators: tile (t, u) holds S^T[k][v] with
+// A partial of dq or dk (value heads that share a q/k head each form one) is
+// kept as quads of 8 bytes: four 15-bit floats (sign, 5 bits of exponent, 9 of
+// mantissa) and 4 bits that scale the quad by a power of 2^16 so that its
+// largest value is in [1/2, 2^15).  A value is off by at most 2^-10 of itself,
+// a quarter of a BF16 rounding, or 2^-24 of the quad's largest.  (As FP32 the
+// partials' way out and in took 28% of a grouped training step, and BF16
+// partials would add as large an error again as the result's own rounding.)
+// A quad with a NaN or an infinity comes back as NaN.
+__device__ __forceinline__ u32x2 pack_quad(f32x4 x) {
+    const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    const unsigned q = __float_as_uint(top) >> 27;                 // biased exponent / 16
+    const float scale = __uint_as_float((253u - 16u * q) << 23);   // 2^(126 - 16q)
+    // (the maxima skip NaN; 0 x is 0 for finite x only)
+    const bool bad = !(x[0] * 0.0f + x[1] * 0.0f + x[2] * 0.0f + x[3] * 0.0f == 0.0f);
+    unsigned m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // FP16, its lowest bit rounded off
+        m[i] = ((unsigned)__builtin_bit_cast(unsigned short, (f16)(x[i] * scale)) + 1u) >> 1;
+    const u32x2 w = {m[0] | m[1] << 15 | q << 30, m[2] | m[3] << 15 | (q >> 2) << 30};
+    return u32x2{bad ? ~0u : w[0], bad ? ~0u : w[1]};
+}
+__device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
+    const unsigned q = w[0] >> 30 | (w[1] >> 30) << 2;
+    const float scale = __uint_as_float((1u + 16u * q) << 23);     // 2^(16q - 126)
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[2 * i] = scale * (float)__builtin_bit_cast(f16, (unsigned short)(w[i] << 1));
+        x[2 * i + 1] = scale * (float)__builtin_bit_cast(f16, (unsigned short)(w[i] >> 14 & 0xfffeu));
+    }
+    return x;
+}
+
+// One workgroup (4 waves) per item and form; wave w owns the state's output
+// channels 32w .. 32w+31 as MFMA accumulators: tile (t, u) holds S^T[k][v] with
 //     k = 16t + 4gq + e,   v = 32w + 16u + n
 // (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
 // rounded to BF16, the operand of S a over channels 32p .. 32p+31.  Per chunk
@@ -170,34 +203,33 @@ __device__ __forceinline__ float fresh(float x) {
 //     S^T = e^{32 l} S^T + B^T (C u),   u_j = e^{l(32-shift-j)}
 // Two operands are rounded to BF16: P, and S where it meets a (each about as
 // large an error as the output's own rounding).  The FP32 products C u go in
-// as BF16 pieces of 8 significant bits each: all three, the exact product,
-// where the state is an output; the first two where it is only read back
-// rounded to BF16.  The state itself stays in FP32 registers.
+// as three BF16 pieces of 8 significant bits each, so exactly; the state
+// itself stays in FP32 registers.
 //
 // The chunks run as a pipeline: while chunk c's y and state are formed, three
 // of the waves form the P^T tiles of chunk c+1, and the rows of chunk c+2 are
 // on their way into registers, from where they go to chunk c's LDS buffer.
 // Two buffers and at most 168 registers let three workgroups share a compute
 // unit.  `reverse` walks the tokens downwards and only shifts the exponents.
-template <bool kOut>
+template <bool kOut, bool kPack>
 __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
-    // one LDS block (elements): two buffers of B rows, C rows, A rows; two of P^T tiles
-    constexpr int LB = 0, LC = SC * D, LA = 2 * SC * D, LBUF = (kOut ? 3 : 2) * SC * D;
-    constexpr int LP = 2 * LBUF, LPBUF = 3 * 256;
+    // one LDS block (elements): two buffers of SETS row blocks; two of P^T tiles
+    constexpr int SETS = kOut ? 3 : 2, SET = SC * D, LBUF = SETS * SET;   // rows of b, c, a
+    constexpr int LB = 0, LC = SET, LA = 2 * SET, LP = 2 * LBUF, LPBUF = 3 * 256;
     __shared__ __align__(16) bf16 lds[LP + (kOut ? 2 * LPBUF : 0)];
 
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63, gq = lane >> 4, n16 = lane & 15;
     const int idx = xcd_order(blockIdx.x, (int)gridDim.x, A.share);
-    const ScanRole R = A.role[idx % A.roles];
-    const Item it = find_item(A.map, idx / A.roles);
+    const ScanJob J = A.job[A.jobs == 1 ? 0 : idx % A.jobs];
+    const Item it = find_item(A.map, idx / A.jobs);
     const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
     if (slot < 0 || slot >= A.slots) return;
-    const int64_t sidx = R.s_by_seg ? it.seg : slot;
+    const int64_t sidx = A.by_seg ? it.seg : slot;
     const int Hv = A.map.Hv;
     const int64_t soff = (sidx * Hv + it.h) * (int64_t)STATE;
-    const bool rev = R.reverse != 0;
+    const bool rev = J.reverse != 0;
     const float l = A.log_decay[it.h];
     const float l2 = log2_decay(l);
     const int shift = rev ? 0 : 1;
@@ -206,67 +238,65 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const float s_add = rev ? scale : 1.0f;       // scale of what the state takes up
 
     // This thread's loads: 16 bytes of rows tid/16 (+ SC_ROWS i) of a chunk.
-    // A row is a uniform base (scalar registers) plus a 32-bit lane offset;
-    // walking down, the base is the group's lowest row.  Rows behind the last
-    // token are not read and count as zero.
+    // The chunk's lowest row is a uniform base (scalar registers), a lane's row
+    // a 32-bit offset.  For rows behind the last token the chunk's first row is
+    // read again and the values are dropped in stage().
     const int lr = tid >> 4, lc = (tid & 15) * 8;
     const int64_t first = rev ? it.tok0 + it.len - 1 : it.tok0;
     const int64_t dir = rev ? -1 : 1;
-    const unsigned lrow = rev ? SC_ROWS - 1 - lr : lr;
-    const int64_t sa = R.sa * 2, sb = R.sb * 2, sc = R.sc * 2;   // bytes per token
-    const unsigned oa = lrow * (unsigned)sa + lc * 2, ob = lrow * (unsigned)sb + lc * 2,
-                   oc = lrow * (unsigned)sc + lc * 2;
-    const int64_t row0 = first - (rev ? SC_ROWS - 1 : 0);
-    const char* pa = kOut ? (const char*)(R.a + (it.h / R.ga) * D) + row0 * sa : nullptr;
-    const char* pb = (const char*)(R.b + (it.h / R.gb) * D) + row0 * sb;
-    const char* pc = (const char*)(R.c + (it.h / R.gc) * D) + row0 * sc;
-    const int64_t ga = SC_ROWS * dir * sa, gb = SC_ROWS * dir * sb, gc = SC_ROWS * dir * sc;
-
-    u32x4 xa[SC_LOADS], xb[SC_LOADS], xc[SC_LOADS];
+    const ScanRows rows[3] = {J.b, J.c, J.a};
+    const char* pr[SETS];
+    int64_t gr[SETS];
+    unsigned off[SETS], up[SETS];   // offset of row lr; of SC_ROWS rows more (modulo 2^32)
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) {
+        const int64_t bytes = rows[i].stride * 2;
+        pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? SC - 1 : 0)) * bytes;
+        gr[i] = SC * dir * bytes;
+        off[i] = (unsigned)(rev ? SC - 1 - lr : lr) * (unsigned)bytes + lc * 2;
+        up[i] = (unsigned)(SC_ROWS * (int)dir) * (unsigned)bytes;
+    }
+    u32x4 x[SETS][SC_LOADS];
     auto fetch = [&](int t0) __attribute__((always_inline)) {
-        if (it.len - t0 >= SC) {
 #pragma unroll
-            for (int i = 0; i < SC_LOADS; ++i) {
-                if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
-                xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
-                xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
-            }
-        } else {
+        for (int j = 0; j < SC_LOADS; ++j) {
+            const bool in = t0 + lr + SC_ROWS * j < it.len;
 #pragma unroll
-            for (int i = 0; i < SC_LOADS; ++i) {
-                xa[i] = xb[i] = xc[i] = u32x4{0u, 0u, 0u, 0u};
-                if (t0 + lr + SC_ROWS * i < it.len) {
-                    if (kOut) xa[i] = *row_ptr<u32x4>(pa + i * ga, oa);
-                    xb[i] = *row_ptr<u32x4>(pb + i * gb, ob);
-                    xc[i] = *row_ptr<u32x4>(pc + i * gc, oc);
-                }
+            for (int i = 0; i < SETS; ++i) {
+                const unsigned top = (rev ? (unsigned)((SC - 1) * rows[i].stride * 2) : 0u) + lc * 2;
+                x[i][j] = *row_ptr<u32x4>(pr[i], in ? off[i] + j * up[i] : top);
             }
         }
-        pa += SC_LOADS * ga;
-        pb += SC_LOADS * gb;
-        pc += SC_LOADS * gc;
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) pr[i] += gr[i];
     };
     const int st_off = lr * D + (((lc >> 3) ^ swz(lr)) << 3);
-    auto stage = [&](int buf) __attribute__((always_inline)) {   // (rows 16 apart share their swz)
+    auto stage = [&](int buf, int t0) __attribute__((always_inline)) {   // (rows 16 apart share their swz)
+        if (t0 + SC > it.len) {
 #pragma unroll
-        for (int i = 0; i < SC_LOADS; ++i) {
-            if (kOut) *(u32x4*)(lds + buf + LA + st_off + SC_ROWS * i * D) = xa[i];
-            *(u32x4*)(lds + buf + LB + st_off + SC_ROWS * i * D) = xb[i];
-            *(u32x4*)(lds + buf + LC + st_off + SC_ROWS * i * D) = xc[i];
+            for (int j = 0; j < SC_LOADS; ++j)
+#pragma unroll
+                for (int i = 0; i < SETS; ++i)
+                    if (t0 + lr + SC_ROWS * j >= it.len) x[i][j] = u32x4{0u, 0u, 0u, 0u};
         }
+#pragma unroll
+        for (int i = 0; i < SETS; ++i)
+#pragma unroll
+            for (int j = 0; j < SC_LOADS; ++j)
+                *(u32x4*)(lds + buf + i * SET + st_off + SC_ROWS * j * D) = x[i][j];
     };
     fetch(0);
 
     // state
     f32x4 S[8][NU];
     const int vrow = 16 * NU * w + n16;   // + 16u
-    const float* s_in = R.s_in;
+    const float* s_in = J.s_in;
     if (s_in == nullptr) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u) S[t][u] = zero4();
-    } else if (!R.s_in_t) {
+    } else if (!J.s_in_t) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -298,8 +328,6 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         u0[e] = s_add * __builtin_amdgcn_exp2f(l2 * (float)(16 - shift - 4 * gq - e));
     }
     Power chunk_decay(l, SC);   // the state's factor per chunk
-    float* const s_out = R.s_out;
-    const bool exact = s_out != nullptr;
 
     // LDS addresses (elements), for p, t = 0 and in the low bits, where xors of
     // 32p and 16t give the others (buffers are multiples of 4096): 4 channels
@@ -311,17 +339,18 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const int tr = trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1);
     const int trc = tr ^ (16 * NU * w);                 // this wave's C columns
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
-    const bool y_f32 = R.y_f32 != 0;
-    const int64_t sy = (int64_t)Hv * D * (y_f32 ? 4 : 2), gy = 16 * dir * sy;
-    char* py = (char*)R.y + ((first - (rev ? 15 : 0)) * Hv + it.h) * D * (y_f32 ? 4 : 2);
-    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * w + 4 * gq) * (y_f32 ? 4 : 2);
+    const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
+    const char* yout = (const char*)J.y;
+    const bool pack = J.pack != 0;
+    int64_t py = ((first - (rev ? 15 : 0)) * Hv + it.h) * D * 2;
+    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * w + 4 * gq) * 2;
 
     // this wave's P^T tile of the chunk in buffer `buf`
     auto form_p = [&](int buf, int pbuf) __attribute__((always_inline)) {
         if (w < 3) {
             const int jrow = w == 1 ? 16 * D : 0, irow = w == 0 ? 0 : 16 * D;
-            f32x4 acc = zero4();
             const int at = buf + r8;
+            f32x4 acc = zero4();
 #pragma unroll
             for (int p = 0; p < 4; ++p)
                 acc = mma32(*(const bf16x8*)(lds + LB + (at ^ (32 * p)) + jrow),
@@ -339,101 +368,103 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         constexpr bool kTail = decltype(tail_c)::value;
         const int rem = kTail ? it.len - t0 : SC;
         const float fs = kTail ? (float)decay_power(l, rem) : chunk_decay.next();
-        // C columns of this wave
-        bf16x4 cf[2][NU];
+        {
+            // C columns of this wave
+            bf16x4 cf[2][NU];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (16 * u)) + 16 * j * D);
-        if (kOut) {
-            f32x4 y[2][NU];
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-                for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                bf16x8 av[2];
-#pragma unroll
-                for (int ti = 0; ti < 2; ++ti)
-                    av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p)) + 16 * ti * D),
-                                  *(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p + 16)) + 16 * ti * D));
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
-#pragma unroll
-                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
-                }
-            }
-            const bf16x4 none = to_bf4(zero4());
-            const bf16x4 p00 = *(const bf16x4*)(lds + LP + pbuf + lane * 4);
-            const bf16x4 p11 = *(const bf16x4*)(lds + LP + pbuf + 256 + lane * 4);
-            const bf16x4 p10 = *(const bf16x4*)(lds + LP + pbuf + 512 + lane * 4);
-            const float f[2] = {y0, fresh(y0) * far};
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
+                for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (16 * u)) + 16 * j * D);
+            if (kOut) {
+                f32x4 y[2][NU];
 #pragma unroll
                 for (int ti = 0; ti < 2; ++ti)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[ti][u][e] *= f[ti];
-                y[0][u] = mma32(cat8(cf[0][u], none), cat8(p00, none), y[0][u]);
-                y[1][u] = mma32(cat8(cf[0][u], cf[1][u]), cat8(p10, p11), y[1][u]);
-            }
+                    for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
 #pragma unroll
-            for (int ti = 0; ti < 2; ++ti) {
-                if (!kTail || 16 * ti + n16 < rem) {
+                for (int p = 0; p < 4; ++p) {
+                    bf16x8 av[2];
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti)
+                        av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p)) + 16 * ti * D),
+                                      *(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p + 16)) + 16 * ti * D));
 #pragma unroll
                     for (int u = 0; u < NU; ++u) {
-                        if (y_f32)
-                            *row_ptr<f32x4>(py + ti * gy + 64 * u, oy) = y[ti][u];
-                        else
-                            *row_ptr<bf16x4>(py + ti * gy + 32 * u, oy) = to_bf4(y[ti][u]);
+                        const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
+#pragma unroll
+                        for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
+                    }
+                }
+                const bf16x4 none = to_bf4(zero4());
+                const bf16* pt = lds + LP + pbuf + lane * 4;
+                const bf16x4 p00 = *(const bf16x4*)pt, p11 = *(const bf16x4*)(pt + 256),
+                             p10 = *(const bf16x4*)(pt + 512);
+                const float yf[2] = {y0, fresh(y0) * far};
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[ti][u][e] *= yf[ti];
+                    y[0][u] = mma32(cat8(cf[0][u], none), cat8(p00, none), y[0][u]);
+                    y[1][u] = mma32(cat8(cf[0][u], cf[1][u]), cat8(p10, p11), y[1][u]);
+                }
+                const char* yb = yout + py;
+#pragma unroll
+                for (int ti = 0; ti < 2; ++ti) {
+                    if (!kTail || 16 * ti + n16 < rem) {
+#pragma unroll
+                        for (int u = 0; u < NU; ++u)
+                            *row_ptr<u32x2>(yb + ti * gy + 32 * u, oy) =
+                                kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
                     }
                 }
             }
-            py += 2 * gy;
-        }
-        // state update
-        bf16x8 c1[NU], c2[NU], c3[NU];
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            bf16x4 x1[2], x2[2], x3[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f32x4 c = from_bf4(cf[j][u]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
-                            : j == 0 ? fresh(u0[e]) * far : u0[e];
-                x1[j] = take_high(c);
-                x2[j] = take_high(c);
-                x3[j] = to_bf4(c);
-            }
-            c1[u] = cat8(x1[0], x1[1]);
-            c2[u] = cat8(x2[0], x2[1]);
-            c3[u] = cat8(x3[0], x3[1]);
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (16 * t))),
-                                   tr_read(lds + LB + ((buf + tr) ^ (16 * t)) + 16 * D));
+            // state update
+            bf16x8 c1[NU], c2[NU], c3[NU];
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                f32x4 acc;
+                bf16x4 x1[2], x2[2], x3[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = S[t][u][e] * fs;
-                acc = mma32(bt, c1[u], acc);
-                acc = mma32(bt, c2[u], acc);
-                if (exact) acc = mma32(bt, c3[u], acc);
-                S[t][u] = acc;
+                for (int j = 0; j < 2; ++j) {
+                    f32x4 c = from_bf4(cf[j][u]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(
+                                                    l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
+                                : j == 0 ? fresh(u0[e]) * far : u0[e];
+                    x1[j] = take_high(c);
+                    x2[j] = take_high(c);
+                    x3[j] = to_bf4(c);
+                }
+                c1[u] = cat8(x1[0], x1[1]);
+                c2[u] = cat8(x2[0], x2[1]);
+                c3[u] = cat8(x3[0], x3[1]);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (16 * t))),
+                                       tr_read(lds + LB + ((buf + tr) ^ (16 * t)) + 16 * D));
+                f32x4 acc[NU];
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[u][e] = S[t][u][e] * fs;
+#pragma unroll
+                for (int u = 0; u < NU; ++u) acc[u] = mma32(bt, c1[u], acc[u]);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) acc[u] = mma32(bt, c2[u], acc[u]);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], acc[u]);
             }
         }
+        py += 2 * gy;
     };
     // the first two chunks' rows and the first one's P
-    stage(0);
+    stage(0, 0);
     if (SC < it.len) {
         fetch(SC);
-        stage(LBUF);
+        stage(LBUF, SC);
     }
     __syncthreads();
     if (kOut) {
@@ -442,22 +473,22 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     }
     int t0 = 0, buf = 0, pbuf = 0;
     while (t0 + SC <= it.len) {
-        const int next = LBUF - buf;
         const bool more = t0 + 2 * SC < it.len;
         if (more) fetch(t0 + 2 * SC);
-        if (kOut && t0 + SC < it.len) form_p(next, LPBUF - pbuf);
+        if (kOut && t0 + SC < it.len) form_p(LBUF - buf, LPBUF - pbuf);
         chunk(t0, buf, pbuf, std::false_type{});
         __syncthreads();
         if (more) {
-            stage(buf);
+            stage(buf, t0 + 2 * SC);
             __syncthreads();
         }
         t0 += SC;
-        buf = next;
+        buf = LBUF - buf;
         pbuf = LPBUF - pbuf;
     }
     if (t0 < it.len) chunk(t0, buf, pbuf, std::true_type{});
 
+    float* s_out = J.s_out;
     if (s_out != nullptr) {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -468,11 +499,15 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 }
 
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
-    const int64_t blocks = a.map.items * a.roles;
+    const dim3 grid((unsigned)(a.map.items * a.jobs)), block(SC_THREADS);
+    bool pack = false;
+    for (int i = 0; i < a.jobs; ++i) pack = pack || a.job[i].pack != 0;
     if (states_only)
-        hipLaunchKernelGGL(decay_scan_kernel<false>, dim3((unsigned)blocks), dim3(SC_THREADS), 0, s, a);
+        hipLaunchKernelGGL((decay_scan_kernel<false, false>), grid, block, 0, s, a);
+    else if (pack)
+        hipLaunchKernelGGL((decay_scan_kernel<true, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL(decay_scan_kernel<true>, dim3((unsigned)blocks), dim3(SC_THREADS), 0, s, a);
+        hipLaunchKernelGGL((decay_scan_kernel<true, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -564,28 +599,29 @@ hipError_t launch_decay_token(const TokenArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Sum over the G value heads of a q/k head, in head order, FP32 to BF16: 8
-// channels per thread.
-__global__ __launch_bounds__(256) void decay_group_sum_kernel(const float* src0, const float* src1, bf16* dst0,
+// Sum over the G value heads of a q/k head, in head order, packed partials to
+// BF16: 8 channels (two quads) per thread.
+__global__ __launch_bounds__(256) void decay_group_sum_kernel(const bf16* src0, const bf16* src1, bf16* dst0,
                                                               bf16* dst1, int64_t vecs, int G) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (token, q/k head, 8 channels)
     if (i >= vecs) return;
     const int64_t row = i >> 4;
     const int c = (int)(i & 15) * 8;
-    const float* src = (blockIdx.y ? src1 : src0) + row * G * D + c;
+    const bf16* src = (blockIdx.y ? src1 : src0) + row * G * D + c;
     f32x4 a = zero4(), b = zero4();
     for (int g = 0; g < G; ++g) {
-        a += *(const f32x4*)(src + g * D);
-        b += *(const f32x4*)(src + g * D + 4);
+        const u32x4 w = *(const u32x4*)(src + g * D);
+        a += unpack_quad(u32x2{w[0], w[1]});
+        b += unpack_quad(u32x2{w[2], w[3]});
     }
     *(bf16x8*)((blockIdx.y ? dst1 : dst0) + row * D + c) = cat8(to_bf4(a), to_bf4(b));
 }
 
-hipError_t launch_decay_group_sum(const float* src0, const float* src1, bf16_t* dst0, bf16_t* dst1,
+hipError_t launch_decay_group_sum(const void* src0, const void* src1, bf16_t* dst0, bf16_t* dst1,
                                   int64_t tokens, int Hqk, int G, hipStream_t s) {
     const int64_t vecs = tokens * Hqk * (D / 8);
-    hipLaunchKernelGGL(decay_group_sum_kernel, dim3((unsigned)((vecs + 255) / 256), 2), dim3(256), 0, s, src0, src1,
-                       (bf16*)dst0, (bf16*)dst1, vecs, G);
+    hipLaunchKernelGGL(decay_group_sum_kernel, dim3((unsigned)((vecs + 255) / 256), 2), dim3(256), 0, s,
+                       (const bf16*)src0, (const bf16*)src1, (bf16*)dst0, (bf16*)dst1, vecs, G);
     return hipGetLastError();
 }
 

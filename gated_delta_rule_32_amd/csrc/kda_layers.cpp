@@ -132,7 +132,7 @@ DecayWs decay_ws(const Decay& d, int seg, bool backward) {
     if (backward) {
         w.seg_r = off;
         off = align256(off + states);
-        const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * sizeof(float) : 0;
+        const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
         w.part_q = off;
         off = align256(off + part);
         w.part_k = off;
@@ -172,28 +172,29 @@ kda_status check_grid(int64_t blocks) {
 kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const void* q, const void* k, const void* v,
                        const float* log_decay, const float* s_in, float* s_out, const int32_t* slot, int64_t slots,
                        void* o, char* ws, hipStream_t stream) {
+    const int G = d.s.G;
     kda::ScanArgs a{};
     a.map = m;
-    a.roles = 1;
-    a.share = d.s.G;
+    a.jobs = 1;
+    a.share = G;
     a.log_decay = log_decay;
     a.scale = d.scale;
     a.slot = slot;
     a.slots = slots;
-    kda::ScanRole& r = a.role[0];
-    r.a = (const kda::bf16_t*)q; r.sa = d.sq; r.ga = d.s.G;
-    r.b = (const kda::bf16_t*)k; r.sb = d.sk; r.gb = d.s.G;
-    r.c = (const kda::bf16_t*)v; r.sc = d.sv; r.gc = 1;
-    r.y = o;
-    r.s_in = s_in;
-    r.s_out = s_out;
+    kda::ScanJob& j = a.job[0];
+    j.b = {(const kda::bf16_t*)k, d.sk, G};
+    j.c = {(const kda::bf16_t*)v, d.sv, 1};
+    j.a = {(const kda::bf16_t*)q, d.sq, G};
+    j.y = o;
+    j.s_in = s_in;
+    j.s_out = s_out;
     hipError_t e;
     if (seg != 0) {
         float* states = (float*)ws;
         kda::ScanArgs b = a;
-        b.role[0].s_in = nullptr;
-        b.role[0].s_out = states;
-        b.role[0].s_by_seg = 1;
+        b.by_seg = 1;
+        b.job[0].s_in = nullptr;
+        b.job[0].s_out = states;
         e = kda::launch_decay_scan(b, true, stream);
         if (e != hipSuccess) return hip_fail(e, "segment state launch");
         kda::ChainArgs c{};
@@ -206,9 +207,9 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
         c.slots = slots;
         e = kda::launch_decay_chain(c, stream);
         if (e != hipSuccess) return hip_fail(e, "segment chain launch");
-        r.s_in = states;
-        r.s_out = nullptr;
-        r.s_by_seg = 1;
+        j.s_in = states;
+        j.s_out = nullptr;
+        a.by_seg = 1;
     }
     e = kda::launch_decay_scan(a, false, stream);
     if (e != hipSuccess) return hip_fail(e, "decay scan launch");
@@ -406,62 +407,55 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
 
         char* ws = (char*)workspace;
         const int G = d.s.G;
-        const int64_t sdo = (int64_t)d.s.Hv * D;
+        const kda::ScanRows rq = {(const kda::bf16_t*)q, d.sq, G}, rk = {(const kda::bf16_t*)k, d.sk, G},
+                            rv = {(const kda::bf16_t*)v, d.sv, 1},
+                            ro = {(const kda::bf16_t*)d_o, (int64_t)d.s.Hv * D, 1};
+        const int pack = G > 1;
         kda::ScanArgs a{};
         a.map = m;
-        a.roles = 3;
+        a.jobs = 3;
         a.share = 3 * G;
         a.log_decay = log_decay;
         a.scale = d.scale;
         a.slots = d.s.N;
-        auto q_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)q; st_ = d.sq; g = G; };
-        auto k_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)k; st_ = d.sk; g = G; };
-        auto v_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)v; st_ = d.sv; g = 1; };
-        auto o_op = [&](const kda::bf16_t*& p, int64_t& st_, int& g) { p = (const kda::bf16_t*)d_o; st_ = sdo; g = 1; };
-        // dq: (do, v, k) forward in time, the state read transposed
-        kda::ScanRole& rq = a.role[0];
-        o_op(rq.a, rq.sa, rq.ga); v_op(rq.b, rq.sb, rq.gb); k_op(rq.c, rq.sc, rq.gc);
-        rq.y = G > 1 ? (void*)(ws + wl.part_q) : dq;
-        rq.y_f32 = G > 1;
-        rq.s_in = initial_state;
-        rq.s_in_t = 1;
-        // dk: (v, do, q) backward in time
-        kda::ScanRole& rk = a.role[1];
-        v_op(rk.a, rk.sa, rk.ga); o_op(rk.b, rk.sb, rk.gb); q_op(rk.c, rk.sc, rk.gc);
-        rk.y = G > 1 ? (void*)(ws + wl.part_k) : dk;
-        rk.y_f32 = G > 1;
-        rk.reverse = 1;
-        rk.s_in = dfinal_state;
-        rk.s_in_t = 1;
+        // dk: (v, do, q) backward in time, the state read transposed
+        kda::ScanJob& jk = a.job[0];
+        jk.a = rv; jk.b = ro; jk.c = rq;
+        jk.y = pack ? (void*)(ws + wl.part_k) : dk;
+        jk.pack = pack;
+        jk.reverse = 1;
+        jk.s_in = dfinal_state;
+        jk.s_in_t = 1;
         // dv: (k, q, do) backward in time; its state ends as dinitial_state
-        kda::ScanRole& rv = a.role[2];
-        k_op(rv.a, rv.sa, rv.ga); q_op(rv.b, rv.sb, rv.gb); o_op(rv.c, rv.sc, rv.gc);
-        rv.y = dv;
-        rv.reverse = 1;
-        rv.s_in = dfinal_state;
-        rv.s_out = dinitial_state;
+        kda::ScanJob& jv = a.job[1];
+        jv.a = rk; jv.b = rq; jv.c = ro;
+        jv.y = dv;
+        jv.reverse = 1;
+        jv.s_in = dfinal_state;
+        jv.s_out = dinitial_state;
+        // dq: (do, v, k) forward in time, the state read transposed
+        kda::ScanJob& jq = a.job[2];
+        jq.a = ro; jq.b = rv; jq.c = rk;
+        jq.y = pack ? (void*)(ws + wl.part_q) : dq;
+        jq.pack = pack;
+        jq.s_in = initial_state;
+        jq.s_in_t = 1;
 
         hipError_t e;
         if (seg != 0) {
             float* fwd = (float*)(ws + wl.seg_f);
             float* bwd = (float*)(ws + wl.seg_r);
-            kda::ScanArgs b = a;
-            b.roles = 2;
-            b.share = 2 * G;
             // the segments' own sums: of v k^T forward, of do q^T backward in time
-            kda::ScanRole& f = b.role[0];
-            f = kda::ScanRole{};
-            k_op(f.b, f.sb, f.gb); v_op(f.c, f.sc, f.gc);
-            f.ga = 1;
-            f.s_out = fwd;
-            f.s_by_seg = 1;
-            kda::ScanRole& r = b.role[1];
-            r = kda::ScanRole{};
-            q_op(r.b, r.sb, r.gb); o_op(r.c, r.sc, r.gc);
-            r.ga = 1;
-            r.reverse = 1;
-            r.s_out = bwd;
-            r.s_by_seg = 1;
+            kda::ScanArgs b = a;
+            b.jobs = 2;
+            b.share = 2 * G;
+            b.by_seg = 1;
+            b.job[0] = b.job[1] = kda::ScanJob{};
+            b.job[0].b = rk; b.job[0].c = rv;
+            b.job[0].s_out = fwd;
+            b.job[1].b = rq; b.job[1].c = ro;
+            b.job[1].s_out = bwd;
+            b.job[1].reverse = 1;
             e = kda::launch_decay_scan(b, true, stream);
             if (e != hipSuccess) return hip_fail(e, "segment state launch");
             kda::ChainArgs c{};
@@ -478,15 +472,15 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
             c.reverse = 1;
             e = kda::launch_decay_chain(c, stream);
             if (e != hipSuccess) return hip_fail(e, "segment chain launch");
-            rq.s_in = fwd;
-            rk.s_in = rv.s_in = bwd;
-            rv.s_out = nullptr;
-            rq.s_by_seg = rk.s_by_seg = rv.s_by_seg = 1;
+            jq.s_in = fwd;
+            jk.s_in = jv.s_in = bwd;
+            jv.s_out = nullptr;
+            a.by_seg = 1;
         }
         e = kda::launch_decay_scan(a, false, stream);
         if (e != hipSuccess) return hip_fail(e, "decay adjoint launch");
         if (G > 1) {
-            e = kda::launch_decay_group_sum((const float*)(ws + wl.part_q), (const float*)(ws + wl.part_k),
+            e = kda::launch_decay_group_sum(ws + wl.part_q, ws + wl.part_k,
                                             (kda::bf16_t*)dq, (kda::bf16_t*)dk, d.s.tokens, d.s.Hqk, G, stream);
             if (e != hipSuccess) return hip_fail(e, "group sum launch");
         }

@@ -25,26 +25,30 @@ struct ItemMap {
     int64_t items;
 };
 
-// One causal form  y_i = s (sum_{j<=i} e^{l(i-j)} (a_i.b_j) c_j) + ... of the
-// decayed scan (kda_decay.hip).  An operand's row of token t and value head
-// h is base + t*stride + (h / group) * 128 (elements).
-struct ScanRole {
-    const bf16_t *a, *b, *c;
-    int64_t sa, sb, sc;
-    int ga, gb, gc;
-    void* y;                 // [tokens][Hv][128]: BF16, or FP32 partials when y_f32
-    int y_f32;
-    int reverse;             // tokens in descending order, state shifted by one decay
+// Token rows that a scan reads: the row of token t and value head h is
+// p + t*stride + (h / group) * 128 (elements).
+struct ScanRows {
+    const bf16_t* p;
+    int64_t stride;
+    int group;
+};
+// One form of the decayed scan, y = a (b^T c) walked over the tokens
+// (kda_decay.hip).
+struct ScanJob {
+    ScanRows b, c, a;        // (states only: no a)
+    void* y;                 // [tokens][Hv][128], 2 bytes each: BF16, or packed partials
+    int pack;
+    int reverse;             // tokens in descending order, states shifted by one decay
     const float* s_in;       // states [.][Hv][128 v][128 k]; null: zero
     int s_in_t;              // the contraction runs over v (s_in read transposed)
     float* s_out;            // states to write, as s_in; null: none
-    int s_by_seg;            // s_in and s_out are indexed by segment, else by slot
 };
 struct ScanArgs {
     ItemMap map;
-    ScanRole role[3];
-    int roles;
-    int share;               // items that read the same operand rows, adjacent in the item order
+    ScanJob job[3];
+    int jobs;                // forms in this launch, the forms of an item side by side
+    int share;               // work items that read the same rows, adjacent in the item order
+    int by_seg;              // states are indexed by segment, else by slot
     const float* log_decay;  // [Hv]
     float scale;
     const int32_t* slot;     // state slot of sequence n; null: n
@@ -80,9 +84,9 @@ struct TokenArgs {
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s);
 hipError_t launch_decay_chain(const ChainArgs& a, hipStream_t s);
 hipError_t launch_decay_token(const TokenArgs& a, hipStream_t s);
-// dst[t][hq] = sum over the G value heads of src[t][hq*G + g] (FP32 in, BF16
-// out), for both (src0, dst0) and (src1, dst1).
-hipError_t launch_decay_group_sum(const float* src0, const float* src1, bf16_t* dst0, bf16_t* dst1,
+// dst[t][hq] = sum over the G value heads of src[t][hq*G + g] (packed
+// partials in, BF16 out), for both (src0, dst0) and (src1, dst1).
+hipError_t launch_decay_group_sum(const void* src0, const void* src1, bf16_t* dst0, bf16_t* dst1,
                                   int64_t tokens, int Hqk, int G, hipStream_t s);
 
 struct QkNormArgs {

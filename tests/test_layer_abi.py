@@ -100,13 +100,13 @@ def test_decay_workspace_sizes():
     # whole sequences, no shared heads: nothing
     p = decay(Hqk=4, segment=64, T=64)
     assert kda.kda_decay_fwd_workspace_bytes(p) == 0 and kda.kda_decay_bwd_workspace_bytes(p) == 0
-    # shared heads: FP32 partials of dq and dk
+    # shared heads: partials of dq and dk, 2 bytes a value
     p = decay(segment=64, T=64)
-    assert kda.kda_decay_bwd_workspace_bytes(p) == 2 * up(64 * 4 * 128 * 4)
+    assert kda.kda_decay_bwd_workspace_bytes(p) == 2 * up(64 * 4 * 128 * 2)
     # segments: a state each, both ways in the backward
     p = decay(segment=64, T=200)
     assert kda.kda_decay_fwd_workspace_bytes(p) == 4 * 4 * state
-    assert kda.kda_decay_bwd_workspace_bytes(p) == 2 * 4 * 4 * state + 2 * up(200 * 4 * 128 * 4)
+    assert kda.kda_decay_bwd_workspace_bytes(p) == 2 * 4 * 4 * state + 2 * up(200 * 4 * 128 * 2)
     assert kda.kda_decay_infer_workspace_bytes(p) == 4 * 4 * state
     assert fwd(p) == NULL
     assert fwd(p, ws=90 * GAP, ws_bytes=4 * 4 * state - 1) == WS
