@@ -125,7 +125,7 @@ __device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 1) & 
 
 // Transposing read: the 16 lanes of group gq address 4 rows x 4 pieces of 4
 // channels, and lane m receives the 4 rows of channel m of those 16.
-__device__ __forceinline__ bf16x4 tr_read(const bf16* p) {
+__device__ __forceinline__ bf16x4 tr_read(const char* p) {
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4*)p));
 }
@@ -147,14 +147,6 @@ __device__ __forceinline__ bf16x4 take_high(f32x4& x) {
     x -= __builtin_bit_cast(f32x4, u);
     return __builtin_bit_cast(bf16x4, u32x2{__builtin_amdgcn_perm(u[1], u[0], 0x07060302u),
                                             __builtin_amdgcn_perm(u[3], u[2], 0x07060302u)});
-}
-
-// x, as a value the compiler cannot know to be the same in every loop round:
-// products of it are formed where they are used instead of being kept in
-// registers over the loop.
-__device__ __forceinline__ float fresh(float x) {
-    asm volatile("" : "+v"(x));
-    return x;
 }
 
 }  // namespace
@@ -201,6 +193,9 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 //     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
 //     S^T = e^{32 l} S^T + B^T (C u),   u_j = e^{l(32-shift-j)}
+// The state is kept divided by the decay since it was last rescaled, so that
+// most chunks only add to it (weights u_j over that decay) and y takes the
+// decay as one more factor; it is rescaled when the decay falls below 2^-24.
 // Two operands are rounded to BF16: P, and S where it meets a (each about as
 // large an error as the output's own rounding).  The FP32 products C u go in
 // as three BF16 pieces of 8 significant bits each, so exactly; the state
@@ -213,10 +208,11 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // unit.  `reverse` walks the tokens downwards and only shifts the exponents.
 template <bool kOut, bool kPack>
 __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
-    // one LDS block (elements): two buffers of SETS row blocks; two of P^T tiles
-    constexpr int SETS = kOut ? 3 : 2, SET = SC * D, LBUF = SETS * SET;   // rows of b, c, a
-    constexpr int LB = 0, LC = SET, LA = 2 * SET, LP = 2 * LBUF, LPBUF = 3 * 256;
-    __shared__ __align__(16) bf16 lds[LP + (kOut ? 2 * LPBUF : 0)];
+    // one LDS block (bytes): two buffers of SETS row blocks; two of P^T tiles
+    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LBUF = SETS * SET;   // rows of b, c, a
+    constexpr int LB = 0, LC = SET, LA = 2 * SET, LP = 2 * LBUF, LPT = 512, LPBUF = 3 * LPT;
+    constexpr int ROWS16 = 16 * D * 2;
+    __shared__ __align__(16) char lds[LP + (kOut ? 2 * LPBUF : 0)];
 
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -258,19 +254,29 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     }
     u32x4 x[SETS][SC_LOADS];
     auto fetch = [&](int t0) __attribute__((always_inline)) {
+        unsigned o[SETS][SC_LOADS];
+        if (t0 + SC <= it.len) {
 #pragma unroll
-        for (int j = 0; j < SC_LOADS; ++j) {
-            const bool in = t0 + lr + SC_ROWS * j < it.len;
+            for (int i = 0; i < SETS; ++i)
 #pragma unroll
-            for (int i = 0; i < SETS; ++i) {
-                const unsigned top = (rev ? (unsigned)((SC - 1) * rows[i].stride * 2) : 0u) + lc * 2;
-                x[i][j] = *row_ptr<u32x4>(pr[i], in ? off[i] + j * up[i] : top);
+                for (int j = 0; j < SC_LOADS; ++j) o[i][j] = off[i] + j * up[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < SC_LOADS; ++j) {
+                const int r = t0 + lr + SC_ROWS * j < it.len ? lr + SC_ROWS * j : 0;
+#pragma unroll
+                for (int i = 0; i < SETS; ++i)
+                    o[i][j] = (unsigned)(rev ? SC - 1 - r : r) * (unsigned)(rows[i].stride * 2) + lc * 2;
             }
         }
 #pragma unroll
+        for (int j = 0; j < SC_LOADS; ++j)
+#pragma unroll
+            for (int i = 0; i < SETS; ++i) x[i][j] = *row_ptr<u32x4>(pr[i], o[i][j]);
+#pragma unroll
         for (int i = 0; i < SETS; ++i) pr[i] += gr[i];
     };
-    const int st_off = lr * D + (((lc >> 3) ^ swz(lr)) << 3);
+    const int st_off = (lr * D + (((lc >> 3) ^ swz(lr)) << 3)) * 2;
     auto stage = [&](int buf, int t0) __attribute__((always_inline)) {   // (rows 16 apart share their swz)
         if (t0 + SC > it.len) {
 #pragma unroll
@@ -283,7 +289,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         for (int i = 0; i < SETS; ++i)
 #pragma unroll
             for (int j = 0; j < SC_LOADS; ++j)
-                *(u32x4*)(lds + buf + i * SET + st_off + SC_ROWS * j * D) = x[i][j];
+                *(u32x4*)(lds + buf + i * SET + st_off + SC_ROWS * j * D * 2) = x[i][j];
     };
     fetch(0);
 
@@ -317,27 +323,32 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     // wave 1 (1, 1), wave 2 (1, 0).
     //     P^T at i - j = 16d + n - 4gq - e:   pf[e] (d = 1 in wave 2, else 0)
     //     Y column i = 16ti + n:              y0 (times far for ti = 1)
-    //     C row j = 16tj + r, r = 4gq + e:    u0[e] (times far for tj = 0)
+    //     C row j = 16tj + 4gq + e:           u0[tj][e]
     const float far = __int_as_float(__builtin_amdgcn_readfirstlane(
         __float_as_int(__builtin_amdgcn_exp2f(l2 * 16.0f))));
     const float y0 = y_state * __builtin_amdgcn_exp2f(l2 * (float)(n16 + shift));
-    float pf[4], u0[4];
+    float pf[4], u0[2][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         pf[e] = scale * __builtin_amdgcn_exp2f(l2 * (float)max((w == 2 ? 16 : 0) + n16 - 4 * gq - e, 0));
-        u0[e] = s_add * __builtin_amdgcn_exp2f(l2 * (float)(16 - shift - 4 * gq - e));
+        u0[1][e] = s_add * __builtin_amdgcn_exp2f(l2 * (float)(16 - shift - 4 * gq - e));
+        u0[0][e] = u0[1][e] * far;
     }
-    Power chunk_decay(l, SC);   // the state's factor per chunk
+    // the state is `held` times S; a chunk's decay and its inverse
+    const double lam = uniform(decay_power(l, SC)), inv = uniform(1.0 / lam);
+    double held = 1.0, over = 1.0;   // over = 1 / held
 
-    // LDS addresses (elements), for p, t = 0 and in the low bits, where xors of
-    // 32p and 16t give the others (buffers are multiples of 4096): 4 channels
+    // LDS addresses (bytes), for p, t = 0 and in the low bits, where xors of 64p
+    // and 32t give the others (buffers are multiples of 8192): 4 channels
     // (32p + 4gq) of row n, 8 channels (32p + 8gq) of row n, and for the
     // transposing reads channels 16t + 4a of row 4gq + n/4 (a = n%4)
-    const int rd = n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1);
-    const int r8 = n16 * D + ((gq ^ swz(n16)) << 3);
+    const int rd = (n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1)) * 2;
+    int rd1 = rd + ROWS16;
+    asm volatile("" : "+v"(rd1));   // (else the two rows' reads merge into one of the wrong order)
+    const int r8 = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
     const int trow = 4 * gq + (n16 >> 2);
-    const int tr = trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1);
-    const int trc = tr ^ (16 * NU * w);                 // this wave's C columns
+    const int tr = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
+    const int trc = tr ^ (32 * NU * w);                 // this wave's C columns
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
     const char* yout = (const char*)J.y;
@@ -348,33 +359,33 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     // this wave's P^T tile of the chunk in buffer `buf`
     auto form_p = [&](int buf, int pbuf) __attribute__((always_inline)) {
         if (w < 3) {
-            const int jrow = w == 1 ? 16 * D : 0, irow = w == 0 ? 0 : 16 * D;
+            const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
             const int at = buf + r8;
             f32x4 acc = zero4();
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                acc = mma32(*(const bf16x8*)(lds + LB + (at ^ (32 * p)) + jrow),
-                            *(const bf16x8*)(lds + LA + (at ^ (32 * p)) + irow), acc);
+                acc = mma32(*(const bf16x8*)(lds + LB + (at ^ (64 * p)) + jrow),
+                            *(const bf16x8*)(lds + LA + (at ^ (64 * p)) + irow), acc);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
                 const bool seen = (w == 2) | (n16 >= 4 * gq + e);
                 acc[e] = seen ? acc[e] * pf[e] : 0.0f;
             }
-            *(bf16x4*)(lds + LP + pbuf + w * 256 + lane * 4) = to_bf4(acc);
+            *(bf16x4*)(lds + LP + pbuf + w * LPT + lane * 8) = to_bf4(acc);
         }
     };
 
     auto chunk = [&](int t0, int buf, int pbuf, auto tail_c) __attribute__((always_inline)) {
         constexpr bool kTail = decltype(tail_c)::value;
         const int rem = kTail ? it.len - t0 : SC;
-        const float fs = kTail ? (float)decay_power(l, rem) : chunk_decay.next();
+        const float y_held = (float)held * y0;
         {
             // C columns of this wave
             bf16x4 cf[2][NU];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (16 * u)) + 16 * j * D);
+                for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (32 * u)) + ROWS16 * j);
             if (kOut) {
                 f32x4 y[2][NU];
 #pragma unroll
@@ -386,8 +397,8 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
                     bf16x8 av[2];
 #pragma unroll
                     for (int ti = 0; ti < 2; ++ti)
-                        av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p)) + 16 * ti * D),
-                                      *(const bf16x4*)(lds + LA + ((buf + rd) ^ (32 * p + 16)) + 16 * ti * D));
+                        av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + (ti ? rd1 : rd)) ^ (64 * p))),
+                                      *(const bf16x4*)(lds + LA + ((buf + (ti ? rd1 : rd)) ^ (64 * p + 32))));
 #pragma unroll
                     for (int u = 0; u < NU; ++u) {
                         const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
@@ -395,19 +406,19 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
                         for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
                     }
                 }
-                const bf16x4 none = to_bf4(zero4());
-                const bf16* pt = lds + LP + pbuf + lane * 4;
-                const bf16x4 p00 = *(const bf16x4*)pt, p11 = *(const bf16x4*)(pt + 256),
-                             p10 = *(const bf16x4*)(pt + 512);
-                const float yf[2] = {y0, fresh(y0) * far};
+                const char* pt = lds + LP + pbuf + lane * 8;
+                const bf16x4 p00 = *(const bf16x4*)pt, p11 = *(const bf16x4*)(pt + LPT),
+                             p10 = *(const bf16x4*)(pt + 2 * LPT);
+                const float yf[2] = {y_held, y_held * far};
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
 #pragma unroll
                     for (int ti = 0; ti < 2; ++ti)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[ti][u][e] *= yf[ti];
-                    y[0][u] = mma32(cat8(cf[0][u], none), cat8(p00, none), y[0][u]);
-                    y[1][u] = mma32(cat8(cf[0][u], cf[1][u]), cat8(p10, p11), y[1][u]);
+                    const bf16x8 c = cat8(cf[0][u], cf[1][u]);
+                    y[0][u] = mma32(c, cat8(p00, to_bf4(zero4())), y[0][u]);
+                    y[1][u] = mma32(c, cat8(p10, p11), y[1][u]);
                 }
                 const char* yb = yout + py;
 #pragma unroll
@@ -421,6 +432,25 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
                 }
             }
             // state update
+            if (kTail) {
+                const double d = decay_power(l, rem);
+                held *= d;
+                over /= d;
+            } else {
+                held = uniform(held * lam);
+                over = uniform(over * inv);
+            }
+            if (held < 0x1p-24) {
+                const float f = (float)held;
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[t][u][e] *= f;
+                held = over = 1.0;
+            }
+            const float g = (float)over;
             bf16x8 c1[NU], c2[NU], c3[NU];
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
@@ -430,9 +460,9 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
                     f32x4 c = from_bf4(cf[j][u]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        c[e] *= kTail ? s_add * __builtin_amdgcn_exp2f(
-                                                    l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
-                                : j == 0 ? fresh(u0[e]) * far : u0[e];
+                        c[e] *= g * (kTail ? s_add * __builtin_amdgcn_exp2f(
+                                                         l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
+                                           : u0[j][e]);
                     x1[j] = take_high(c);
                     x2[j] = take_high(c);
                     x3[j] = to_bf4(c);
@@ -443,19 +473,14 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (16 * t))),
-                                       tr_read(lds + LB + ((buf + tr) ^ (16 * t)) + 16 * D));
-                f32x4 acc[NU];
+                const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (32 * t))),
+                                       tr_read(lds + LB + ((buf + tr) ^ (32 * t)) + ROWS16));
 #pragma unroll
-                for (int u = 0; u < NU; ++u)
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c1[u], S[t][u]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[u][e] = S[t][u][e] * fs;
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c2[u], S[t][u]);
 #pragma unroll
-                for (int u = 0; u < NU; ++u) acc[u] = mma32(bt, c1[u], acc[u]);
-#pragma unroll
-                for (int u = 0; u < NU; ++u) acc[u] = mma32(bt, c2[u], acc[u]);
-#pragma unroll
-                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], acc[u]);
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], S[t][u]);
             }
         }
         py += 2 * gy;
@@ -494,7 +519,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                *(f32x4*)(s_out + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq) = S[t][u];
+                *(f32x4*)(s_out + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq) = S[t][u] * (float)held;
     }
 }
 
