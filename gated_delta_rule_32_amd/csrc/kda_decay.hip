@@ -23,8 +23,6 @@ constexpr int SC = 32;            // tokens per chunk
 constexpr int NU = 2;             // 16-channel tiles of the output per wave
 constexpr int SC_WAVES = 8 / NU;
 constexpr int SC_THREADS = 64 * SC_WAVES;
-constexpr int SC_ROWS = SC_THREADS / 16;   // rows that one load instruction of the workgroup covers
-constexpr int SC_LOADS = SC / SC_ROWS;
 constexpr int STATE = D * D;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -140,6 +138,35 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* row_ptr(const vo
     return (__attribute__((address_space(1))) T*)((__attribute__((address_space(1))) char*)b + off);
 }
 
+// Moves 16 bytes per lane from base + off (off per lane) to LDS at dst (uniform)
+// + 16 lane.
+__device__ __forceinline__ void to_lds(const char* base, unsigned off, char* dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)row_ptr<const char>(base, off),
+                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+// Waits until at most N of this wave's vector memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
+}
+// Workgroup barrier for LDS contents: this wave's LDS operations are complete
+// before it; memory operations stay on their side of it.  (__syncthreads would
+// also wait for the stores to global memory.)
+__device__ __forceinline__ void barrier_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// x, as a value the compiler cannot know to be the same in every loop round:
+// what is formed from it is formed where it is used instead of being kept in
+// registers over the loop.
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Takes the leading 8 significant bits of every element off x and returns
 // them as BF16 (the remainder is exact).
 __device__ __forceinline__ bf16x4 take_high(f32x4& x) {
@@ -201,18 +228,22 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // as three BF16 pieces of 8 significant bits each, so exactly; the state
 // itself stays in FP32 registers.
 //
-// The chunks run as a pipeline: while chunk c's y and state are formed, three
-// of the waves form the P^T tiles of chunk c+1, and the rows of chunk c+2 are
-// on their way into registers, from where they go to chunk c's LDS buffer.
+// The rows of the next chunk travel from memory to the other of two LDS
+// buffers (without passing through registers) while this one is computed:
+//     before the first barrier   P^T (one tile in each of three waves), the
+//                                state's part of Y, the pieces of C u
+//     before the second          C^T P^T, stores, the state's update
 // Two buffers and at most 168 registers let three workgroups share a compute
 // unit.  `reverse` walks the tokens downwards and only shifts the exponents.
 template <bool kOut, bool kPack>
 __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
-    // one LDS block (bytes): two buffers of SETS row blocks; two of P^T tiles
-    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LBUF = SETS * SET;   // rows of b, c, a
-    constexpr int LB = 0, LC = SET, LA = 2 * SET, LP = 2 * LBUF, LPT = 512, LPBUF = 3 * LPT;
+    // LDS (bytes): a buffer holds the rows of b, c and a; the buffers are
+    // objects of their own, so that the compiler sees that what is read from
+    // one does not wait for what is on its way into the other
+    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = SET, LA = 2 * SET, LPT = 512;
     constexpr int ROWS16 = 16 * D * 2;
-    __shared__ __align__(16) char lds[LP + (kOut ? 2 * LPBUF : 0)];
+    __shared__ __align__(16) char lds[2 * SETS * SET];
+    __shared__ __align__(16) char lds_p[kOut ? 3 * LPT : 16];
 
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -233,65 +264,41 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const float y_state = rev ? 1.0f : scale;     // scale of the state's part of y
     const float s_add = rev ? scale : 1.0f;       // scale of what the state takes up
 
-    // This thread's loads: 16 bytes of rows tid/16 (+ SC_ROWS i) of a chunk.
-    // The chunk's lowest row is a uniform base (scalar registers), a lane's row
-    // a 32-bit offset.  For rows behind the last token the chunk's first row is
-    // read again and the values are dropped in stage().
-    const int lr = tid >> 4, lc = (tid & 15) * 8;
+    // Loads: one instruction of a wave moves 4 rows of 256 bytes (16 lanes a
+    // row) to 1 KiB of LDS in lane order; a lane fetches the block that belongs
+    // there.  A chunk's rows 4w .. 4w+3 and 16 more are wave w's.  The address
+    // is a uniform base (the chunk's lowest row) plus a 32-bit lane offset.
     const int64_t first = rev ? it.tok0 + it.len - 1 : it.tok0;
     const int64_t dir = rev ? -1 : 1;
+    const int lrow = 4 * w + gq;
     const ScanRows rows[3] = {J.b, J.c, J.a};
     const char* pr[SETS];
-    int64_t gr[SETS];
-    unsigned off[SETS], up[SETS];   // offset of row lr; of SC_ROWS rows more (modulo 2^32)
+    int64_t bytes[SETS];
+    unsigned off[SETS];
 #pragma unroll
     for (int i = 0; i < SETS; ++i) {
-        const int64_t bytes = rows[i].stride * 2;
-        pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? SC - 1 : 0)) * bytes;
-        gr[i] = SC * dir * bytes;
-        off[i] = (unsigned)(rev ? SC - 1 - lr : lr) * (unsigned)bytes + lc * 2;
-        up[i] = (unsigned)(SC_ROWS * (int)dir) * (unsigned)bytes;
+        bytes[i] = rows[i].stride * 2;
+        pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? 15 : 0)) * bytes[i];
+        off[i] = (unsigned)(rev ? 15 - lrow : lrow) * (unsigned)bytes[i] + ((n16 ^ swz(lrow)) << 4);
     }
-    u32x4 x[SETS][SC_LOADS];
-    auto fetch = [&](int t0) __attribute__((always_inline)) {
-        unsigned o[SETS][SC_LOADS];
-        if (t0 + SC <= it.len) {
+    auto fetch = [&](char* buf, int t0) __attribute__((always_inline)) {
+        const int rem = it.len - t0;
 #pragma unroll
-            for (int i = 0; i < SETS; ++i)
-#pragma unroll
-                for (int j = 0; j < SC_LOADS; ++j) o[i][j] = off[i] + j * up[i];
-        } else {
-#pragma unroll
-            for (int j = 0; j < SC_LOADS; ++j) {
-                const int r = t0 + lr + SC_ROWS * j < it.len ? lr + SC_ROWS * j : 0;
+        for (int j = 0; j < 2; ++j) {
+            if (rem >= SC || lrow + 16 * j < rem) {
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
-                    o[i][j] = (unsigned)(rev ? SC - 1 - r : r) * (unsigned)(rows[i].stride * 2) + lc * 2;
+                    to_lds(pr[i] + j * 16 * dir * bytes[i], off[i], buf + i * SET + (16 * j + 4 * w) * D * 2);
+            } else {   // rows behind the last token are not read and count as zero
+#pragma unroll
+                for (int i = 0; i < SETS; ++i)
+                    *(u32x4*)(buf + i * SET + (16 * j + 4 * w) * D * 2 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
             }
         }
 #pragma unroll
-        for (int j = 0; j < SC_LOADS; ++j)
-#pragma unroll
-            for (int i = 0; i < SETS; ++i) x[i][j] = *row_ptr<u32x4>(pr[i], o[i][j]);
-#pragma unroll
-        for (int i = 0; i < SETS; ++i) pr[i] += gr[i];
+        for (int i = 0; i < SETS; ++i) pr[i] += SC * dir * bytes[i];
     };
-    const int st_off = (lr * D + (((lc >> 3) ^ swz(lr)) << 3)) * 2;
-    auto stage = [&](int buf, int t0) __attribute__((always_inline)) {   // (rows 16 apart share their swz)
-        if (t0 + SC > it.len) {
-#pragma unroll
-            for (int j = 0; j < SC_LOADS; ++j)
-#pragma unroll
-                for (int i = 0; i < SETS; ++i)
-                    if (t0 + lr + SC_ROWS * j >= it.len) x[i][j] = u32x4{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int i = 0; i < SETS; ++i)
-#pragma unroll
-            for (int j = 0; j < SC_LOADS; ++j)
-                *(u32x4*)(lds + buf + i * SET + st_off + SC_ROWS * j * D * 2) = x[i][j];
-    };
-    fetch(0);
+    fetch(lds, 0);
 
     // state
     f32x4 S[8][NU];
@@ -338,17 +345,14 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const double lam = uniform(decay_power(l, SC)), inv = uniform(1.0 / lam);
     double held = 1.0, over = 1.0;   // over = 1 / held
 
-    // LDS addresses (bytes), for p, t = 0 and in the low bits, where xors of 64p
-    // and 32t give the others (buffers are multiples of 8192): 4 channels
-    // (32p + 4gq) of row n, 8 channels (32p + 8gq) of row n, and for the
-    // transposing reads channels 16t + 4a of row 4gq + n/4 (a = n%4)
-    const int rd = (n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1)) * 2;
-    int rd1 = rd + ROWS16;
-    asm volatile("" : "+v"(rd1));   // (else the two rows' reads merge into one of the wrong order)
-    const int r8 = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
+    // LDS offsets (bytes), for p, t = 0 and in the low bits, where xors of 64p
+    // and 32t give the others: 4 channels (32p + 4gq) of row n, 8 channels
+    // (32p + 8gq) of row n, and for the transposing reads channels 16t + 4a of
+    // row 4gq + n/4 (a = n%4)
+    const int rd_ = (n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1)) * 2;
+    const int r8_ = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
     const int trow = 4 * gq + (n16 >> 2);
-    const int tr = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
-    const int trc = tr ^ (32 * NU * w);                 // this wave's C columns
+    const int tr_ = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
     const char* yout = (const char*)J.y;
@@ -356,162 +360,147 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     int64_t py = ((first - (rev ? 15 : 0)) * Hv + it.h) * D * 2;
     const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * w + 4 * gq) * 2;
 
-    // this wave's P^T tile of the chunk in buffer `buf`
-    auto form_p = [&](int buf, int pbuf) __attribute__((always_inline)) {
-        if (w < 3) {
-            const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
-            const int at = buf + r8;
-            f32x4 acc = zero4();
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                acc = mma32(*(const bf16x8*)(lds + LB + (at ^ (64 * p)) + jrow),
-                            *(const bf16x8*)(lds + LA + (at ^ (64 * p)) + irow), acc);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
-                const bool seen = (w == 2) | (n16 >= 4 * gq + e);
-                acc[e] = seen ? acc[e] * pf[e] : 0.0f;
-            }
-            *(bf16x4*)(lds + LP + pbuf + w * LPT + lane * 8) = to_bf4(acc);
-        }
-    };
-
-    auto chunk = [&](int t0, int buf, int pbuf, auto tail_c) __attribute__((always_inline)) {
+    // One chunk in `buf`, the next one's rows on their way into `other`.
+    auto chunk = [&](int t0, const char* __restrict__ buf, char* __restrict__ other, auto tail_c) __attribute__((always_inline)) {
         constexpr bool kTail = decltype(tail_c)::value;
         const int rem = kTail ? it.len - t0 : SC;
+        if (!kTail && t0 + SC < it.len) fetch(other, t0 + SC);
+        // (formed anew per chunk, rather than kept in a register each)
+        const int rd = fresh(rd_), rd1 = fresh(rd_ + ROWS16), r8 = fresh(r8_), tr = fresh(tr_);
         const float y_held = (float)held * y0;
-        {
-            // C columns of this wave
-            bf16x4 cf[2][NU];
+        const double d = kTail ? uniform(decay_power(l, rem)) : lam;
+        held = uniform(held * d);
+        over = uniform(kTail ? over / d : over * inv);
+        const bool rescale = held < 0x1p-24;
+        const float down = (float)held;
+        if (rescale) held = over = 1.0;
+        const float g = (float)over;
+
+        f32x4 y[2][NU];
+        if (kOut) {
+            if (w < 3) {   // this wave's P^T tile
+                const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
+                f32x4 acc = zero4();
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int p = 0; p < 4; ++p)
+                    acc = mma32(*(const bf16x8*)(buf + LB + (r8 ^ (64 * p)) + jrow),
+                                *(const bf16x8*)(buf + LA + (r8 ^ (64 * p)) + irow), acc);
 #pragma unroll
-                for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(lds + LC + ((buf + trc) ^ (32 * u)) + ROWS16 * j);
-            if (kOut) {
-                f32x4 y[2][NU];
+                for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
+                    const bool seen = (w == 2) | (n16 >= 4 * gq + e);
+                    acc[e] = seen ? acc[e] * pf[e] : 0.0f;
+                }
+                *(bf16x4*)(lds_p + w * LPT + lane * 8) = to_bf4(acc);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti)
+#pragma unroll
+                for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                bf16x8 av[2];
+#pragma unroll
+                for (int ti = 0; ti < 2; ++ti)
+                    av[ti] = cat8(*(const bf16x4*)(buf + LA + ((ti ? rd1 : rd) ^ (64 * p))),
+                                  *(const bf16x4*)(buf + LA + ((ti ? rd1 : rd) ^ (64 * p + 32))));
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
+                }
+            }
+        }
+        if (kOut) barrier_lds();
+        if (rescale) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[t][u][e] *= down;
+        }
+        // C columns of this wave
+        bf16x4 cf[2][NU];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (tr ^ (32 * (NU * w + u))) + ROWS16 * j);
+        if (kOut) {
+            const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
+                         p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
+            const float yf[2] = {y_held, y_held * far};
+            const char* yb = yout + py;
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
 #pragma unroll
                 for (int ti = 0; ti < 2; ++ti)
 #pragma unroll
-                    for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    bf16x8 av[2];
-#pragma unroll
-                    for (int ti = 0; ti < 2; ++ti)
-                        av[ti] = cat8(*(const bf16x4*)(lds + LA + ((buf + (ti ? rd1 : rd)) ^ (64 * p))),
-                                      *(const bf16x4*)(lds + LA + ((buf + (ti ? rd1 : rd)) ^ (64 * p + 32))));
-#pragma unroll
-                    for (int u = 0; u < NU; ++u) {
-                        const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
-#pragma unroll
-                        for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
-                    }
-                }
-                const char* pt = lds + LP + pbuf + lane * 8;
-                const bf16x4 p00 = *(const bf16x4*)pt, p11 = *(const bf16x4*)(pt + LPT),
-                             p10 = *(const bf16x4*)(pt + 2 * LPT);
-                const float yf[2] = {y_held, y_held * far};
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-#pragma unroll
-                    for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[ti][u][e] *= yf[ti];
-                    const bf16x8 c = cat8(cf[0][u], cf[1][u]);
-                    y[0][u] = mma32(c, cat8(p00, to_bf4(zero4())), y[0][u]);
-                    y[1][u] = mma32(c, cat8(p10, p11), y[1][u]);
-                }
-                const char* yb = yout + py;
-#pragma unroll
-                for (int ti = 0; ti < 2; ++ti) {
-                    if (!kTail || 16 * ti + n16 < rem) {
-#pragma unroll
-                        for (int u = 0; u < NU; ++u)
-                            *row_ptr<u32x2>(yb + ti * gy + 32 * u, oy) =
-                                kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
-                    }
-                }
+                    for (int e = 0; e < 4; ++e) y[ti][u][e] *= yf[ti];
+                const bf16x8 c = cat8(cf[0][u], cf[1][u]);
+                y[0][u] = mma32(c, cat8(p00, to_bf4(zero4())), y[0][u]);
+                y[1][u] = mma32(c, cat8(p10, p11), y[1][u]);
             }
-            // state update
-            if (kTail) {
-                const double d = decay_power(l, rem);
-                held *= d;
-                over /= d;
-            } else {
-                held = uniform(held * lam);
-                over = uniform(over * inv);
-            }
-            if (held < 0x1p-24) {
-                const float f = (float)held;
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
+            for (int ti = 0; ti < 2; ++ti) {
+                if (!kTail || 16 * ti + n16 < rem) {
 #pragma unroll
                     for (int u = 0; u < NU; ++u)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) S[t][u][e] *= f;
-                held = over = 1.0;
-            }
-            const float g = (float)over;
-            bf16x8 c1[NU], c2[NU], c3[NU];
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                bf16x4 x1[2], x2[2], x3[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    f32x4 c = from_bf4(cf[j][u]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[e] *= g * (kTail ? s_add * __builtin_amdgcn_exp2f(
-                                                         l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
-                                           : u0[j][e]);
-                    x1[j] = take_high(c);
-                    x2[j] = take_high(c);
-                    x3[j] = to_bf4(c);
+                        *row_ptr<u32x2>(yb + ti * gy + 32 * u, oy) =
+                            kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
                 }
-                c1[u] = cat8(x1[0], x1[1]);
-                c2[u] = cat8(x2[0], x2[1]);
-                c3[u] = cat8(x3[0], x3[1]);
             }
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const bf16x8 bt = cat8(tr_read(lds + LB + ((buf + tr) ^ (32 * t))),
-                                       tr_read(lds + LB + ((buf + tr) ^ (32 * t)) + ROWS16));
-#pragma unroll
-                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c1[u], S[t][u]);
-#pragma unroll
-                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c2[u], S[t][u]);
-#pragma unroll
-                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], S[t][u]);
-            }
+            py += 2 * gy;
         }
-        py += 2 * gy;
+        // the pieces of C u
+        bf16x8 c1[NU], c2[NU], c3[NU];
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            bf16x4 x1[2], x2[2], x3[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f32x4 c = from_bf4(cf[j][u]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[e] *= g * (kTail ? s_add * __builtin_amdgcn_exp2f(
+                                                     l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
+                                       : u0[j][e]);
+                x1[j] = take_high(c);
+                x2[j] = take_high(c);
+                x3[j] = to_bf4(c);
+            }
+            c1[u] = cat8(x1[0], x1[1]);
+            c2[u] = cat8(x2[0], x2[1]);
+            c3[u] = cat8(x3[0], x3[1]);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const bf16x8 bt = cat8(tr_read(buf + LB + (tr ^ (32 * t))), tr_read(buf + LB + (tr ^ (32 * t)) + ROWS16));
+#pragma unroll
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c1[u], S[t][u]);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c2[u], S[t][u]);
+#pragma unroll
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], S[t][u]);
+        }
+        if (!kTail) {
+            // the next chunk's rows have arrived when at most this chunk's
+            // stores, issued after them, are outstanding
+            if (kOut)
+                wait_vm<2 * NU>();
+            else
+                wait_vm<0>();
+            barrier_lds();
+        }
     };
-    // the first two chunks' rows and the first one's P
-    stage(0, 0);
-    if (SC < it.len) {
-        fetch(SC);
-        stage(LBUF, SC);
+    wait_vm<0>();
+    barrier_lds();
+    int t0 = 0, at = 0;
+    for (; t0 + SC <= it.len; t0 += SC) {
+        chunk(t0, lds + at, lds + (SETS * SET - at), std::false_type{});
+        at = SETS * SET - at;
     }
-    __syncthreads();
-    if (kOut) {
-        form_p(0, 0);
-        __syncthreads();
-    }
-    int t0 = 0, buf = 0, pbuf = 0;
-    while (t0 + SC <= it.len) {
-        const bool more = t0 + 2 * SC < it.len;
-        if (more) fetch(t0 + 2 * SC);
-        if (kOut && t0 + SC < it.len) form_p(LBUF - buf, LPBUF - pbuf);
-        chunk(t0, buf, pbuf, std::false_type{});
-        __syncthreads();
-        if (more) {
-            stage(buf, t0 + 2 * SC);
-            __syncthreads();
-        }
-        t0 += SC;
-        buf = LBUF - buf;
-        pbuf = LPBUF - pbuf;
-    }
-    if (t0 < it.len) chunk(t0, buf, pbuf, std::true_type{});
+    if (t0 < it.len) chunk(t0, lds + at, nullptr, std::true_type{});
 
     float* s_out = J.s_out;
     if (s_out != nullptr) {
