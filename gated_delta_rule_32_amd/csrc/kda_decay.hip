@@ -213,9 +213,10 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 
 // One workgroup (4 waves) per item and form; wave w owns the state's output
 // channels 32w .. 32w+31 as MFMA accumulators: tile (t, u) holds S^T[k][v] with
-//     k = 16t + 4gq + e,   v = 32w + 16u + n
+//     k = 16t + 4gq + e,   v = 32w + 8(n/4) + 4u + n%4
 // (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
-// rounded to BF16, the operand of S a over channels 32p .. 32p+31.  Per chunk
+// rounded to BF16, the operand of S a over channels 32p .. 32p+31, and the two
+// tiles u of Y^T give a lane 8 neighbouring channels of one token to store.  Per chunk
 // of 32 tokens:
 //     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 
     // state
     f32x4 S[8][NU];
-    const int vrow = 16 * NU * w + n16;   // + 16u
+    const int vrow = 32 * w + 8 * (n16 >> 2) + (n16 & 3);   // + 4u
     const float* s_in = J.s_in;
     if (s_in == nullptr) {
 #pragma unroll
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                S[t][u] = *(const f32x4*)(s_in + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq);
+                S[t][u] = *(const f32x4*)(s_in + soff + (vrow + 4 * u) * D + 16 * t + 4 * gq);
     } else {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -322,7 +323,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             for (int u = 0; u < NU; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    S[t][u][e] = s_in[soff + (16 * t + 4 * gq + e) * D + vrow + 16 * u];
+                    S[t][u][e] = s_in[soff + (16 * t + 4 * gq + e) * D + vrow + 4 * u];
     }
 
     // Powers of e^l, constant over the item's full chunks; each is a product
@@ -353,12 +354,14 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const int r8_ = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
     const int trow = 4 * gq + (n16 >> 2);
     const int tr_ = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
+    // (C: channels 8a .. 8a+3 of row 4gq + n/4, where xors of 64w and 8u give the others)
+    const int trc_ = (trow * D + (((n16 & 3) ^ swz(trow)) << 3)) * 2;
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
     const char* yout = (const char*)J.y;
     const bool pack = J.pack != 0;
     int64_t py = ((first - (rev ? 15 : 0)) * Hv + it.h) * D * 2;
-    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * w + 4 * gq) * 2;
+    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (32 * w + 8 * gq) * 2;
 
     // One chunk in `buf`, the next one's rows on their way into `other`.
     auto chunk = [&](int t0, const char* __restrict__ buf, char* __restrict__ other, auto tail_c) __attribute__((always_inline)) {
@@ -366,7 +369,8 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         const int rem = kTail ? it.len - t0 : SC;
         if (!kTail && t0 + SC < it.len) fetch(other, t0 + SC);
         // (formed anew per chunk, rather than kept in a register each)
-        const int rd = fresh(rd_), rd1 = fresh(rd_ + ROWS16), r8 = fresh(r8_), tr = fresh(tr_);
+        const int rd = fresh(rd_), rd1 = fresh(rd_ + ROWS16), r8 = fresh(r8_), tr = fresh(tr_),
+                  trc = fresh(trc_);
         const float y_held = (float)held * y0;
         const double d = kTail ? uniform(decay_power(l, rem)) : lam;
         held = uniform(held * d);
@@ -425,7 +429,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (tr ^ (32 * (NU * w + u))) + ROWS16 * j);
+            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (trc ^ (64 * w + 8 * u)) + ROWS16 * j);
         if (kOut) {
             const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
                          p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
@@ -443,12 +447,12 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             }
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti) {
-                if (!kTail || 16 * ti + n16 < rem) {
+                u32x2 q[2];
 #pragma unroll
-                    for (int u = 0; u < NU; ++u)
-                        *row_ptr<u32x2>(yb + ti * gy + 32 * u, oy) =
-                            kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
-                }
+                for (int u = 0; u < 2; ++u)
+                    q[u] = kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
+                if (!kTail || 16 * ti + n16 < rem)
+                    *row_ptr<u32x4>(yb + ti * gy, oy) = u32x4{q[0][0], q[0][1], q[1][0], q[1][1]};
             }
             py += 2 * gy;
         }
@@ -487,7 +491,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             // the next chunk's rows have arrived when at most this chunk's
             // stores, issued after them, are outstanding
             if (kOut)
-                wait_vm<2 * NU>();
+                wait_vm<2>();
             else
                 wait_vm<0>();
             barrier_lds();
@@ -508,7 +512,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                *(f32x4*)(s_out + soff + (vrow + 16 * u) * D + 16 * t + 4 * gq) = S[t][u] * (float)held;
+                *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + 16 * t + 4 * gq) = S[t][u] * (float)held;
     }
 }
 
