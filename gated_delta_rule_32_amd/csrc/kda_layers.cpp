@@ -106,18 +106,33 @@ int64_t total_segs(const Decay& d, int seg) {
     return n;
 }
 
-// Tokens per segment of a scan over `roles` forms, or 0 for whole sequences.
-// A whole-sequence scan runs one workgroup per (form, sequence, value head)
-// and two fit a compute unit, so with fewer than 512 of them the card is not
-// full; cutting the sequences into segments costs another pass over two of
-// the three operands and 192 KiB of FP32 state traffic per segment and head.
-int auto_segment(const Decay& d, int roles) {
+// Tokens per segment of a scan over `forms` forms (o, or dq, dk and dv), or 0
+// for whole sequences: whichever an estimate says is faster.  Measured: a
+// workgroup alone on its compute unit takes 1.85 us per chunk of 32 tokens,
+// and the card gets through one chunk of one head every 7.3 ns.  So whole
+// sequences take the longest one's latency or the total's throughput.
+// Segments shorten the first, for a pass that forms the segments' states
+// (1.2 us a chunk, 4.5 ns in all; for the backward both ways), their way
+// through memory (45 ns each) and two more launches.  In us, whole sequences
+// against segments, forward: 16 heads x 32768 tokens 1796 / 213, 32 x 8192
+// 467 / 104, 16 x 1024 63 / 34, 4 sequences x 32 heads x 4096 242 / 213,
+// 8 x 32 x 2048 137 / 214; backward: 16 x 32768 1811 / 439, 2 x 32 x 2048
+// 127 / 124, 4 x 32 x 4096 358 / 422.
+int auto_segment(const Decay& d, int forms) {
     if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
-    const int64_t tasks = (int64_t)d.s.N * d.s.Hv * roles;
-    if (tasks >= 512 || d.s.max_len <= 256) return 0;
-    int64_t seg = (d.s.tokens * d.s.Hv * roles / 768 + 63) / 64 * 64;
-    seg = std::max<int64_t>(seg, 256);
-    return d.s.max_len > seg ? (int)seg : 0;
+    double chunks = 0;
+    for (int64_t len : d.s.len) chunks += (double)((len + 31) / 32);
+    chunks *= d.s.Hv;
+    const int passes = forms == 1 ? 1 : 2;
+    const double whole = std::max(1.85 * (double)((d.s.max_len + 31) / 32), 0.0073 * forms * chunks);
+    // two segments per compute unit (forward), one (backward, three forms each), not below 128 (192) tokens
+    const int64_t items = forms == 1 ? 512 : 256;
+    int64_t seg = (d.s.tokens * d.s.Hv / items + 63) / 64 * 64;
+    seg = std::max<int64_t>(seg, forms == 1 ? 128 : 192);
+    if (d.s.max_len <= seg) return 0;
+    const double cut = std::max(3.05 * (double)(seg / 32), (0.0073 * forms + 0.0045 * passes) * chunks) + 15.0 +
+                       0.045 * passes * (double)(total_segs(d, (int)seg) * d.s.Hv);
+    return cut < 0.95 * whole ? (int)seg : 0;
 }
 
 struct DecayWs {
@@ -167,6 +182,12 @@ kda_status check_grid(int64_t blocks) {
     return KDA_OK;
 }
 
+// Work items that go to one XCD side by side (xcd_order): the value heads of a
+// q/k head, whose rows they share, and at least 8 heads of neighbouring rows
+// (packed 8 x 1024 x 96 heads: training step 660 us with 1, 645 us with 2 to
+// 32; mixed prefill 705 us with 1, 680 us with 8, 697 us with 32).
+int xcd_share(int G) { return (8 + G - 1) / G * G; }
+
 // o's form over whole sequences or segments; the states come from `s_in` and
 // go to `s_out`, both by slot.
 kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const void* q, const void* k, const void* v,
@@ -176,7 +197,7 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
     kda::ScanArgs a{};
     a.map = m;
     a.jobs = 1;
-    a.share = G;
+    a.share = xcd_share(G);
     a.log_decay = log_decay;
     a.scale = d.scale;
     a.slot = slot;
@@ -414,7 +435,7 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
         kda::ScanArgs a{};
         a.map = m;
         a.jobs = 3;
-        a.share = 3 * G;
+        a.share = 3 * xcd_share(G);
         a.log_decay = log_decay;
         a.scale = d.scale;
         a.slots = d.s.N;
@@ -448,7 +469,7 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
             // the segments' own sums: of v k^T forward, of do q^T backward in time
             kda::ScanArgs b = a;
             b.jobs = 2;
-            b.share = 2 * G;
+            b.share = 2 * xcd_share(G);
             b.by_seg = 1;
             b.job[0] = b.job[1] = kda::ScanJob{};
             b.job[0].b = rk; b.job[0].c = rv;

@@ -211,7 +211,8 @@ def test_chunk_factors_do_not_drift(l, segment):
     itself.  1024 roundings of the product, independent from element to
     element with standard deviation 2^-24 / sqrt(3) at most, add up to
     sqrt(1024) of one, and their mean over the 16384 elements to 1/128 of that:
-    bars of 6 standard deviations for both.  A factor rounded the same way in
+    bars of 6 standard deviations for both, and for the mean 2^-24 more, the
+    last rounding of the product of the factors, which all elements share.  A factor rounded the same way in
     every chunk would move the mean by up to 1024 x 2^-25 = 3e-5.  (Segment
     65536: no segments; 0: as many as the library takes.)"""
     import gated_delta_rule_32_amd as kda
@@ -223,7 +224,7 @@ def test_chunk_factors_do_not_drift(l, segment):
     off = lu.f64(fs) / (lu.f64(s0) * math.exp(float(np.float32(l)) * L)) - 1
     std = 32 * 2.0 ** -24 / 3 ** 0.5
     print(f"max {np.abs(off).max() / std:.2f}, mean {abs(off.mean()) / std:.4f} standard deviations", flush=True)
-    assert np.abs(off).max() <= 6 * std and abs(off.mean()) <= 6 * std / 128
+    assert np.abs(off).max() <= 6 * std and abs(off.mean()) <= 6 * std / 128 + 2.0 ** -24
 
 
 def test_same_call_twice_gives_the_same_bits():
