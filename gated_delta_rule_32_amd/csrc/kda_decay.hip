@@ -20,9 +20,6 @@ namespace kda {
 namespace {
 
 constexpr int SC = 32;            // tokens per chunk
-constexpr int NU = 2;             // 16-channel tiles of the output per wave
-constexpr int SC_WAVES = 8 / NU;
-constexpr int SC_THREADS = 64 * SC_WAVES;
 constexpr int STATE = D * D;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -147,6 +144,7 @@ __device__ __forceinline__ void to_lds(const char* base, unsigned off, char* dst
 // Waits until at most N of this wave's vector memory operations are outstanding.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
+    asm volatile("" ::: "memory");   // what was issued before it stays before it
     __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
 }
 // Workgroup barrier for LDS contents: this wave's LDS operations are complete
@@ -211,12 +209,14 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
     return x;
 }
 
-// One workgroup (4 waves) per item and form; wave w owns the state's output
-// channels 32w .. 32w+31 as MFMA accumulators: tile (t, u) holds S^T[k][v] with
-//     k = 16t + 4gq + e,   v = 32w + 8(n/4) + 4u + n%4
+// One workgroup per item and form (kParts = 2: two, each with half of the
+// state's output channels), a wave for every NU tiles of 16 channels.  Wave
+// wv holds the state as MFMA accumulators: tile (t, u) is S^T[k][v] with
+//     k = 16t + 4gq + e,   v = 32wv + 8(n/4) + 4u + n%4   (NU = 1: 16wv + n)
 // (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
 // rounded to BF16, the operand of S a over channels 32p .. 32p+31, and the two
-// tiles u of Y^T give a lane 8 neighbouring channels of one token to store.  Per chunk
+// tiles u of Y^T give a lane 8 neighbouring channels of one token to store
+// (8-byte stores cost the packed forward 4%, the training step 7%).  Per chunk
 // of 32 tokens:
 //     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
@@ -230,17 +230,17 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // itself stays in FP32 registers.
 //
 // The rows of the next chunk travel from memory to the other of two LDS
-// buffers (without passing through registers) while this one is computed:
-//     before the first barrier   P^T (one tile in each of three waves), the
-//                                state's part of Y, the pieces of C u
+// buffers, without passing through registers, while this one is computed:
+//     before the first barrier   P^T (one tile in each of three waves) and the
+//                                state's part of Y
 //     before the second          C^T P^T, stores, the state's update
 // Two buffers and at most 168 registers let three workgroups share a compute
-// unit.  `reverse` walks the tokens downwards and only shifts the exponents.
-template <bool kOut, bool kPack>
-__global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
-    // LDS (bytes): a buffer holds the rows of b, c and a; the buffers are
-    // objects of their own, so that the compiler sees that what is read from
-    // one does not wait for what is on its way into the other
+// unit (one and two: 2.1 and 3.7 us per chunk and unit, three 5.6, which is
+// the rate of the memory).  `reverse` walks the tokens downwards and only
+// shifts the exponents.
+template <int NU, int kParts, bool kOut, bool kPack>
+__global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) void decay_scan_kernel(ScanArgs A) {
+    // LDS (bytes): two buffers with the rows of b, c and a; the P^T tiles
     constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = SET, LA = 2 * SET, LPT = 512;
     constexpr int ROWS16 = 16 * D * 2;
     __shared__ __align__(16) char lds[2 * SETS * SET];
@@ -249,7 +249,10 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int lane = tid & 63, gq = lane >> 4, n16 = lane & 15;
-    const int idx = xcd_order(blockIdx.x, (int)gridDim.x, A.share);
+    int idx = xcd_order(blockIdx.x, (int)gridDim.x, A.share * kParts);
+    const int part = idx % kParts;
+    idx /= kParts;
+    const int wv = w + 8 / NU / kParts * part;   // this wave among the columns
     const ScanJob J = A.job[A.jobs == 1 ? 0 : idx % A.jobs];
     const Item it = find_item(A.map, idx / A.jobs);
     const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
@@ -267,11 +270,12 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 
     // Loads: one instruction of a wave moves 4 rows of 256 bytes (16 lanes a
     // row) to 1 KiB of LDS in lane order; a lane fetches the block that belongs
-    // there.  A chunk's rows 4w .. 4w+3 and 16 more are wave w's.  The address
+    // there.  Wave w takes rows 4w .. 4w+3 (and, with four waves, 16 more).  The address
     // is a uniform base (the chunk's lowest row) plus a 32-bit lane offset.
     const int64_t first = rev ? it.tok0 + it.len - 1 : it.tok0;
     const int64_t dir = rev ? -1 : 1;
     const int lrow = 4 * w + gq;
+    constexpr int STEP = 32 / NU / kParts;   // rows that one instruction of every wave covers
     const ScanRows rows[3] = {J.b, J.c, J.a};
     const char* pr[SETS];
     int64_t bytes[SETS];
@@ -279,13 +283,13 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 #pragma unroll
     for (int i = 0; i < SETS; ++i) {
         bytes[i] = rows[i].stride * 2;
-        pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? 15 : 0)) * bytes[i];
-        off[i] = (unsigned)(rev ? 15 - lrow : lrow) * (unsigned)bytes[i] + ((n16 ^ swz(lrow)) << 4);
+        pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? STEP - 1 : 0)) * bytes[i];
+        off[i] = (unsigned)(rev ? STEP - 1 - lrow : lrow) * (unsigned)bytes[i] + ((n16 ^ swz(lrow)) << 4);
     }
     auto fetch = [&](char* buf, int t0) __attribute__((always_inline)) {
         const int rem = it.len - t0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NU * kParts; ++j) {
             if (rem >= SC || lrow + 16 * j < rem) {
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
@@ -303,7 +307,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 
     // state
     f32x4 S[8][NU];
-    const int vrow = 32 * w + 8 * (n16 >> 2) + (n16 & 3);   // + 4u
+    const int vrow = NU == 2 ? 32 * wv + 8 * (n16 >> 2) + (n16 & 3) : 16 * wv + n16;   // + 4u
     const float* s_in = J.s_in;
     if (s_in == nullptr) {
 #pragma unroll
@@ -354,16 +358,19 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     const int r8_ = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
     const int trow = 4 * gq + (n16 >> 2);
     const int tr_ = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
-    // (C: channels 8a .. 8a+3 of row 4gq + n/4, where xors of 64w and 8u give the others)
-    const int trc_ = (trow * D + (((n16 & 3) ^ swz(trow)) << 3)) * 2;
+    // (C with two tiles a wave: channels 8a .. 8a+3 of row 4gq + n/4, where xors
+    // of 64w and 8u give the others)
+    const int trc_ = NU == 2 ? (trow * D + (((n16 & 3) ^ swz(trow)) << 3)) * 2 : tr_;
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
     const char* yout = (const char*)J.y;
     const bool pack = J.pack != 0;
     int64_t py = ((first - (rev ? 15 : 0)) * Hv + it.h) * D * 2;
-    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (32 * w + 8 * gq) * 2;
+    const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * wv + 4 * NU * gq) * 2;
 
-    // One chunk in `buf`, the next one's rows on their way into `other`.
+    // One chunk in `buf`, the next one's rows on their way into `other`.  (As
+    // restrict pointers they show the compiler that what is read from the one
+    // need not wait for what is on its way into the other.)
     auto chunk = [&](int t0, const char* __restrict__ buf, char* __restrict__ other, auto tail_c) __attribute__((always_inline)) {
         constexpr bool kTail = decltype(tail_c)::value;
         const int rem = kTail ? it.len - t0 : SC;
@@ -429,7 +436,7 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (trc ^ (64 * w + 8 * u)) + ROWS16 * j);
+            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (trc ^ (32 * NU * wv + 8 * u)) + ROWS16 * j);
         if (kOut) {
             const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
                          p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
@@ -447,12 +454,16 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             }
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti) {
-                u32x2 q[2];
+                u32x2 q[NU];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < NU; ++u)
                     q[u] = kPack && pack ? pack_quad(y[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
-                if (!kTail || 16 * ti + n16 < rem)
-                    *row_ptr<u32x4>(yb + ti * gy, oy) = u32x4{q[0][0], q[0][1], q[1][0], q[1][1]};
+                if (!kTail || 16 * ti + n16 < rem) {
+                    if constexpr (NU == 2)
+                        *row_ptr<u32x4>(yb + ti * gy, oy) = u32x4{q[0][0], q[0][1], q[1][0], q[1][1]};
+                    else
+                        *row_ptr<u32x2>(yb + ti * gy, oy) = q[0];
+                }
             }
             py += 2 * gy;
         }
@@ -488,8 +499,8 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
             for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], S[t][u]);
         }
         if (!kTail) {
-            // the next chunk's rows have arrived when at most this chunk's
-            // stores, issued after them, are outstanding
+            // the next chunk's rows have arrived when at most this chunk's two
+            // stores, issued after them, are outstanding (they complete in order)
             if (kOut)
                 wait_vm<2>();
             else
@@ -516,16 +527,33 @@ __global__ __launch_bounds__(SC_THREADS, 3) void decay_scan_kernel(ScanArgs A) {
     }
 }
 
+template <int NU, int kParts>
+static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStream_t s) {
+    const dim3 grid((unsigned)(a.map.items * a.jobs * kParts)), block(512 / NU / kParts);
+    if (states_only)
+        hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, false, false>), grid, block, 0, s, a);
+    else if (pack)
+        hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, true, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, true, false>), grid, block, 0, s, a);
+}
+
+// With enough workgroups to share compute units, four waves with two tiles
+// each spend the least on reading the rows out of LDS.  With one workgroup per
+// unit at most, eight waves shorten a chunk (us per chunk of 32 tokens: 1.5
+// instead of 1.85; 384 workgroups of 1024 tokens: 119 us instead of 109), and
+// with one for every second unit, two workgroups of half the columns each (1.3;
+// 256 items x 2048 tokens: 155 us instead of 120).
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
-    const dim3 grid((unsigned)(a.map.items * a.jobs)), block(SC_THREADS);
     bool pack = false;
     for (int i = 0; i < a.jobs; ++i) pack = pack || a.job[i].pack != 0;
-    if (states_only)
-        hipLaunchKernelGGL((decay_scan_kernel<false, false>), grid, block, 0, s, a);
-    else if (pack)
-        hipLaunchKernelGGL((decay_scan_kernel<true, true>), grid, block, 0, s, a);
+    const int64_t groups = a.map.items * a.jobs;
+    if (groups <= 128)
+        launch_scan<1, 2>(a, states_only, pack, s);
+    else if (groups <= 256)
+        launch_scan<1, 1>(a, states_only, pack, s);
     else
-        hipLaunchKernelGGL((decay_scan_kernel<true, false>), grid, block, 0, s, a);
+        launch_scan<2, 1>(a, states_only, pack, s);
     return hipGetLastError();
 }
 

@@ -108,30 +108,36 @@ int64_t total_segs(const Decay& d, int seg) {
 
 // Tokens per segment of a scan over `forms` forms (o, or dq, dk and dv), or 0
 // for whole sequences: whichever an estimate says is faster.  Measured: a
-// workgroup alone on its compute unit takes 1.85 us per chunk of 32 tokens,
-// and the card gets through one chunk of one head every 7.3 ns.  So whole
-// sequences take the longest one's latency or the total's throughput.
-// Segments shorten the first, for a pass that forms the segments' states
-// (1.2 us a chunk, 4.5 ns in all; for the backward both ways), their way
-// through memory (45 ns each) and two more launches.  In us, whole sequences
-// against segments, forward: 16 heads x 32768 tokens 1796 / 213, 32 x 8192
-// 467 / 104, 16 x 1024 63 / 34, 4 sequences x 32 heads x 4096 242 / 213,
-// 8 x 32 x 2048 137 / 214; backward: 16 x 32768 1811 / 439, 2 x 32 x 2048
-// 127 / 124, 4 x 32 x 4096 358 / 422.
+// chunk of 32 tokens takes a workgroup 1.45, 1.6 or 1.85 us (see
+// launch_decay_scan), and the card gets through one chunk of one head every
+// 7.3 ns.  So whole sequences take the longest one's latency or the total's
+// throughput.  Segments shorten the first, for a pass that forms the segments'
+// states (1.2 us a chunk, 4.5 ns in all; for the backward both ways), their
+// way through memory (15 ns each) and two more launches.  In us, whole
+// sequences against segments, forward: 16 heads x 32768 tokens 1462 / 200,
+// 32 x 8192 372 / 108, 16 x 1024 50 / 30, 96 x 4096 192 / 160, 4 sequences x
+// 32 heads x 4096 190 / 212, 8 x 32 x 2048 128 / 217; backward: 16 x 32768
+// 1480 / 432, 16 x 1024 53 / 42, 2 x 32 x 2048 110 / 121, 4 x 32 x 4096 351 /
+// 436.
+double chunk_us(int64_t groups) { return groups <= 128 ? 1.45 : groups <= 256 ? 1.6 : 1.85; }
+
 int auto_segment(const Decay& d, int forms) {
     if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
     double chunks = 0;
     for (int64_t len : d.s.len) chunks += (double)((len + 31) / 32);
     chunks *= d.s.Hv;
     const int passes = forms == 1 ? 1 : 2;
-    const double whole = std::max(1.85 * (double)((d.s.max_len + 31) / 32), 0.0073 * forms * chunks);
+    const double whole = std::max(chunk_us((int64_t)d.s.N * d.s.Hv * forms) * (double)((d.s.max_len + 31) / 32),
+                                  0.0073 * forms * chunks);
     // two segments per compute unit (forward), one (backward, three forms each), not below 128 (192) tokens
     const int64_t items = forms == 1 ? 512 : 256;
     int64_t seg = (d.s.tokens * d.s.Hv / items + 63) / 64 * 64;
     seg = std::max<int64_t>(seg, forms == 1 ? 128 : 192);
     if (d.s.max_len <= seg) return 0;
-    const double cut = std::max(3.05 * (double)(seg / 32), (0.0073 * forms + 0.0045 * passes) * chunks) + 15.0 +
-                       0.045 * passes * (double)(total_segs(d, (int)seg) * d.s.Hv);
+    const int64_t cut_items = total_segs(d, (int)seg) * d.s.Hv;
+    const double cut = std::max((chunk_us(cut_items * forms) + 1.2) * (double)(seg / 32),
+                                (0.0073 * forms + 0.0045 * passes) * chunks) +
+                       12.0 + 0.015 * passes * (double)cut_items;
     return cut < 0.95 * whole ? (int)seg : 0;
 }
 
