@@ -27,6 +27,10 @@ constexpr int64_t kState = (int64_t)D * D;
 // Largest token stride (elements): the kernels add up to 31 of them in 32 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 25;
 
+// Most rows of a row norm: the kernels number them in 32 bits, with room for
+// the last step behind them (2^31 rows are 512 GiB).
+constexpr int64_t kMaxRows = (int64_t)1 << 31;
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Runs an entry point's body; an exception (host memory) becomes a status.
@@ -273,6 +277,7 @@ kda_status check_qknorm(const kda_qknorm_problem* p, kda::QkNormArgs& a) {
     if (p->table_rows < 1 || p->table_rows > ((int64_t)1 << 40))
         return fail(KDA_ERR_SHAPE, "table_rows out of range (%lld)", (long long)p->table_rows);
     a.tokens = (int64_t)p->B * p->T;
+    if (a.tokens * (p->Hq + p->Hk) > kMaxRows) return fail(KDA_ERR_SHAPE, "too many rows (tokens x heads)");
     a.T = p->T;
     a.Hq = p->Hq;
     a.Hk = p->Hk;
@@ -322,6 +327,8 @@ kda_status check_gnorm(const kda_gnorm_problem* p, kda::GNormArgs& a) {
     if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
         return fail(KDA_ERR_SHAPE, "eps must be finite and positive (got %g)", (double)p->eps);
     a.tokens = (int64_t)p->B * p->T;
+    if (p->H > kMaxStride / D || a.tokens * p->H > kMaxRows)
+        return fail(KDA_ERR_SHAPE, "too many rows (tokens x heads)");
     a.H = p->H;
     a.silu = p->activation == KDA_GATE_SILU;
     a.eps = p->eps;

@@ -94,6 +94,7 @@ struct QkNormArgs {
     int T;                   // tokens per batch row (positions null: token index within its row)
     int Hq, Hk;
     int rot, interleaved;
+    int per;                 // heads of a token that 16 lanes take (set by the launch)
     float eps;
     const bf16_t *q, *k;
     int64_t sq, sk;          // token strides (elements)

@@ -21,9 +21,27 @@ constexpr int RN_GROUPS = RN_THREADS / 16;   // rows in flight per workgroup
 // Workgroups of a backward pass: four per compute unit, fewer when there are
 // fewer rows.  (Its partials are one row of sums per workgroup.)
 constexpr int RN_BWD_BLOCKS = 1024;
-// Forward: enough workgroups to fill the card eight times over at one row
-// per 16 lanes, then more rows each.
-constexpr int64_t RN_FWD_BLOCKS = 2048;
+
+// A pass that moves more than the 256 MB that the last cache before HBM holds
+// reads and writes without retention (non-temporal): nothing of it would be
+// found there again.  Gated norm of 96 heads, forward and backward: 8192 tokens
+// 300 -> 280 us, 4096 tokens 155 -> 145 us.  Below, it costs: the forward of
+// 2048 tokens (150 MB) takes 24.6 us with retention, 26 us without.
+constexpr int64_t RN_STREAM_BYTES = (int64_t)256 << 20;
+bool streams(int64_t rows, int tensors) { return rows * (D * 2) * tensors > RN_STREAM_BYTES; }
+
+template <bool kStream, class T>
+__device__ __forceinline__ T load(const bf16* p) {
+    if constexpr (kStream) return __builtin_nontemporal_load((const T*)p);
+    return *(const T*)p;
+}
+template <bool kStream, class T>
+__device__ __forceinline__ void store(bf16* p, T v) {
+    if constexpr (kStream)
+        __builtin_nontemporal_store(v, (T*)p);
+    else
+        *(T*)p = v;
+}
 
 struct Row8 {
     float x[8];
@@ -77,11 +95,12 @@ __device__ __forceinline__ void turn(Row8& r, f32x4 cs, f32x4 sn, bool pairs, fl
 
 }  // namespace
 
-template <bool kPairs, bool kBwd>
+// 16 lanes take `per` heads of one token (a unit), so that the position and the
+// angles are read once for all of them.
+template <bool kPairs, bool kBwd, bool kStream>
 __global__ __launch_bounds__(RN_THREADS) void qknorm_kernel(QkNormArgs a) {
     const int c = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const int H = a.Hq + a.Hk;
-    const int64_t rows = a.tokens * H;
+    const int H = a.Hq + a.Hk, half = a.rot >> 1;
     const Quads qd = quads(c, a.rot, kPairs);
     float wq[8], wk[8], gq[8], gk[8];
 #pragma unroll
@@ -93,19 +112,12 @@ __global__ __launch_bounds__(RN_THREADS) void qknorm_kernel(QkNormArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.0f;
-    const int half = a.rot >> 1;
-    for (int64_t row = (int64_t)blockIdx.x * RN_GROUPS + grp; row < rows; row += (int64_t)gridDim.x * RN_GROUPS) {
-        const int64_t t = row / H;
-        const int h = (int)(row - t * H);
-        const bool isq = h < a.Hq;
-        const bf16* src = isq ? (const bf16*)a.q + t * a.sq + h * D : (const bf16*)a.k + t * a.sk + (h - a.Hq) * D;
-        const int64_t out = isq ? (t * a.Hq + h) * D : (t * a.Hk + h - a.Hq) * D;
-        Row8 x, dy;
-        unpack(x, *(const bf16x4*)(src + qd.lo), *(const bf16x4*)(src + qd.hi));
-        if (kBwd) {
-            const bf16* d = (const bf16*)(isq ? a.dyq : a.dyk) + out;
-            unpack(dy, *(const bf16x4*)(d + qd.lo), *(const bf16x4*)(d + qd.hi));
-        }
+    const unsigned parts = (unsigned)((H + a.per - 1) / a.per);
+    const unsigned units = (unsigned)a.tokens * parts;
+    for (unsigned u = blockIdx.x * RN_GROUPS + grp; u < units; u += gridDim.x * RN_GROUPS) {
+        const unsigned tok = u / parts;
+        const int h0 = (int)(u - tok * parts) * a.per, h1 = min(h0 + a.per, H);
+        const int64_t t = tok;
         // a position outside the table turns its token's rows into NaN
         f32x4 cs = {1.f, 1.f, 1.f, 1.f}, sn = zero4();
         const int64_t pos = a.positions != nullptr ? a.positions[t] : t % a.T;
@@ -116,33 +128,41 @@ __global__ __launch_bounds__(RN_THREADS) void qknorm_kernel(QkNormArgs a) {
             cs = *(const f32x4*)(a.cos + pos * half + 4 * c);
             sn = *(const f32x4*)(a.sin + pos * half + 4 * c);
         }
-        const float r = inv_rms(x, a.eps);
-        if (!kBwd) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x.x[e] = x.x[e] * r * (isq ? wq[e] : wk[e]);
-            turn(x, cs, sn, kPairs, 1.0f);
-            bf16* y = (bf16*)(isq ? a.yq : a.yk) + out;
-            *(bf16x4*)(y + qd.lo) = pack4(x.x);
-            *(bf16x4*)(y + qd.hi) = pack4(x.x + 4);
-        } else {
-            // dn = R^T dy; dw += dn x^; dx = r (w dn - x^ mean(w dn x^))
-            turn(dy, cs, sn, kPairs, -1.0f);
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x.x[e] *= r;
-                const float g = dy.x[e] * x.x[e];
-                gq[e] += isq ? g : 0.0f;
-                gk[e] += isq ? 0.0f : g;
-                dy.x[e] *= isq ? wq[e] : wk[e];
-                s += dy.x[e] * x.x[e];
+        for (int h = h0; h < h1; ++h) {
+            const bool isq = h < a.Hq;
+            const bf16* src = isq ? (const bf16*)a.q + t * a.sq + h * D : (const bf16*)a.k + t * a.sk + (h - a.Hq) * D;
+            const int64_t out = isq ? (t * a.Hq + h) * D : (t * a.Hk + h - a.Hq) * D;
+            Row8 x, dy;
+            unpack(x, load<kStream, bf16x4>(src + qd.lo), load<kStream, bf16x4>(src + qd.hi));
+            if (kBwd) {
+                const bf16* d = (const bf16*)(isq ? a.dyq : a.dyk) + out;
+                unpack(dy, load<kStream, bf16x4>(d + qd.lo), load<kStream, bf16x4>(d + qd.hi));
             }
-            s = row16_sum(s) * (1.0f / D);
+            const float r = inv_rms(x, a.eps);
+            if (!kBwd) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x.x[e] = r * (dy.x[e] - x.x[e] * s);
-            bf16* y = (bf16*)(isq ? a.dq : a.dk) + out;
-            *(bf16x4*)(y + qd.lo) = pack4(x.x);
-            *(bf16x4*)(y + qd.hi) = pack4(x.x + 4);
+                for (int e = 0; e < 8; ++e) x.x[e] = x.x[e] * r * (isq ? wq[e] : wk[e]);
+                turn(x, cs, sn, kPairs, 1.0f);
+            } else {
+                // dn = R^T dy; dw += dn x^; dx = r (w dn - x^ mean(w dn x^))
+                turn(dy, cs, sn, kPairs, -1.0f);
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x.x[e] *= r;
+                    const float g = dy.x[e] * x.x[e];
+                    gq[e] += isq ? g : 0.0f;
+                    gk[e] += isq ? 0.0f : g;
+                    dy.x[e] *= isq ? wq[e] : wk[e];
+                    s += dy.x[e] * x.x[e];
+                }
+                s = row16_sum(s) * (1.0f / D);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x.x[e] = r * (dy.x[e] - x.x[e] * s);
+            }
+            bf16* y = kBwd ? (bf16*)(isq ? a.dq : a.dk) + out : (bf16*)(isq ? a.yq : a.yk) + out;
+            store<kStream>(y + qd.lo, pack4(x.x));
+            store<kStream>(y + qd.hi, pack4(x.x + 4));
         }
     }
     if (kBwd) {
@@ -162,25 +182,26 @@ __global__ __launch_bounds__(RN_THREADS) void qknorm_kernel(QkNormArgs a) {
     }
 }
 
-template <bool kSilu, bool kBwd>
+template <bool kSilu, bool kBwd, bool kStream>
 __global__ __launch_bounds__(RN_THREADS) void gnorm_kernel(GNormArgs a) {
     const int c = threadIdx.x & 15, grp = threadIdx.x >> 4;
-    const int64_t rows = a.tokens * a.H;
+    const unsigned rows = (unsigned)a.tokens * (unsigned)a.H;
     float w[8], gw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         w[e] = a.w[8 * c + e];
         gw[e] = 0.0f;
     }
-    for (int64_t row = (int64_t)blockIdx.x * RN_GROUPS + grp; row < rows; row += (int64_t)gridDim.x * RN_GROUPS) {
-        const int64_t t = row / a.H;
-        const int h = (int)(row - t * a.H);
-        const int64_t out = row * D + 8 * c;
+    for (unsigned row = blockIdx.x * RN_GROUPS + grp; row < rows; row += gridDim.x * RN_GROUPS) {
+        const unsigned tok = row / (unsigned)a.H;
+        const int h = (int)(row - tok * (unsigned)a.H);
+        const int64_t t = tok;
+        const int64_t out = (int64_t)row * D + 8 * c;
         Row8 x, g, dy;
-        const bf16x8 xv = *(const bf16x8*)((const bf16*)a.x + t * a.sx + h * D + 8 * c);
-        const bf16x8 gv = *(const bf16x8*)((const bf16*)a.g + t * a.sg + h * D + 8 * c);
+        const bf16x8 xv = load<kStream, bf16x8>((const bf16*)a.x + t * a.sx + h * D + 8 * c);
+        const bf16x8 gv = load<kStream, bf16x8>((const bf16*)a.g + t * a.sg + h * D + 8 * c);
         bf16x8 dv;
-        if (kBwd) dv = *(const bf16x8*)((const bf16*)a.dy + out);
+        if (kBwd) dv = load<kStream, bf16x8>((const bf16*)a.dy + out);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x.x[e] = (float)xv[e];
@@ -206,7 +227,7 @@ __global__ __launch_bounds__(RN_THREADS) void gnorm_kernel(GNormArgs a) {
             }
         }
         if (!kBwd) {
-            *(bf16x8*)((bf16*)a.y + out) = cat8(pack4(x.x), pack4(x.x + 4));
+            store<kStream>((bf16*)a.y + out, cat8(pack4(x.x), pack4(x.x + 4)));
         } else {
             float s = 0.0f;
 #pragma unroll
@@ -214,8 +235,8 @@ __global__ __launch_bounds__(RN_THREADS) void gnorm_kernel(GNormArgs a) {
             s = row16_sum(s) * (1.0f / D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x.x[e] = r * (dy.x[e] - x.x[e] * s);
-            *(bf16x8*)((bf16*)a.dx + out) = cat8(pack4(x.x), pack4(x.x + 4));
-            *(bf16x8*)((bf16*)a.dg + out) = cat8(pack4(g.x), pack4(g.x + 4));
+            store<kStream>((bf16*)a.dx + out, cat8(pack4(x.x), pack4(x.x + 4)));
+            store<kStream>((bf16*)a.dg + out, cat8(pack4(g.x), pack4(g.x + 4)));
         }
     }
     if (kBwd) {
@@ -240,6 +261,7 @@ __global__ __launch_bounds__(RN_THREADS) void colsum_kernel(const float* part, i
     const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
     const int col = blockIdx.x * 8 + c;
     float s = 0.0f;
+#pragma unroll 8
     for (int i = r; i < blocks; i += 32) s += part[(int64_t)i * cols + col];
     sums[r][c] = s;
     __syncthreads();
@@ -260,27 +282,65 @@ int rownorm_blocks(int64_t rows) {
 }
 
 namespace {
-unsigned fwd_blocks(int64_t rows) {
-    const int64_t need = (rows + RN_GROUPS - 1) / RN_GROUPS;
-    return (unsigned)(need < RN_FWD_BLOCKS ? need : RN_FWD_BLOCKS);
+
+// Heads per unit: up to 8, fewer where that would leave a compute unit less than
+// four workgroups.  (16384 tokens x 40 heads, forward and backward: 162 us at 8,
+// 165 at 4, 178 at 2, 212 at 1, 190 at 16.)
+int heads_per_unit(int64_t tokens, int H) {
+    int per = 8;
+    while (per > 1 && tokens * ((H + per - 1) / per) < (int64_t)RN_GROUPS * 1024) per >>= 1;
+    return per;
 }
+
+// A forward pass has a group of lanes for every unit or row (up to a launch's
+// 2^32 threads, then it loops as well); a backward pass loops, to sum its weight
+// gradients.
+dim3 forward_grid(int64_t groups) {
+    const int64_t need = (groups + RN_GROUPS - 1) / RN_GROUPS, most = (int64_t)1 << 23;
+    return dim3((unsigned)(need < most ? need : most));
+}
+
+template <bool kPairs, bool kBwd>
+void launch_qknorm(const QkNormArgs& a, bool stream, dim3 grid, hipStream_t s) {
+    if (stream)
+        hipLaunchKernelGGL((qknorm_kernel<kPairs, kBwd, true>), grid, dim3(RN_THREADS), 0, s, a);
+    else
+        hipLaunchKernelGGL((qknorm_kernel<kPairs, kBwd, false>), grid, dim3(RN_THREADS), 0, s, a);
+}
+template <bool kSilu, bool kBwd>
+void launch_gnorm(const GNormArgs& a, bool stream, dim3 grid, hipStream_t s) {
+    if (stream)
+        hipLaunchKernelGGL((gnorm_kernel<kSilu, kBwd, true>), grid, dim3(RN_THREADS), 0, s, a);
+    else
+        hipLaunchKernelGGL((gnorm_kernel<kSilu, kBwd, false>), grid, dim3(RN_THREADS), 0, s, a);
+}
+
 }  // namespace
 
-hipError_t launch_qknorm_fwd(const QkNormArgs& a, hipStream_t s) {
-    const dim3 grid(fwd_blocks(a.tokens * (a.Hq + a.Hk)));
+hipError_t launch_qknorm_fwd(const QkNormArgs& args, hipStream_t s) {
+    QkNormArgs a = args;
+    const int H = a.Hq + a.Hk;
+    a.per = heads_per_unit(a.tokens, H);
+    const int64_t units = a.tokens * ((H + a.per - 1) / a.per);
+    const bool stream = streams(a.tokens * H, 2);
+    const dim3 grid = forward_grid(units);
     if (a.interleaved)
-        hipLaunchKernelGGL((qknorm_kernel<true, false>), grid, dim3(RN_THREADS), 0, s, a);
+        launch_qknorm<true, false>(a, stream, grid, s);
     else
-        hipLaunchKernelGGL((qknorm_kernel<false, false>), grid, dim3(RN_THREADS), 0, s, a);
+        launch_qknorm<false, false>(a, stream, grid, s);
     return hipGetLastError();
 }
 
-hipError_t launch_qknorm_bwd(const QkNormArgs& a, hipStream_t s) {
-    const int blocks = rownorm_blocks(a.tokens * (a.Hq + a.Hk));
+hipError_t launch_qknorm_bwd(const QkNormArgs& args, hipStream_t s) {
+    QkNormArgs a = args;
+    const int H = a.Hq + a.Hk;
+    a.per = heads_per_unit(a.tokens, H);
+    const bool stream = streams(a.tokens * H, 3);
+    const int blocks = rownorm_blocks(a.tokens * H);
     if (a.interleaved)
-        hipLaunchKernelGGL((qknorm_kernel<true, true>), dim3(blocks), dim3(RN_THREADS), 0, s, a);
+        launch_qknorm<true, true>(a, stream, dim3(blocks), s);
     else
-        hipLaunchKernelGGL((qknorm_kernel<false, true>), dim3(blocks), dim3(RN_THREADS), 0, s, a);
+        launch_qknorm<false, true>(a, stream, dim3(blocks), s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(colsum_kernel, dim3(2 * D / 8), dim3(RN_THREADS), 0, s, (const float*)a.part, blocks, 2 * D,
@@ -289,20 +349,24 @@ hipError_t launch_qknorm_bwd(const QkNormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_gnorm_fwd(const GNormArgs& a, hipStream_t s) {
-    const dim3 grid(fwd_blocks(a.tokens * a.H));
+    const int64_t rows = a.tokens * a.H;
+    const bool stream = streams(rows, 3);
+    const dim3 grid = forward_grid(rows);
     if (a.silu)
-        hipLaunchKernelGGL((gnorm_kernel<true, false>), grid, dim3(RN_THREADS), 0, s, a);
+        launch_gnorm<true, false>(a, stream, grid, s);
     else
-        hipLaunchKernelGGL((gnorm_kernel<false, false>), grid, dim3(RN_THREADS), 0, s, a);
+        launch_gnorm<false, false>(a, stream, grid, s);
     return hipGetLastError();
 }
 
 hipError_t launch_gnorm_bwd(const GNormArgs& a, hipStream_t s) {
-    const int blocks = rownorm_blocks(a.tokens * a.H);
+    const int64_t rows = a.tokens * a.H;
+    const bool stream = streams(rows, 5);
+    const int blocks = rownorm_blocks(rows);
     if (a.silu)
-        hipLaunchKernelGGL((gnorm_kernel<true, true>), dim3(blocks), dim3(RN_THREADS), 0, s, a);
+        launch_gnorm<true, true>(a, stream, dim3(blocks), s);
     else
-        hipLaunchKernelGGL((gnorm_kernel<false, true>), dim3(blocks), dim3(RN_THREADS), 0, s, a);
+        launch_gnorm<false, true>(a, stream, dim3(blocks), s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(colsum_kernel, dim3(D / 8), dim3(RN_THREADS), 0, s, (const float*)a.part, blocks, D, a.dw, a.dw);
