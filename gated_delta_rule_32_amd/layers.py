@@ -21,6 +21,8 @@ _ACTIVATIONS = {"sigmoid": GATE_SIGMOID, "silu": GATE_SILU}
 _BF, _F32 = torch.bfloat16, torch.float32
 _vp = ctypes.c_void_p
 _size = ctypes.c_size_t
+_byref = ctypes.byref
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class KdaDecayProblem(ctypes.Structure):
@@ -106,80 +108,66 @@ def _ws(t: Optional[torch.Tensor]):
     return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
 
 
-def _stream(t: torch.Tensor, stream: Optional[int]) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
-
-
-class _On:
-    """The device of a call's tensors as the current one while it launches."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(f, stream, t, *args) -> None:
+    """f(*args, stream), by default on the current stream of t's device, which is
+    the current one for the call."""
+    i = t.get_device()
+    _require(i >= 0, "tensors must be on a GPU")
+    if stream is None:
+        stream = _raw_stream(i)  # (current_stream builds an object: 2 us)
+    if i == torch.cuda.current_device():
+        _check(f(*args, stream))
+    else:
+        with torch.cuda.device(i):
+            _check(f(*args, stream))
 
 
 def kda_decay_fwd(p: KdaDecayProblem, q, k, v, log_decay, initial_state, o, final_state,
                   workspace: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """C kda_decay_fwd on torch tensors (no shape checks beyond the library's)."""
-    with _On(q.device):
-        _check(_lib.kda_decay_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                                  _ptr(o), _ptr(final_state), *_ws(workspace), _stream(q, stream)))
+    _call(_lib.kda_decay_fwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
+          _ptr(o), _ptr(final_state), *_ws(workspace))
 
 
 def kda_decay_bwd(p: KdaDecayProblem, q, k, v, log_decay, initial_state, d_o, dfinal_state, dq, dk, dv,
                   dinitial_state, workspace: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """C kda_decay_bwd on torch tensors."""
-    with _On(q.device):
-        _check(_lib.kda_decay_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                                  _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinitial_state),
-                                  *_ws(workspace), _stream(q, stream)))
+    _call(_lib.kda_decay_bwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
+          _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinitial_state), *_ws(workspace))
 
 
 def kda_decay_infer(p: KdaDecayProblem, q, k, v, log_decay, state_pool, state_indices, state_indices_cpu, o,
                     workspace: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> None:
     """C kda_decay_infer on torch tensors."""
-    with _On(q.device):
-        _check(_lib.kda_decay_infer(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_pool),
-                                    state_pool.shape[0], _ptr(state_indices), _ptr(state_indices_cpu), _ptr(o),
-                                    *_ws(workspace), _stream(q, stream)))
+    _call(_lib.kda_decay_infer, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_pool),
+          state_pool.shape[0], _ptr(state_indices), _ptr(state_indices_cpu), _ptr(o), *_ws(workspace))
 
 
 def kda_qknorm_fwd(p: KdaQkNormProblem, q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out,
                    stream: Optional[int] = None) -> None:
     """C kda_qknorm_fwd on torch tensors."""
-    with _On(q.device):
-        _check(_lib.kda_qknorm_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                                   _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), _stream(q, stream)))
+    _call(_lib.kda_qknorm_fwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+          _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out))
 
 
 def kda_qknorm_bwd(p: KdaQkNormProblem, q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk,
                    dq_weight, dk_weight, workspace: torch.Tensor, stream: Optional[int] = None) -> None:
     """C kda_qknorm_bwd on torch tensors."""
-    with _On(q.device):
-        _check(_lib.kda_qknorm_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                                   _ptr(sin), _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk),
-                                   _ptr(dq_weight), _ptr(dk_weight), *_ws(workspace), _stream(q, stream)))
+    _call(_lib.kda_qknorm_bwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+          _ptr(sin), _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight),
+          _ptr(dk_weight), *_ws(workspace))
 
 
 def kda_gnorm_fwd(p: KdaGNormProblem, x, gate, weight, y, stream: Optional[int] = None) -> None:
     """C kda_gnorm_fwd on torch tensors."""
-    with _On(x.device):
-        _check(_lib.kda_gnorm_fwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(y), _stream(x, stream)))
+    _call(_lib.kda_gnorm_fwd, stream, x, _byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(y))
 
 
 def kda_gnorm_bwd(p: KdaGNormProblem, x, gate, weight, dy, dx, dgate, dweight, workspace: torch.Tensor,
                   stream: Optional[int] = None) -> None:
     """C kda_gnorm_bwd on torch tensors."""
-    with _On(x.device):
-        _check(_lib.kda_gnorm_bwd(ctypes.byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dgate),
-                                  _ptr(dweight), *_ws(workspace), _stream(x, stream)))
+    _call(_lib.kda_gnorm_bwd, stream, x, _byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dx),
+          _ptr(dgate), _ptr(dweight), *_ws(workspace))
 
 
 # ---------------------------------------------------------------------------
@@ -198,9 +186,10 @@ def _dense(name, t, dtype, shape, device):
 def _rows(name, t, shape, device) -> int:
     """The token stride of a BF16 [B, T, H, 128] operand: dense, or a slice of
     wider token rows."""
-    _require(isinstance(t, torch.Tensor) and t.dtype == _BF, f"{name} must be a bfloat16 tensor")
-    _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _require(t.device == device, f"{name} must be on {device}, got {t.device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF and t.shape == shape and t.device == device):
+        _require(isinstance(t, torch.Tensor) and t.dtype is _BF, f"{name} must be a bfloat16 tensor")
+        _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        _require(False, f"{name} must be on {device}, got {t.device}")
     B, T, H, D = shape
     if t.is_contiguous():
         return H * D
@@ -213,9 +202,15 @@ def _rows(name, t, shape, device) -> int:
 
 
 def _cuda(t) -> torch.device:
-    _require(isinstance(t, torch.Tensor) and t.dim() == 4, "token tensors must be [B, T, H, 128]")
-    _require(t.device.type == "cuda", f"tensors must be on a GPU, got {t.device}")
+    if not (isinstance(t, torch.Tensor) and t.dim() == 4 and t.is_cuda):
+        _require(isinstance(t, torch.Tensor) and t.dim() == 4, "token tensors must be [B, T, H, 128]")
+        _require(False, f"tensors must be on a GPU, got {t.device}")
     return t.device
+
+
+def _new(t: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, cu_seqlens_cpu, segment) -> KdaDecayProblem:
@@ -223,11 +218,9 @@ def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, cu_seqlens_cpu, segmen
     _cuda(v)
     B, T, Hqk, _ = q.shape
     Hv = v.shape[2]
-    p = KdaDecayProblem()
-    p.B, p.T, p.Hqk, p.Hv, p.N = B, T, Hqk, Hv, B
-    p.q_stride = _rows("q", q, (B, T, Hqk, HEAD_DIM), dev)
-    p.k_stride = _rows("k", k, (B, T, Hqk, HEAD_DIM), dev)
-    p.v_stride = _rows("v", v, (B, T, Hv, HEAD_DIM), dev)
+    qk = (B, T, Hqk, HEAD_DIM)
+    p = KdaDecayProblem(B, T, Hqk, Hv, B, None, None, 0.0, 0, _rows("q", q, qk, dev), _rows("k", k, qk, dev),
+                        _rows("v", v, (B, T, Hv, HEAD_DIM), dev))
     _dense("log_decay", log_decay, _F32, (Hv,), dev)
     if cu_seqlens is not None:
         _require(cu_seqlens_cpu is not None, "packed calls need cu_seqlens_cpu")
@@ -241,13 +234,16 @@ def _decay_problem(q, k, v, log_decay, scale, cu_seqlens, cu_seqlens_cpu, segmen
         p.N = cu_seqlens.numel() - 1
         p.cu_seqlens = cu_seqlens.data_ptr()
         p.cu_seqlens_host = cu_seqlens_cpu.data_ptr()
+        # the struct holds raw pointers: keep the tensors alive with it
+        p._keep = (cu_seqlens, cu_seqlens_cpu)
     else:
         _require(cu_seqlens_cpu is None, "cu_seqlens_cpu must be omitted for fixed layout")
-    p.scale = 0.0 if scale is None else float(scale)
-    _require(scale is None or p.scale > 0.0, f"scale must be positive, got {scale}")
-    p.segment = int(segment)
-    # the struct holds raw pointers: keep the tensors alive with it
-    p._keep = (cu_seqlens, cu_seqlens_cpu)
+    if scale is not None:
+        p.scale = float(scale)
+        if not p.scale > 0.0:
+            _require(False, f"scale must be positive, got {scale}")
+    if segment != 0:
+        p.segment = int(segment)
     return p
 
 
@@ -291,7 +287,7 @@ def decay_attention_training_forward(q, k, v, log_decay, initial_state=None, cu_
     states = (p.N, p.Hv, HEAD_DIM, HEAD_DIM)
     if initial_state is not None:
         _dense("initial_state", initial_state, _F32, states, dev)
-    o = torch.empty((p.B, p.T, p.Hv, HEAD_DIM), dtype=_BF, device=dev) if out is None else out
+    o = _new(v) if out is None else out
     if out is not None:
         _dense("out", o, _BF, (p.B, p.T, p.Hv, HEAD_DIM), dev)
     fs = torch.empty(states, dtype=_F32, device=dev) if final_state_out is None else final_state_out
@@ -320,8 +316,7 @@ def decay_attention_training_backward(context: DecayAttentionTrainingContext, do
     if dfinal_state is not None:
         _dense("dfinal_state", dfinal_state, _F32, states, dev)
     if out is None:
-        out = (torch.empty(q.shape, dtype=_BF, device=dev), torch.empty(k.shape, dtype=_BF, device=dev),
-               torch.empty(v.shape, dtype=_BF, device=dev), torch.empty(states, dtype=_F32, device=dev))
+        out = (_new(q), _new(k), _new(v), torch.empty(states, dtype=_F32, device=dev))
     else:
         _require(len(out) == 4, "out must hold four tensors")
         for name, t, dtype, shape in zip(("dq", "dk", "dv", "dinitial_state"), out, (_BF, _BF, _BF, _F32),
@@ -355,7 +350,7 @@ def decay_attention(q, k, v, log_decay, initial_state=None, scale=None, cu_seqle
         _dense("ssm_state_indices_cpu", ssm_state_indices_cpu, torch.int32, (p.N,), torch.device("cpu"))
     else:
         _require(ssm_state_indices_cpu is None, "ssm_state_indices_cpu needs ssm_state_indices")
-    o = torch.empty((p.B, p.T, p.Hv, HEAD_DIM), dtype=_BF, device=dev) if output is None else output
+    o = _new(v) if output is None else output
     if output is not None:
         _dense("output", o, _BF, (p.B, p.T, p.Hv, HEAD_DIM), dev)
     ws = None if p.T == 1 else _workspace(kda_decay_infer_workspace_bytes(p), workspace, dev)
@@ -380,22 +375,16 @@ def _qknorm_problem(q, k, q_weight, k_weight, cos, sin, positions, eps, interlea
     _cuda(k)
     B, T, Hq, _ = q.shape
     Hk = k.shape[2]
-    p = KdaQkNormProblem()
-    p.B, p.T, p.Hq, p.Hk = B, T, Hq, Hk
-    p.q_stride = _rows("q", q, (B, T, Hq, HEAD_DIM), dev)
-    p.k_stride = _rows("k", k, (B, T, Hk, HEAD_DIM), dev)
+    q_stride, k_stride = _rows("q", q, (B, T, Hq, HEAD_DIM), dev), _rows("k", k, (B, T, Hk, HEAD_DIM), dev)
     _dense("q_weight", q_weight, _F32, (HEAD_DIM,), dev)
     _dense("k_weight", k_weight, _F32, (HEAD_DIM,), dev)
     _require(isinstance(cos, torch.Tensor) and cos.dim() == 2, "cos must be [rows, rot_dim/2]")
-    _dense("cos", cos, _F32, cos.shape, dev)
-    _dense("sin", sin, _F32, cos.shape, dev)
+    rows, half = angles = cos.shape
+    _dense("cos", cos, _F32, angles, dev)
+    _dense("sin", sin, _F32, angles, dev)
     if positions is not None:
         _dense("positions", positions, torch.int64, (B, T), dev)
-    p.rot_dim = 2 * cos.shape[1]
-    p.table_rows = cos.shape[0]
-    p.eps = float(eps)
-    p.interleaved = int(bool(interleaved))
-    return p
+    return KdaQkNormProblem(B, T, Hq, Hk, 2 * half, bool(interleaved), float(eps), rows, q_stride, k_stride)
 
 
 def qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None, *, eps: float = 1e-6,
@@ -408,7 +397,7 @@ def qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None, *, 
     channels: pairs (p, p + rot_dim/2), or (2p, 2p+1) when interleaved."""
     p = _qknorm_problem(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     if out is None:
-        out = (torch.empty(q.shape, dtype=_BF, device=q.device), torch.empty(k.shape, dtype=_BF, device=q.device))
+        out = (_new(q), _new(k))
     else:
         _require(len(out) == 2, "out must hold two tensors")
         _dense("q_out", out[0], _BF, q.shape, q.device)
@@ -427,8 +416,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
     _dense("dq_out", dq_out, _BF, q.shape, dev)
     _dense("dk_out", dk_out, _BF, k.shape, dev)
     if out is None:
-        out = (torch.empty(q.shape, dtype=_BF, device=dev), torch.empty(k.shape, dtype=_BF, device=dev),
-               torch.empty(HEAD_DIM, dtype=_F32, device=dev), torch.empty(HEAD_DIM, dtype=_F32, device=dev))
+        out = (_new(q), _new(k), _new(q_weight), _new(k_weight))
     else:
         _require(len(out) == 4, "out must hold four tensors")
         for name, t, dtype, shape in zip(("dq", "dk", "dq_weight", "dk_weight"), out, (_BF, _BF, _F32, _F32),
@@ -445,15 +433,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
 def _gnorm_problem(x, gate, weight, eps, activation) -> KdaGNormProblem:
     dev = _cuda(x)
     B, T, H, _ = x.shape
-    _require(activation in _ACTIVATIONS, f"activation must be one of {tuple(_ACTIVATIONS)}, got {activation!r}")
-    p = KdaGNormProblem()
-    p.B, p.T, p.H = B, T, H
-    p.activation = _ACTIVATIONS[activation]
-    p.eps = float(eps)
-    p.x_stride = _rows("x", x, (B, T, H, HEAD_DIM), dev)
-    p.gate_stride = _rows("gate", gate, (B, T, H, HEAD_DIM), dev)
+    if activation not in _ACTIVATIONS:
+        _require(False, f"activation must be one of {tuple(_ACTIVATIONS)}, got {activation!r}")
+    shape = (B, T, H, HEAD_DIM)
     _dense("weight", weight, _F32, (HEAD_DIM,), dev)
-    return p
+    return KdaGNormProblem(B, T, H, _ACTIVATIONS[activation], float(eps), _rows("x", x, shape, dev),
+                           _rows("gate", gate, shape, dev))
 
 
 def gated_norm_forward(x, gate, weight, *, eps: float = 1e-6, activation: str = "sigmoid",
@@ -463,7 +448,7 @@ def gated_norm_forward(x, gate, weight, *, eps: float = 1e-6, activation: str = 
     weight: FP32 [128]."""
     p = _gnorm_problem(x, gate, weight, eps, activation)
     if out is None:
-        out = torch.empty(x.shape, dtype=_BF, device=x.device)
+        out = _new(x)
     else:
         _dense("out", out, _BF, x.shape, x.device)
     kda_gnorm_fwd(p, x, gate, weight, out)
@@ -477,8 +462,7 @@ def gated_norm_backward(dy, x, gate, weight, *, eps: float = 1e-6, activation: s
     dev = x.device
     _dense("dy", dy, _BF, x.shape, dev)
     if out is None:
-        out = (torch.empty(x.shape, dtype=_BF, device=dev), torch.empty(x.shape, dtype=_BF, device=dev),
-               torch.empty(HEAD_DIM, dtype=_F32, device=dev))
+        out = (_new(x), _new(x), _new(weight))
     else:
         _require(len(out) == 3, "out must hold three tensors")
         for name, t, dtype, shape in zip(("dx", "dgate", "dweight"), out, (_BF, _BF, _F32),
