@@ -212,12 +212,13 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // One workgroup per item and form (kParts = 2: two, each with half of the
 // state's output channels), a wave for every NU tiles of 16 channels.  Wave
 // wv holds the state as MFMA accumulators: tile (t, u) is S^T[k][v] with
-//     k = 16t + 4gq + e,   v = 32wv + 8(n/4) + 4u + n%4   (NU = 1: 16wv + n)
-// (lane 16gq + n, element e), so that tiles t = 2p and 2p+1 together are,
-// rounded to BF16, the operand of S a over channels 32p .. 32p+31, and the two
-// tiles u of Y^T give a lane 8 neighbouring channels of one token to store
-// (8-byte stores cost the packed forward 4%, the training step 7%).  Per chunk
-// of 32 tokens:
+//     k = 32(t/2) + 8gq + 4(t%2) + e,   v = 32wv + 8(n/4) + 4u + n%4
+// (NU = 1: v = 16wv + n; lane 16gq + n, element e), so that tiles t = 2p and
+// 2p+1 together are, rounded to BF16, the operand of S a over channels 32p ..
+// 32p+31 in the order in which one 16-byte read takes them from a's rows, and
+// the two tiles u of Y^T give a lane 8 neighbouring channels of one token to
+// store (8-byte stores cost the packed forward 4%, the training step 7%).  Per
+// chunk of 32 tokens:
 //     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
 //     S^T = e^{32 l} S^T + B^T (C u),   u_j = e^{l(32-shift-j)}
@@ -235,13 +236,17 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 //                                state's part of Y
 //     before the second          C^T P^T, stores, the state's update
 // Two buffers and at most 168 registers let three workgroups share a compute
-// unit (one and two: 2.1 and 3.7 us per chunk and unit, three 5.6, which is
-// the rate of the memory).  `reverse` walks the tokens downwards and only
+// unit.  What they wait for is memory: the forward of 8 x 1024 tokens of 96
+// heads takes 196 us, 191 us without its products, 141 us without its stores as
+// well.  (96 heads' rows 24 KB apart fall on few of the memory's channels: 95
+// heads take 176 us.)  A single workgroup waits for itself: 1.35 us per chunk,
+// 1.1 us of it without loads.  `reverse` walks the tokens downwards and only
 // shifts the exponents.
 template <int NU, int kParts, bool kOut, bool kPack>
-__global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) void decay_scan_kernel(ScanArgs A) {
-    // LDS (bytes): two buffers with the rows of b, c and a; the P^T tiles
-    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = SET, LA = 2 * SET, LPT = 512;
+__global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
+    // LDS (bytes): the rows of b, c and a, two buffers each that differ in address
+    // bit SET; the P^T tiles
+    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = 2 * SET, LA = 4 * SET, LPT = 512;
     constexpr int ROWS16 = 16 * D * 2;
     __shared__ __align__(16) char lds[2 * SETS * SET];
     __shared__ __align__(16) char lds_p[kOut ? 3 * LPT : 16];
@@ -286,28 +291,29 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
         pr[i] = (const char*)(rows[i].p + (it.h / rows[i].group) * D) + (first - (rev ? STEP - 1 : 0)) * bytes[i];
         off[i] = (unsigned)(rev ? STEP - 1 - lrow : lrow) * (unsigned)bytes[i] + ((n16 ^ swz(lrow)) << 4);
     }
-    auto fetch = [&](char* buf, int t0) __attribute__((always_inline)) {
+    auto fetch = [&](char* buf, int at, int t0) __attribute__((always_inline)) {
         const int rem = it.len - t0;
 #pragma unroll
         for (int j = 0; j < NU * kParts; ++j) {
             if (rem >= SC || lrow + 16 * j < rem) {
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
-                    to_lds(pr[i] + j * 16 * dir * bytes[i], off[i], buf + i * SET + (16 * j + 4 * w) * D * 2);
+                    to_lds(pr[i] + j * 16 * dir * bytes[i], off[i], buf + at + 2 * i * SET + (16 * j + 4 * w) * D * 2);
             } else {   // rows behind the last token are not read and count as zero
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
-                    *(u32x4*)(buf + i * SET + (16 * j + 4 * w) * D * 2 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+                    *(u32x4*)(buf + at + 2 * i * SET + (16 * j + 4 * w) * D * 2 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
             }
         }
 #pragma unroll
         for (int i = 0; i < SETS; ++i) pr[i] += SC * dir * bytes[i];
     };
-    fetch(lds, 0);
+    fetch(lds, 0, 0);
 
     // state
     f32x4 S[8][NU];
     const int vrow = NU == 2 ? 32 * wv + 8 * (n16 >> 2) + (n16 & 3) : 16 * wv + n16;   // + 4u
+    auto krow = [&](int t) __attribute__((always_inline)) { return 32 * (t >> 1) + 8 * gq + 4 * (t & 1); };
     const float* s_in = J.s_in;
     if (s_in == nullptr) {
 #pragma unroll
@@ -319,7 +325,7 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                S[t][u] = *(const f32x4*)(s_in + soff + (vrow + 4 * u) * D + 16 * t + 4 * gq);
+                S[t][u] = *(const f32x4*)(s_in + soff + (vrow + 4 * u) * D + krow(t));
     } else {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -327,7 +333,7 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
             for (int u = 0; u < NU; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    S[t][u][e] = s_in[soff + (16 * t + 4 * gq + e) * D + vrow + 4 * u];
+                    S[t][u][e] = s_in[soff + (krow(t) + e) * D + vrow + 4 * u];
     }
 
     // Powers of e^l, constant over the item's full chunks; each is a product
@@ -347,20 +353,21 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
         u0[0][e] = u0[1][e] * far;
     }
     // the state is `held` times S; a chunk's decay and its inverse
-    const double lam = uniform(decay_power(l, SC)), inv = uniform(1.0 / lam);
+    const double lam = decay_power(l, SC), inv = 1.0 / lam;
     double held = 1.0, over = 1.0;   // over = 1 / held
+    // chunks until that is below 2^-24 (at least one)
+    const int every = __builtin_amdgcn_readfirstlane((int)fminf(24.0f / (SC * fabsf(l2)), 0x1p30f)) + 1;
+    int left = every;
 
-    // LDS offsets (bytes), for p, t = 0 and in the low bits, where xors of 64p
-    // and 32t give the others: 4 channels (32p + 4gq) of row n, 8 channels
-    // (32p + 8gq) of row n, and for the transposing reads channels 16t + 4a of
-    // row 4gq + n/4 (a = n%4)
-    const int rd_ = (n16 * D + (((gq >> 1) ^ swz(n16)) << 3) + 4 * (gq & 1)) * 2;
+    // LDS offsets (bytes) for p = 0, where an xor of 64p gives the others: 8
+    // channels (32p + 8gq) of row n, and for the transposing reads of row
+    // 4gq + n/4 the piece a = n%4, channels 32p + 8a .. +3 (+ 4 for odd tiles) of b
+    // and 32wv + 8a .. +3 (NU = 1: 16wv + 4a) of c
     const int r8_ = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
-    const int trow = 4 * gq + (n16 >> 2);
-    const int tr_ = (trow * D + ((((n16 & 3) >> 1) ^ swz(trow)) << 3) + 4 * (n16 & 1)) * 2;
-    // (C with two tiles a wave: channels 8a .. 8a+3 of row 4gq + n/4, where xors
-    // of 64w and 8u give the others)
-    const int trc_ = NU == 2 ? (trow * D + (((n16 & 3) ^ swz(trow)) << 3)) * 2 : tr_;
+    const int trow = 4 * gq + (n16 >> 2), piece = n16 & 3;
+    const int tr_ = (trow * D + ((piece ^ swz(trow)) << 3)) * 2;
+    const int trc_ = NU == 2 ? (trow * D + (((4 * wv + piece) ^ swz(trow)) << 3)) * 2
+                             : (trow * D + (((2 * wv + (piece >> 1)) ^ swz(trow)) << 3) + 4 * (piece & 1)) * 2;
     // output rows of 16 tokens: a uniform base and a 32-bit lane offset
     const int64_t sy = (int64_t)Hv * D * 2, gy = 16 * dir * sy;
     const char* yout = (const char*)J.y;
@@ -368,34 +375,72 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
     int64_t py = ((first - (rev ? 15 : 0)) * Hv + it.h) * D * 2;
     const unsigned oy = (unsigned)(rev ? 15 - n16 : n16) * (unsigned)sy + (16 * NU * wv + 4 * NU * gq) * 2;
 
-    // One chunk in `buf`, the next one's rows on their way into `other`.  (As
-    // restrict pointers they show the compiler that what is read from the one
-    // need not wait for what is on its way into the other.)
-    auto chunk = [&](int t0, const char* __restrict__ buf, char* __restrict__ other, auto tail_c) __attribute__((always_inline)) {
-        constexpr bool kTail = decltype(tail_c)::value;
+    // One chunk, from `buf` + at, the next one's rows on their way into `other` +
+    // (SET - at).  (Both are `lds`; as restrict pointers they show the compiler
+    // that what is read through the one need not wait for what is on its way
+    // into the other.)
+    auto chunk = [&](int t0, int at, const char* __restrict__ buf, char* __restrict__ other,
+                     auto tail_c) __attribute__((always_inline)) {
+        constexpr bool kTail = decltype(tail_c)::value, kDeep = NU == 1 && kParts == 2;
         const int rem = kTail ? it.len - t0 : SC;
-        if (!kTail && t0 + SC < it.len) fetch(other, t0 + SC);
+        if (!kTail && t0 + SC < it.len) fetch(other, SET - at, t0 + SC);
         // (formed anew per chunk, rather than kept in a register each)
-        const int rd = fresh(rd_), rd1 = fresh(rd_ + ROWS16), r8 = fresh(r8_), tr = fresh(tr_),
-                  trc = fresh(trc_);
+        const int r8 = fresh(r8_) + at, tr = fresh(tr_) + at, trc = fresh(trc_) + at;
         const float y_held = (float)held * y0;
-        const double d = kTail ? uniform(decay_power(l, rem)) : lam;
-        held = uniform(held * d);
-        over = uniform(kTail ? over / d : over * inv);
-        const bool rescale = held < 0x1p-24;
+        const double d = kTail ? decay_power(l, rem) : lam;
+        held *= d;
+        over = kTail ? over / d : over * inv;
+        const bool rescale = --left == 0;
         const float down = (float)held;
-        if (rescale) held = over = 1.0;
+        if (rescale) {
+            held = over = 1.0;
+            left = every;
+        }
         const float g = (float)over;
 
         f32x4 y[2][NU];
+        bf16x8 av[4][2], bt[8], pb[4], pa[4];
+        bf16x4 cf[2][NU];
+        const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
+        auto read_p = [&](int p) __attribute__((always_inline)) {
+            pb[p] = *(const bf16x8*)(buf + ((r8 + jrow) ^ (64 * p)) + LB);
+            pa[p] = *(const bf16x8*)(buf + ((r8 + irow) ^ (64 * p)) + LA);
+        };
+        auto read_a = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+            for (int ti = 0; ti < 2; ++ti)
+                av[p][ti] = *(const bf16x8*)(buf + (r8 ^ (64 * p)) + LA + ti * ROWS16);
+        };
+        auto read_b = [&](int t) __attribute__((always_inline)) {
+            const char* row = buf + (tr ^ (64 * (t >> 1))) + LB + 8 * (t & 1);
+            bt[t] = cat8(tr_read(row), tr_read(row + ROWS16));
+        };
+        auto read_c = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + trc + LC + 8 * u + ROWS16 * j);
+        };
+        if (kDeep) {   // one workgroup per unit has the registers to read everything at once (1.47 -> 1.35 us)
+            if (kOut) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) read_p(p);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) read_a(p);
+            }
+            read_c();
+#pragma unroll
+            for (int t = 0; t < 8; ++t) read_b(t);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (kOut) {
             if (w < 3) {   // this wave's P^T tile
-                const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
                 f32x4 acc = zero4();
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    acc = mma32(*(const bf16x8*)(buf + LB + (r8 ^ (64 * p)) + jrow),
-                                *(const bf16x8*)(buf + LA + (r8 ^ (64 * p)) + irow), acc);
+                for (int p = 0; p < 4; ++p) {
+                    if (!kDeep) read_p(p);
+                    acc = mma32(pb[p], pa[p], acc);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
                     const bool seen = (w == 2) | (n16 >= 4 * gq + e);
@@ -409,16 +454,12 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
                 for (int u = 0; u < NU; ++u) y[ti][u] = zero4();
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                bf16x8 av[2];
-#pragma unroll
-                for (int ti = 0; ti < 2; ++ti)
-                    av[ti] = cat8(*(const bf16x4*)(buf + LA + ((ti ? rd1 : rd) ^ (64 * p))),
-                                  *(const bf16x4*)(buf + LA + ((ti ? rd1 : rd) ^ (64 * p + 32))));
+                if (!kDeep) read_a(p);
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
 #pragma unroll
-                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[ti], y[ti][u]);
+                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[p][ti], y[ti][u]);
                 }
             }
         }
@@ -432,11 +473,7 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
                     for (int e = 0; e < 4; ++e) S[t][u][e] *= down;
         }
         // C columns of this wave
-        bf16x4 cf[2][NU];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + LC + (trc ^ (32 * NU * wv + 8 * u)) + ROWS16 * j);
+        if (!kDeep) read_c();
         if (kOut) {
             const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
                          p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
@@ -490,13 +527,13 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const bf16x8 bt = cat8(tr_read(buf + LB + (tr ^ (32 * t))), tr_read(buf + LB + (tr ^ (32 * t)) + ROWS16));
+            if (!kDeep) read_b(t);
 #pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c1[u], S[t][u]);
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c1[u], S[t][u]);
 #pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c2[u], S[t][u]);
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c2[u], S[t][u]);
 #pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt, c3[u], S[t][u]);
+            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c3[u], S[t][u]);
         }
         if (!kTail) {
             // the next chunk's rows have arrived when at most this chunk's two
@@ -512,10 +549,10 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
     barrier_lds();
     int t0 = 0, at = 0;
     for (; t0 + SC <= it.len; t0 += SC) {
-        chunk(t0, lds + at, lds + (SETS * SET - at), std::false_type{});
-        at = SETS * SET - at;
+        chunk(t0, at, lds, lds, std::false_type{});
+        at = SET - at;
     }
-    if (t0 < it.len) chunk(t0, lds + at, nullptr, std::true_type{});
+    if (t0 < it.len) chunk(t0, at, lds, lds, std::true_type{});
 
     float* s_out = J.s_out;
     if (s_out != nullptr) {
@@ -523,7 +560,7 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 || kParts == 2 ? 3 : 4) 
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + 16 * t + 4 * gq) = S[t][u] * (float)held;
+                *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + krow(t)) = S[t][u] * (float)held;
     }
 }
 
@@ -542,7 +579,7 @@ static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStrea
 // each spend the least on reading the rows out of LDS.  With one workgroup per
 // unit at most, eight waves shorten a chunk (us per chunk of 32 tokens: 1.5
 // instead of 1.85; 384 workgroups of 1024 tokens: 119 us instead of 109), and
-// with one for every second unit, two workgroups of half the columns each (1.3;
+// with one for every second unit, two workgroups of half the columns each (1.35;
 // 256 items x 2048 tokens: 155 us instead of 120).
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
     bool pack = false;
