@@ -9,6 +9,10 @@
 
 namespace kda {
 
+// A kernel that moves more than the last cache before HBM holds (256 MB) reads
+// and writes without retention: nothing of it would be found there again.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+
 // Where a call's work items lie.  An item is (sequence n, value head h), or
 // (sequence n, segment j, value head h) when the sequences are cut into
 // segments of seg_len tokens (0: they are not).  With `task` null every

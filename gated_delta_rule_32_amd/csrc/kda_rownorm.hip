@@ -22,13 +22,11 @@ constexpr int RN_GROUPS = RN_THREADS / 16;   // rows in flight per workgroup
 // fewer rows.  (Its partials are one row of sums per workgroup.)
 constexpr int RN_BWD_BLOCKS = 1024;
 
-// A pass that moves more than the 256 MB that the last cache before HBM holds
-// reads and writes without retention (non-temporal): nothing of it would be
-// found there again.  Gated norm of 96 heads, forward and backward: 8192 tokens
-// 300 -> 280 us, 4096 tokens 155 -> 145 us.  Below, it costs: the forward of
-// 2048 tokens (150 MB) takes 24.6 us with retention, 26 us without.
-constexpr int64_t RN_STREAM_BYTES = (int64_t)256 << 20;
-bool streams(int64_t rows, int tensors) { return rows * (D * 2) * tensors > RN_STREAM_BYTES; }
+// Whether a pass over `rows` rows of that many tensors is too large to be found
+// in a cache again.  Gated norm of 96 heads, forward and backward: 8192 tokens 300 -> 280 us
+// non-temporal, 4096 tokens 155 -> 145 us; the forward of 2048 tokens (150 MB)
+// takes 24.6 us with retention, 26 us without.
+bool streams(int64_t rows, int tensors) { return rows * (D * 2) * tensors > kStreamBytes; }
 
 template <bool kStream, class T>
 __device__ __forceinline__ T load(const bf16* p) {
