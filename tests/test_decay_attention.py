@@ -146,7 +146,6 @@ def test_slices_of_wider_rows(segment):
 def test_results_do_not_depend_on_the_packing():
     """A sequence's results are the same bits alone and between others, and NaN
     rows of the neighbours do not reach it."""
-    import gated_delta_rule_32_amd as kda
     inp = Inp([40, 100, 9], True, 1, 2, seed=7)
     got = train(inp)
     alone = Inp([100], False, 1, 2, seed=7)
@@ -165,7 +164,6 @@ def test_results_do_not_depend_on_the_packing():
     got = train(inp)
     for i in (0, 2, 3, 4):
         assert torch.equal(got[i][:, 40:140], ref[i])
-    assert kda.kda_last_error is not None
 
 
 def test_segments_agree_with_whole_sequences():
