@@ -198,6 +198,8 @@ def _rows(name, t, shape, device) -> int:
     if T == 1:  # the token stride is free; the rows are the batch's
         st = sb if B > 1 else H * D
     _require(B == 1 or sb == T * st, f"{name}'s batch rows must be T token strides apart")
+    # (0, an expanded tensor's, would mean dense rows to the library)
+    _require(st >= H * D, f"{name}'s token rows must not overlap")
     return st
 
 

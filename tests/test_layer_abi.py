@@ -193,6 +193,16 @@ def test_binding_refuses_tensors():
         layers._rows("x", wide.float(), (2, 4, 6, 128), cpu)
 
 
+def test_binding_refuses_expanded_rows():
+    """A token stride of 0 must not reach the library, where it means dense rows."""
+    one = torch.zeros((1, 1, 2, 128), dtype=torch.bfloat16)
+    long = torch.zeros(4000, dtype=torch.bfloat16)
+    for x in (one.expand(1, 5, 2, 128), one.expand(5, 1, 2, 128), one.expand(3, 5, 2, 128),
+              long.as_strided((1, 5, 2, 128), (640, 128, 128, 1))):
+        with pytest.raises(ValueError, match="token"):
+            kda._layers._rows("x", x, tuple(x.shape), torch.device("cpu"))
+
+
 def test_rotary_table():
     cos, sin = kda.rotary_table(100000, 64, theta=500000.0, device="cpu")
     assert cos.shape == sin.shape == (100000, 32) and cos.dtype == torch.float32
