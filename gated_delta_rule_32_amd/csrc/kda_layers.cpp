@@ -187,9 +187,16 @@ kda_status make_map(const Decay& d, int seg, hipStream_t stream, SeqPlan& plan, 
     return KDA_OK;
 }
 
+// A launch holds less than 2^32 threads; workgroups of 256 here.
 kda_status check_grid(int64_t blocks) {
-    if (blocks > (int64_t)INT32_MAX) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks");
+    if (blocks >= (int64_t)1 << 24) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks or tokens");
     return KDA_OK;
+}
+// The scan's grid for `jobs` forms, and with segments the chain's.
+kda_status check_scan_grid(const Decay& d, int seg, const kda::ItemMap& m, int jobs) {
+    kda_status s = check_grid(m.items * jobs);
+    if (s == KDA_OK && seg != 0) s = check_grid((int64_t)d.s.N * d.s.Hv * 16);
+    return s;
 }
 
 // Work items that go to one XCD side by side (xcd_order): the value heads of a
@@ -397,7 +404,7 @@ kda_status kda_decay_fwd(const kda_decay_problem* pp, const void* q, const void*
         SeqPlan plan;
         kda::ItemMap m;
         if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
-        if ((s = check_grid(std::max(m.items, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
+        if ((s = check_scan_grid(d, seg, m, 1)) != KDA_OK) return s;
         return run_forward(d, seg, m, q, k, v, log_decay, initial_state, final_state, nullptr, d.s.N, o,
                            (char*)workspace, stream);
     });
@@ -436,8 +443,8 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
         SeqPlan plan;
         kda::ItemMap m;
         if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
-        if ((s = check_grid(std::max(3 * m.items, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
-        if ((s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
+        if ((s = check_scan_grid(d, seg, m, 3)) != KDA_OK) return s;
+        if (d.s.G > 1 && (s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
 
         char* ws = (char*)workspace;
         const int G = d.s.G;
@@ -579,7 +586,7 @@ kda_status kda_decay_infer(const kda_decay_problem* pp, const void* q, const voi
         SeqPlan plan;
         kda::ItemMap m;
         if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
-        if ((s = check_grid(std::max(m.items * 4, (int64_t)d.s.N * d.s.Hv * 16))) != KDA_OK) return s;
+        if ((s = serial ? check_grid(m.items * 4) : check_scan_grid(d, seg, m, 1)) != KDA_OK) return s;
         if (!serial)
             return run_forward(d, seg, m, q, k, v, log_decay, state_pool, state_pool, state_indices, pool_slots, o,
                                (char*)workspace, stream);

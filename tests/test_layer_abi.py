@@ -94,6 +94,16 @@ def test_decay_refuses_arguments():
     assert infer(decay(B=2, N=2), idx=[3, 3]) == SHAPE
 
 
+def test_decay_refuses_more_than_a_launch():
+    """2^24 workgroups of 256 threads are more than one launch holds."""
+    far = lambda names: {n: (i + 1) << 46 for i, n in enumerate(names.split())}  # noqa: E731
+    p = decay(B=1 << 18, N=1 << 18, T=1, Hqk=64, Hv=64)
+    assert fwd(p, **far("q k v l s0 o fs")) == SHAPE
+    assert bwd(p, **far("q k v l s0 do ds dq dk dv di")) == SHAPE
+    p = decay(B=1 << 16, N=1 << 16, T=1, Hqk=64, Hv=64)
+    assert infer(p, slots=1 << 16, **far("q k v l pool o")) == SHAPE
+
+
 def test_decay_workspace_sizes():
     state = 128 * 128 * 4
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
