@@ -264,8 +264,9 @@ def _workspace(need, given, device):
 # ---------------------------------------------------------------------------
 @dataclass
 class DecayAttentionTrainingContext:
-    """What the backward needs of the forward: its problem and its inputs with
-    their versions (no device memory of its own)."""
+    """What the backward needs of the forward: its problem and its inputs
+    (cu_seqlens and its CPU mirror among them) with their versions (no device
+    memory of its own)."""
     problem: KdaDecayProblem
     inputs: tuple
     versions: tuple
@@ -297,7 +298,7 @@ def decay_attention_training_forward(q, k, v, log_decay, initial_state=None, cu_
         _dense("final_state_out", fs, _F32, states, dev)
     ws = _workspace(kda_decay_fwd_workspace_bytes(p), workspace, dev)
     kda_decay_fwd(p, q, k, v, log_decay, initial_state, o, fs, ws)
-    inputs = (q, k, v, log_decay, initial_state)
+    inputs = (q, k, v, log_decay, initial_state, cu_seqlens, cu_seqlens_cpu)
     versions = tuple(None if t is None else t._version for t in inputs)
     return o, fs, DecayAttentionTrainingContext(p, inputs, versions)
 
@@ -311,7 +312,7 @@ def decay_attention_training_backward(context: DecayAttentionTrainingContext, do
     p, inputs = context.problem, context.inputs
     now = tuple(None if t is None else t._version for t in inputs)
     _require(now == context.versions, "an input changed after the forward (tensor version)")
-    q, k, v, log_decay, s0 = inputs
+    q, k, v, log_decay, s0, _, _ = inputs
     dev = q.device
     states = (p.N, p.Hv, HEAD_DIM, HEAD_DIM)
     _dense("do", do, _BF, v.shape, dev)

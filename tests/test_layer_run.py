@@ -456,6 +456,18 @@ def test_outputs_beyond_32_bits():
         assert torch.equal(a, b) and torch.equal(pool[2099:], alone) and not pool[:2099].any()
 
 
+def test_context_checks_the_sequences_too():
+    """The backward reads the lengths again: changed in between, it refuses."""
+    import gated_delta_rule_32_amd as kda
+    x = torch.zeros((1, 40, 1, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 15, 40])
+    _, _, ctx = kda.decay_attention_training_forward(x, x, x, torch.zeros(1, device="cuda"), cu_seqlens=cu.cuda(),
+                                                     cu_seqlens_cpu=cu)
+    cu[1] = 20
+    with pytest.raises(ValueError, match="changed after the forward"):
+        kda.decay_attention_training_backward(ctx, x)
+
+
 # ---------------------------------------------------------------------------
 # NaN stays where it is
 # ---------------------------------------------------------------------------
