@@ -376,10 +376,12 @@ kda_status kda_infer(const kda_infer_problem* p,
  *   - Schedules.  Only packed calls (cu_seqlens) of kda_decay_* use the cached
  *     schedule; every other call may be captured at once.  A workspace is used
  *     by one call at a time: graphs or streams that may overlap need their own.
- * Inputs are read once; values at tokens behind a sequence's end, and in other
- * sequences, are never read for it.  Finite inputs are expected: a NaN or an
- * infinity in a token's row may reach every output of that sequence and head
- * from its 16-token tile on, also at earlier tokens of the tile.
+ * Values at tokens behind a sequence's end, and in other sequences, are never
+ * read for it.  Finite inputs are expected: in a scan a
+ * NaN or an infinity in a token's row may reach every output of that sequence
+ * and head from its chunk of 32 tokens on (walking backward for dk and dv),
+ * also at tokens of the chunk that precede it; in a row norm it stays in its row
+ * and the weight gradients.
  * ------------------------------------------------------------------------- */
 
 /* Linear attention with a constant decay per value head.  For every sequence
