@@ -239,9 +239,11 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // unit.  What they wait for is memory: the forward of 8 x 1024 tokens of 96
 // heads takes 196 us, 191 us without its products, 141 us without its stores as
 // well.  (96 heads' rows 24 KB apart fall on few of the memory's channels: 95
-// heads take 176 us.)  A single workgroup waits for itself: 1.35 us per chunk,
-// 1.1 us of it without loads.  `reverse` walks the tokens downwards and only
-// shifts the exponents.
+// heads take 176 us.)  A single workgroup waits for itself, so with one per
+// unit (kDeep) a chunk's LDS reads are issued together, ahead of the next
+// chunk's loads, and half of the state's update moves before the first barrier
+// (48 heads x 2048 tokens: 76 us instead of 89).  `reverse` walks the tokens
+// downwards and only shifts the exponents.
 template <int NU, int kParts, bool kOut, bool kPack>
 __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
     // LDS (bytes): the rows of b, c and a, two buffers each that differ in address
@@ -383,7 +385,8 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
                      auto tail_c) __attribute__((always_inline)) {
         constexpr bool kTail = decltype(tail_c)::value, kDeep = NU == 1 && kParts == 2;
         const int rem = kTail ? it.len - t0 : SC;
-        if (!kTail && t0 + SC < it.len) fetch(other, SET - at, t0 + SC);
+        const bool more = !kTail && t0 + SC < it.len;
+        if (!kDeep && more) fetch(other, SET - at, t0 + SC);
         // (formed anew per chunk, rather than kept in a register each)
         const int r8 = fresh(r8_) + at, tr = fresh(tr_) + at, trc = fresh(trc_) + at;
         const float y_held = (float)held * y0;
@@ -399,12 +402,11 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
         const float g = (float)over;
 
         f32x4 y[2][NU];
-        bf16x8 av[4][2], bt[8], pb[4], pa[4];
+        bf16x8 av[4][2], bt[8], pb[4];
         bf16x4 cf[2][NU];
-        const int jrow = w == 1 ? ROWS16 : 0, irow = w == 0 ? 0 : ROWS16;
+        const int r8p = r8 + (w == 1 ? ROWS16 : 0);
         auto read_p = [&](int p) __attribute__((always_inline)) {
-            pb[p] = *(const bf16x8*)(buf + ((r8 + jrow) ^ (64 * p)) + LB);
-            pa[p] = *(const bf16x8*)(buf + ((r8 + irow) ^ (64 * p)) + LA);
+            pb[p] = *(const bf16x8*)(buf + (r8p ^ (64 * p)) + LB);
         };
         auto read_a = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
@@ -421,25 +423,30 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 #pragma unroll
                 for (int u = 0; u < NU; ++u) cf[j][u] = tr_read(buf + trc + LC + 8 * u + ROWS16 * j);
         };
-        if (kDeep) {   // one workgroup per unit has the registers to read everything at once (1.47 -> 1.35 us)
+        if (kDeep) {   // all of the chunk's reads at once, before the next chunk's loads are issued
             if (kOut) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) read_p(p);
-#pragma unroll
                 for (int p = 0; p < 4; ++p) read_a(p);
+                if (w < 3) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) read_p(p);
+                }
             }
             read_c();
 #pragma unroll
             for (int t = 0; t < 8; ++t) read_b(t);
             __builtin_amdgcn_sched_barrier(0);
+            if (more) fetch(other, SET - at, t0 + SC);
         }
         if (kOut) {
-            if (w < 3) {   // this wave's P^T tile
-                f32x4 acc = zero4();
+            f32x4 acc = zero4();   // this wave's P^T tile
+            if (kDeep && w < 3) {
+                if (w == 0) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (!kDeep) read_p(p);
-                    acc = mma32(pb[p], pa[p], acc);
+                    for (int p = 0; p < 4; ++p) acc = mma32(pb[p], av[p][0], acc);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) acc = mma32(pb[p], av[p][1], acc);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
@@ -455,6 +462,11 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 if (!kDeep) read_a(p);
+                if (!kDeep && w < 3) {
+                    read_p(p);
+                    const bf16x8 a = w == 0 ? av[p][0] : av[p][1];
+                    acc = mma32(pb[p], a, acc);
+                }
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
@@ -462,18 +474,70 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
                     for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[p][ti], y[ti][u]);
                 }
             }
+            if (!kDeep && w < 3) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
+                    const bool seen = (w == 2) | (n16 >= 4 * gq + e);
+                    acc[e] = seen ? acc[e] * pf[e] : 0.0f;
+                }
+                *(bf16x4*)(lds_p + w * LPT + lane * 8) = to_bf4(acc);
+            }
+        }
+        // the pieces of C u
+        bf16x8 c1[NU], c2[NU], c3[NU];
+        auto form_pieces = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                bf16x4 x1[2], x2[2], x3[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f32x4 c = from_bf4(cf[j][u]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[e] *= g * (kTail ? s_add * __builtin_amdgcn_exp2f(
+                                                         l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
+                                           : u0[j][e]);
+                    x1[j] = take_high(c);
+                    x2[j] = take_high(c);
+                    x3[j] = to_bf4(c);
+                }
+                c1[u] = cat8(x1[0], x1[1]);
+                c2[u] = cat8(x2[0], x2[1]);
+                c3[u] = cat8(x3[0], x3[1]);
+            }
+        };
+        auto update = [&](int from, int to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int t = from; t < to; ++t) {
+                if (!kDeep) read_b(t);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c1[u], S[t][u]);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c2[u], S[t][u]);
+#pragma unroll
+                for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c3[u], S[t][u]);
+            }
+        };
+        auto rescale_state = [&]() __attribute__((always_inline)) {
+            if (rescale) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int u = 0; u < NU; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[t][u][e] *= down;
+            }
+        };
+        if (kDeep) {   // half of the update beside P^T, the other half beside what follows it
+            rescale_state();
+            form_pieces();
+            update(0, 4);
         }
         if (kOut) barrier_lds();
-        if (rescale) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int u = 0; u < NU; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[t][u][e] *= down;
+        if (!kDeep) {
+            rescale_state();
+            read_c();
         }
-        // C columns of this wave
-        if (!kDeep) read_c();
         if (kOut) {
             const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
                          p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
@@ -504,37 +568,8 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
             }
             py += 2 * gy;
         }
-        // the pieces of C u
-        bf16x8 c1[NU], c2[NU], c3[NU];
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            bf16x4 x1[2], x2[2], x3[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f32x4 c = from_bf4(cf[j][u]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    c[e] *= g * (kTail ? s_add * __builtin_amdgcn_exp2f(
-                                                     l2 * (float)max(rem - shift - 16 * j - 4 * gq - e, 0))
-                                       : u0[j][e]);
-                x1[j] = take_high(c);
-                x2[j] = take_high(c);
-                x3[j] = to_bf4(c);
-            }
-            c1[u] = cat8(x1[0], x1[1]);
-            c2[u] = cat8(x2[0], x2[1]);
-            c3[u] = cat8(x3[0], x3[1]);
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (!kDeep) read_b(t);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c1[u], S[t][u]);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c2[u], S[t][u]);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) S[t][u] = mma32(bt[t], c3[u], S[t][u]);
-        }
+        if (!kDeep) form_pieces();
+        update(kDeep ? 4 : 0, 8);
         if (!kTail) {
             // the next chunk's rows have arrived when at most this chunk's two
             // stores, issued after them, are outstanding (they complete in order)
@@ -579,7 +614,7 @@ static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStrea
 // each spend the least on reading the rows out of LDS.  With one workgroup per
 // unit at most, eight waves shorten a chunk (us per chunk of 32 tokens: 1.5
 // instead of 1.85; 384 workgroups of 1024 tokens: 119 us instead of 109), and
-// with one for every second unit, two workgroups of half the columns each (1.35;
+// with one for every second unit, two workgroups of half the columns each (1.1;
 // 256 items x 2048 tokens: 155 us instead of 120).
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
     bool pack = false;

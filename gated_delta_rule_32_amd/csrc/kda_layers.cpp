@@ -112,18 +112,18 @@ int64_t total_segs(const Decay& d, int seg) {
 
 // Tokens per segment of a scan over `forms` forms (o, or dq, dk and dv), or 0
 // for whole sequences: whichever an estimate says is faster.  Measured: a
-// chunk of 32 tokens takes a workgroup 1.45, 1.6 or 1.85 us (see
-// launch_decay_scan), and the card gets through one chunk of one head every
-// 7.3 ns.  So whole sequences take the longest one's latency or the total's
-// throughput.  Segments shorten the first, for a pass that forms the segments'
-// states (1.2 us a chunk, 4.5 ns in all; for the backward both ways), their
-// way through memory (15 ns each) and two more launches.  In us, whole
-// sequences against segments, forward: 16 heads x 32768 tokens 1462 / 200,
-// 32 x 8192 372 / 108, 16 x 1024 50 / 30, 96 x 4096 192 / 160, 4 sequences x
-// 32 heads x 4096 190 / 212, 8 x 32 x 2048 128 / 217; backward: 16 x 32768
-// 1480 / 432, 16 x 1024 53 / 42, 2 x 32 x 2048 110 / 121, 4 x 32 x 4096 351 /
-// 436.
-double chunk_us(int64_t groups) { return groups <= 128 ? 1.45 : groups <= 256 ? 1.6 : 1.85; }
+// chunk of 32 tokens takes a workgroup 1.1 (few of them) to 1.5 us, 1.6 or
+// 1.85 us (see launch_decay_scan), and the card gets through one chunk of one
+// head every 7.3 ns.  So whole sequences take the longest one's latency or the
+// total's throughput.  Segments shorten the first, for a pass that forms the
+// segments' states (1.2 us a chunk, 4.5 ns in all; for the backward both
+// ways), their way through memory (15 ns each) and two more launches.  In us,
+// whole sequences against segments, forward: 16 heads x 32768 tokens 1183 /
+// 212, 32 x 8192 276 / 106, 16 x 1024 40 / 29, 96 x 4096 182 / 163, 4 sequences
+// x 32 heads x 4096 183 / 208, 8 x 32 x 2048 126 / 210; backward: 16 x 32768
+// 1181 / 440, 16 x 4096 144 / 81, 2 x 32 x 2048 100 / 114, 4 x 32 x 4096 340 /
+// 423.
+double chunk_us(int64_t groups) { return groups <= 128 ? 1.05 + 0.0035 * (double)groups : groups <= 256 ? 1.6 : 1.85; }
 
 int auto_segment(const Decay& d, int forms) {
     if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
