@@ -632,9 +632,12 @@ hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s)
 // Chains the segments of each (sequence, value head): with R_j the own sum of
 // segment j (its state from zero), the state before it in walking order is
 // X_{j+1} = R_j + e^{l len_j} X_j.  Element by element: one thread per four
-// elements, the next segment's sums fetched a step ahead.
+// elements, the sums of the next four segments on their way.  (16 heads x 32
+// segments, 67 MB: 15.3 us one segment ahead, 13.6 us four ahead.)
 __global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
     const ItemMap& m = A.map;
+    const ChainJob& J = A.job[blockIdx.y];
+    constexpr int AHEAD = 4;
     const int64_t task = blockIdx.x >> 4;   // 16 blocks of 1024 elements per state
     const int n = (int)(task / m.Hv), h = (int)(task - (int64_t)n * m.Hv);
     const int e = (int)(blockIdx.x & 15) * 1024 + threadIdx.x * 4;
@@ -647,24 +650,31 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
     const float l = A.log_decay[h];
     Power full(l, m.seg_len);
     const float f_last = (float)decay_power(l, len - (segs - 1) * m.seg_len);
-    f32x4 x = A.s_in != nullptr ? *(const f32x4*)(A.s_in + at) : zero4();
+    f32x4 x = J.s_in != nullptr ? *(const f32x4*)(J.s_in + at) : zero4();
     const int64_t step = (int64_t)m.Hv * STATE;
-    float* p = A.seg + (base * m.Hv + h) * STATE + e;
-    auto place = [&](int i) __attribute__((always_inline)) { return A.reverse ? segs - 1 - i : i; };
-    f32x4 next = *(const f32x4*)(p + place(0) * step);
-    for (int i = 0; i < segs; ++i) {
-        const int j = place(i);
-        const f32x4 r = next;
-        next = *(const f32x4*)(p + place(min(i + 1, segs - 1)) * step);
-        *(f32x4*)(p + j * step) = x;
-        x = r + x * (j == segs - 1 ? f_last : full.next());
+    float* p = J.seg + (base * m.Hv + h) * STATE + e;
+    auto place = [&](int i) __attribute__((always_inline)) { return J.reverse ? segs - 1 - i : i; };
+    auto sum = [&](int i) __attribute__((always_inline)) { return *(const f32x4*)(p + place(min(i, segs - 1)) * step); };
+    f32x4 next[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) next[u] = sum(u);
+    for (int i = 0; i < segs; i += AHEAD) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (i + u >= segs) break;
+            const int j = place(i + u);
+            const f32x4 r = next[u];
+            next[u] = sum(i + u + AHEAD);   // (behind the last: not used)
+            *(f32x4*)(p + j * step) = x;
+            x = r + x * (j == segs - 1 ? f_last : full.next());
+        }
     }
-    if (A.s_out != nullptr) *(f32x4*)(A.s_out + at) = x;
+    if (J.s_out != nullptr) *(f32x4*)(J.s_out + at) = x;
 }
 
 hipError_t launch_decay_chain(const ChainArgs& a, hipStream_t s) {
     const int64_t blocks = (int64_t)a.map.N * a.map.Hv * 16;
-    hipLaunchKernelGGL(decay_chain_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(decay_chain_kernel, dim3((unsigned)blocks, a.jobs), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

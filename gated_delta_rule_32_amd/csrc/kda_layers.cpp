@@ -237,10 +237,9 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
         if (e != hipSuccess) return hip_fail(e, "segment state launch");
         kda::ChainArgs c{};
         c.map = m;
+        c.jobs = 1;
+        c.job[0] = {states, s_in, s_out, 0};
         c.log_decay = log_decay;
-        c.seg = states;
-        c.s_in = s_in;
-        c.s_out = s_out;
         c.slot = slot;
         c.slots = slots;
         e = kda::launch_decay_chain(c, stream);
@@ -501,16 +500,11 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
             if (e != hipSuccess) return hip_fail(e, "segment state launch");
             kda::ChainArgs c{};
             c.map = m;
+            c.jobs = 2;
+            c.job[0] = {fwd, initial_state, nullptr, 0};
+            c.job[1] = {bwd, dfinal_state, dinitial_state, 1};
             c.log_decay = log_decay;
             c.slots = d.s.N;
-            c.seg = fwd;
-            c.s_in = initial_state;
-            e = kda::launch_decay_chain(c, stream);
-            if (e != hipSuccess) return hip_fail(e, "segment chain launch");
-            c.seg = bwd;
-            c.s_in = dfinal_state;
-            c.s_out = dinitial_state;
-            c.reverse = 1;
             e = kda::launch_decay_chain(c, stream);
             if (e != hipSuccess) return hip_fail(e, "segment chain launch");
             jq.s_in = fwd;

@@ -60,16 +60,20 @@ struct ScanArgs {
 };
 
 // The segments' states chained: start states in place of the segments' own
-// sums.  `reverse`: from the last segment to the first.
-struct ChainArgs {
-    ItemMap map;
-    const float* log_decay;
+// sums, for `jobs` sets of them.  `reverse`: from the last segment to the first.
+struct ChainJob {
     float* seg;              // [segments][Hv][128][128]
     const float* s_in;       // [.][Hv][128][128], by slot; null: zero
     float* s_out;            // [.][Hv][128][128], by slot; null: none
+    int reverse;
+};
+struct ChainArgs {
+    ItemMap map;
+    ChainJob job[2];
+    int jobs;
+    const float* log_decay;
     const int32_t* slot;
     int64_t slots;
-    int reverse;
 };
 
 struct TokenArgs {
