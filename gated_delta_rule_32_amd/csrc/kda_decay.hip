@@ -439,14 +439,21 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
             if (more) fetch(other, SET - at, t0 + SC);
         }
         if (kOut) {
-            f32x4 acc = zero4();   // this wave's P^T tile
-            if (kDeep && w < 3) {
-                if (w == 0) {
+            if (w < 3) {   // this wave's P^T tile
+                f32x4 acc = zero4();
+                if (kDeep && w == 0) {
 #pragma unroll
                     for (int p = 0; p < 4; ++p) acc = mma32(pb[p], av[p][0], acc);
-                } else {
+                } else if (kDeep) {
 #pragma unroll
                     for (int p = 0; p < 4; ++p) acc = mma32(pb[p], av[p][1], acc);
+                } else {
+                    const int r8a = r8 + (w == 0 ? 0 : ROWS16);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        read_p(p);
+                        acc = mma32(pb[p], *(const bf16x8*)(buf + (r8a ^ (64 * p)) + LA), acc);
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
@@ -462,25 +469,12 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 if (!kDeep) read_a(p);
-                if (!kDeep && w < 3) {
-                    read_p(p);
-                    const bf16x8 a = w == 0 ? av[p][0] : av[p][1];
-                    acc = mma32(pb[p], a, acc);
-                }
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
 #pragma unroll
                     for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[p][ti], y[ti][u]);
                 }
-            }
-            if (!kDeep && w < 3) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {  // a later token's row never counts, whatever it holds
-                    const bool seen = (w == 2) | (n16 >= 4 * gq + e);
-                    acc[e] = seen ? acc[e] * pf[e] : 0.0f;
-                }
-                *(bf16x4*)(lds_p + w * LPT + lane * 8) = to_bf4(acc);
             }
         }
         // the pieces of C u
@@ -612,10 +606,11 @@ static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStrea
 
 // With enough workgroups to share compute units, four waves with two tiles
 // each spend the least on reading the rows out of LDS.  With one workgroup per
-// unit at most, eight waves shorten a chunk (us per chunk of 32 tokens: 1.5
-// instead of 1.85; 384 workgroups of 1024 tokens: 119 us instead of 109), and
-// with one for every second unit, two workgroups of half the columns each (1.1;
-// 256 items x 2048 tokens: 155 us instead of 120).
+// unit at most, eight waves shorten a chunk, and with one for every second
+// unit, two workgroups of half the columns each.  Forward in us (four waves;
+// eight waves; halves): 288 workgroups of 1024 tokens 94, 106, 103; 192 of 2048
+// 125, 108, 139; 150 of 2048 117, 103, 117; 128 of 2048 -, 98, 86; 48 of 2048
+// -, 97, 77.
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
     bool pack = false;
     for (int i = 0; i < a.jobs; ++i) pack = pack || a.job[i].pack != 0;
