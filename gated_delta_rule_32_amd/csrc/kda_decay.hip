@@ -136,10 +136,11 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* row_ptr(const vo
 }
 
 // Moves 16 bytes per lane from base + off (off per lane) to LDS at dst (uniform)
-// + 16 lane.
+// + 16 lane; kStream: non-temporal.
+template <bool kStream>
 __device__ __forceinline__ void to_lds(const char* base, unsigned off, char* dst) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)row_ptr<const char>(base, off),
-                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                     (__attribute__((address_space(3))) void*)dst, 16, 0, kStream ? 2 : 0);
 }
 // Waits until at most N of this wave's vector memory operations are outstanding.
 template <int N>
@@ -238,13 +239,13 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // Two buffers and at most 168 registers let three workgroups share a compute
 // unit.  What they wait for is memory: the forward of 8 x 1024 tokens of 96
 // heads takes 196 us, 191 us without its products, 141 us without its stores as
-// well.  (96 heads' rows 24 KB apart fall on few of the memory's channels: 95
-// heads take 176 us.)  A single workgroup waits for itself, so with one per
+// well.  (Rows of 96 heads, 24 KB apart, put a head's b, c and a on the same few
+// memory channels: with room for 97 heads a row it takes 13 us less.)  A single workgroup waits for itself, so with one per
 // unit (kDeep) a chunk's LDS reads are issued together, ahead of the next
 // chunk's loads, and half of the state's update moves before the first barrier
 // (48 heads x 2048 tokens: 76 us instead of 89).  `reverse` walks the tokens
 // downwards and only shifts the exponents.
-template <int NU, int kParts, bool kOut, bool kPack>
+template <int NU, int kParts, bool kOut, bool kPack, bool kStream = false>
 __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
     // LDS (bytes): the rows of b, c and a, two buffers each that differ in address
     // bit SET; the P^T tiles
@@ -300,7 +301,7 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
             if (rem >= SC || lrow + 16 * j < rem) {
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
-                    to_lds(pr[i] + j * 16 * dir * bytes[i], off[i], buf + at + 2 * i * SET + (16 * j + 4 * w) * D * 2);
+                    to_lds<kStream>(pr[i] + j * 16 * dir * bytes[i], off[i], buf + at + 2 * i * SET + (16 * j + 4 * w) * D * 2);
             } else {   // rows behind the last token are not read and count as zero
 #pragma unroll
                 for (int i = 0; i < SETS; ++i)
@@ -600,6 +601,8 @@ static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStrea
         hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, false, false>), grid, block, 0, s, a);
     else if (pack)
         hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, true, true>), grid, block, 0, s, a);
+    else if (a.stream)
+        hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, true, false, NU == 2>), grid, block, 0, s, a);
     else
         hipLaunchKernelGGL((decay_scan_kernel<NU, kParts, true, false>), grid, block, 0, s, a);
 }

@@ -53,6 +53,7 @@ struct ScanArgs {
     int jobs;                // forms in this launch, the forms of an item side by side
     int share;               // work items that read the same rows, adjacent in the item order
     int by_seg;              // states are indexed by segment, else by slot
+    int stream;              // rows are read once and not found in a cache again
     const float* log_decay;  // [Hv]
     float scale;
     const int32_t* slot;     // state slot of sequence n; null: n

@@ -326,6 +326,24 @@ def test_many_sequences_decode_like_few():
     assert torch.equal(pool, parts)
 
 
+def test_large_forward_like_a_small_one():
+    """A forward that exceeds the caches (non-temporal) gives the bits of one over
+    the first half of every sequence."""
+    import gated_delta_rule_32_amd as kda
+    g = torch.Generator(device="cuda").manual_seed(28)
+    q, k, v = (torch.randn((12, 1000, 24, 128), generator=g, device="cuda").bfloat16() for _ in range(3))
+    assert 4 * 12 * 1000 * 24 * 256 > 2 ** 28 > 4 * 12 * 500 * 24 * 256
+    l = -0.2 * torch.rand(24, generator=g, device="cuda")
+    half = [x[:, :500].contiguous() for x in (q, k, v)]
+    a = kda.decay_attention_training_forward(q, k, v, l, segment=65536)[0]
+    b, state, _ = kda.decay_attention_training_forward(*half, l, segment=65536)
+    assert torch.equal(a[:, :500], b)
+    # and the second half from the state in between (in other chunks: 500 = 15 x 32 + 20)
+    rest = [x[:, 500:].contiguous() for x in (q, k, v)]
+    c = kda.decay_attention_training_forward(*rest, l, state, segment=65536)[0]
+    assert rel(c, lu.f64(a[:, 500:])) <= 2 * lu.U
+
+
 def weight_bar(rows):
     """Of the sum of absolute values: a lane adds every 16384th row (and up to 8
     in a run), 16 lanes, 1024 workgroups in runs of 32 are added up, each sum off
