@@ -218,8 +218,9 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
     // Rows that no other head reads, more than the caches hold: non-temporal loads.
     // Forward of 8 sequences x 96 heads x 1024 tokens 208 -> 198 us, x 512 122 ->
     // 109, x 64 (50 MB) 33 -> 37; 32 sequences x 16 q/k and 64 value heads, whose
-    // q and k are read four times, 695 -> 800.  (Not in the states' pass: its rows
-    // are read again, and one prompt of 32768 tokens x 16 heads takes 224 instead of 189.)
+    // q and k are read four times, 695 -> 800.  (Not in the states' pass, whose rows
+    // are read again: one sequence of 16384 tokens x 64 heads takes 386 us so, 396
+    // with them in both passes or neither.)
     a.stream = G == 1 && 4 * d.s.tokens * d.s.Hv * D * 2 > kda::kStreamBytes;
     a.log_decay = log_decay;
     a.scale = d.scale;
