@@ -240,11 +240,11 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // unit.  What they wait for is memory: the forward of 8 x 1024 tokens of 96
 // heads takes 196 us, 191 us without its products, 141 us without its stores as
 // well.  (Rows of 96 heads, 24 KB apart, put a head's b, c and a on the same few
-// memory channels: with room for 97 heads a row it takes 13 us less.)  A single workgroup waits for itself, so with one per
-// unit (kDeep) a chunk's LDS reads are issued together, ahead of the next
-// chunk's loads, and half of the state's update moves before the first barrier
-// (48 heads x 2048 tokens: 76 us instead of 89).  `reverse` walks the tokens
-// downwards and only shifts the exponents.
+// memory channels: with room for 97 heads a row it takes 13 us less.)  A single
+// workgroup waits for itself, so with one per unit (kDeep) a chunk's LDS reads
+// are issued together, ahead of the next chunk's loads, and half of the state's
+// update moves before the first barrier (48 heads x 2048 tokens: 76 us instead
+// of 89).  `reverse` walks the tokens downwards and only shifts the exponents.
 template <int NU, int kParts, bool kOut, bool kPack, bool kStream = false>
 __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
     // LDS (bytes): the rows of b, c and a, two buffers each that differ in address

@@ -200,10 +200,15 @@ kda_status check_scan_grid(const Decay& d, int seg, const kda::ItemMap& m, int j
 }
 
 // Work items that go to one XCD side by side (xcd_order): the value heads of a
-// q/k head, whose rows they share, and at least 8 heads of neighbouring rows
-// (packed 8 x 1024 x 96 heads: training step 660 us with 1, 645 us with 2 to
-// 32; mixed prefill 705 us with 1, 680 us with 8, 697 us with 32).
-int xcd_share(int G) { return (8 + G - 1) / G * G; }
+// q/k head, whose rows they share, and about 8 heads of neighbouring rows.  Of
+// single heads an odd number, so that an XCD's blocks start at different memory
+// channels; but not in the backward, whose three forms share rows and lose that
+// in the blocks that a window of 8 XCDs leaves over.  In us, side by side 1, 3,
+// 8, 11, 16, 31: forward of 8 x 1024 x 96 heads 196, 188, 197, 189, 195, 187, of
+// 32 x 1024 x 32 278, 267, 286, 269, 279, 267; backward of 8 x 2048 x 32 with 8
+// 282, with 11 296.  In fours, 4, 8, 12, 16, 32: mixed prefill 673, 671, 669, 669,
+// 685; 4 x 4096 x 8 q/k and 32 value heads, training step 580, 569, 590, 558, 596.
+int xcd_share(int G, bool backward) { return G == 1 && !backward ? 11 : (8 + G - 1) / G * G; }
 
 // o's form over whole sequences or segments; the states come from `s_in` and
 // go to `s_out`, both by slot.
@@ -214,7 +219,7 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
     kda::ScanArgs a{};
     a.map = m;
     a.jobs = 1;
-    a.share = xcd_share(G);
+    a.share = xcd_share(G, false);
     // Rows that no other head reads, more than the caches hold: non-temporal loads.
     // Forward of 8 sequences x 96 heads x 1024 tokens 208 -> 198 us, x 512 122 ->
     // 109, x 64 (50 MB) 33 -> 37; 32 sequences x 16 q/k and 64 value heads, whose
@@ -461,7 +466,7 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
         kda::ScanArgs a{};
         a.map = m;
         a.jobs = 3;
-        a.share = 3 * xcd_share(G);
+        a.share = 3 * xcd_share(G, true);
         a.log_decay = log_decay;
         a.scale = d.scale;
         a.slots = d.s.N;
@@ -495,7 +500,7 @@ kda_status kda_decay_bwd(const kda_decay_problem* pp, const void* q, const void*
             // the segments' own sums: of v k^T forward, of do q^T backward in time
             kda::ScanArgs b = a;
             b.jobs = 2;
-            b.share = 2 * xcd_share(G);
+            b.share = 2 * xcd_share(G, true);
             b.by_seg = 1;
             b.job[0] = b.job[1] = kda::ScanJob{};
             b.job[0].b = rk; b.job[0].c = rv;
