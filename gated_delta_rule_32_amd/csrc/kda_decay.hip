@@ -215,7 +215,7 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // wv holds the state as MFMA accumulators: tile (t, u) is S^T[k][v] with
 //     k = 32(t/2) + 8gq + 4(t%2) + e,   v = 32wv + 8(n/4) + 4u + n%4
 // (NU = 1: v = 16wv + n; lane 16gq + n, element e), so that tiles t = 2p and
-// 2p+1 together are, rounded to BF16, the operand of S a over channels 32p ..
+// 2p+1 together are, as BF16, the operand of S a over channels 32p ..
 // 32p+31 in the order in which one 16-byte read takes them from a's rows, and
 // the two tiles u of Y^T give a lane 8 neighbouring channels of one token to
 // store (8-byte stores cost the packed forward 4%, the training step 7%).  Per
@@ -226,10 +226,13 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // The state is kept divided by the decay since it was last rescaled, so that
 // most chunks only add to it (weights u_j over that decay) and y takes the
 // decay as one more factor; it is rescaled when the decay falls below 2^-24.
-// Two operands are rounded to BF16: P, and S where it meets a (each about as
-// large an error as the output's own rounding).  The FP32 products C u go in
-// as three BF16 pieces of 8 significant bits each, so exactly; the state
-// itself stays in FP32 registers.
+// P, and S where it meets a, go in as two BF16 pieces, off by at most 2^-18 of
+// themselves, so that the output's own rounding is the only one to be seen.
+// (Rounded to BF16 each would add as large an error as that rounding: o, dq, dk
+// and dv were off by 2.35e-3 of their norm instead of 1.66e-3.  P's second piece
+// takes 1% of a packed training step, S's 11%, half of it in the products and
+// half in taking S apart.)  The FP32 products C u go in as three BF16 pieces of 8
+// significant bits each, so exactly; the state itself stays in FP32 registers.
 //
 // The rows of the next chunk travel from memory to the other of two LDS
 // buffers, without passing through registers, while this one is computed:
@@ -249,7 +252,7 @@ template <int NU, int kParts, bool kOut, bool kPack, bool kStream = false>
 __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
     // LDS (bytes): the rows of b, c and a, two buffers each that differ in address
     // bit SET; the P^T tiles
-    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = 2 * SET, LA = 4 * SET, LPT = 512;
+    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LB = 0, LC = 2 * SET, LA = 4 * SET, LPT = 1024;
     constexpr int ROWS16 = 16 * D * 2;
     __shared__ __align__(16) char lds[2 * SETS * SET];
     __shared__ __align__(16) char lds_p[kOut ? 3 * LPT : 16];
@@ -461,7 +464,9 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
                     const bool seen = (w == 2) | (n16 >= 4 * gq + e);
                     acc[e] = seen ? acc[e] * pf[e] : 0.0f;
                 }
-                *(bf16x4*)(lds_p + w * LPT + lane * 8) = to_bf4(acc);
+                bf16x4 hi, lo;
+                split4_rne(acc, hi, lo);
+                *(bf16x8*)(lds_p + w * LPT + lane * 16) = cat8(hi, lo);
             }
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti)
@@ -472,9 +477,14 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
                 if (!kDeep) read_a(p);
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
-                    const bf16x8 sp = cat8(to_bf4(S[2 * p][u]), to_bf4(S[2 * p + 1][u]));
+                    bf16x4 hi[2], lo[2];
 #pragma unroll
-                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(sp, av[p][ti], y[ti][u]);
+                    for (int i = 0; i < 2; ++i) split4_rne(S[2 * p + i][u], hi[i], lo[i]);
+                    const bf16x8 s1 = cat8(hi[0], hi[1]), s2 = cat8(lo[0], lo[1]);
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(s1, av[p][ti], y[ti][u]);
+#pragma unroll
+                    for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(s2, av[p][ti], y[ti][u]);
                 }
             }
         }
@@ -534,8 +544,11 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
             read_c();
         }
         if (kOut) {
-            const bf16x4 p00 = *(const bf16x4*)(lds_p + lane * 8), p11 = *(const bf16x4*)(lds_p + LPT + lane * 8),
-                         p10 = *(const bf16x4*)(lds_p + 2 * LPT + lane * 8);
+            // 4 rows of a tile each, first pieces before second ones
+            const bf16x8 p00 = *(const bf16x8*)(lds_p + lane * 16), p11 = *(const bf16x8*)(lds_p + LPT + lane * 16),
+                         p10 = *(const bf16x8*)(lds_p + 2 * LPT + lane * 16);
+            const bf16x8 p1h = __builtin_shufflevector(p10, p11, 0, 1, 2, 3, 8, 9, 10, 11),
+                         p1l = __builtin_shufflevector(p10, p11, 4, 5, 6, 7, 12, 13, 14, 15);
             const float yf[2] = {y_held, y_held * far};
             const char* yb = yout + py;
 #pragma unroll
@@ -545,8 +558,9 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[ti][u][e] *= yf[ti];
                 const bf16x8 c = cat8(cf[0][u], cf[1][u]);
-                y[0][u] = mma32(c, cat8(p00, to_bf4(zero4())), y[0][u]);
-                y[1][u] = mma32(c, cat8(p10, p11), y[1][u]);
+                y[0][u] = mma32(cat8(cf[0][u], cf[0][u]), p00, y[0][u]);   // both pieces in one product
+                y[1][u] = mma32(c, p1h, y[1][u]);
+                y[1][u] = mma32(c, p1l, y[1][u]);
             }
 #pragma unroll
             for (int ti = 0; ti < 2; ++ti) {
