@@ -180,11 +180,11 @@ __device__ __forceinline__ bf16x4 take_high(f32x4& x) {
 // A partial of dq or dk (value heads that share a q/k head each form one) is
 // kept as quads of 8 bytes: four 15-bit floats (sign, 5 bits of exponent, 9 of
 // mantissa) and 4 bits that scale the quad by a power of 2^16 so that its
-// largest value is in [1/2, 2^15).  A value is off by at most 2^-10 of itself,
-// a quarter of a BF16 rounding, or 2^-24 of the quad's largest.  (As FP32 the
-// partials' way out and in took 28% of a grouped training step, and BF16
-// partials would add as large an error again as the result's own rounding.)
-// A quad with a NaN or an infinity comes back as NaN.
+// largest value is in [1/2, 2^15).  A value is rounded once, to nearest: off by at
+// most 2^-10 of itself, a quarter of a BF16 rounding, or 2^-23 of the quad's
+// largest.  (As FP32 the partials' way out and in took 28% of a grouped training
+// step, and BF16 partials would add as large an error again as the result's own
+// rounding.)  A quad with a NaN or an infinity comes back as NaN.
 __device__ __forceinline__ u32x2 pack_quad(f32x4 x) {
     const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
     const unsigned q = __float_as_uint(top) >> 27;                 // biased exponent / 16
@@ -193,8 +193,15 @@ __device__ __forceinline__ u32x2 pack_quad(f32x4 x) {
     const bool bad = !(x[0] * 0.0f + x[1] * 0.0f + x[2] * 0.0f + x[3] * 0.0f == 0.0f);
     unsigned m[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)   // FP16, its lowest bit rounded off
-        m[i] = ((unsigned)__builtin_bit_cast(unsigned short, (f16)(x[i] * scale)) + 1u) >> 1;
+    for (int i = 0; i < 4; ++i) {
+        // to 10 significant bits, or below FP16's normal values to a multiple of
+        // 2^-23 (a last bit of 1.5): an FP16 value with its lowest bit clear
+        const float v = x[i] * scale;
+        const unsigned u = __float_as_uint(v);
+        const float r = fabsf(v) < 0x1p-14f ? (v + 1.5f) - 1.5f
+                                            : __uint_as_float((u + 0x1fffu + (u >> 14 & 1u)) & ~0x3fffu);
+        m[i] = (unsigned)__builtin_bit_cast(unsigned short, (f16)r) >> 1;
+    }
     const u32x2 w = {m[0] | m[1] << 15 | q << 30, m[2] | m[3] << 15 | (q >> 2) << 30};
     return u32x2{bad ? ~0u : w[0], bad ? ~0u : w[1]};
 }

@@ -70,3 +70,83 @@ def test_prefill_is_rounded_once():
     out, _ = kda.decay_attention(*(inp.dev(x) for x in (inp.q, inp.k, inp.v, inp.l)), inp.s0.cuda(),
                                  cu_seqlens=inp.dev(inp.cu), cu_seqlens_cpu=inp.cu)
     check_one_rounding("o", out, inp.reference()[0], inp.energies()[0])
+
+
+# ---------------------------------------------------------------------------
+# packed partials of shared heads
+# ---------------------------------------------------------------------------
+# A partial keeps 10 significant bits, rounded once: off by at most 2^-10 of
+# itself, or, far below the largest of its quad of channels, 2^-23 of that one.
+PACK, PACK_SMALL = 2.0 ** -10, 2.0 ** -23
+
+
+def shared_sum(x, y):
+    """dq and dk as the sums of two given partials each: one token per sequence,
+    two value heads on one q/k head, no decay, q = k = 0, and do and v that pick
+    row 0 of the states, so that dq is x[:, 0] + y[:, 0] (the initial state's
+    rows) and dk is x[:, 1] + y[:, 1] (the final state's adjoint's)."""
+    import gated_delta_rule_32_amd as kda
+    n = x.shape[0]
+    zero = torch.zeros((n, 1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    pick = torch.zeros((n, 1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    pick[..., 0] = 1.0
+    states = [torch.zeros((n, 2, 128, 128), device="cuda") for _ in range(2)]
+    for i in range(2):
+        states[i][:, 0, 0], states[i][:, 1, 0] = x[:, i].cuda(), y[:, i].cuda()
+    _, _, ctx = kda.decay_attention_training_forward(zero, zero, pick, torch.zeros(2, device="cuda"), states[0], scale=1.0)
+    dq, dk, _, _ = kda.decay_attention_training_backward(ctx, pick, states[1])
+    return torch.stack((dq[:, 0, 0], dk[:, 0, 0]), 1).double().cpu()
+
+
+def test_partials_of_shared_heads_are_rounded_once():
+    """x has 16 significant bits, which the two BF16 pieces of a state hold, and
+    the other head's partial is -bf16(x), which no rounding touches, so that the
+    sum (a few last bits, exact in BF16) shows what became of x.  Rounded to nearest,
+    the deviations of 131072 values have a standard deviation of at most 2^-10 /
+    sqrt(3) of themselves and a mean of nothing: bar 6 standard deviations of the
+    mean, 6 x 2^-10 / sqrt(3) / sqrt(131072) = 9.3e-6.  (Rounded twice, with all ties away from zero,
+    they had a mean of 3.5e-4 and a worst value of 1.5 x 2^-10.)"""
+    g = torch.Generator().manual_seed(33)
+    n = 512
+    x = (1 + torch.randint(2 ** 15, (n, 2, 128), generator=g) * 2.0 ** -15).float()
+    x = x * torch.exp2(torch.randint(-3, 4, (n, 2, 128), generator=g).float())
+    x = x * torch.where(torch.rand((n, 2, 128), generator=g) < 0.5, -1.0, 1.0)
+    near = x.bfloat16().float()
+    kept = shared_sum(x, -near) + near.double()
+    off = (kept / x.double() - 1).numpy()
+    bar = 6 * PACK / 3 ** 0.5 / off.size ** 0.5
+    print(f"worst {np.abs(off).max() / PACK:.3f} x 2^-10, mean {off.mean():.2e} (bar {bar:.1e})", flush=True)
+    assert np.abs(off).max() <= PACK and abs(off.mean()) <= bar
+
+
+def test_small_partials_beside_large_ones():
+    """Channels of a quad 2^0 to 2^40 apart, at several sizes of the whole."""
+    g = torch.Generator().manual_seed(34)
+    n = 64
+    x = torch.randn((n, 2, 128), generator=g) * torch.exp2(-40 * torch.rand((n, 2, 128), generator=g))
+    x = x * torch.exp2(torch.randint(-60, 61, (n, 1, 1), generator=g).float())
+    got, ref = shared_sum(x, torch.zeros_like(x)), x.double()
+    top = ref.abs().unflatten(-1, (-1, 4)).amax(-1, keepdim=True).expand(-1, -1, -1, 4).flatten(-2)
+    bar = (lu.U * (1 + PACK) + PACK + 2.0 ** -17) * ref.abs() + PACK_SMALL * top
+    worst = ((got - ref).abs() / bar).max()
+    print(f"{worst:.3f} of the bar", flush=True)
+    assert worst <= 1.0
+
+
+@pytest.mark.parametrize("segment", [0, 64])
+def test_gradients_of_shared_heads(segment):
+    """Against the sum of the single heads' gradients, whose absolute values say
+    what the partials lose."""
+    inp = Inp([150, 31, 64], True, 2, 6, seed=35)
+    got = train(inp, segment)
+    alone = Inp([150, 31, 64], True, 6, 6, seed=35)
+    for name in ("q", "k"):
+        setattr(alone, name, getattr(inp, name).repeat_interleave(3, 2))
+    for name in ("v", "do", "s0", "ds"):
+        setattr(alone, name, getattr(inp, name))
+    (dq, dk, _, _), _ = alone.gradients()
+    energies = inp.energies()
+    for name, x, heads, energy in (("dq", got[2], dq, energies[1]), ("dk", got[3], dk, energies[2])):
+        heads = heads.reshape(1, 245, 2, 3, 128)
+        top = np.abs(heads).reshape(1, 245, 2, 3, 32, 4).max(-1, keepdims=True).repeat(4, -1).reshape(heads.shape)
+        check_one_rounding(name, x, heads.sum(3), energy, PACK * np.abs(heads).sum(3) + PACK_SMALL * top.sum(3))
