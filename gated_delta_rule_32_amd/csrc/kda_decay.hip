@@ -701,7 +701,10 @@ hipError_t launch_decay_chain(const ChainArgs& a, hipStream_t s) {
 // tokens).  A workgroup takes 32 of the 128 state rows of one (sequence,
 // value head): a half wave holds a row (4 channels a lane), each wave 4 pairs
 // of rows, so every load and store moves 1 KiB of contiguous state, and o is
-// a sum over the half wave.  No LDS, no barrier; everything FP32.  Bound by the
+// a sum over the half wave.  No LDS, no barrier; everything FP32.  The decay is
+// applied as the sum of two FP32 values: rounded to one, it would be off the same
+// way in every token of a decode (e^-3.3e-5 by 2.1e-8, after 65536 tokens 1.4e-3),
+// while the roundings of the state go both ways.  Bound by the
 // state's way in and out; non-temporal (kStream) when that exceeds kStreamBytes:
 // 128 sequences of 64 heads 205 -> 179 us, 64 of them 105 -> 91 us, 32 of them
 // (268 MB) 46 us either way.
@@ -721,7 +724,8 @@ __global__ __launch_bounds__(256) void decay_token_kernel(TokenArgs A) {
         const f32x4* p = (const f32x4*)(S + (row0 + 8 * j) * D);
         x[j] = kStream ? __builtin_nontemporal_load(p) : *p;
     }
-    const float f = (float)decay_power(A.log_decay[it.h], 1);
+    const double lam = decay_power(A.log_decay[it.h], 1);
+    const float f = (float)lam, f_low = (float)(lam - (double)f);
     const int hq = it.h / A.G;
     const bf16* q = (const bf16*)A.q + it.tok0 * A.sq + hq * D + ch;
     const bf16* k = (const bf16*)A.k + it.tok0 * A.sk + hq * D + ch;
@@ -736,7 +740,7 @@ __global__ __launch_bounds__(256) void decay_token_kernel(TokenArgs A) {
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[j][e] = x[j][e] * f + vj * kf[e];
+                x[j][e] = fmaf(vj, kf[e], fmaf(x[j][e], f, x[j][e] * f_low));
                 sum += x[j][e] * qf[e];
             }
             sum = row16_sum(sum);

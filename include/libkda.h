@@ -428,7 +428,9 @@ kda_status kda_decay_bwd(const kda_decay_problem* p, const void* q, const void* 
  * NULL); other slots are not touched.  The indices must be distinct and in
  * range, checked on the host mirror (given iff state_indices is).  A slot
  * that the device copy places outside the pool (a replayed graph's inactive
- * sequence, say -1) is skipped, and its rows of o are left as they were. */
+ * sequence, say -1) is skipped, and its rows of o are left as they were.
+ * Token by token the state is rounded to FP32 once per token, to nearest: a
+ * decay of less than 2^-25 a token changes nothing there. */
 kda_status kda_decay_infer(const kda_decay_problem* p, const void* q, const void* k, const void* v,
                            const float* log_decay, float* state_pool, int64_t pool_slots,
                            const int32_t* state_indices, const int32_t* state_indices_host, void* o,

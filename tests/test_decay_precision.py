@@ -150,3 +150,42 @@ def test_gradients_of_shared_heads(segment):
         heads = heads.reshape(1, 245, 2, 3, 128)
         top = np.abs(heads).reshape(1, 245, 2, 3, 32, 4).max(-1, keepdims=True).repeat(4, -1).reshape(heads.shape)
         check_one_rounding(name, x, heads.sum(3), energy, PACK * np.abs(heads).sum(3) + PACK_SMALL * top.sum(3))
+
+
+# ---------------------------------------------------------------------------
+# long decodes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("l", [-1e-5, -3.3e-5, -1.7e-4, -0.25])
+@pytest.mark.parametrize("tokens", [1, 8])
+def test_decode_does_not_drift(l, tokens):
+    """A state decays over 16384 decoded tokens of zeros to e^{16384 l} of itself.
+    Each token rounds it once (and a far smaller product), to nearest: standard
+    deviation at most 2^-24 / sqrt(3) of the state, sqrt(16384) of it in the end if
+    the roundings are independent, and of the mean over 16384 elements 1/128 of
+    that; bars of 6 standard deviations.  A factor rounded to FP32 would move the
+    mean by up to 16384 x 2^-25 = 4.9e-4.
+
+    Under a weak decay the roundings of neighbouring tokens are alike, also of exact
+    products.  A token takes d = (1 - e^l) x off x, D = d / ulp is between 2^23
+    (1 - e^l) and twice that, and the rounding is that of D to a whole number.  D
+    shrinks by (1 - e^l) D a token, so that it takes p = 1 / ((1 - e^l) D) <= 1 /
+    ((1 - e^l)^2 2^23) tokens from one whole number to the next.  Over such a period
+    the roundings go evenly through -1/2 .. 1/2 ulp and cancel; a part of one leaves
+    at most the sum over a half's tokens with one sign, p / 8 ulp, where an ulp is
+    at most 2^-23 of x.  Every binade that the state passes through starts anew:
+    (1 + binades) p / 8 x 2^-23 more, for the mean as well (l = -1e-5: p = 1192,
+    1.8e-5 a binade)."""
+    import gated_delta_rule_32_amd as kda
+    L = 16384 if l > -0.1 else 64
+    x = torch.zeros((1, tokens, 1, 128), dtype=torch.bfloat16, device="cuda")
+    s0 = torch.rand((1, 1, 128, 128), generator=torch.Generator().manual_seed(36)) + 1
+    decay = torch.tensor([l], device="cuda")
+    pool, out = s0.cuda(), torch.empty_like(x)
+    for _ in range(L // tokens):
+        kda.decay_attention(x, x, x, decay, pool, output=out)
+    off = lu.f64(pool) / (lu.f64(s0) * np.exp(float(np.float32(l)) * L)) - 1
+    std = L ** 0.5 * 2.0 ** -24 / 3 ** 0.5
+    alike = (1 + np.ceil(-l * L / np.log(2))) / (8 * np.expm1(l) ** 2 * 2.0 ** 23) * 2.0 ** -23
+    print(f"max {np.abs(off).max():.2e} (bar {6 * std + alike:.2e}), mean {abs(off.mean()):.2e} "
+          f"(bar {6 * std / 128 + alike:.2e})", flush=True)
+    assert np.abs(off).max() <= 6 * std + alike and abs(off.mean()) <= 6 * std / 128 + alike
