@@ -214,7 +214,10 @@ __global__ __launch_bounds__(RN_THREADS) void gnorm_kernel(GNormArgs a) {
             // (g = -inf: sigmoid 0, and g sigmoid(g) tends to 0 as well)
             act[e] = kSilu ? (sg > 0.0f ? g.x[e] * sg : g.x[e] < 0.0f ? 0.0f : g.x[e] * sg) : sg;
             if (kBwd) {
-                const float slope = kSilu ? sg + act[e] * (1.0f - sg) : sg * (1.0f - sg);
+                // sigmoid(-g) for 1 - sigmoid(g), whose digits cancel where the gate is open
+                // (1% off at a gate of 12, 0 from 17 on)
+                const float away = sigmoidf_(-g.x[e]);
+                const float slope = kSilu ? sg + act[e] * away : sg * away;
                 x.x[e] *= r;
                 const float u = dy.x[e] * x.x[e];
                 gw[e] += u * act[e];
