@@ -217,7 +217,8 @@ __global__ __launch_bounds__(RN_THREADS) void gnorm_kernel(GNormArgs a) {
                 // sigmoid(-g) for 1 - sigmoid(g), whose digits cancel where the gate is open
                 // (1% off at a gate of 12, 0 from 17 on)
                 const float away = sigmoidf_(-g.x[e]);
-                const float slope = kSilu ? sg + act[e] * away : sg * away;
+                // (g = inf: g sigmoid(-g) tends to 0)
+                const float slope = kSilu ? sg + (away > 0.0f ? act[e] * away : 0.0f) : sg * away;
                 x.x[e] *= r;
                 const float u = dy.x[e] * x.x[e];
                 gw[e] += u * act[e];

@@ -55,3 +55,23 @@ def test_silu_slope_of_open_and_closed_gates():
     s, t = 1 / (1 + np.exp(-g)), 1 / (1 + np.exp(g))
     ref = terms * slopes(g, True)
     lu.check_bars("dgate", dg, ref, lu.U * (1 + lu.U) * np.abs(ref) + FINE * np.abs(terms) * s * (1 + np.abs(g) * t))
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_slopes_of_infinite_gates(act):
+    """Gates of minus and plus infinity and of the type's lowest and highest value:
+    the slope is 0, but 1 for an open SiLU gate; a closed gate's dx is 0 too."""
+    top = torch.finfo(torch.bfloat16).max
+    gate = torch.tensor([-math.inf, -top, math.inf, top])[None, :, None, None].expand(1, 4, 2, 128)
+    dx, dg, _, terms = gate_gradient(gate.to(torch.bfloat16).contiguous(), act, 43)
+    assert not dg[0, :2].any() and not dx[0, :2].any()
+    ref = terms[0, 2:] if act == "silu" else np.zeros_like(terms[0, 2:])
+    lu.check_bars("dgate", dg[0, 2:], ref, (lu.U * (1 + lu.U) + FINE) * np.abs(ref))
+
+
+def test_a_nan_gate_is_seen():
+    gate = torch.zeros((1, 1, 1, 128), dtype=torch.bfloat16)
+    gate[0, 0, 0, 5] = math.nan
+    for act in ("sigmoid", "silu"):
+        dg = gate_gradient(gate, act, 44)[1]
+        assert torch.isnan(dg[0, 0, 0, 5]) and torch.isfinite(dg[0, 0, 0, :5]).all() and torch.isfinite(dg[0, 0, 0, 6:]).all()
