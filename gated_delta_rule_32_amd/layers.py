@@ -22,7 +22,8 @@ _BF, _F32 = torch.bfloat16, torch.float32
 _vp = ctypes.c_void_p
 _size = ctypes.c_size_t
 _byref = ctypes.byref
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (a torch built without GPU support has none; it makes no GPU tensors either)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class KdaDecayProblem(ctypes.Structure):

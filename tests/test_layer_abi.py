@@ -290,3 +290,16 @@ def test_oracle_gated_norm_gradients_by_differences(silu):
         d = r.randn(*a[i].shape)
         f = lambda y: (lo.gated_norm(*[y if j == i else a[j] for j in range(3)], silu, 1e-3) * dy).sum()  # noqa: E731
         assert _difference(f, a[i], d) == pytest.approx((grads[i] * d).sum(), rel=1e-6)
+
+
+def test_package_imports_with_a_torch_without_gpu_support():
+    """The package's host-only calls need nothing of torch's GPU bindings, which
+    such a build lacks."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "import gated_delta_rule_32_amd as kda\n"
+            "assert kda.kda_version() > 0 and kda.kda_gnorm_bwd_workspace_bytes(kda.KdaGNormProblem(1, 1, 1, 0, 1e-6)) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
