@@ -189,3 +189,33 @@ def test_decode_does_not_drift(l, tokens):
     print(f"max {np.abs(off).max():.2e} (bar {6 * std + alike:.2e}), mean {abs(off.mean()):.2e} "
           f"(bar {6 * std / 128 + alike:.2e})", flush=True)
     assert np.abs(off).max() <= 6 * std + alike and abs(off.mean()) <= 6 * std / 128 + alike
+
+
+# ---------------------------------------------------------------------------
+# segments
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("segment", [0, 64, 256])
+def test_segments_agree_with_one_walk(segment):
+    """All results in segments against those of whole sequences (segments of 65536
+    tokens, which take no workspace).  States: a chunk of 32 tokens adds to them in
+    three products, a rescaling and a segment's end round once more, each off by at
+    most 2^-23 of the sum of absolute values; 25 chunks, 4 roundings each, both
+    routes.  The others: one BF16 rounding each, which may fall to either side."""
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([777, 130], True, 2, 2, seed=37)
+    p = kda.KdaDecayProblem(1, 907, 2, 2, 2, inp.cu.data_ptr(), inp.cu.data_ptr(), 0.0, 65536)
+    assert kda.kda_decay_fwd_workspace_bytes(p) == kda.kda_decay_bwd_workspace_bytes(p) == 0
+    p.segment = segment
+    # (0: whatever the library takes)
+    assert segment == 0 or min(kda.kda_decay_fwd_workspace_bytes(p), kda.kda_decay_bwd_workspace_bytes(p)) > 0
+    whole, cut = train(inp, 65536), train(inp, segment)
+    (dq, dk, dv, dinit), minit = inp.gradients()
+    o, final, _, mfinal = inp.reference()
+    bar = 25 * 4 * 2.0 ** -23
+    for name, i, ref, major in (("final_state", 1, final, mfinal), ("dinitial_state", 5, dinit, minit)):
+        lu.check_bars(name, whole[i], ref, bar * major)
+        lu.check_bars(name, cut[i], lu.f64(whole[i]), 2 * bar * major)
+    for name, i, ref, energy in zip(("o", "dq", "dk", "dv"), (0, 2, 3, 4), (o, dq, dk, dv), inp.energies()):
+        check_one_rounding(name, cut[i], ref, energy)
+        lu.check_bars(name, cut[i], lu.f64(whole[i]),
+                      2 * (lu.U * (1 + lu.U) * np.abs(ref) + FINE * np.sqrt(energy)))
