@@ -664,6 +664,7 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
     if (slot < 0 || slot >= A.slots) return;
     const int64_t at = (slot * m.Hv + h) * (int64_t)STATE + e;
     const int len = m.task != nullptr ? m.seq_len[n] : m.len;
+    if (len <= A.skip) return;
     const int segs = (len + m.seg_len - 1) / m.seg_len;
     const int64_t base = m.task != nullptr ? m.tape_off[n] + n : (int64_t)n * segs;
     const float l = A.log_decay[h];

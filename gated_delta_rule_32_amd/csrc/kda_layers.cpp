@@ -211,10 +211,11 @@ kda_status check_scan_grid(const Decay& d, int seg, const kda::ItemMap& m, int j
 int xcd_share(int G, bool backward) { return G == 1 && !backward ? 11 : (8 + G - 1) / G * G; }
 
 // o's form over whole sequences or segments; the states come from `s_in` and
-// go to `s_out`, both by slot.
-kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const void* q, const void* k, const void* v,
-                       const float* log_decay, const float* s_in, float* s_out, const int32_t* slot, int64_t slots,
-                       void* o, char* ws, hipStream_t stream) {
+// go to `s_out`, both by slot.  m's items are those of the sequences longer
+// than `skip` tokens.
+kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, int64_t skip, const void* q, const void* k,
+                       const void* v, const float* log_decay, const float* s_in, float* s_out, const int32_t* slot,
+                       int64_t slots, void* o, char* ws, hipStream_t stream) {
     const int G = d.s.G;
     kda::ScanArgs a{};
     a.map = m;
@@ -251,6 +252,7 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
         c.map = m;
         c.jobs = 1;
         c.job[0] = {states, s_in, s_out, 0};
+        c.skip = (int)skip;
         c.log_decay = log_decay;
         c.slot = slot;
         c.slots = slots;
@@ -265,8 +267,37 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, const voi
     return KDA_OK;
 }
 
-// Longest sequence that the token-serial kernel takes in kda_decay_infer.
+// kda_decay_infer takes sequences of up to this many tokens token by token, each
+// by its own length, so that a user's tokens are computed the same way whoever else
+// is in the batch.
 constexpr int64_t kTokenSerialMax = 8;
+
+// How a call of kda_decay_infer runs: its `chunked` longer sequences in chunks
+// (segments of `seg` tokens, 0: whole), the others token by token.  A packed call's
+// schedule has the longer ones first.
+struct InferPlan {
+    int64_t chunked = 0, segs = 0;   // segs: the chunked sequences' segments
+    int seg = 0;
+    size_t ws = 0;
+};
+InferPlan infer_plan(const Decay& d) {
+    InferPlan r;
+    if (d.s.max_len <= kTokenSerialMax) return r;
+    Decay c;
+    c.segment = d.segment;
+    c.s.Hv = d.s.Hv;
+    c.s.max_len = d.s.max_len;
+    for (int64_t len : d.s.len)
+        if (len > kTokenSerialMax) {
+            c.s.len.push_back(len);
+            c.s.tokens += len;
+        }
+    r.chunked = c.s.N = (int)c.s.len.size();
+    r.seg = auto_segment(c, 1);
+    if (r.seg != 0) r.segs = total_segs(c, r.seg);
+    r.ws = decay_ws(d, r.seg, false).total;   // (segments are numbered among all sequences)
+    return r;
+}
 
 kda_status check_ws(const void* ws, size_t bytes, size_t need) {
     if (need == 0) return KDA_OK;
@@ -274,8 +305,6 @@ kda_status check_ws(const void* ws, size_t bytes, size_t need) {
     if (bytes < need) return fail(KDA_ERR_WORKSPACE_SIZE, "workspace has %zu bytes, needs %zu", bytes, need);
     return check_align(ws, "workspace");
 }
-
-bool token_serial(const Decay& d) { return d.s.max_len <= kTokenSerialMax; }
 
 // ---------------------------------------------------------------------------
 // row norms
@@ -416,7 +445,7 @@ kda_status kda_decay_fwd(const kda_decay_problem* pp, const void* q, const void*
         kda::ItemMap m;
         if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
         if ((s = check_scan_grid(d, seg, m, 1)) != KDA_OK) return s;
-        return run_forward(d, seg, m, q, k, v, log_decay, initial_state, final_state, nullptr, d.s.N, o,
+        return run_forward(d, seg, m, 0, q, k, v, log_decay, initial_state, final_state, nullptr, d.s.N, o,
                            (char*)workspace, stream);
     });
 }
@@ -541,7 +570,7 @@ kda_status kda_decay_infer_workspace_bytes(const kda_decay_problem* pp, size_t* 
         kda_status s = check_decay(pp, d);
         if (s != KDA_OK) return s;
         if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
-        *bytes = token_serial(d) ? 0 : decay_ws(d, auto_segment(d, 1), false).total;
+        *bytes = infer_plan(d).ws;
         return KDA_OK;
     });
 }
@@ -575,10 +604,8 @@ kda_status kda_decay_infer(const kda_decay_problem* pp, const void* q, const voi
             return fail(KDA_ERR_SHAPE, "without state_indices the pool needs N=%d slots (has %lld)", d.s.N,
                         (long long)pool_slots);
         }
-        const bool serial = token_serial(d);
-        const int seg = serial ? 0 : auto_segment(d, 1);
-        const size_t need = serial ? 0 : decay_ws(d, seg, false).total;
-        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const InferPlan ip = infer_plan(d);
+        if ((s = check_ws(workspace, workspace_bytes, ip.ws)) != KDA_OK) return s;
         const std::vector<Span> ins = {
             {q, strided_bytes(d.s.tokens, d.sq, d.s.Hqk), "q"}, {k, strided_bytes(d.s.tokens, d.sk, d.s.Hqk), "k"},
             {v, strided_bytes(d.s.tokens, d.sv, d.s.Hv), "v"}, {log_decay, (size_t)d.s.Hv * 4, "log_decay"},
@@ -586,18 +613,26 @@ kda_status kda_decay_infer(const kda_decay_problem* pp, const void* q, const voi
             {state_indices, state_indices ? (size_t)d.s.N * 4 : 0, "state_indices"}};
         s = check_overlap({{o, (size_t)d.s.tokens * d.s.Hv * D * 2, "o"},
                            {state_pool, (size_t)pool_slots * d.s.Hv * kState * 4, "state_pool"},
-                           {workspace, need, "workspace"}}, ins);
+                           {workspace, ip.ws, "workspace"}}, ins);
         if (s != KDA_OK) return s;
         hipStream_t stream = (hipStream_t)stream_;
         SeqPlan plan;
         kda::ItemMap m;
-        if ((s = make_map(d, seg, stream, plan, m)) != KDA_OK) return s;
-        if ((s = serial ? check_grid(m.items * 4) : check_scan_grid(d, seg, m, 1)) != KDA_OK) return s;
-        if (!serial)
-            return run_forward(d, seg, m, q, k, v, log_decay, state_pool, state_pool, state_indices, pool_slots, o,
-                               (char*)workspace, stream);
+        if ((s = make_map(d, ip.seg, stream, plan, m)) != KDA_OK) return s;
+        m.items = (ip.seg ? ip.segs : ip.chunked) * d.s.Hv;
+        const int64_t serial = d.s.N - ip.chunked;
+        if ((s = check_scan_grid(d, ip.seg, m, 1)) != KDA_OK || (s = check_grid(serial * d.s.Hv * 4)) != KDA_OK)
+            return s;
+        if (ip.chunked != 0) {
+            s = run_forward(d, ip.seg, m, kTokenSerialMax, q, k, v, log_decay, state_pool, state_pool, state_indices,
+                            pool_slots, o, (char*)workspace, stream);
+            if (s != KDA_OK || serial == 0) return s;
+        }
         kda::TokenArgs t{};
         t.map = m;
+        t.map.seg_len = 0;
+        t.map.items = serial * d.s.Hv;
+        if (d.packed) t.map.task = m.task + ip.chunked * d.s.Hv;
         t.q = (const kda::bf16_t*)q; t.sq = d.sq;
         t.k = (const kda::bf16_t*)k; t.sk = d.sk;
         t.v = (const kda::bf16_t*)v; t.sv = d.sv;

@@ -72,6 +72,7 @@ struct ChainArgs {
     ItemMap map;
     ChainJob job[2];
     int jobs;
+    int skip;                // sequences of at most this many tokens are left out
     const float* log_decay;
     const int32_t* slot;
     int64_t slots;

@@ -422,13 +422,15 @@ kda_status kda_decay_bwd(const kda_decay_problem* p, const void* q, const void* 
                          const float* dfinal_state, void* dq, void* dk, void* dv, float* dinitial_state,
                          void* workspace, size_t workspace_bytes, void* stream);
 
-/* Decode (sequences of a few tokens, token by token) and prefill (longer
+/* Decode (sequences of up to 8 tokens, token by token) and prefill (longer
  * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated
- * in place: sequence n reads and writes slot state_indices[n] (slot n when
- * NULL); other slots are not touched.  The indices must be distinct and in
- * range, checked on the host mirror (given iff state_indices is).  A slot
- * that the device copy places outside the pool (a replayed graph's inactive
- * sequence, say -1) is skipped, and its rows of o are left as they were.
+ * in place.  One call may hold both: each sequence runs by its own length, and
+ * one of up to 8 tokens gives the same bits whatever else is in the call.
+ * Sequence n reads and writes slot state_indices[n] (slot n when NULL); other
+ * slots are not touched.  The indices must be distinct and in range, checked on
+ * the host mirror (given iff state_indices is).  A slot that the device copy
+ * places outside the pool (a replayed graph's inactive sequence, say -1) is
+ * skipped, and its rows of o are left as they were.
  * Token by token the state is rounded to FP32 once per token, to nearest: a
  * decay of less than 2^-25 a token changes nothing there. */
 kda_status kda_decay_infer(const kda_decay_problem* p, const void* q, const void* k, const void* v,
