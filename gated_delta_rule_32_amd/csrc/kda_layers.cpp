@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <exception>
 #include <vector>
@@ -61,6 +62,14 @@ kda_status check_align(std::initializer_list<std::pair<const void*, const char*>
         kda_status s = check_align(p.first, p.second);
         if (s != KDA_OK) return s;
     }
+    return KDA_OK;
+}
+
+// (Below the normal numbers the reciprocal square root takes eps for 0, and a row of
+// zeros would come out as NaN.)
+kda_status check_eps(float eps) {
+    if (!(eps >= FLT_MIN) || !std::isfinite(eps))
+        return fail(KDA_ERR_SHAPE, "eps must be finite and a positive normal number (got %g)", (double)eps);
     return KDA_OK;
 }
 
@@ -319,8 +328,8 @@ kda_status check_qknorm(const kda_qknorm_problem* p, kda::QkNormArgs& a) {
         return fail(KDA_ERR_SHAPE, "rot_dim must be a multiple of 8 in [8, 128] (got %d)", p->rot_dim);
     if (p->interleaved != 0 && p->interleaved != 1)
         return fail(KDA_ERR_SHAPE, "interleaved must be 0 or 1 (got %d)", p->interleaved);
-    if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
-        return fail(KDA_ERR_SHAPE, "eps must be finite and positive (got %g)", (double)p->eps);
+    kda_status s = check_eps(p->eps);
+    if (s != KDA_OK) return s;
     if (p->table_rows < 1 || p->table_rows > ((int64_t)1 << 40))
         return fail(KDA_ERR_SHAPE, "table_rows out of range (%lld)", (long long)p->table_rows);
     a.tokens = (int64_t)p->B * p->T;
@@ -334,7 +343,6 @@ kda_status check_qknorm(const kda_qknorm_problem* p, kda::QkNormArgs& a) {
     a.rows = p->table_rows;
     a.sq = p->q_stride;
     a.sk = p->k_stride;
-    kda_status s;
     if ((s = check_stride(a.sq, p->Hq, "q")) != KDA_OK || (s = check_stride(a.sk, p->Hk, "k")) != KDA_OK) return s;
     return KDA_OK;
 }
@@ -371,8 +379,8 @@ kda_status check_gnorm(const kda_gnorm_problem* p, kda::GNormArgs& a) {
         return fail(KDA_ERR_SHAPE, "B, T and H must be >= 1 (got %d %d %d)", p->B, p->T, p->H);
     if (p->activation != KDA_GATE_SIGMOID && p->activation != KDA_GATE_SILU)
         return fail(KDA_ERR_SHAPE, "unknown activation %d", p->activation);
-    if (!(p->eps > 0.0f) || !std::isfinite(p->eps))
-        return fail(KDA_ERR_SHAPE, "eps must be finite and positive (got %g)", (double)p->eps);
+    kda_status s = check_eps(p->eps);
+    if (s != KDA_OK) return s;
     a.tokens = (int64_t)p->B * p->T;
     if (p->H > kMaxStride / D || a.tokens * p->H > kMaxRows)
         return fail(KDA_ERR_SHAPE, "too many rows (tokens x heads)");
@@ -381,7 +389,6 @@ kda_status check_gnorm(const kda_gnorm_problem* p, kda::GNormArgs& a) {
     a.eps = p->eps;
     a.sx = p->x_stride;
     a.sg = p->gate_stride;
-    kda_status s;
     if ((s = check_stride(a.sx, p->H, "x")) != KDA_OK || (s = check_stride(a.sg, p->H, "gate")) != KDA_OK) return s;
     return KDA_OK;
 }

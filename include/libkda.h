@@ -446,12 +446,13 @@ kda_status kda_decay_infer(const kda_decay_problem* p, const void* q, const void
  * [B][T][Hq][128], k BF16 [B][T][Hk][128], weights FP32 [128].  positions:
  * device INT64 [B][T], or NULL for the token's index in its row.  A position
  * outside the table makes its token's outputs (and, in the backward, the
- * weight gradients) NaN. */
+ * weight gradients) NaN.  The squares are summed in FP32: a row's values may be
+ * up to about 1e18. */
 typedef struct {
     int32_t B, T, Hq, Hk;
     int32_t rot_dim;
     int32_t interleaved;
-    float eps;
+    float eps;               /* a positive normal number (at least FLT_MIN) */
     int64_t table_rows;
     int64_t q_stride, k_stride;
 } kda_qknorm_problem;
@@ -475,7 +476,7 @@ kda_status kda_qknorm_bwd(const kda_qknorm_problem* p, const void* q, const void
 typedef struct {
     int32_t B, T, H;
     int32_t activation;   /* KDA_GATE_SIGMOID or KDA_GATE_SILU */
-    float eps;
+    float eps;            /* as in kda_qknorm_problem */
     int64_t x_stride, gate_stride;
 } kda_gnorm_problem;
 

@@ -75,3 +75,17 @@ def test_a_nan_gate_is_seen():
     for act in ("sigmoid", "silu"):
         dg = gate_gradient(gate, act, 44)[1]
         assert torch.isnan(dg[0, 0, 0, 5]) and torch.isfinite(dg[0, 0, 0, :5]).all() and torch.isfinite(dg[0, 0, 0, 6:]).all()
+
+
+def test_rows_of_zeros_at_the_smallest_eps():
+    import gated_delta_rule_32_amd as kda
+    x = torch.zeros((1, 2, 1, 128), dtype=torch.bfloat16)
+    x[0, 1] = 3.0
+    one, w = torch.ones_like(x).cuda(), torch.ones(128, device="cuda")
+    eps = 2.0 ** -126
+    y = kda.gated_norm_forward(x.cuda(), one, w, eps=eps)
+    d = kda.gated_norm_backward(one, x.cuda(), one, w, eps=eps)
+    cos, sin = kda.rotary_table(2, 128)
+    q = kda.qk_norm_rope_forward(x.cuda(), x.cuda(), w, w, cos, sin, eps=eps)
+    assert not y[0, 0].any() and not q[0][0, 0].any() and all(torch.isfinite(t).all() for t in (y, *d, *q))
+    lu.check_bars("y", y[0, 1], np.full((1, 128), 1 / (1 + math.exp(-1))), lu.U)

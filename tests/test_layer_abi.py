@@ -303,3 +303,15 @@ def test_package_imports_with_a_torch_without_gpu_support():
             "assert kda.kda_version() > 0 and kda.kda_gnorm_bwd_workspace_bytes(kda.KdaGNormProblem(1, 1, 1, 0, 1e-6)) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("eps,status", [(1e-40, SHAPE), (1.1e-38, SHAPE), (2.0 ** -126, OK), (1e-30, OK)])
+def test_row_norms_refuse_an_eps_below_the_normal_numbers(eps, status):
+    """The kernels would take it for 0, and turn a row of zeros into NaN."""
+    n = ctypes.c_size_t()
+    assert kda._lib.kda_qknorm_bwd_workspace_bytes(ctypes.byref(qk(eps=eps)), ctypes.byref(n)) == status
+    assert kda._lib.kda_gnorm_bwd_workspace_bytes(ctypes.byref(gn(eps=eps)), ctypes.byref(n)) == status
+    if status != OK:
+        a, b = ptrs(14), ptrs(8)
+        assert kda._lib.kda_qknorm_fwd(ctypes.byref(qk(eps=eps)), *a[:9], None) == status
+        assert kda._lib.kda_gnorm_fwd(ctypes.byref(gn(eps=eps)), *b[:4], None) == status
