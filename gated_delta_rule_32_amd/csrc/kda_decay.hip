@@ -607,11 +607,18 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 
     float* s_out = J.s_out;
     if (s_out != nullptr) {
+        // the decay as the sum of two FP32 values: calls that take up the state one after
+        // another apply it over and over (a decay of one rounded value would drift)
+        const float f = (float)held, f_low = (float)(held - (double)f);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
-            for (int u = 0; u < NU; ++u)
-                *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + krow(t)) = S[t][u] * (float)held;
+            for (int u = 0; u < NU; ++u) {
+                f32x4 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(S[t][u][e], f, S[t][u][e] * f_low);
+                *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + krow(t)) = x;
+            }
     }
 }
 

@@ -219,3 +219,32 @@ def test_segments_agree_with_one_walk(segment):
         check_one_rounding(name, cut[i], ref, energy)
         lu.check_bars(name, cut[i], lu.f64(whole[i]),
                       2 * (lu.U * (1 + lu.U) * np.abs(ref) + FINE * np.sqrt(energy)))
+
+
+@pytest.mark.parametrize("l", [-1e-5, -3.3e-5, -1.7e-4])
+@pytest.mark.parametrize("tokens", [9, 33, 100])
+def test_prefill_in_pieces_does_not_drift(l, tokens):
+    """The same for a prompt that comes in 2048 pieces of a few chunks: a piece decays
+    the state by e^{tokens l} and rounds it once.  That sequence of exact products,
+    each rounded to nearest, is followed in 64 bits; the kernel's product is off by
+    2^-47 before its rounding, which so goes the other way about once in 2^-24 / 2^-47
+    = 2^23 cases, 4 times among 2048 x 16384, and mostly in different elements: bar
+    4 last bits of one element, 2^-23 each, and 4 x 2^-23 / 16384 x 4 for the mean.  A
+    factor rounded to FP32 would move the mean by up to 2048 x 2^-25 = 6.1e-5.  (The
+    sequence itself is up to 1.2e-7 off on average where e^{tokens l} makes the
+    roundings of neighbouring values alike.)"""
+    import gated_delta_rule_32_amd as kda
+    calls = 2048
+    x = torch.zeros((1, tokens, 1, 128), dtype=torch.bfloat16, device="cuda")
+    s0 = torch.rand((1, 1, 128, 128), generator=torch.Generator().manual_seed(38)) + 1
+    decay = torch.tensor([l], device="cuda")
+    pool, out = s0.cuda(), torch.empty_like(x)
+    for _ in range(calls):
+        kda.decay_attention(x, x, x, decay, pool, output=out)
+    factor, ideal = np.exp(float(np.float32(l)) * tokens), s0.numpy()
+    for _ in range(calls):
+        ideal = (ideal.astype(np.float64) * factor).astype(np.float32)
+    off = lu.f64(pool) / ideal.astype(np.float64) - 1
+    print(f"max {np.abs(off).max():.2e} (bar {4 * 2.0 ** -23:.2e}), mean {abs(off.mean()):.2e} (bar {2.0 ** -33:.2e})",
+          flush=True)
+    assert np.abs(off).max() <= 4 * 2.0 ** -23 and abs(off.mean()) <= 2.0 ** -33
