@@ -37,10 +37,6 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
     return ((int64_t)hi << 32) | lo;
 }
 
-__device__ __forceinline__ double uniform(double x) {
-    return __builtin_bit_cast(double, uniform64(__builtin_bit_cast(int64_t, x)));
-}
-
 __device__ __forceinline__ Item find_item(const ItemMap& m, int64_t i) {
     Item it;
     const int64_t r = i / m.Hv;
@@ -93,23 +89,15 @@ __device__ __forceinline__ double decay_power(float l, int n) {  // e^{l n}, n >
     return n == 0 ? 1.0 : exp((double)l * n);
 }
 
-// e^{l n} as a factor that is applied over and over: rounded to FP32 it would
-// be off the same way every time, so `corr` carries the quotient of the true
-// power to the product of the factors given out, and that product stays within
-// half a step of the true power however many there are.
-struct Power {
-    double lam, inv, corr;
-    __device__ __forceinline__ Power(float l, int n) {
-        lam = uniform(decay_power(l, n));
-        inv = uniform(lam > 1e-30 ? 1.0 / lam : 0.0);
-        corr = 1.0;
-    }
-    __device__ __forceinline__ float next() {
-        const double want = lam * corr;
-        const float f = (float)want;
-        corr = inv != 0.0 ? 1.0 + (want - (double)f) * inv : 1.0;
-        return f;
-    }
+// A decay that a state is multiplied by over and over, by segments, tokens or calls:
+// rounded to one FP32 value it would be off the same way every time, and the state
+// would drift.  It is applied as the sum of two, to 2^-48 of itself.
+struct Factor {
+    float f, low;
+    __device__ __forceinline__ explicit Factor(double x) : f((float)x), low((float)(x - (double)(float)x)) {}
+    // x times the factor, plus y
+    __device__ __forceinline__ float apply(float x, float y) const { return fmaf(x, f, fmaf(x, low, y)); }
+    __device__ __forceinline__ float apply(float x) const { return fmaf(x, f, x * low); }
 };
 
 // LDS rows of 128 channels are 16 blocks of 8 channels; block b of row r is
@@ -607,16 +595,14 @@ __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 
 
     float* s_out = J.s_out;
     if (s_out != nullptr) {
-        // the decay as the sum of two FP32 values: calls that take up the state one after
-        // another apply it over and over (a decay of one rounded value would drift)
-        const float f = (float)held, f_low = (float)(held - (double)f);
+        const Factor decay(held);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 f32x4 x;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = fmaf(S[t][u][e], f, S[t][u][e] * f_low);
+                for (int e = 0; e < 4; ++e) x[e] = decay.apply(S[t][u][e]);
                 *(f32x4*)(s_out + soff + (vrow + 4 * u) * D + krow(t)) = x;
             }
     }
@@ -675,8 +661,7 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
     const int segs = (len + m.seg_len - 1) / m.seg_len;
     const int64_t base = m.task != nullptr ? m.tape_off[n] + n : (int64_t)n * segs;
     const float l = A.log_decay[h];
-    Power full(l, m.seg_len);
-    const float f_last = (float)decay_power(l, len - (segs - 1) * m.seg_len);
+    const Factor full(decay_power(l, m.seg_len)), last(decay_power(l, len - (segs - 1) * m.seg_len));
     f32x4 x = J.s_in != nullptr ? *(const f32x4*)(J.s_in + at) : zero4();
     const int64_t step = (int64_t)m.Hv * STATE;
     float* p = J.seg + (base * m.Hv + h) * STATE + e;
@@ -693,7 +678,8 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(ChainArgs A) {
             const f32x4 r = next[u];
             next[u] = sum(i + u + AHEAD);   // (behind the last: not used)
             *(f32x4*)(p + j * step) = x;
-            x = r + x * (j == segs - 1 ? f_last : full.next());
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[c] = (j == segs - 1 ? last : full).apply(x[c], r[c]);
         }
     }
     if (J.s_out != nullptr) *(f32x4*)(J.s_out + at) = x;
@@ -709,10 +695,9 @@ hipError_t launch_decay_chain(const ChainArgs& a, hipStream_t s) {
 // tokens).  A workgroup takes 32 of the 128 state rows of one (sequence,
 // value head): a half wave holds a row (4 channels a lane), each wave 4 pairs
 // of rows, so every load and store moves 1 KiB of contiguous state, and o is
-// a sum over the half wave.  No LDS, no barrier; everything FP32.  The decay is
-// applied as the sum of two FP32 values: rounded to one, it would be off the same
-// way in every token of a decode (e^-3.3e-5 by 2.1e-8, after 65536 tokens 1.4e-3),
-// while the roundings of the state go both ways.  Bound by the
+// a sum over the half wave.  No LDS, no barrier; everything FP32.  (With a decay
+// rounded to one FP32 value a decode of 65536 tokens at l = -3.3e-5 would end 1.4e-3
+// off.)  Bound by the
 // state's way in and out; non-temporal (kStream) when that exceeds kStreamBytes:
 // 128 sequences of 64 heads 205 -> 179 us, 64 of them 105 -> 91 us, 32 of them
 // (268 MB) 46 us either way.
@@ -732,8 +717,7 @@ __global__ __launch_bounds__(256) void decay_token_kernel(TokenArgs A) {
         const f32x4* p = (const f32x4*)(S + (row0 + 8 * j) * D);
         x[j] = kStream ? __builtin_nontemporal_load(p) : *p;
     }
-    const double lam = decay_power(A.log_decay[it.h], 1);
-    const float f = (float)lam, f_low = (float)(lam - (double)f);
+    const Factor decay(decay_power(A.log_decay[it.h], 1));
     const int hq = it.h / A.G;
     const bf16* q = (const bf16*)A.q + it.tok0 * A.sq + hq * D + ch;
     const bf16* k = (const bf16*)A.k + it.tok0 * A.sk + hq * D + ch;
@@ -748,7 +732,7 @@ __global__ __launch_bounds__(256) void decay_token_kernel(TokenArgs A) {
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[j][e] = fmaf(vj, kf[e], fmaf(x[j][e], f, x[j][e] * f_low));
+                x[j][e] = fmaf(vj, kf[e], decay.apply(x[j][e]));
                 sum += x[j][e] * qf[e];
             }
             sum = row16_sum(sum);

@@ -248,3 +248,23 @@ def test_prefill_in_pieces_does_not_drift(l, tokens):
     print(f"max {np.abs(off).max():.2e} (bar {4 * 2.0 ** -23:.2e}), mean {abs(off.mean()):.2e} (bar {2.0 ** -33:.2e})",
           flush=True)
     assert np.abs(off).max() <= 4 * 2.0 ** -23 and abs(off.mean()) <= 2.0 ** -33
+
+
+@pytest.mark.parametrize("l", [-1e-5, -3.3e-5, -1.7e-4])
+def test_prefill_in_segmented_pieces_does_not_drift(l):
+    """Pieces of 200 tokens in segments of 64, 64, 64 and 8, each of which decays the
+    state and rounds it once: bars as above for 4 x 512 roundings."""
+    import gated_delta_rule_32_amd as kda
+    x = torch.zeros((1, 200, 1, 128), dtype=torch.bfloat16, device="cuda")
+    s0 = torch.rand((1, 1, 128, 128), generator=torch.Generator().manual_seed(39)) + 1
+    decay = torch.tensor([l], device="cuda")
+    pool, out = s0.cuda(), torch.empty_like(x)
+    for _ in range(512):
+        kda.decay_attention(x, x, x, decay, pool, output=out, segment=64)
+    ideal = s0.numpy()
+    for n in [64, 64, 64, 8] * 512:
+        ideal = (ideal.astype(np.float64) * np.exp(float(np.float32(l)) * n)).astype(np.float32)
+    off = lu.f64(pool) / ideal.astype(np.float64) - 1
+    print(f"max {np.abs(off).max():.2e} (bar {4 * 2.0 ** -23:.2e}), mean {abs(off.mean()):.2e} (bar {2.0 ** -33:.2e})",
+          flush=True)
+    assert np.abs(off).max() <= 4 * 2.0 ** -23 and abs(off.mean()) <= 2.0 ** -33
