@@ -278,8 +278,11 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, int64_t s
 
 // kda_decay_infer takes sequences of up to this many tokens token by token, each
 // by its own length, so that a user's tokens are computed the same way whoever else
-// is in the batch.
-constexpr int64_t kTokenSerialMax = 8;
+// is in the batch.  Token by token against one chunk, in us, for sequences of 2, 4, 8
+// and 16 tokens: one sequence of 32 heads 5.6, 6.3, 9.7, 16.6 against 7.0; 8 of them 7.9,
+// 10.1, 14.0, 21.7 against 11.1; 32 of them 23.7, 29.1, 41, 66 against 26.8 to 28; 128 of
+// 64 heads 175, 204, 290, 469 against 212, 216, 225, 235.
+constexpr int64_t kTokenSerialMax = 4;
 
 // How a call of kda_decay_infer runs: its `chunked` longer sequences in chunks
 // (segments of `seg` tokens, 0: whole), the others token by token.  A packed call's

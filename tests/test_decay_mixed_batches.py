@@ -12,11 +12,11 @@ pytestmark = pytest.mark.gpu
 
 BATCHES = {  # lengths, Hqk, Hv, segment
     "one_prompt": ([1, 1, 70, 1], 2, 2, 0),
-    "edges": ([8, 9, 1, 300, 5, 2], 2, 4, 0),
-    "segments": ([8, 9, 1, 300, 5, 2], 2, 4, 64),
+    "edges": ([4, 9, 1, 300, 5, 2], 2, 4, 0),
+    "segments": ([4, 9, 1, 300, 5, 2], 2, 4, 64),
     "segments_auto": ([1, 2000, 1], 1, 2, 0),
     "many": ([1, 40, 3] * 30, 4, 4, 0),
-    "last_is_long": ([7, 6, 5, 64], 1, 3, 64),
+    "last_is_long": ([4, 3, 2, 64], 1, 3, 64),
 }
 
 
@@ -52,7 +52,7 @@ def test_short_sequences_do_not_see_the_batch(case):
     rest = [i for i in range(pool0.shape[0]) if i not in slots]
     assert torch.equal(pool[rest].cpu(), pool0[rest])
     for n, length in enumerate(inp.lengths):
-        if length > 8:
+        if length > 4:
             continue
         want, state = alone(inp, slots, pool0, n)
         at = int(inp.cu[n])
@@ -65,7 +65,7 @@ def test_prompts_do_not_see_the_short_sequences(segment):
     inp, slots, pool0, _ = batch("edges")
     pool = pool0.cuda()
     out = pool_call(inp, pool, slots, segment=segment)
-    long = [n for n, length in enumerate(inp.lengths) if length > 8]
+    long = [n for n, length in enumerate(inp.lengths) if length > 4]
     part = Inp([inp.lengths[n] for n in long], True, inp.Hqk, inp.Hv)
     rows = torch.cat([torch.arange(int(inp.cu[n]), int(inp.cu[n + 1])) for n in long])
     part.q, part.k, part.v = (x[:, rows].contiguous() for x in (inp.q, inp.k, inp.v))
