@@ -625,16 +625,18 @@ static void launch_scan(const ScanArgs& a, bool states_only, bool pack, hipStrea
 // each spend the least on reading the rows out of LDS.  With one workgroup per
 // unit at most, eight waves shorten a chunk, and with one for every second
 // unit, two workgroups of half the columns each.  Forward in us (four waves;
-// eight waves; halves): 288 workgroups of 1024 tokens 94, 106, 103; 192 of 2048
-// 125, 108, 139; 150 of 2048 117, 103, 117; 128 of 2048 -, 98, 86; 48 of 2048
-// -, 97, 77.
+// eight waves; halves): 48 workgroups of 2048 tokens 137, 113, 99; 128 134, 110, 98;
+// 150 135, 118, 134; 192 140, 127, 140; 256 141, 138, 155; 288 195, 202, -; 384 207, 218,
+// -.  Backward, three workgroups a (sequence, head), whose walks differ: 144 of 2048
+// tokens 139, 118, 126; 288 of 4096 386, 367, -; 384 of 4096 with shared heads 510, 473,
+// -; 432 of 2048 212, 209, -; 504 229, 230, -; 576 286, 293, 316.
 hipError_t launch_decay_scan(const ScanArgs& a, bool states_only, hipStream_t s) {
     bool pack = false;
     for (int i = 0; i < a.jobs; ++i) pack = pack || a.job[i].pack != 0;
     const int64_t groups = a.map.items * a.jobs;
     if (groups <= 128)
         launch_scan<1, 2>(a, states_only, pack, s);
-    else if (groups <= 256)
+    else if (groups <= (a.jobs == 3 ? 400 : 256))
         launch_scan<1, 1>(a, states_only, pack, s);
     else
         launch_scan<2, 1>(a, states_only, pack, s);
