@@ -121,18 +121,28 @@ int64_t total_segs(const Decay& d, int seg) {
 
 // Tokens per segment of a scan over `forms` forms (o, or dq, dk and dv), or 0
 // for whole sequences: whichever an estimate says is faster.  Measured: a
-// chunk of 32 tokens takes a workgroup 1.1 (few of them) to 1.5 us, 1.6 or
-// 1.85 us (see launch_decay_scan), and the card gets through one chunk of one
-// head every 7.3 ns.  So whole sequences take the longest one's latency or the
-// total's throughput.  Segments shorten the first, for a pass that forms the
+// chunk of 32 tokens takes a workgroup 1.4 (few of them), 1.7 to 2.1 (up to one per
+// compute unit) or 3 us (several, see launch_decay_scan), and the card gets through one
+// chunk of one head every 7.3 ns.  So whole sequences take the longest one's latency or
+// the total's throughput.  Segments shorten the first, for a pass that forms the
 // segments' states (1.2 us a chunk, 4.5 ns in all; for the backward both
 // ways), their way through memory (15 ns each) and two more launches.  In us,
-// whole sequences against segments, forward: 16 heads x 32768 tokens 1183 /
-// 212, 32 x 8192 276 / 106, 16 x 1024 40 / 29, 96 x 4096 182 / 163, 4 sequences
-// x 32 heads x 4096 183 / 208, 8 x 32 x 2048 126 / 210; backward: 16 x 32768
-// 1181 / 440, 16 x 4096 144 / 81, 2 x 32 x 2048 100 / 114, 4 x 32 x 4096 340 /
-// 423.
-double chunk_us(int64_t groups) { return groups <= 128 ? 1.05 + 0.0035 * (double)groups : groups <= 256 ? 1.6 : 1.85; }
+// whole sequences against the segments of this rule, forward: 4 heads x 512 tokens 26
+// / 21, 16 x 1024 49 / 30, 64 x 1024 51 / 47, 16 x 4096 182 / 49, 32 x 8192 368 / 125, 16 x
+// 32768 1420 / 223, 96 x 4096 184 / 189, 2 sequences x 32 heads x 2048 93 / 72; against
+// segments of 1024, 4 x 32 x 4096 188 / 208, 8 x 32 x 2048 138 / 211; backward: 16 x 1024
+// 52 / 40, 16 x 4096 182 / 86, 32 x 8192 358 / 252, 16 x 32768 1420 / 475; against segments
+// of 512, 2 x 32 x 2048 112 / 127, of 576, 3 x 16 x 3000 161 / 168, of 1024, 4 x 32 x 4096 387
+// / 494.
+// How long the segments are, in us for those of 128, 192, 256, 384, 512, 1024 and 2048
+// tokens, forward: 16 heads x 1024 tokens 29, 31, 32, 39, 47, -, -; 32 x 2048 54, 56, 45,
+// 52, 52, 82, -; 32 x 8192 174, 139, 123, 115, 109, 108, 155; 16 x 32768 375, 279, 256, 237,
+// 221, 205, 221; backward: 16 x 1024 41, 40, 39, 46, 50, -, -; 32 x 2048 95, 87, 79, 93, 84,
+// 92, -; 32 x 8192 365, 320, 292, 278, 261, 239, 286; 16 x 32768 725, 637, 577, 530, 501, 486,
+// 468.
+double chunk_us(int64_t groups) {
+    return groups <= 128 ? 1.4 + 0.0006 * (double)groups : groups <= 256 ? 1.25 + 0.003 * (double)groups : 3.0;
+}
 
 int auto_segment(const Decay& d, int forms) {
     if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
@@ -140,12 +150,16 @@ int auto_segment(const Decay& d, int forms) {
     for (int64_t len : d.s.len) chunks += (double)((len + 31) / 32);
     chunks *= d.s.Hv;
     const int passes = forms == 1 ? 1 : 2;
-    const double whole = std::max(chunk_us((int64_t)d.s.N * d.s.Hv * forms) * (double)((d.s.max_len + 31) / 32),
-                                  0.0073 * forms * chunks);
-    // two segments per compute unit (forward), one (backward, three forms each), not below 128 (192) tokens
-    const int64_t items = forms == 1 ? 512 : 256;
-    int64_t seg = (d.s.tokens * d.s.Hv / items + 63) / 64 * 64;
-    seg = std::max<int64_t>(seg, forms == 1 ? 128 : 192);
+    const double whole = 4.0 + std::max(chunk_us((int64_t)d.s.N * d.s.Hv * forms) * (double)((d.s.max_len + 31) / 32),
+                                        0.0073 * forms * chunks);
+    auto per_item = [&](int64_t items) { return (d.s.tokens * d.s.Hv / items + 63) / 64 * 64; };
+    // backward, three forms a segment: one segment per compute unit, not below 192 tokens;
+    // forward: one while that makes it at most 256 tokens long, not below 128, otherwise two
+    int64_t seg = per_item(256);
+    if (forms != 1)
+        seg = std::max<int64_t>(seg, 192);
+    else
+        seg = seg <= 256 ? std::max<int64_t>(seg, 128) : std::max<int64_t>(per_item(512), 256);
     if (d.s.max_len <= seg) return 0;
     const int64_t cut_items = total_segs(d, (int)seg) * d.s.Hv;
     const double cut = std::max((chunk_us(cut_items * forms) + 1.2) * (double)(seg / 32),
@@ -213,10 +227,10 @@ kda_status check_scan_grid(const Decay& d, int seg, const kda::ItemMap& m, int j
 // single heads an odd number, so that an XCD's blocks start at different memory
 // channels; but not in the backward, whose three forms share rows and lose that
 // in the blocks that a window of 8 XCDs leaves over.  In us, side by side 1, 3,
-// 8, 11, 16, 31: forward of 8 x 1024 x 96 heads 196, 188, 197, 189, 195, 187, of
-// 32 x 1024 x 32 278, 267, 286, 269, 279, 267; backward of 8 x 2048 x 32 with 8
-// 282, with 11 296.  In fours, 4, 8, 12, 16, 32: mixed prefill 673, 671, 669, 669,
-// 685; 4 x 4096 x 8 q/k and 32 value heads, training step 580, 569, 590, 558, 596.
+// 8, 11, 16, 31: forward of 32 x 1024 tokens x 32 heads 279, 268, 279, 268, 274, 267, of 8
+// x 1024 x 96 221 to 223 whichever; backward of 8 x 2048 x 32 334, 333, 331, 336, 331, 333.
+// In fours, 4, 4, 8, 12, 16, 32: forward of 32 x 2048 x 16 q/k and 64 value heads 845, 843,
+// 836, 842, 835, 837; 4 x 4096 x 8 and 32, both directions 710, 708, 708, 730, 706, 722.
 int xcd_share(int G, bool backward) { return G == 1 && !backward ? 11 : (8 + G - 1) / G * G; }
 
 // o's form over whole sequences or segments; the states come from `s_in` and
@@ -231,11 +245,10 @@ kda_status run_forward(const Decay& d, int seg, const kda::ItemMap& m, int64_t s
     a.jobs = 1;
     a.share = xcd_share(G, false);
     // Rows that no other head reads, more than the caches hold: non-temporal loads.
-    // Forward of 8 sequences x 96 heads x 1024 tokens 208 -> 198 us, x 512 122 ->
-    // 109, x 64 (50 MB) 33 -> 37; 32 sequences x 16 q/k and 64 value heads, whose
-    // q and k are read four times, 695 -> 800.  (Not in the states' pass, whose rows
-    // are read again: one sequence of 16384 tokens x 64 heads takes 386 us so, 396
-    // with them in both passes or neither.)
+    // Forward of 8 sequences x 96 heads x 1024 tokens 202 -> 196 us, x 512 124 ->
+    // 118, x 64 (50 MB) 30.0 -> 30.6; 32 sequences x 2048 tokens x 16 q/k and 64 value heads,
+    // whose q and k are read four times, 838 -> 901.  (Not in the states' pass, whose rows
+    // are read again; one sequence of 16384 tokens x 64 heads takes 386 us either way.)
     a.stream = G == 1 && 4 * d.s.tokens * d.s.Hv * D * 2 > kda::kStreamBytes;
     a.log_decay = log_decay;
     a.scale = d.scale;
