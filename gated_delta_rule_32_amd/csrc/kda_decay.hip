@@ -171,7 +171,7 @@ __device__ __forceinline__ bf16x4 take_high(f32x4& x) {
 // largest value is in [1/2, 2^15).  A value is rounded once, to nearest: off by at
 // most 2^-10 of itself, a quarter of a BF16 rounding, or 2^-23 of the quad's
 // largest.  (As FP32 the partials' way out and in took 28% of a grouped training
-// step, and BF16 partials would add as large an error again as the result's own
+// step then, and BF16 partials would add as large an error again as the result's own
 // rounding.)  A quad with a NaN or an infinity comes back as NaN.
 __device__ __forceinline__ u32x2 pack_quad(f32x4 x) {
     const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
@@ -213,7 +213,7 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 // 2p+1 together are, as BF16, the operand of S a over channels 32p ..
 // 32p+31 in the order in which one 16-byte read takes them from a's rows, and
 // the two tiles u of Y^T give a lane 8 neighbouring channels of one token to
-// store (8-byte stores cost the packed forward 4%, the training step 7%).  Per
+// store (8-byte stores cost the packed forward 4%, the training step 7% then).  Per
 // chunk of 32 tokens:
 //     P^T = B A^T (16x16 tiles with j <= i, times s e^{l(i-j)})
 //     Y^T = (S A^T) diag(e^{l(i+shift)}) + C^T P^T
@@ -235,14 +235,16 @@ __device__ __forceinline__ f32x4 unpack_quad(u32x2 w) {
 //                                state's part of Y
 //     before the second          C^T P^T, stores, the state's update
 // Two buffers and at most 168 registers let three workgroups share a compute
-// unit.  What they wait for is memory: the forward of 8 x 1024 tokens of 96
-// heads takes 196 us, 191 us without its products, 141 us without its stores as
-// well.  (Rows of 96 heads, 24 KB apart, put a head's b, c and a on the same few
+// unit.  The forward of 8 x 1024 tokens of 96 heads takes 191 to 205 us: 907 MB, each
+// row read once, at 4.4 to 4.7 TB/s, with the vector units issuing 65% and the matrix
+// units busy 44% of the time, so that neither memory nor arithmetic has much room left.
+// (Rows of 96 heads, 24 KB apart, put a head's b, c and a on the same few
 // memory channels: with room for 97 heads a row it takes 13 us less.)  A single
 // workgroup waits for itself, so with one per unit (kDeep) a chunk's LDS reads
 // are issued together, ahead of the next chunk's loads, and half of the state's
-// update moves before the first barrier (48 heads x 2048 tokens: 76 us instead
-// of 89).  `reverse` walks the tokens downwards and only shifts the exponents.
+// update moves before the first barrier (2048 tokens of 48 heads 98 us instead of 100,
+// of 16 heads 93 instead of 97).  `reverse` walks the tokens downwards and only shifts the
+// exponents.
 template <int NU, int kParts, bool kOut, bool kPack, bool kStream = false>
 __global__ __launch_bounds__(512 / NU / kParts, NU == 2 ? 3 : kParts == 2 ? 2 : 4) void decay_scan_kernel(ScanArgs A) {
     // LDS (bytes): the rows of b, c and a, two buffers each that differ in address
