@@ -381,7 +381,9 @@ kda_status kda_infer(const kda_infer_problem* p,
  * NaN or an infinity in a token's row may reach every output of that sequence
  * and head from its chunk of 32 tokens on (walking backward for dk and dv),
  * also at tokens of the chunk that precede it; in a row norm it stays in its row
- * and the weight gradients.
+ * and the weight gradients.  A scan keeps its state divided by decays down to
+ * 2^-24, so that states, and the products of one token that enter them, should
+ * stay below 2^100.
  * ------------------------------------------------------------------------- */
 
 /* Linear attention with a constant decay per value head.  For every sequence
