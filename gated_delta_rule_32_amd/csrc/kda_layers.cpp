@@ -125,8 +125,10 @@ int64_t total_segs(const Decay& d, int seg) {
 // compute unit) or 3 us (several, see launch_decay_scan), and the card gets through one
 // chunk of one head every 7.3 ns.  So whole sequences take the longest one's latency or
 // the total's throughput.  Segments shorten the first, for a pass that forms the
-// segments' states (1.2 us a chunk, 4.5 ns in all; for the backward both
-// ways), their way through memory (15 ns each) and two more launches.  In us,
+// segments' states (for the backward both ways), their way through memory (15 ns
+// each) and two more launches.  That pass takes 1.2 us a chunk with few workgroups, 1.9
+// with one per compute unit, 2.6 (16 heads x 32768 tokens, 5 ns a chunk in all) to 4.6 (32 x
+// 8192, 9 ns) with two; the estimate takes the low ends, 1.2 us and 4.5 ns.  In us,
 // whole sequences against the segments of this rule, forward: 4 heads x 512 tokens 26
 // / 21, 16 x 1024 49 / 30, 64 x 1024 51 / 47, 16 x 4096 182 / 49, 32 x 8192 368 / 125, 16 x
 // 32768 1420 / 223, 96 x 4096 184 / 189, 2 sequences x 32 heads x 2048 93 / 72; against

@@ -338,7 +338,8 @@ def decay_attention(q, k, v, log_decay, initial_state=None, scale=None, cu_seqle
     (output, pool).  initial_state is the pool [P, Hv, 128, 128], updated in
     place: sequence n reads and writes slot ssm_state_indices[n] (int32, with
     its CPU mirror), or slot n.  None starts every sequence from zero in a new
-    pool of N slots."""
+    pool of N slots.  Sequences of up to 4 tokens run token by token, longer ones
+    in chunks, whatever else is in the call."""
     dev = _cuda(q)
     p = _decay_problem(q, k, v, log_decay, scale, cu_seqlens, cu_seqlens_cpu, segment)
     if initial_state is None:
