@@ -534,11 +534,22 @@ def recurrent_kda(q, k, v, g, beta, A_log=None, dt_bias=None, scale=None, initia
 # uses the names above)
 from . import layers as _layers  # noqa: E402
 from .layers import (  # noqa: E402,F401
-    GATE_SIGMOID, GATE_SILU, DecayAttentionTrainingContext, KdaDecayProblem, KdaGNormProblem, KdaQkNormProblem,
-    decay_attention, decay_attention_training_backward, decay_attention_training_forward, gated_norm_backward,
+    GATE_SIGMOID, GATE_SILU, DecayAttentionTrainingContext, KdaDecayProblem, KdaGNormProblem, KdaLNormProblem,
+    KdaQkNormProblem, decay_attention, decay_attention_training_backward, decay_attention_training_forward, gated_norm_backward,
     gated_norm_forward, kda_decay_bwd, kda_decay_bwd_workspace_bytes, kda_decay_fwd, kda_decay_fwd_workspace_bytes,
     kda_decay_infer, kda_decay_infer_workspace_bytes, kda_gnorm_bwd, kda_gnorm_bwd_workspace_bytes, kda_gnorm_fwd,
-    kda_qknorm_bwd, kda_qknorm_bwd_workspace_bytes, kda_qknorm_fwd, qk_norm_rope_backward, qk_norm_rope_forward,
-    rotary_table)
+    kda_lnorm_bwd, kda_lnorm_bwd_workspace_bytes, kda_lnorm_fwd,
+    kda_qknorm_bwd, kda_qknorm_bwd_workspace_bytes, kda_qknorm_fwd, layer_norm_backward, layer_norm_forward,
+    qk_norm_rope_backward, qk_norm_rope_forward, rotary_table)
 
 EXPORTED += _layers.EXPORTED
+
+# The gated delta rule, and the verification of drafted tokens
+from . import delta as _delta  # noqa: E402
+from .delta import (  # noqa: E402,F401
+    GatedDeltaRuleTrainingContext, KdaDeltaProblem, gated_delta_rule, gated_delta_rule_training_forward, kda_delta_fwd,
+    kda_delta_fwd_workspace_bytes, kda_delta_infer, kda_delta_infer_workspace_bytes)
+from . import verify as _verify  # noqa: E402
+from .verify import KdaVerifyProblem, kda_verify, kda_verify_workspace_bytes, verify_drafts  # noqa: E402,F401
+
+EXPORTED += _delta.EXPORTED + _verify.EXPORTED

@@ -39,6 +39,11 @@ SOURCES = [
     "kda_layers.cpp",
     "kda_decay.hip",
     "kda_rownorm.hip",
+    "kda_delta_api.cpp",
+    "kda_delta.hip",
+    "kda_verify_api.cpp",
+    "kda_verify.hip",
+    "kda_lnorm.hip",
 ]
 
 FLAGS = [

@@ -1,0 +1,311 @@
+// C ABI of the gated delta rule (kda_delta_*): argument checks, workspace layout and
+// launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "../../include/libkda.h"
+#include "kda_checks.h"
+#include "kda_delta.h"
+
+namespace {
+
+using namespace kda_host;
+
+struct Delta {
+    Seqs s;
+    int B = 0, T = 0;
+    bool packed = false;
+    float scale = 0;
+    int unit = 0;
+    int64_t sq = 0, sk = 0, sv = 0;
+    int segment = 0;       // the caller's choice; 0: automatic
+};
+
+kda_status check_delta(const kda_delta_problem* p, Delta& d) {
+    if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
+    kda_status s = check_seqs(p->B, p->T, p->Hqk, p->Hv, p->N, p->cu_seqlens, p->cu_seqlens_host, d.s);
+    if (s != KDA_OK) return s;
+    d.B = p->B;
+    d.T = p->T;
+    d.packed = p->cu_seqlens != nullptr;
+    d.scale = p->scale == 0.0f ? 1.0f / std::sqrt(128.0f) : p->scale;
+    if (!(d.scale > 0.0f) || !std::isfinite(d.scale))
+        return fail(KDA_ERR_SCALE, "scale must be 0 or finite and positive (got %g)", (double)p->scale);
+    if (p->use_qk_l2norm != 0 && p->use_qk_l2norm != 1)
+        return fail(KDA_ERR_SHAPE, "use_qk_l2norm must be 0 or 1 (got %d)", p->use_qk_l2norm);
+    d.unit = p->use_qk_l2norm;
+    d.sq = p->q_stride;
+    d.sk = p->k_stride;
+    d.sv = p->v_stride;
+    if ((s = check_stride(d.sq, p->Hqk, "q")) != KDA_OK || (s = check_stride(d.sk, p->Hqk, "k")) != KDA_OK ||
+        (s = check_stride(d.sv, p->Hv, "v")) != KDA_OK)
+        return s;
+    if ((int64_t)p->Hv * D > kMaxStride) return fail(KDA_ERR_SHAPE, "too many value heads (%d)", p->Hv);
+    if (p->segment < 0 || p->segment % 64 != 0)
+        return fail(KDA_ERR_ROUTE, "segment must be 0 or a positive multiple of 64 (got %d)", p->segment);
+    d.segment = p->segment;
+    return KDA_OK;
+}
+
+int64_t total_blocks(const Delta& d) {
+    int64_t n = 0;
+    for (int64_t len : d.s.len) n += (len + kda::DB - 1) / kda::DB;
+    return n;
+}
+
+// The chunks' records and decays.
+struct RecordWs {
+    size_t rec = 0, fac = 0, total = 0;
+};
+RecordWs record_ws(const Delta& d, int64_t blocks, size_t off = 0) {
+    RecordWs w;
+    w.rec = off;
+    off = align256(off + (size_t)blocks * d.s.Hv * 2 * kda::REC * sizeof(float));
+    w.fac = off;
+    w.total = align256(off + (size_t)blocks * d.s.Hv * 4 * sizeof(float));
+    return w;
+}
+
+// The item maps of a call (whole sequences, and blocks of 64 tokens) and its hold on the
+// device schedule (packed calls).
+kda_status make_maps(const Delta& d, hipStream_t stream, SeqPlan& plan, kda::DeltaArgs& a) {
+    kda::ItemMap m{};
+    m.N = d.s.N;
+    m.Hv = d.s.Hv;
+    m.len = d.T;
+    if (d.packed) {
+        kda_status s = get_seq_plan(d.s, d.B, d.T, d.packed, kda::DB, stream, plan);
+        if (s != KDA_OK) return s;
+        m.task = plan.dev.task;
+        m.seg = plan.seg;
+        m.seq_start = plan.dev.seq_start;
+        m.seq_len = plan.dev.seq_len;
+        m.tape_off = plan.dev.tape_off;
+    }
+    a.map = m;
+    a.map.items = (int64_t)d.s.N * d.s.Hv;
+    a.blocks = m;
+    a.blocks.seg_len = kda::DB;
+    a.blocks.items = total_blocks(d) * d.s.Hv;
+    return KDA_OK;
+}
+
+void set_inputs(const Delta& d, const void* q, const void* k, const void* v, const void* g, const void* beta,
+                kda::DeltaArgs& a) {
+    a.q = (const kda::bf16_t*)q;
+    a.k = (const kda::bf16_t*)k;
+    a.v = (const kda::bf16_t*)v;
+    a.sq = d.sq;
+    a.sk = d.sk;
+    a.sv = d.sv;
+    a.G = d.s.G;
+    a.g = (const kda::bf16_t*)g;
+    a.beta = (const kda::bf16_t*)beta;
+    a.unit = d.unit;
+    a.scale = d.scale;
+}
+
+std::vector<Span> input_spans(const kda_delta_problem* pp, const Delta& d, const void* q, const void* k, const void* v,
+                              const void* g, const void* beta) {
+    const size_t gates = (size_t)d.s.tokens * d.s.Hv * 2;
+    return {{q, strided_bytes(d.s.tokens, d.sq, d.s.Hqk), "q"}, {k, strided_bytes(d.s.tokens, d.sk, d.s.Hqk), "k"},
+            {v, strided_bytes(d.s.tokens, d.sv, d.s.Hv), "v"}, {g, gates, "g"}, {beta, gates, "beta"},
+            {pp->cu_seqlens, d.packed ? (size_t)(d.s.N + 1) * 8 : 0, "cu_seqlens"}};
+}
+
+// kda_delta_infer takes sequences of up to this many tokens token by token, each by its own
+// length, so that a user's tokens are computed the same way whoever else is in the batch.
+constexpr int64_t kTokenSerialMax = 8;
+
+// Whether some sequence runs in chunks, and how many do (a packed call's schedule has them
+// first), with how many blocks.
+struct InferPlan {
+    int64_t chunked = 0, blocks = 0;
+    RecordWs ws;
+};
+InferPlan infer_plan(const Delta& d, int spec) {
+    InferPlan r;
+    if (spec > 0 || d.s.max_len <= kTokenSerialMax) return r;
+    for (int64_t len : d.s.len)
+        if (len > kTokenSerialMax) {
+            ++r.chunked;
+            r.blocks += (len + kda::DB - 1) / kda::DB;
+        }
+    r.ws = record_ws(d, total_blocks(d));   // (blocks are numbered among all sequences)
+    return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_delta_fwd_workspace_bytes(const kda_delta_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = record_ws(d, total_blocks(d)).total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void* k, const void* v, const void* g,
+                         const void* beta, const float* initial_state, void* o, float* final_state,
+                         void* workspace, size_t workspace_bytes, void* stream_) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !g || !beta || !o)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_delta_fwd is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {initial_state, "initial_state"}, {o, "o"},
+                         {final_state, "final_state"}});
+        if (s != KDA_OK) return s;
+        const RecordWs w = record_ws(d, total_blocks(d));
+        if ((s = check_ws(workspace, workspace_bytes, w.total)) != KDA_OK) return s;
+        const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
+        std::vector<Span> ins = input_spans(pp, d, q, k, v, g, beta);
+        ins.push_back({initial_state, initial_state ? st : 0, "initial_state"});
+        s = check_overlap({{o, (size_t)d.s.tokens * d.s.Hv * D * 2, "o"},
+                           {final_state, final_state ? st : 0, "final_state"},
+                           {workspace, w.total, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::DeltaArgs a{};
+        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
+        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
+        set_inputs(d, q, k, v, g, beta, a);
+        a.rec = (float*)((char*)workspace + w.rec);
+        a.fac = (float*)((char*)workspace + w.fac);
+        a.o = (kda::bf16_t*)o;
+        a.s_in = initial_state;
+        a.s_out = final_state;
+        a.slots = d.s.N;
+        hipError_t e = kda::launch_delta_prepare(a, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+        e = kda::launch_delta_scan(a, kda::kDeltaOut, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_delta_infer_workspace_bytes(const kda_delta_problem* pp, int32_t num_spec_tokens, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        if (num_spec_tokens < 0)
+            return fail(KDA_ERR_SHAPE, "num_spec_tokens must be >= 0 (got %d)", num_spec_tokens);
+        *bytes = infer_plan(d, num_spec_tokens).ws.total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_delta_infer(const kda_delta_problem* pp, const void* q, const void* k, const void* v, const void* g,
+                           const void* beta, float* state_pool, int64_t pool_slots, const int32_t* state_indices,
+                           const int32_t* state_indices_host, int32_t num_spec_tokens,
+                           const int32_t* num_accepted_tokens, void* o, void* workspace, size_t workspace_bytes,
+                           void* stream_) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !g || !beta || !state_pool || !o)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_delta_infer is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {state_pool, "state_pool"}, {o, "o"}});
+        if (s != KDA_OK) return s;
+        if (pool_slots < 1 || pool_slots > ((int64_t)1 << 40) / ((int64_t)d.s.Hv * kState))
+            return fail(KDA_ERR_SHAPE, "pool_slots out of range (%lld)", (long long)pool_slots);
+        if ((state_indices == nullptr) != (state_indices_host == nullptr))
+            return fail(KDA_ERR_NULL_ARG, "state_indices and state_indices_host go together");
+        const int spec = num_spec_tokens;
+        if (spec < 0) return fail(KDA_ERR_SHAPE, "num_spec_tokens must be >= 0 (got %d)", spec);
+        if (spec == 0 && num_accepted_tokens != nullptr)
+            return fail(KDA_ERR_SHAPE, "num_accepted_tokens needs num_spec_tokens > 0");
+        if (spec > 0) {
+            if (state_indices == nullptr)
+                return fail(KDA_ERR_NULL_ARG, "drafted tokens need state_indices [N][1+S]");
+            for (int n = 0; n < d.s.N; ++n)
+                if (d.s.len[n] != 1 + (int64_t)spec)
+                    return fail(KDA_ERR_SEQLENS, "sequence %d has %lld tokens; drafted tokens need 1+S=%lld", n,
+                                (long long)d.s.len[n], 1 + (long long)spec);
+        }
+        const int64_t n_idx = (int64_t)d.s.N * (1 + (int64_t)spec);
+        if (state_indices_host != nullptr) {
+            std::vector<int32_t> sorted(state_indices_host, state_indices_host + n_idx);
+            for (int64_t i = 0; i < n_idx; ++i)
+                if (sorted[i] < 0 || sorted[i] >= pool_slots)
+                    return fail(KDA_ERR_SHAPE, "state_indices[%lld] = %d is outside the pool", (long long)i, sorted[i]);
+            std::sort(sorted.begin(), sorted.end());
+            for (int64_t i = 1; i < n_idx; ++i)
+                if (sorted[i] == sorted[i - 1])
+                    return fail(KDA_ERR_SHAPE, "pool slot %d is named twice", sorted[i]);
+        } else if (pool_slots < d.s.N) {
+            return fail(KDA_ERR_SHAPE, "without state_indices the pool needs N=%d slots (has %lld)", d.s.N,
+                        (long long)pool_slots);
+        }
+        const InferPlan ip = infer_plan(d, spec);
+        if ((s = check_ws(workspace, workspace_bytes, ip.ws.total)) != KDA_OK) return s;
+        std::vector<Span> ins = input_spans(pp, d, q, k, v, g, beta);
+        ins.push_back({state_indices, state_indices ? (size_t)n_idx * 4 : 0, "state_indices"});
+        ins.push_back({num_accepted_tokens, num_accepted_tokens ? (size_t)d.s.N * 4 : 0, "num_accepted_tokens"});
+        s = check_overlap({{o, (size_t)d.s.tokens * d.s.Hv * D * 2, "o"},
+                           {state_pool, (size_t)pool_slots * d.s.Hv * kState * 4, "state_pool"},
+                           {workspace, ip.ws.total, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::DeltaArgs a{};
+        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
+        const int64_t serial = d.s.N - ip.chunked;
+        a.map.items = ip.chunked * d.s.Hv;
+        a.blocks.items = ip.blocks * d.s.Hv;
+        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK ||
+            (s = check_grid(serial * d.s.Hv * 4)) != KDA_OK)
+            return s;
+        hipError_t e;
+        if (ip.chunked != 0) {
+            set_inputs(d, q, k, v, g, beta, a);
+            a.rec = (float*)((char*)workspace + ip.ws.rec);
+            a.fac = (float*)((char*)workspace + ip.ws.fac);
+            a.o = (kda::bf16_t*)o;
+            a.s_in = a.s_out = state_pool;
+            a.slot = state_indices;
+            a.slots = pool_slots;
+            e = kda::launch_delta_prepare(a, stream);
+            if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+            e = kda::launch_delta_scan(a, kda::kDeltaOut, stream);
+            if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+            if (serial == 0) return KDA_OK;
+        }
+        kda::DeltaTokenArgs t{};
+        t.map = a.map;
+        t.map.items = serial * d.s.Hv;
+        if (d.packed) t.map.task = a.map.task + ip.chunked * d.s.Hv;
+        t.q = (const kda::bf16_t*)q; t.sq = d.sq;
+        t.k = (const kda::bf16_t*)k; t.sk = d.sk;
+        t.v = (const kda::bf16_t*)v; t.sv = d.sv;
+        t.G = d.s.G;
+        t.g = (const kda::bf16_t*)g;
+        t.beta = (const kda::bf16_t*)beta;
+        t.unit = d.unit;
+        t.scale = d.scale;
+        t.o = (kda::bf16_t*)o;
+        t.pool = state_pool;
+        t.slot = state_indices;
+        t.slots = pool_slots;
+        t.each = 1 + spec;
+        t.accepted = num_accepted_tokens;
+        e = kda::launch_delta_token(t, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta decode launch");
+        return KDA_OK;
+    });
+}
+
+}  // extern "C"

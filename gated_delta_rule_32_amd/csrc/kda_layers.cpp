@@ -1,82 +1,25 @@
 // C ABI of the linear-attention layer operators: argument checks, workspace
 // layout and launches of kda_decay_* (linear attention with a constant decay
-// per head), kda_qknorm_* (query/key norm and rotary rotation) and
-// kda_gnorm_* (gated norm of the heads' outputs).
+// per head), kda_qknorm_* (query/key norm and rotary rotation),
+// kda_gnorm_* (gated norm of the heads' outputs) and kda_lnorm_* (layer norm of token
+// rows).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
-#include <exception>
 #include <vector>
 
 #include "../../include/libkda.h"
-#include "kda_host.h"
+#include "kda_checks.h"
 #include "kda_layers.h"
 
 namespace {
 
-using kda_host::check_overlap;
-using kda_host::fail;
-using kda_host::hip_fail;
-using kda_host::SeqPlan;
-using kda_host::Seqs;
-using kda_host::Span;
-
-constexpr int D = 128;
-constexpr int64_t kState = (int64_t)D * D;
-// Largest token stride (elements): the kernels add up to 31 of them in 32 bits.
-constexpr int64_t kMaxStride = (int64_t)1 << 25;
+using namespace kda_host;
 
 // Most rows of a row norm: the kernels number them in 32 bits, with room for
 // the last step behind them (2^31 rows are 512 GiB).
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// Runs an entry point's body; an exception (host memory) becomes a status.
-template <class F>
-kda_status guarded(F f) {
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        return fail(KDA_ERR_HIP, "host error: %s", e.what());
-    }
-}
-
-// 0 means dense rows.
-kda_status check_stride(int64_t& stride, int heads, const char* name) {
-    if (stride == 0) stride = (int64_t)heads * D;
-    if (stride < (int64_t)heads * D || stride > kMaxStride || stride % 8 != 0)
-        return fail(KDA_ERR_SHAPE, "%s token stride must be a multiple of 8 in [%d, %lld] (got %lld)", name, heads * D,
-                    (long long)kMaxStride, (long long)stride);
-    return KDA_OK;
-}
-
-kda_status check_align(const void* p, const char* name) {
-    if (((uintptr_t)p & 15) != 0) return fail(KDA_ERR_SHAPE, "%s must be 16-byte aligned", name);
-    return KDA_OK;
-}
-kda_status check_align(std::initializer_list<std::pair<const void*, const char*>> ps) {
-    for (const auto& p : ps) {
-        kda_status s = check_align(p.first, p.second);
-        if (s != KDA_OK) return s;
-    }
-    return KDA_OK;
-}
-
-// (Below the normal numbers the reciprocal square root takes eps for 0, and a row of
-// zeros would come out as NaN.)
-kda_status check_eps(float eps) {
-    if (!(eps >= FLT_MIN) || !std::isfinite(eps))
-        return fail(KDA_ERR_SHAPE, "eps must be finite and a positive normal number (got %g)", (double)eps);
-    return KDA_OK;
-}
-
-// Bytes from a strided operand's first element to behind its last.
-size_t strided_bytes(int64_t tokens, int64_t stride, int heads) {
-    return (size_t)((tokens - 1) * stride + (int64_t)heads * D) * 2;
-}
 
 // ---------------------------------------------------------------------------
 // linear attention with a constant decay per head
@@ -212,11 +155,6 @@ kda_status make_map(const Decay& d, int seg, hipStream_t stream, SeqPlan& plan, 
     return KDA_OK;
 }
 
-// A launch holds less than 2^32 threads; workgroups of 256 here.
-kda_status check_grid(int64_t blocks) {
-    if (blocks >= (int64_t)1 << 24) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks or tokens");
-    return KDA_OK;
-}
 // The scan's grid for `jobs` forms, and with segments the chain's.
 kda_status check_scan_grid(const Decay& d, int seg, const kda::ItemMap& m, int jobs) {
     kda_status s = check_grid(m.items * jobs);
@@ -326,13 +264,6 @@ InferPlan infer_plan(const Decay& d) {
     return r;
 }
 
-kda_status check_ws(const void* ws, size_t bytes, size_t need) {
-    if (need == 0) return KDA_OK;
-    if (ws == nullptr) return fail(KDA_ERR_NULL_ARG, "workspace is NULL (needs %zu bytes)", need);
-    if (bytes < need) return fail(KDA_ERR_WORKSPACE_SIZE, "workspace has %zu bytes, needs %zu", bytes, need);
-    return check_align(ws, "workspace");
-}
-
 // ---------------------------------------------------------------------------
 // row norms
 // ---------------------------------------------------------------------------
@@ -413,6 +344,27 @@ kda_status check_gnorm(const kda_gnorm_problem* p, kda::GNormArgs& a) {
 size_t gnorm_ws(const kda::GNormArgs& a) {
     return (size_t)kda::rownorm_blocks(a.tokens * a.H) * D * sizeof(float);
 }
+
+kda_status check_lnorm(const kda_lnorm_problem* p, kda::LNormArgs& a) {
+    if (p == nullptr) return fail(KDA_ERR_NULL_ARG, "problem is NULL");
+    if (p->rows < 1 || p->rows >= (int64_t)1 << 31) return fail(KDA_ERR_SHAPE, "rows out of range (%lld)", (long long)p->rows);
+    if (p->C < 8 || p->C > kda::kMaxChannels || p->C % 8 != 0)
+        return fail(KDA_ERR_SHAPE, "C must be a multiple of 8 in [8, %d] (got %d)", kda::kMaxChannels, p->C);
+    kda_status s = check_eps(p->eps);
+    if (s != KDA_OK) return s;
+    a.rows = p->rows;
+    a.C = p->C;
+    a.inv = 1.0f / (float)p->C;
+    a.eps = p->eps;
+    a.sx = p->x_stride == 0 ? p->C : p->x_stride;
+    if (a.sx < p->C || a.sx > (int64_t)1 << 40 || a.sx % 8 != 0)
+        return fail(KDA_ERR_SHAPE, "x row stride must be a multiple of 8 and at least C=%d (got %lld)", p->C, (long long)a.sx);
+    return KDA_OK;
+}
+size_t lnorm_ws(const kda::LNormArgs& a) {
+    return (size_t)kda::lnorm_part_rows(a.rows, a.C) * 2 * a.C * sizeof(float);
+}
+size_t lnorm_x_bytes(const kda::LNormArgs& a) { return (size_t)((a.rows - 1) * a.sx + a.C) * 2; }
 
 }  // namespace
 
@@ -803,6 +755,68 @@ kda_status kda_gnorm_bwd(const kda_gnorm_problem* pp, const void* x, const void*
         a.part = (float*)workspace;
         hipError_t e = kda::launch_gnorm_bwd(a, (hipStream_t)stream);
         if (e != hipSuccess) return hip_fail(e, "gated norm backward launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_lnorm_fwd(const kda_lnorm_problem* pp, const void* x, const float* weight, const float* bias, void* y,
+                         void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::LNormArgs a{};
+        kda_status s = check_lnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (!x || !weight || !y) return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_lnorm_fwd is NULL");
+        if ((s = check_align({{x, "x"}, {weight, "weight"}, {bias, "bias"}, {y, "y"}})) != KDA_OK) return s;
+        const size_t col = (size_t)a.C * 4;
+        s = check_overlap({{y, (size_t)a.rows * a.C * 2, "y"}},
+                          {{x, lnorm_x_bytes(a), "x"}, {weight, col, "weight"}, {bias, bias ? col : 0, "bias"}});
+        if (s != KDA_OK) return s;
+        a.x = (const kda::bf16_t*)x;
+        a.w = weight;
+        a.b = bias;
+        a.y = (kda::bf16_t*)y;
+        hipError_t e = kda::launch_lnorm(a, false, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "layer norm launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_lnorm_bwd_workspace_bytes(const kda_lnorm_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        kda::LNormArgs a{};
+        kda_status s = check_lnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = lnorm_ws(a);
+        return KDA_OK;
+    });
+}
+
+kda_status kda_lnorm_bwd(const kda_lnorm_problem* pp, const void* x, const float* weight, const void* dy, void* dx,
+                         float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    return guarded([&]() -> kda_status {
+        kda::LNormArgs a{};
+        kda_status s = check_lnorm(pp, a);
+        if (s != KDA_OK) return s;
+        if (!x || !weight || !dy || !dx || !dweight)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_lnorm_bwd is NULL");
+        if ((s = check_align({{x, "x"}, {weight, "weight"}, {dy, "dy"}, {dx, "dx"}})) != KDA_OK) return s;
+        const size_t need = lnorm_ws(a);
+        if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
+        const size_t row = (size_t)a.rows * a.C * 2, col = (size_t)a.C * 4;
+        s = check_overlap({{dx, row, "dx"}, {dweight, col, "dweight"}, {dbias, dbias ? col : 0, "dbias"},
+                           {workspace, need, "workspace"}},
+                          {{x, lnorm_x_bytes(a), "x"}, {weight, col, "weight"}, {dy, row, "dy"}});
+        if (s != KDA_OK) return s;
+        a.x = (const kda::bf16_t*)x;
+        a.w = weight;
+        a.dy = (const kda::bf16_t*)dy;
+        a.dx = (kda::bf16_t*)dx;
+        a.dw = dweight;
+        a.db = dbias;
+        a.part = (float*)workspace;
+        hipError_t e = kda::launch_lnorm(a, true, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e, "layer norm backward launch");
         return KDA_OK;
     });
 }

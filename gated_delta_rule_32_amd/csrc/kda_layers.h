@@ -138,4 +138,22 @@ hipError_t launch_qknorm_bwd(const QkNormArgs& a, hipStream_t s);
 hipError_t launch_gnorm_fwd(const GNormArgs& a, hipStream_t s);
 hipError_t launch_gnorm_bwd(const GNormArgs& a, hipStream_t s);
 
+struct LNormArgs {
+    int64_t rows;
+    int C;                   // channels, a multiple of 8
+    float inv;               // 1 / C
+    float eps;
+    const bf16_t* x;
+    int64_t sx;              // row stride (elements)
+    const float *w, *b;      // b: null for none
+    bf16_t* y;
+    const bf16_t* dy;
+    bf16_t* dx;
+    float *dw, *db;          // db: null for none
+    float* part;             // [lnorm_part_rows][2][C]
+};
+constexpr int kMaxChannels = 32768;   // of a row that the widest workgroup holds
+int64_t lnorm_part_rows(int64_t rows, int C);
+hipError_t launch_lnorm(const LNormArgs& a, bool bwd, hipStream_t s);
+
 }  // namespace kda

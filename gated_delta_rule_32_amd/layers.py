@@ -1,7 +1,7 @@
 """Python binding of libkda's linear-attention layer operators: linear
 attention with a constant decay per head (training forward and backward,
 decode and prefill), the query/key norm with rotary rotation in front of it,
-and the gated norm of the heads' outputs behind it.
+the gated norm of the heads' outputs behind it, and the layer norm of token rows.
 
 Argument marshalling only, as in the package itself: the low-level functions
 carry the C names (include/libkda.h), the others take and return tensors.
@@ -52,6 +52,12 @@ class KdaGNormProblem(ctypes.Structure):
     ]
 
 
+class KdaLNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+    ]
+
+
 def _declare(name, problem, *args):
     f = getattr(_lib, name)
     f.restype = ctypes.c_int
@@ -69,11 +75,15 @@ _declare("kda_qknorm_bwd", KdaQkNormProblem, *[_vp] * 14, _size, _vp)
 _declare("kda_gnorm_fwd", KdaGNormProblem, *[_vp] * 5)
 _declare("kda_gnorm_bwd_workspace_bytes", KdaGNormProblem, ctypes.POINTER(_size))
 _declare("kda_gnorm_bwd", KdaGNormProblem, *[_vp] * 8, _size, _vp)
+_declare("kda_lnorm_fwd", KdaLNormProblem, *[_vp] * 5)
+_declare("kda_lnorm_bwd_workspace_bytes", KdaLNormProblem, ctypes.POINTER(_size))
+_declare("kda_lnorm_bwd", KdaLNormProblem, *[_vp] * 7, _size, _vp)
 
 EXPORTED = ("kda_decay_fwd_workspace_bytes", "kda_decay_bwd_workspace_bytes", "kda_decay_infer_workspace_bytes",
             "kda_decay_fwd", "kda_decay_bwd", "kda_decay_infer", "kda_qknorm_fwd",
             "kda_qknorm_bwd_workspace_bytes", "kda_qknorm_bwd", "kda_gnorm_fwd",
-            "kda_gnorm_bwd_workspace_bytes", "kda_gnorm_bwd")
+            "kda_gnorm_bwd_workspace_bytes", "kda_gnorm_bwd", "kda_lnorm_fwd", "kda_lnorm_bwd_workspace_bytes",
+            "kda_lnorm_bwd")
 
 
 # ---------------------------------------------------------------------------
@@ -103,6 +113,10 @@ def kda_qknorm_bwd_workspace_bytes(p: KdaQkNormProblem) -> int:
 
 def kda_gnorm_bwd_workspace_bytes(p: KdaGNormProblem) -> int:
     return _bytes("kda_gnorm_bwd_workspace_bytes", p)
+
+
+def kda_lnorm_bwd_workspace_bytes(p: KdaLNormProblem) -> int:
+    return _bytes("kda_lnorm_bwd_workspace_bytes", p)
 
 
 def _ws(t: Optional[torch.Tensor]):
@@ -169,6 +183,18 @@ def kda_gnorm_bwd(p: KdaGNormProblem, x, gate, weight, dy, dx, dgate, dweight, w
     """C kda_gnorm_bwd on torch tensors."""
     _call(_lib.kda_gnorm_bwd, stream, x, _byref(p), _ptr(x), _ptr(gate), _ptr(weight), _ptr(dy), _ptr(dx),
           _ptr(dgate), _ptr(dweight), *_ws(workspace))
+
+
+def kda_lnorm_fwd(p: KdaLNormProblem, x, weight, bias, y, stream: Optional[int] = None) -> None:
+    """C kda_lnorm_fwd on torch tensors."""
+    _call(_lib.kda_lnorm_fwd, stream, x, _byref(p), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y))
+
+
+def kda_lnorm_bwd(p: KdaLNormProblem, x, weight, dy, dx, dweight, dbias, workspace: torch.Tensor,
+                  stream: Optional[int] = None) -> None:
+    """C kda_lnorm_bwd on torch tensors."""
+    _call(_lib.kda_lnorm_bwd, stream, x, _byref(p), _ptr(x), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dweight),
+          _ptr(dbias), *_ws(workspace))
 
 
 # ---------------------------------------------------------------------------
@@ -475,4 +501,61 @@ def gated_norm_backward(dy, x, gate, weight, *, eps: float = 1e-6, activation: s
             _dense(name, t, dtype, shape, dev)
     ws = _workspace(kda_gnorm_bwd_workspace_bytes(p), workspace, dev)
     kda_gnorm_bwd(p, x, gate, weight, dy, *out, ws)
+    return tuple(out)
+
+
+# ---------------------------------------------------------------------------
+# layer norm of token rows
+# ---------------------------------------------------------------------------
+def _lnorm_problem(x, weight, eps) -> KdaLNormProblem:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is _BF and x.dim() >= 1 and x.numel() > 0):
+        _require(isinstance(x, torch.Tensor) and x.dtype is _BF, "x must be a bfloat16 tensor")
+        _require(x.dim() >= 1 and x.numel() > 0, "x must be [..., C] and not empty")
+        _require(False, f"tensors must be on a GPU, got {x.device}")
+    C = x.shape[-1]
+    _dense("weight", weight, _F32, (C,), x.device)
+    rows = x.numel() // C
+    stride = C
+    if not x.is_contiguous():
+        _require(x.stride(-1) == 1 or C == 1, "x must have dense channels")
+        # rows a fixed distance apart, whatever the leading dimensions
+        at = [(n, st) for n, st in zip(x.shape[:-1], x.stride()[:-1]) if n > 1]
+        if at:
+            stride = at[-1][1]
+            _require(stride >= C, "x's rows must not overlap")
+            _require(all(a[1] == b[0] * b[1] for a, b in zip(at, at[1:])), "x's rows must be a fixed distance apart")
+    return KdaLNormProblem(rows, C, float(eps), stride)
+
+
+def layer_norm_forward(x, weight, bias=None, *, eps: float = 1e-5, out: Optional[torch.Tensor] = None):
+    """weight * (x - mean) / sqrt(mean((x - mean)^2) + eps) + bias over the last
+    dimension.  x: BF16 [..., C], C a multiple of 8 up to 32768, dense or a slice of
+    wider rows; weight, bias: FP32 [C] (bias None: none)."""
+    p = _lnorm_problem(x, weight, eps)
+    if bias is not None:
+        _dense("bias", bias, _F32, weight.shape, x.device)
+    if out is None:
+        out = _new(x)
+    else:
+        _dense("out", out, _BF, x.shape, x.device)
+    kda_lnorm_fwd(p, x, weight, bias, out)
+    return out
+
+
+def layer_norm_backward(dy, x, weight, *, eps: float = 1e-5, out: Optional[Sequence[torch.Tensor]] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Gradients (dx, dweight, dbias) from layer_norm_forward's adjoint and inputs
+    (none depends on the bias)."""
+    p = _lnorm_problem(x, weight, eps)
+    dev = x.device
+    _dense("dy", dy, _BF, x.shape, dev)
+    if out is None:
+        out = (_new(x), _new(weight), _new(weight))
+    else:
+        _require(len(out) == 3, "out must hold three tensors")
+        for name, t, dtype, shape in zip(("dx", "dweight", "dbias"), out, (_BF, _F32, _F32),
+                                         (x.shape, weight.shape, weight.shape)):
+            _dense(name, t, dtype, shape, dev)
+    ws = _workspace(kda_lnorm_bwd_workspace_bytes(p), workspace, dev)
+    kda_lnorm_bwd(p, x, weight, dy, *out, ws)
     return tuple(out)

@@ -489,6 +489,114 @@ kda_status kda_gnorm_bwd(const kda_gnorm_problem* p, const void* x, const void* 
                          const void* dy, void* dx, void* dgate, float* dweight, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated delta rule with one decay per value head and token.  For every
+ * sequence and value head h, with the q/k head h / (Hv/Hqk), an FP32
+ * value-first state S[v][k] starts at initial_state and, token by token,
+ *     S <- exp(g) S;   S <- S + beta (v - S k) k^T;   o = scale S q .
+ * With use_qk_l2norm q and k are taken at unit length, x / sqrt(|x|^2 + 1e-6).
+ * g, beta BF16 [B][T][Hv]: g is the decay's logarithm and must be <= 0 (minus
+ * infinity forgets every earlier token; below -11356 counts as that), beta as it is
+ * applied.  Neither is checked.  q, k, v may be slices of wider token rows.
+ * The rules of the operators above hold here too: finite inputs are expected (a NaN or an infinity in a
+ * token's row may reach every output of its sequence and head from its block of 64
+ * tokens on, in the backward all of them), all sums and the states are FP32.
+ * A key's length is the caller's: with beta |k|^2 above 2 the rule itself grows without
+ * bound.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t B, T, Hqk, Hv, N;        /* as in kda_problem */
+    const int64_t* cu_seqlens;       /* device INT64 [N+1], or NULL for fixed layout */
+    const int64_t* cu_seqlens_host;  /* host mirror, NULL iff cu_seqlens is NULL */
+    float scale;                     /* 0 selects 1/sqrt(128); else finite and positive */
+    int32_t use_qk_l2norm;           /* 0 or 1 */
+    int32_t segment;                 /* tokens per segment when the sequences are split to fill the
+                                        card: 0 automatic, else a multiple of 64 (for testing) */
+    int64_t q_stride, k_stride, v_stride;  /* token strides in elements; 0: dense */
+} kda_delta_problem;
+
+/* Workspace bytes (0 when none is needed; the workspace may then be NULL). */
+kda_status kda_delta_fwd_workspace_bytes(const kda_delta_problem* p, size_t* bytes);
+
+/* Training forward.  q, k BF16 [B][T][Hqk][128], v, o BF16 [B][T][Hv][128],
+ * states FP32 [N][Hv][128][128].  initial_state NULL starts from zero;
+ * final_state may be NULL.  Nothing is saved for the backward, which reads
+ * the inputs again. */
+kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
+                         const void* beta, const float* initial_state, void* o, float* final_state,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode (sequences of up to 8 tokens, token by token) and prefill (longer
+ * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated
+ * in place.  One call may hold both: each sequence runs by its own length, and
+ * one of up to 8 tokens gives the same bits whatever else is in the call.
+ * Sequence n reads and writes slot state_indices[n] (slot n when NULL); other
+ * slots are not touched.  The indices must be distinct and in range, checked on
+ * the host mirror (given iff state_indices is).  A slot that the device copy
+ * places outside the pool (a replayed graph's inactive sequence, say -1) is
+ * skipped, and its rows of o are left as they were.
+ * Drafted tokens (num_spec_tokens = S > 0): every sequence has exactly 1+S
+ * tokens and state_indices holds 1+S distinct slots per sequence ([N][1+S]).
+ * The state starts from slot state_indices[n][a-1], a = num_accepted_tokens[n]
+ * (device) clamped to [1, 1+S] (1 when NULL), and the state after token s goes to
+ * slot state_indices[n][s]; one that the device copy places outside the pool is not
+ * stored.  Token by token, whatever S is.  kda_verify gives num_accepted_tokens. */
+kda_status kda_delta_infer_workspace_bytes(const kda_delta_problem* p, int32_t num_spec_tokens, size_t* bytes);
+kda_status kda_delta_infer(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
+                           const void* beta, float* state_pool, int64_t pool_slots, const int32_t* state_indices,
+                           const int32_t* state_indices_host, int32_t num_spec_tokens,
+                           const int32_t* num_accepted_tokens, void* o, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Verification of drafted tokens, by which a call that follows the drafts goes on
+ * (num_accepted_tokens of kda_infer and kda_delta_infer).  Sequence n has up to S
+ * drafts x_0, x_1, ... (draft_tokens INT32 [N][S]; draft_lens INT32 [N], clamped to
+ * [0, S], or NULL for S each).  Row i of target_probs (FP32, rows [N][1+S] of V
+ * values) holds the target's probabilities p_i of the token at draft i's place, row
+ * len those of the token behind the last draft; row i of draft_probs (rows [N][S]) those
+ * that draft i was drawn from, q_i (NULL: drafts that are certain, q_i = 1 at x_i and 0
+ * elsewhere).  Draft i stands while every draft before it does and
+ *     uniform[n][i] q_i(x_i) < p_i(x_i)
+ * (a draft outside [0, V) never does).  With j drafts standing, one token is drawn
+ * from the positive part of p_j - q_j (from p_j when j is len, or where that part is
+ * zero throughout): the first index with a weight whose running sum is above
+ * uniform[n][S] (taken as 0 when negative or NaN) times the total, or the last index with a
+ * weight when none is.  tokens (INT32 [N][1+S]) becomes x_0 .. x_{j-1}, the drawn
+ * token (-1 when no probability is positive), then -1; num_accepted (INT32 [N])
+ * becomes 1 + j.  Comparisons and sums are formed in 64 bits; a NaN counts as 0.  Rows may be of any
+ * alignment to 4 bytes, `*_stride` elements apart (0: V).  Only row j is read whole.
+ * May be captured into a graph at once.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t N, S, V;
+    int64_t target_stride, draft_stride;
+} kda_verify_problem;
+
+kda_status kda_verify_workspace_bytes(const kda_verify_problem* p, size_t* bytes);
+kda_status kda_verify(const kda_verify_problem* p, const int32_t* draft_tokens, const int32_t* draft_lens,
+                      const float* target_probs, const float* draft_probs, const float* uniform, int32_t* tokens,
+                      int32_t* num_accepted, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm of token rows:  y = weight (x - m) / sqrt(mean((x - m)^2) + eps) + bias
+ * with m = mean(x).  x, y, dy, dx BF16 [rows][C], C a multiple of 8 up to 32768;
+ * weight, bias FP32 [C], bias and dbias may be NULL.  x may be a slice of wider rows,
+ * x_stride elements apart (0: C; a multiple of 8).  The backward takes the forward's
+ * x; dweight and dbias sum over all rows in a fixed order.  A row's values may be up
+ * to about 1e17 (their squares are summed in FP32). */
+typedef struct {
+    int64_t rows;
+    int32_t C;
+    float eps;               /* as in kda_qknorm_problem */
+    int64_t x_stride;
+} kda_lnorm_problem;
+
+kda_status kda_lnorm_fwd(const kda_lnorm_problem* p, const void* x, const float* weight, const float* bias, void* y,
+                         void* stream);
+kda_status kda_lnorm_bwd_workspace_bytes(const kda_lnorm_problem* p, size_t* bytes);
+kda_status kda_lnorm_bwd(const kda_lnorm_problem* p, const void* x, const float* weight, const void* dy, void* dx,
+                         float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,336 @@
+"""GPU parity of the gated delta rule (kda_delta_*) against the FP64 recurrence:
+training forward, prefill, decode and drafted tokens on a state pool, at the lengths, head
+layouts, strides and gates where the chunked kernels can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+from tests import delta_util as du
+from tests import layer_util as lu
+from tests.delta_util import Inp
+
+pytestmark = pytest.mark.gpu
+
+CASES = {  # lengths, packed, Hqk, Hv, unit, gates
+    "one_token": ([1], False, 1, 1, True, "layer"),
+    "batch_of_one_token": ([1] * 5, False, 2, 2, True, "mixed"),
+    "chunk_edges": ([1, 15, 16, 17, 31, 32, 33, 63, 64, 65], True, 1, 2, True, "mixed"),
+    "block_edges": ([127, 128, 129, 97], True, 2, 2, True, "layer"),
+    "grouped": ([100] * 2, False, 2, 8, True, "layer"),
+    "grouped_ragged": ([70, 3, 200], True, 1, 3, False, "mixed"),
+    "odd_heads": ([90, 41], True, 5, 5, False, "strong"),
+    "no_decay": ([150, 33], True, 1, 2, True, "none"),
+    "long": ([1100], False, 2, 2, True, "layer"),
+    "many_tasks": ([40] * 11, False, 12, 12, True, "layer"),          # eight waves a workgroup
+    "more_tasks": ([40] * 10, False, 16, 32, True, "mixed"),          # four waves a workgroup
+}
+
+
+def call_forward(inp, scale=None, wrap=lambda x: x, **more):
+    import gated_delta_rule_32_amd as kda
+    q, k, v = (wrap(inp.dev(x)) for x in (inp.q, inp.k, inp.v))
+    r = kda.gated_delta_rule_training_forward(q, k, v, inp.dev(inp.g), inp.dev(inp.beta), inp.dev(inp.s0), inp.dev(inp.cu),
+                                              scale, use_qk_l2norm=inp.unit, cu_seqlens_cpu=inp.cu, **more)
+    torch.cuda.synchronize()
+    return r
+
+
+def check_forward(inp, got, scale=du.SCALE):
+    o, final, (wo, wfinal), _ = inp.reference(scale)
+    du.check_o("o", got[0], o, wo)
+    du.check_state("final_state", got[1], final, wfinal)
+
+
+@pytest.mark.parametrize("case", list(CASES))
+def test_forward(case):
+    lengths, packed, Hqk, Hv, unit, gates = CASES[case]
+    print(f"[delta] forward {case}", flush=True)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=len(case), unit=unit, gates=gates)
+    check_forward(inp, call_forward(inp))
+
+
+def test_forward_without_initial_state():
+    inp = Inp([5, 150, 64], True, 1, 2, seed=3, state=False)
+    check_forward(inp, call_forward(inp))
+
+
+def test_forward_custom_scale():
+    inp = Inp([80], False, 1, 1, seed=5)
+    check_forward(inp, call_forward(inp, scale=0.25), scale=0.25)
+
+
+def wide(x):
+    """A slice of wider token rows, the rest of which is NaN."""
+    B, T, H, _ = x.shape
+    w = torch.full((B, T, H + 3, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w[:, :, 1:H + 1] = x
+    return w[:, :, 1:H + 1]
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_forward_of_slices(packed):
+    inp = Inp([77, 130] if packed else [77, 77], packed, 2, 4, seed=6)
+    got = call_forward(inp, wrap=wide)
+    want = call_forward(inp)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_forward(inp, got)
+
+
+def test_sequences_do_not_see_each_other():
+    """A packed sequence gives the bits of a call of its own, whatever stands beside
+    it; NaN in the others stay there."""
+    inp = Inp([70, 33, 100], True, 2, 2, seed=7, gates="mixed")
+    a, b = 70, 103
+    alone = Inp([33], False, 2, 2, unit=True)
+    alone.q, alone.k, alone.v, alone.g, alone.beta = (x[:, a:b].contiguous() for x in (inp.q, inp.k, inp.v, inp.g, inp.beta))
+    alone.s0 = inp.s0[1:2].clone()
+    want = call_forward(alone)
+    for x in (inp.q, inp.k, inp.v, inp.g, inp.beta):
+        x[:, :a] = float("nan")
+        x[:, b:] = float("nan")
+    got = call_forward(inp)
+    assert torch.equal(got[0][:, a:b], want[0])
+    assert torch.equal(got[1][1], want[1][0])
+
+
+def test_zero_rows():
+    """Keys and queries of zeros (padding) at unit length stay zeros."""
+    inp = Inp([70], False, 1, 1, seed=8)
+    inp.k[:, 20:50] = 0
+    inp.q[:, 10:40] = 0
+    got = call_forward(inp)
+    check_forward(inp, got)
+    assert not got[0][:, 10:40].any()
+
+
+def test_equal_keys():
+    """The same key over and over, beta 1, no decay: every token replaces what the last one
+    wrote, and the chunk's matrix is all ones."""
+    inp = Inp([100], False, 1, 2, seed=9, gates="none")
+    inp.k[:] = inp.k[:, :1]
+    inp.beta.fill_(1.0)
+    check_forward(inp, call_forward(inp))
+
+
+# ---------------------------------------------------------------------------
+# state pool
+# ---------------------------------------------------------------------------
+def pool_call(inp, pool, slots, accepted=None, output=None, dev_slots=None, **more):
+    import gated_delta_rule_32_amd as kda
+    host = None if slots is None else torch.tensor(slots, dtype=torch.int32)
+    dev = host.cuda() if dev_slots is None and host is not None else dev_slots
+    spec = {} if accepted is None else dict(num_spec_tokens=host.shape[1] - 1, num_accepted_tokens=accepted)
+    out, same = kda.gated_delta_rule(inp.dev(inp.q), inp.dev(inp.k), inp.dev(inp.v), inp.dev(inp.g), inp.dev(inp.beta), pool,
+                                     cu_seqlens=inp.dev(inp.cu), cu_seqlens_cpu=inp.cu, ssm_state_indices=dev,
+                                     ssm_state_indices_cpu=host, output=output, use_qk_l2norm=inp.unit, **spec, **more)
+    torch.cuda.synchronize()
+    assert same is pool
+    return out
+
+
+BATCHES = {  # lengths, packed, Hqk, Hv
+    "decode": ([1] * 7, False, 2, 4),
+    "decode_packed": ([1] * 5, True, 1, 1),
+    "few_tokens": ([3] * 4, False, 2, 2),
+    "prefill": ([70, 70], False, 2, 6),
+    "prefill_packed": ([129, 9, 64], True, 3, 3),
+    "mixed": ([8, 9, 1, 300, 5, 2], True, 2, 4),
+    "last_is_long": ([4, 3, 2, 64], True, 1, 3),
+}
+
+
+@pytest.mark.parametrize("case", list(BATCHES))
+def test_pool(case):
+    lengths, packed, Hqk, Hv = BATCHES[case]
+    print(f"[delta] pool {case}", flush=True)
+    n = len(lengths)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=31 + len(case), unit=case != "decode", gates="mixed")
+    slots = torch.randperm(n + 3, generator=torch.Generator().manual_seed(4))[:n].tolist()
+    pool0 = torch.randn((n + 3, Hv, 128, 128), generator=torch.Generator().manual_seed(5))
+    inp.s0 = pool0[slots]
+    pool = pool0.cuda()
+    out = pool_call(inp, pool, slots)
+    o, final, (wo, wfinal), _ = inp.reference()
+    du.check_o("o", out, o, wo)
+    du.check_state("pool", pool[slots], final, wfinal)
+    rest = [i for i in range(n + 3) if i not in slots]
+    assert torch.equal(pool[rest].cpu(), pool0[rest])
+    for i, length in enumerate(lengths):     # token by token: the bits of a call of its own
+        if length > 8 or not packed:
+            continue
+        at = int(inp.cu[i])
+        one = Inp([length], False, Hqk, Hv, unit=inp.unit)
+        one.q, one.k, one.v, one.g, one.beta = (x[:, at:at + length].contiguous()
+                                                for x in (inp.q, inp.k, inp.v, inp.g, inp.beta))
+        own = pool0.cuda()
+        assert torch.equal(pool_call(one, own, [slots[i]])[0], out[0, at:at + length])
+        assert torch.equal(own[slots[i]], pool[slots[i]])
+
+
+def test_pool_without_indices_and_without_a_pool():
+    import gated_delta_rule_32_amd as kda
+    for T in (1, 40):
+        inp = Inp([T] * 2, False, 1, 2, seed=9, state=False)
+        o, final, (wo, wfinal), _ = inp.reference()
+        pool = torch.zeros((3, 2, 128, 128), device="cuda")
+        pool[2] = 5.0
+        du.check_o("o", pool_call(inp, pool, None), o, wo)
+        du.check_state("pool", pool[:2], final, wfinal)
+        assert (pool[2] == 5.0).all()
+        out, new = kda.gated_delta_rule(*(inp.dev(x) for x in (inp.q, inp.k, inp.v, inp.g, inp.beta)), use_qk_l2norm=True)
+        torch.cuda.synchronize()
+        du.check_o("o", out, o, wo)
+        du.check_state("new pool", new, final, wfinal)
+
+
+def test_pieces_of_a_prompt():
+    """A prompt in pieces, by chunks and token by token, ends where the whole one does."""
+    inp = Inp([200], False, 1, 2, seed=10)
+    pool = inp.s0.cuda()
+    outs, at = [], 0
+    for length in (64, 7, 1, 100, 8, 20):
+        part = Inp([length], False, 1, 2)
+        part.q, part.k, part.v, part.g, part.beta = (x[:, at:at + length].contiguous()
+                                                     for x in (inp.q, inp.k, inp.v, inp.g, inp.beta))
+        outs.append(pool_call(part, pool, [0]))
+        at += length
+    o, final, (wo, wfinal), _ = inp.reference()
+    du.check_o("o", torch.cat(outs, 1), o, wo)
+    du.check_state("pool", pool, final, wfinal)
+
+
+@pytest.mark.parametrize("S,packed", [(1, False), (4, True), (10, False)])
+def test_drafted_tokens(S, packed):
+    n, Hqk, Hv = 5, 1, 3
+    inp = Inp([1 + S] * n, packed, Hqk, Hv, seed=11 + S, gates="mixed")
+    g = torch.Generator().manual_seed(S)
+    slots = torch.randperm(n * (1 + S) + 4, generator=g)[:n * (1 + S)].reshape(n, 1 + S)
+    pool0 = torch.randn((n * (1 + S) + 4, Hv, 128, 128), generator=g)
+    accepted = torch.tensor([1, 1 + S, 0, 99, (S + 2) // 2], dtype=torch.int32)   # 0 and 99 are clamped
+    first = slots[torch.arange(n), accepted.clamp(1, 1 + S).long() - 1]
+    inp.s0 = pool0[first]
+    pool = pool0.cuda()
+    out = pool_call(inp, pool, slots.tolist(), accepted.cuda())
+    o, _, (wo, wfinal), states = inp.reference()
+    du.check_o("o", out, o, wo)
+    for i in range(n):
+        for t in range(1 + S):
+            du.check_state(f"state {i} {t}", pool[slots[i, t]][None], states[i, t][None], wfinal[i:i + 1] + 1.0 * np.abs(states[i, t]).max())
+    rest = [i for i in range(pool0.shape[0]) if i not in slots.reshape(-1).tolist()]
+    assert torch.equal(pool[rest].cpu(), pool0[rest])
+    # without numbers of accepted tokens: from the first slot
+    inp.s0 = pool0[slots[:, 0]]
+    import gated_delta_rule_32_amd as kda
+    pool = pool0.cuda()
+    host = slots.to(torch.int32).contiguous()
+    out, _ = kda.gated_delta_rule(*(inp.dev(x) for x in (inp.q, inp.k, inp.v, inp.g, inp.beta)), pool,
+                                  cu_seqlens=inp.dev(inp.cu), cu_seqlens_cpu=inp.cu, ssm_state_indices=host.cuda(),
+                                  ssm_state_indices_cpu=host, num_spec_tokens=S, use_qk_l2norm=True)
+    torch.cuda.synchronize()
+    o, _, (wo, _), _ = inp.reference()
+    du.check_o("o", out, o, wo)
+
+
+@pytest.mark.parametrize("T", [1, 6, 100])
+def test_slots_outside_the_pool(T):
+    """A slot that the device copy places outside the pool is skipped, its rows left as
+    they were."""
+    inp = Inp([T] * 3, False, 1, 2, seed=12)
+    pool0 = torch.randn((3, 2, 128, 128))
+    pool = pool0.cuda()
+    dev = torch.tensor([2, -1, 3], dtype=torch.int32, device="cuda")
+    out = torch.full((3, T, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    pool_call(inp, pool, [2, 0, 1], output=out, dev_slots=dev)
+    assert torch.equal(pool[:2].cpu(), pool0[:2])
+    assert not torch.equal(pool[2].cpu(), pool0[2])
+    assert (out[1:] == 7.0).all() and not (out[0] == 7.0).all(-1).any()
+
+
+def test_drafted_slots_outside_the_pool():
+    """A token's slot outside the pool is not stored; a sequence whose first slot is outside is
+    skipped."""
+    inp = Inp([3, 3], False, 1, 1, seed=13)
+    pool0 = torch.randn((8, 1, 128, 128))
+    inp.s0 = pool0[[0, 3]]
+    dev = torch.tensor([[0, -1, 2], [8, 4, 5]], dtype=torch.int32, device="cuda")
+    out = torch.full((2, 3, 1, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    pool = pool0.cuda()
+    ones = torch.ones(2, dtype=torch.int32, device="cuda")
+    pool_call(inp, pool, [[0, 1, 2], [3, 4, 5]], ones, output=out, dev_slots=dev)
+    _, _, (_, wfinal), states = inp.reference()
+    for t, slot in ((0, 0), (2, 2)):
+        du.check_state("state", pool[slot:slot + 1], states[0, t][None], wfinal[:1] + np.abs(states[0, t]).max())
+    keep = [1, 3, 4, 5, 6, 7]
+    assert torch.equal(pool[keep].cpu(), pool0[keep])
+    assert (out[1] == 7.0).all()
+
+
+def test_weak_decays_over_many_tokens():
+    """2^13 tokens one by one at a decay of 2^-15 a token: the state keeps to the exact
+    powers (a decay rounded to FP32 would drift by 2^-24 a token, one way)."""
+    import gated_delta_rule_32_amd as kda
+    T, steps = 8, 1024
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    g = torch.full((1, T, 1), -2.0 ** -15, dtype=torch.bfloat16, device="cuda")
+    s0 = torch.rand((1, 1, 128, 128), generator=torch.Generator().manual_seed(1)) + 1.0
+    pool = s0.cuda()
+    for _ in range(steps):
+        kda.gated_delta_rule(z(1, T, 1, 128), z(1, T, 1, 128), z(1, T, 1, 128), g, z(1, T, 1), pool)
+    torch.cuda.synchronize()
+    want = s0.double().numpy() * np.exp(-2.0 ** -15 * T * steps)
+    # one rounding a token, of either sign: 2^-24 sqrt(tokens) = 2^-17.5, and as much again
+    assert (np.abs(lu.f64(pool) - want) / want).max() <= 2.0 ** -16.5
+
+
+# ---------------------------------------------------------------------------
+# streams and graphs
+# ---------------------------------------------------------------------------
+def test_forward_on_another_stream():
+    inp = Inp([200, 31], True, 1, 2, seed=13)
+    want = call_forward(inp)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = call_forward(inp)
+    s.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_captured_decode_and_prefill():
+    """A decode and a prefill call in one graph, replayed with eager work between: every
+    replay gives the eager bits; a slot of -1 put in later is skipped."""
+    import gated_delta_rule_32_amd as kda
+    one, many = Inp([1] * 3, False, 1, 2, seed=14), Inp([70] * 2, False, 1, 2, seed=15)
+    pool0 = torch.randn((6, 2, 128, 128), generator=torch.Generator().manual_seed(3))
+    pool = pool0.cuda()
+    slots = [torch.tensor(x, dtype=torch.int32) for x in ([4, 0, 2], [1, 3])]
+    dev = [x.cuda() for x in slots]
+    args = [[i.dev(x) for x in (i.q, i.k, i.v, i.g, i.beta)] for i in (one, many)]
+    outs = [torch.empty_like(a[2]) for a in args]
+    p = kda.KdaDeltaProblem(2, 70, 1, 2, 2)
+    p.use_qk_l2norm = 1
+    ws = torch.empty(kda.kda_delta_infer_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+
+    def run(pool, outs):
+        for a, o, d, h in zip(args, outs, dev, slots):
+            kda.gated_delta_rule(*a, pool, ssm_state_indices=d, ssm_state_indices_cpu=h, output=o, use_qk_l2norm=True,
+                                 workspace=ws)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(pool, outs)
+    eager, eager_outs = pool0.cuda(), [torch.empty_like(o) for o in outs]
+    pool.copy_(pool0)
+    for i in range(4):
+        if i == 2:
+            dev[0][1] = -1
+        for o in outs + eager_outs:
+            o.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        run(eager, eager_outs)
+        torch.cuda.synchronize()
+        assert torch.equal(pool, eager)
+        for a, b in zip(outs, eager_outs):
+            assert torch.equal(a, b)
