@@ -547,7 +547,8 @@ EXPORTED += _layers.EXPORTED
 # The gated delta rule, and the verification of drafted tokens
 from . import delta as _delta  # noqa: E402
 from .delta import (  # noqa: E402,F401
-    GatedDeltaRuleTrainingContext, KdaDeltaProblem, gated_delta_rule, gated_delta_rule_training_forward, kda_delta_fwd,
+    GatedDeltaRuleTrainingContext, KdaDeltaProblem, gated_delta_rule, gated_delta_rule_training_backward,
+    gated_delta_rule_training_forward, kda_delta_bwd, kda_delta_bwd_workspace_bytes, kda_delta_fwd,
     kda_delta_fwd_workspace_bytes, kda_delta_infer, kda_delta_infer_workspace_bytes)
 from . import verify as _verify  # noqa: E402
 from .verify import KdaVerifyProblem, kda_verify, kda_verify_workspace_bytes, verify_drafts  # noqa: E402,F401

@@ -41,6 +41,7 @@ SOURCES = [
     "kda_rownorm.hip",
     "kda_delta_api.cpp",
     "kda_delta.hip",
+    "kda_delta_grad.hip",
     "kda_verify_api.cpp",
     "kda_verify.hip",
     "kda_lnorm.hip",

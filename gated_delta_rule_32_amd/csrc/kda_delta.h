@@ -43,6 +43,24 @@ struct DeltaArgs {
     const bf16_t* d_o;          // [tokens][Hv][128]
 };
 
+// The gradients of a block of tokens from what the two scans left: the state before the
+// block and the adjoint behind it, the rows W of the forward and Y of the backward.
+struct DeltaGradArgs {
+    ItemMap blocks;
+    const bf16_t *q, *k;
+    int64_t sq, sk;
+    int G;
+    int unit;
+    float scale;
+    const float* rec;
+    const bf16_t* d_o;
+    const bf16_t *s_planes, *z_planes;    // [blocks][Hv][2][128 v][128 k]
+    const bf16_t *w_planes, *y_planes;    // [blocks][Hv][2 chunks][2][128 v][32 tokens]
+    void *dq, *dk;                        // [tokens][Hv][128]: BF16, or packed partials
+    int pack;
+    bf16_t *dv, *dg, *dbeta;
+};
+
 // Token-serial form on the state pool.
 struct DeltaTokenArgs {
     ItemMap map;                // no segments
@@ -63,6 +81,8 @@ struct DeltaTokenArgs {
 hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s);
 enum DeltaMode { kDeltaOut = 0, kDeltaRecord = 1 };
 hipError_t launch_delta_scan(const DeltaArgs& a, DeltaMode mode, hipStream_t s);
+hipError_t launch_delta_adjoint(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s);
 hipError_t launch_delta_token(const DeltaTokenArgs& a, hipStream_t s);
 
 struct VerifyArgs {

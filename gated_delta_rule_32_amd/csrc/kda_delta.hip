@@ -16,32 +16,17 @@
 // C serves both, and does not depend on the state: a kernel of its own forms it for all
 // chunks at once.  q and k at unit length enter as they are, with one over their length as
 // a factor of their token.
-#include "kda_delta.h"
-#include "kda_scan.hpp"
+#include "kda_delta.hpp"
 
 namespace kda {
 
 namespace {
-
-constexpr int SC = 32;            // tokens per chunk
-constexpr float NORM_EPS = 1e-6f;
-
-// FP32 as three BF16 pieces of 8 significant bits each.
-__device__ __forceinline__ void split3(f32x4 x, bf16x4& a, bf16x4& b, bf16x4& c) {
-    a = take_high(x);
-    b = take_high(x);
-    c = to_bf4(x);
-}
 
 // G in base 2 is kept finite, so that a difference of two stays a number: e^-inf and
 // 2^-16384 are both 0.
 __device__ __forceinline__ double log2_gate(bf16 g) {
     const double x = (double)(float)g * 1.4426950408889634074;
     return x < -16384.0 ? -16384.0 : x;
-}
-// 2^(Gi - Gj), from the sums' two parts.
-__device__ __forceinline__ float decay2(float hi, float li, float hj, float lj) {
-    return __builtin_amdgcn_exp2f((hi - hj) + (li - lj));
 }
 
 }  // namespace

@@ -69,6 +69,34 @@ RecordWs record_ws(const Delta& d, int64_t blocks, size_t off = 0) {
     return w;
 }
 
+// The backward's workspace: records, planes of the states before and the adjoints behind the
+// blocks, planes of the rows W and Y, and partials of dq and dk where value heads share them.
+struct GradWs {
+    RecordWs r;
+    size_t s = 0, z = 0, w = 0, y = 0, part_q = 0, part_k = 0, total = 0;
+};
+GradWs grad_ws(const Delta& d) {
+    GradWs g;
+    const int64_t blocks = total_blocks(d);
+    g.r = record_ws(d, blocks);
+    size_t off = g.r.total;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    const size_t items = (size_t)blocks * d.s.Hv;
+    g.s = take(items * 2 * kState * 2);
+    g.z = take(items * 2 * kState * 2);
+    g.w = take(items * 2 * kda::DB * D * 2);
+    g.y = take(items * 2 * kda::DB * D * 2);
+    const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
+    g.part_q = take(part);
+    g.part_k = take(part);
+    g.total = off;
+    return g;
+}
+
 // The item maps of a call (whole sequences, and blocks of 64 tokens) and its hold on the
 // device schedule (packed calls).
 kda_status make_maps(const Delta& d, hipStream_t stream, SeqPlan& plan, kda::DeltaArgs& a) {
@@ -190,6 +218,102 @@ kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void*
         if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
         e = kda::launch_delta_scan(a, kda::kDeltaOut, stream);
         if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+        return KDA_OK;
+    });
+}
+
+kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* pp, size_t* bytes) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
+        *bytes = grad_ws(d).total;
+        return KDA_OK;
+    });
+}
+
+kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void* k, const void* v, const void* g,
+                         const void* beta, const float* initial_state, const void* d_o, const float* dfinal_state,
+                         void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dinitial_state, void* workspace,
+                         size_t workspace_bytes, void* stream_) {
+    return guarded([&]() -> kda_status {
+        Delta d;
+        kda_status s = check_delta(pp, d);
+        if (s != KDA_OK) return s;
+        if (!q || !k || !v || !g || !beta || !d_o || !dq || !dk || !dv || !dg || !dbeta)
+            return fail(KDA_ERR_NULL_ARG, "a tensor argument of kda_delta_bwd is NULL");
+        s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {initial_state, "initial_state"}, {d_o, "do"},
+                         {dfinal_state, "dfinal_state"}, {dq, "dq"}, {dk, "dk"}, {dv, "dv"},
+                         {dinitial_state, "dinitial_state"}});
+        if (s != KDA_OK) return s;
+        const GradWs wl = grad_ws(d);
+        if ((s = check_ws(workspace, workspace_bytes, wl.total)) != KDA_OK) return s;
+        const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
+        const size_t tq = (size_t)d.s.tokens * d.s.Hqk * D * 2, tv = (size_t)d.s.tokens * d.s.Hv * D * 2,
+                     tg = (size_t)d.s.tokens * d.s.Hv * 2;
+        std::vector<Span> ins = input_spans(pp, d, q, k, v, g, beta);
+        ins.push_back({initial_state, initial_state ? st : 0, "initial_state"});
+        ins.push_back({d_o, tv, "do"});
+        ins.push_back({dfinal_state, dfinal_state ? st : 0, "dfinal_state"});
+        s = check_overlap({{dq, tq, "dq"}, {dk, tq, "dk"}, {dv, tv, "dv"}, {dg, tg, "dg"}, {dbeta, tg, "dbeta"},
+                           {dinitial_state, dinitial_state ? st : 0, "dinitial_state"},
+                           {workspace, wl.total, "workspace"}}, ins);
+        if (s != KDA_OK) return s;
+        hipStream_t stream = (hipStream_t)stream_;
+        SeqPlan plan;
+        kda::DeltaArgs a{};
+        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
+        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
+        if (d.s.G > 1 && (s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
+        char* ws = (char*)workspace;
+        set_inputs(d, q, k, v, g, beta, a);
+        a.rec = (float*)(ws + wl.r.rec);
+        a.fac = (float*)(ws + wl.r.fac);
+        a.slots = d.s.N;
+        a.d_o = (const kda::bf16_t*)d_o;
+        hipError_t e = kda::launch_delta_prepare(a, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+        a.s_in = initial_state;
+        a.state_planes = (kda::bf16_t*)(ws + wl.s);
+        a.row_planes = (kda::bf16_t*)(ws + wl.w);
+        e = kda::launch_delta_scan(a, kda::kDeltaRecord, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+        a.s_in = dfinal_state;
+        a.s_out = dinitial_state;
+        a.state_planes = (kda::bf16_t*)(ws + wl.z);
+        a.row_planes = (kda::bf16_t*)(ws + wl.y);
+        e = kda::launch_delta_adjoint(a, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta adjoint launch");
+        const bool pack = d.s.G > 1;
+        kda::DeltaGradArgs b{};
+        b.blocks = a.blocks;
+        b.q = a.q;
+        b.k = a.k;
+        b.sq = a.sq;
+        b.sk = a.sk;
+        b.G = a.G;
+        b.unit = a.unit;
+        b.scale = a.scale;
+        b.rec = a.rec;
+        b.d_o = a.d_o;
+        b.s_planes = (const kda::bf16_t*)(ws + wl.s);
+        b.z_planes = (const kda::bf16_t*)(ws + wl.z);
+        b.w_planes = (const kda::bf16_t*)(ws + wl.w);
+        b.y_planes = (const kda::bf16_t*)(ws + wl.y);
+        b.dq = pack ? (void*)(ws + wl.part_q) : dq;
+        b.dk = pack ? (void*)(ws + wl.part_k) : dk;
+        b.pack = pack;
+        b.dv = (kda::bf16_t*)dv;
+        b.dg = (kda::bf16_t*)dg;
+        b.dbeta = (kda::bf16_t*)dbeta;
+        e = kda::launch_delta_grad(b, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta gradient launch");
+        if (pack) {
+            e = kda::launch_decay_group_sum(ws + wl.part_q, ws + wl.part_k, (kda::bf16_t*)dq, (kda::bf16_t*)dk, d.s.tokens,
+                                            d.s.Hqk, d.s.G, stream);
+            if (e != hipSuccess) return hip_fail(e, "group sum launch");
+        }
         return KDA_OK;
     });
 }

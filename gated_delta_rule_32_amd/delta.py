@@ -31,11 +31,14 @@ class KdaDeltaProblem(ctypes.Structure):
 
 _declare("kda_delta_fwd_workspace_bytes", KdaDeltaProblem, ctypes.POINTER(_size))
 _declare("kda_delta_fwd", KdaDeltaProblem, *[_vp] * 9, _size, _vp)
+_declare("kda_delta_bwd_workspace_bytes", KdaDeltaProblem, ctypes.POINTER(_size))
+_declare("kda_delta_bwd", KdaDeltaProblem, *[_vp] * 15, _size, _vp)
 _declare("kda_delta_infer_workspace_bytes", KdaDeltaProblem, ctypes.c_int32, ctypes.POINTER(_size))
 _declare("kda_delta_infer", KdaDeltaProblem, *[_vp] * 6, ctypes.c_int64, *[_vp] * 2, ctypes.c_int32, *[_vp] * 3, _size,
          _vp)
 
-EXPORTED = ("kda_delta_fwd_workspace_bytes", "kda_delta_fwd", "kda_delta_infer_workspace_bytes", "kda_delta_infer")
+EXPORTED = ("kda_delta_fwd_workspace_bytes", "kda_delta_fwd", "kda_delta_bwd_workspace_bytes", "kda_delta_bwd",
+            "kda_delta_infer_workspace_bytes", "kda_delta_infer")
 
 
 def kda_delta_fwd_workspace_bytes(p: KdaDeltaProblem) -> int:
@@ -47,6 +50,18 @@ def kda_delta_fwd(p: KdaDeltaProblem, q, k, v, g, beta, initial_state, o, final_
     """C kda_delta_fwd on torch tensors (no shape checks beyond the library's)."""
     _call(_lib.kda_delta_fwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
           _ptr(initial_state), _ptr(o), _ptr(final_state), *_ws(workspace))
+
+
+def kda_delta_bwd_workspace_bytes(p: KdaDeltaProblem) -> int:
+    return _bytes("kda_delta_bwd_workspace_bytes", p)
+
+
+def kda_delta_bwd(p: KdaDeltaProblem, q, k, v, g, beta, initial_state, d_o, dfinal_state, dq, dk, dv, dg, dbeta,
+                  dinitial_state, workspace: torch.Tensor, stream: Optional[int] = None) -> None:
+    """C kda_delta_bwd on torch tensors."""
+    _call(_lib.kda_delta_bwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+          _ptr(initial_state), _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
+          _ptr(dinitial_state), *_ws(workspace))
 
 
 def kda_delta_infer_workspace_bytes(p: KdaDeltaProblem, num_spec_tokens: int = 0) -> int:
@@ -137,6 +152,34 @@ def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_s
     inputs = (q, k, v, g, beta, initial_state, cu_seqlens, cu_seqlens_cpu)
     versions = tuple(None if t is None else t._version for t in inputs)
     return o, fs, GatedDeltaRuleTrainingContext(p, inputs, versions)
+
+
+def gated_delta_rule_training_backward(context: GatedDeltaRuleTrainingContext, do, dfinal_state=None,
+                                       out: Optional[Sequence[torch.Tensor]] = None,
+                                       workspace: Optional[torch.Tensor] = None):
+    """Gradients (dq, dk, dv, dg, dbeta, dinitial_state) of <do, o> +
+    <dfinal_state, final_state> (dfinal_state None: zero)."""
+    _require(context is not None, "context is required")
+    p, inputs = context.problem, context.inputs
+    now = tuple(None if t is None else t._version for t in inputs)
+    _require(now == context.versions, "an input changed after the forward (tensor version)")
+    q, k, v, g, beta, s0, _, _ = inputs
+    dev = q.device
+    states = (p.N, p.Hv, HEAD_DIM, HEAD_DIM)
+    _dense("do", do, _BF, v.shape, dev)
+    if dfinal_state is not None:
+        _dense("dfinal_state", dfinal_state, _F32, states, dev)
+    if out is None:
+        out = (_new(q), _new(k), _new(v), _new(g), _new(beta), torch.empty(states, dtype=_F32, device=dev))
+    else:
+        _require(len(out) == 6, "out must hold six tensors")
+        for name, t, dtype, shape in zip(("dq", "dk", "dv", "dg", "dbeta", "dinitial_state"), out,
+                                         (_BF, _BF, _BF, _BF, _BF, _F32),
+                                         (q.shape, k.shape, v.shape, g.shape, beta.shape, states)):
+            _dense(name, t, dtype, shape, dev)
+    ws = _workspace(kda_delta_bwd_workspace_bytes(p), workspace, dev)
+    kda_delta_bwd(p, q, k, v, g, beta, s0, do, dfinal_state, *out, ws)
+    return tuple(out)
 
 
 def gated_delta_rule(q, k, v, g, beta, initial_state=None, scale=None, cu_seqlens=None, ssm_state_indices=None,

@@ -526,6 +526,18 @@ kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* 
                          const void* beta, const float* initial_state, void* o, float* final_state,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* Training backward: the gradients of <do, o> + <dfinal_state, S_final> with
+ * respect to the inputs as they were given (with use_qk_l2norm through the
+ * norm).  dfinal_state NULL counts as zero; dinitial_state may be NULL.  dq and dk
+ * sum over the value heads that share a q/k head, in head order; dg and dbeta are BF16
+ * [B][T][Hv].  The workspace holds every block's states: about 200 KiB per 64 tokens and value
+ * head. */
+kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, size_t* bytes);
+kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
+                         const void* beta, const float* initial_state, const void* d_o, const float* dfinal_state,
+                         void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dinitial_state,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Decode (sequences of up to 8 tokens, token by token) and prefill (longer
  * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated
  * in place.  One call may hold both: each sequence runs by its own length, and

@@ -54,44 +54,69 @@ def delta_forward(q, k, v, g, beta, state, lengths, packed, scale, unit):
 
 
 def delta_backward(q, k, v, g, beta, state, do, dfinal, lengths, packed, scale, unit):
-    """(dq, dk, dv, dg, dbeta, dinitial) of <do, o> + <dfinal, final state>, by the
-    adjoint of the recurrence: with Z the state's adjoint,
+    """((dq, dk, dv, dg, dbeta, dinitial), weights, parts) of <do, o> + <dfinal, final
+    state>, by the adjoint of the recurrence: with Z the state's adjoint,
         Z += scale do q^T;  u = Z k;  dbeta = u.w;  dv = beta u;
         dq = scale S^T do;  dk = beta Z^T w - beta X^T u  (X the decayed state before);
-        Z -= beta u k^T;  dg = <Z, X>;  Z <- e^g Z."""
+        Z -= beta u k^T;  dg = <Z, X>;  Z <- e^g Z.
+    `weights` bounds the sizes of what each gradient's sums hold: M of the state's rows as in
+    delta_forward, and for Z's rows NZ <- NZ + scale |do| |q| + |beta u| |k| and MZ <- MZ + scale
+    |do| |q| + |beta| NZ |k|^2, both decaying with Z (of the last, dinitial, per row).  `parts`: for
+    dq and dk the sums over the value heads of their absolute parts."""
     q, k, v, g, beta, state, do, dfinal = map(_f64, (q, k, v, g, beta, state, do, dfinal))
     Hqk = q.shape[2]
     G = v.shape[2] // Hqk
     (q, nq), (k, nk) = _unit(q, unit), _unit(k, unit)
-    dq, dk, dv, dg, dbeta = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v), np.zeros_like(g), np.zeros_like(beta)
-    dinit = np.zeros_like(state)
+    grads = dq, dk, dv, dg, dbeta = [np.zeros_like(x) for x in (q, k, v, g, beta)]
+    weights = wq, wk, wv, wg, wb = [np.zeros_like(x) for x in grads]
+    pq, pk = np.zeros_like(q), np.zeros_like(k)
+    dinit, winit = np.zeros_like(state), np.zeros(state.shape[:3])
     shared = lambda x: x.reshape(Hqk, G, -1).sum(1)  # noqa: E731
     for n, (b, t0, L) in enumerate(_spans(lengths, packed, q.shape[1])):
         S, X = state[n].copy(), []
+        N = M = np.linalg.norm(S, axis=-1)
         for t in range(t0, t0 + L):
-            kt = np.repeat(k[b, t], G, 0)
-            S = np.exp(g[b, t])[:, None, None] * S
-            X.append(S)
-            S = S + (beta[b, t][:, None] * (v[b, t] - np.einsum("hvk,hk->hv", S, kt)))[:, :, None] * kt[:, None, :]
+            kt, a, bt = np.repeat(k[b, t], G, 0), np.exp(g[b, t])[:, None], beta[b, t][:, None]
+            nkt = np.linalg.norm(kt, axis=-1)[:, None]
+            S, N, M = a[..., None] * S, a * N, a * M
+            X.append((S, M))
+            w = v[b, t] - np.einsum("hvk,hk->hv", S, kt)
+            S = S + (bt * w)[:, :, None] * kt[:, None, :]
+            M = M + np.abs(bt) * (np.abs(v[b, t]) + N * nkt) * nkt
+            N = N + np.abs(bt * w) * nkt
         Z = dfinal[n].copy()
+        NZ = MZ = np.linalg.norm(Z, axis=-1)
         for t in reversed(range(t0, t0 + L)):
-            kt, qt, bt, x = np.repeat(k[b, t], G, 0), np.repeat(q[b, t], G, 0), beta[b, t][:, None], X[t - t0]
+            kt, qt, bt, (x, m) = np.repeat(k[b, t], G, 0), np.repeat(q[b, t], G, 0), beta[b, t][:, None], X[t - t0]
+            nkt, nqt = (np.linalg.norm(y, axis=-1)[:, None] for y in (kt, qt))
             w = v[b, t] - np.einsum("hvk,hk->hv", x, kt)
             after = x + (bt * w)[:, :, None] * kt[:, None, :]
-            Z = Z + scale * do[b, t][:, :, None] * qt[:, None, :]
+            d = scale * do[b, t]
+            Z, NZ, MZ = Z + d[:, :, None] * qt[:, None, :], NZ + np.abs(d) * nqt, MZ + np.abs(d) * nqt
             u = np.einsum("hvk,hk->hv", Z, kt)
-            gq = scale * np.einsum("hvk,hv->hk", after, do[b, t])
+            gq = np.einsum("hvk,hv->hk", after, d)
             gk = np.einsum("hvk,hv->hk", Z, bt * w) - np.einsum("hvk,hv->hk", x, bt * u)
             dbeta[b, t], dv[b, t] = (u * w).sum(-1), bt * u
+            mw = np.abs(v[b, t]) + m * nkt               # sizes of w's terms
+            ma = m + np.abs(bt) * mw * nkt               # of the state behind the token
+            cq = (ma * np.abs(d)).sum(-1, keepdims=True)
+            ck = (np.abs(bt) * (MZ * mw + m * MZ * nkt)).sum(-1, keepdims=True)
+            wb[b, t], wv[b, t] = (MZ * nkt * mw).sum(-1), np.abs(bt) * MZ * nkt
             Z = Z - (bt * u)[:, :, None] * kt[:, None, :]
-            dg[b, t] = (Z * x).sum((-1, -2))
-            Z = np.exp(g[b, t])[:, None, None] * Z
+            MZ = MZ + np.abs(bt) * NZ * nkt * nkt
+            NZ = NZ + np.abs(bt * u) * nkt
+            dg[b, t], wg[b, t] = (Z * x).sum((-1, -2)), (MZ * m).sum(-1)
+            a = np.exp(g[b, t])[:, None]
+            Z, NZ, MZ = a[..., None] * Z, a * NZ, a * MZ
             if unit:
-                for d, hat, size in ((gq, qt, np.repeat(nq[b, t], G, 0)), (gk, kt, np.repeat(nk[b, t], G, 0))):
-                    d[:] = (d - hat * (d * hat).sum(-1, keepdims=True)) / size
+                sq, sk = np.repeat(nq[b, t], G, 0), np.repeat(nk[b, t], G, 0)
+                gq, gk = ((y - hat * (y * hat).sum(-1, keepdims=True)) / size for y, hat, size in ((gq, qt, sq), (gk, kt, sk)))
+                cq, ck = cq / sq, ck / sk
             dq[b, t], dk[b, t] = shared(gq), shared(gk)
-        dinit[n] = Z
-    return dq, dk, dv, dg, dbeta, dinit
+            wq[b, t], wk[b, t] = shared(cq), shared(ck)
+            pq[b, t], pk[b, t] = shared(np.abs(gq)), shared(np.abs(gk))
+        dinit[n], winit[n] = Z, MZ
+    return (*grads, dinit), (*weights, winit), (pq, pk)
 
 
 def verify(drafts, lens, target, draft, uniform):

@@ -13,6 +13,11 @@ rounding is off.
     products and written rows in two (2^-17 each): 2^-14 of the weights, and its own rounding, u |o|.
   - The norm of a BF16 result's error: one rounding's errors are spread evenly, u/sqrt(3) of the value in
     the mean square at most; 3/4 u leaves 30% for the parts above.
+  - A gradient's sums take the states before and behind a block as two BF16 pieces (off by
+    2^-16), the rows W and Y and the block's matrices as two (2^-17): four products of such
+    pairs add up in dk, and 2^-13 of the weights covers them.  dq and dk of shared heads are
+    sums of partials that are rounded to 10 bits: 2^-10 of the partials' sizes.  dinitial_state is as exact
+    as a final state.
 """
 from __future__ import annotations
 
@@ -27,6 +32,7 @@ from tests import layer_util as lu
 SCALE = 1.0 / math.sqrt(128.0)
 STATE = 2.0 ** -18
 PARTS = 2.0 ** -14
+GRADS = 2.0 ** -13
 
 
 class Inp:
@@ -94,3 +100,18 @@ def check_o(name, got, ref, weights):
 def check_state(name, got, ref, weights):
     """`weights`: of the state's rows."""
     lu.check_bars(name, got, ref, STATE * weights[..., None] * np.ones_like(ref))
+
+
+def check_gradients(inp, got, scale=SCALE):
+    """got: dq, dk, dv, dg, dbeta, dinitial_state."""
+    refs, weights, parts = inp.gradients(scale)
+    for i, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        x, ref = lu.f64(got[i]), refs[i]
+        extra = 2.0 ** -10 * parts[i] if i < 2 and inp.Hv > inp.Hqk else 0.0
+        lu.check_bars(name, torch.from_numpy(x), ref, lu.U * np.abs(ref) + GRADS * weights[i] + extra)
+        rel = np.linalg.norm(x - ref) / max(np.linalg.norm(ref), 1e-30)
+        # (a few values' norm is no mean square: two tokens' gates are held to their own roundings)
+        print(f"{name:14s} rel {rel:.2e} (bar {0.75 * lu.U:.2e})", flush=True)
+        if ref.size >= 64 and np.linalg.norm(ref) > 2.0 ** -10 * np.linalg.norm(weights[i]):
+            assert rel <= 0.75 * lu.U, name
+    check_state("dinitial_state", got[5], refs[5], weights[5])

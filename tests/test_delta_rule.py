@@ -1,6 +1,6 @@
 """GPU parity of the gated delta rule (kda_delta_*) against the FP64 recurrence:
-training forward, prefill, decode and drafted tokens on a state pool, at the lengths, head
-layouts, strides and gates where the chunked kernels can go wrong."""
+training forward and backward, prefill, decode and drafted tokens on a state pool, at the
+lengths, head layouts, strides and gates where the chunked kernels can go wrong."""
 import numpy as np
 import pytest
 import torch
@@ -110,6 +110,166 @@ def test_equal_keys():
     inp.k[:] = inp.k[:, :1]
     inp.beta.fill_(1.0)
     check_forward(inp, call_forward(inp))
+
+
+# ---------------------------------------------------------------------------
+# training
+# ---------------------------------------------------------------------------
+def train(inp, scale=None, wrap=lambda x: x, **more):
+    import gated_delta_rule_32_amd as kda
+    o, fs, ctx = call_forward(inp, scale, wrap, **more)
+    grads = kda.gated_delta_rule_training_backward(ctx, inp.dev(inp.do), inp.dev(inp.ds))
+    torch.cuda.synchronize()
+    return (o, fs) + grads
+
+
+@pytest.mark.parametrize("case", list(CASES))
+def test_training_step(case):
+    lengths, packed, Hqk, Hv, unit, gates = CASES[case]
+    print(f"[delta] training step {case}", flush=True)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=100 + len(case), unit=unit, gates=gates)
+    got = train(inp)
+    check_forward(inp, got)
+    du.check_gradients(inp, got[2:])
+
+
+def test_training_step_without_states():
+    """initial_state and dfinal_state None count as zero."""
+    inp = Inp([5, 150, 64], True, 1, 2, seed=3, state=False)
+    du.check_gradients(inp, train(inp)[2:])
+
+
+def test_training_step_custom_scale():
+    inp = Inp([80], False, 1, 1, seed=5)
+    du.check_gradients(inp, train(inp, scale=0.25)[2:], scale=0.25)
+
+
+def test_training_step_of_slices():
+    inp = Inp([77, 130], True, 2, 4, seed=6)
+    got, want = train(inp, wrap=wide), train(inp)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_training_step_of_equal_keys():
+    inp = Inp([100], False, 1, 2, seed=9, gates="none")
+    inp.k[:] = inp.k[:, :1]
+    inp.beta.fill_(1.0)
+    du.check_gradients(inp, train(inp)[2:])
+
+
+def test_gradients_of_zero_rows():
+    """Rows of zeros at unit length: finite gradients, the norm's slope there being 1 /
+    sqrt(1e-6)."""
+    inp = Inp([70], False, 1, 1, seed=8)
+    inp.k[:, 20:50] = 0
+    inp.q[:, 10:40] = 0
+    du.check_gradients(inp, train(inp)[2:])
+
+
+def test_gradients_do_not_see_other_sequences():
+    inp = Inp([70, 33, 100], True, 2, 2, seed=7, gates="mixed")
+    a, b = 70, 103
+    names = ("q", "k", "v", "g", "beta", "do")
+    alone = Inp([33], False, 2, 2, unit=True)
+    for n in names:
+        setattr(alone, n, getattr(inp, n)[:, a:b].contiguous())
+    alone.s0, alone.ds = inp.s0[1:2].clone(), inp.ds[1:2].clone()
+    want = train(alone)
+    for n in names:
+        getattr(inp, n)[:, :a] = float("nan")
+        getattr(inp, n)[:, b:] = float("nan")
+    got = train(inp)
+    for i in (0, 2, 3, 4, 5, 6):
+        assert torch.equal(got[i][:, a:b], want[i]), i
+    assert torch.equal(got[1][1], want[1][0]) and torch.equal(got[7][1], want[7][0])
+
+
+def test_gradients_behind_a_strong_decay():
+    """A decay of e^-60 between two halves: what passes it is far below what does not, and
+    its gate's gradient is small and right all the same."""
+    inp = Inp([64], False, 1, 2, seed=10, gates="none")
+    inp.g[:, 20] = -60.0
+    inp.ds.zero_()
+    got = train(inp)
+    du.check_gradients(inp, got[2:])
+    refs, weights, _ = inp.gradients()
+    # (its weight has the factor e^-60 too: no other token's size may show)
+    x, ref = lu.f64(got[5])[:, 20], refs[3][:, 20]
+    assert np.abs(x).max() <= 2.0 ** -60 and (np.abs(x - ref) <= lu.U * np.abs(ref) + du.GRADS * weights[3][:, 20] + 2.0 ** -40 * np.abs(refs[3]).max()).all()
+
+
+def test_training_step_on_another_stream_and_the_same_bits_again():
+    inp = Inp([200, 31], True, 1, 2, seed=13)
+    want = train(inp)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = train(inp)
+    s.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_captured_training_step(packed):
+    """Forward and backward in one graph, replayed with eager calls between; every replay
+    gives the eager bits, on changed inputs too.  A fixed-layout call needs no call before
+    the capture."""
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([150, 7, 143] if packed else [150, 150], packed, 1, 2, seed=14)
+    d = {n: inp.dev(getattr(inp, n)) for n in ("q", "k", "v", "g", "beta", "do", "s0", "ds", "cu")}
+    if packed:  # the schedule: made by one call, seen on the device by a second
+        train(inp)
+        train(inp)
+    p = kda.KdaDeltaProblem(inp.B, inp.T, 1, 2, inp.N)
+    p.use_qk_l2norm = 1
+    if packed:
+        p.cu_seqlens, p.cu_seqlens_host = d["cu"].data_ptr(), inp.cu.data_ptr()
+    outs = [torch.empty_like(d[n]) for n in ("v", "s0", "q", "k", "v", "g", "beta", "s0")]
+    need = max(kda.kda_delta_fwd_workspace_bytes(p), kda.kda_delta_bwd_workspace_bytes(p))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ins = [d[n] for n in ("q", "k", "v", "g", "beta", "s0")]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_delta_fwd(p, *ins, outs[0], outs[1], ws)
+        kda.kda_delta_bwd(p, *ins, d["do"], d["ds"], *outs[2:], ws)
+    for _ in range(3):
+        for x in outs:
+            x.zero_()
+        ws.fill_(255)    # (NaN: nothing of an earlier pass may be read)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = train(inp)
+        for a, b in zip(want, outs):
+            assert torch.equal(a, b)
+        inp.v = inp.v.flip(1).contiguous()
+        d["v"].copy_(inp.v)
+
+
+def test_context_checks_versions():
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([20], False, 1, 1)
+    args = [inp.dev(x) for x in (inp.q, inp.k, inp.v, inp.g, inp.beta)]
+    _, _, ctx = kda.gated_delta_rule_training_forward(*args)
+    args[3].add_(0)
+    with pytest.raises(ValueError, match="changed after the forward"):
+        kda.gated_delta_rule_training_backward(ctx, inp.dev(inp.do))
+
+
+def test_capture_of_a_packed_call_without_a_schedule_is_refused():
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([11, 222, 35], True, 1, 1, seed=15)
+    d = [inp.dev(x) for x in (inp.q, inp.k, inp.v, inp.g, inp.beta)]
+    cu = inp.dev(inp.cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(kda.KdaValueError) as e:
+            kda.gated_delta_rule_training_forward(*d, cu_seqlens=cu, cu_seqlens_cpu=inp.cu)
+        d[0].add_(0)  # something to capture
+    assert e.value.status == kda.KDA_ERR_CAPTURE
 
 
 # ---------------------------------------------------------------------------
