@@ -9,15 +9,28 @@
 
 namespace kda {
 
-// What a chunk of 32 tokens needs beside its rows, per value head (floats): the matrix C
-// that solves the chunk's delta rule, as its strictly lower 16 x 16 tiles row by row, and
-// arrays of 32 over the tokens i, with G the running sum of the log-decays in the chunk:
-// the decay from the chunk's start times one over k's length, the decay to its end times
-// the same, the decay from the start times the scale over q's length, beta, G in base 2 as
-// the sum of two floats, the scale over q's length, one over k's length.
-constexpr int REC_C11 = 0, REC_C22 = 256, REC_C21 = 512, REC_CX = 768, REC_CE = 800, REC_CO = 832, REC_BETA = 864,
-              REC_GH = 896, REC_GL = 928, REC_A = 960, REC_RK = 992, REC = 1024;
+// What a chunk of 32 tokens needs beside its rows, per value head: a record of REC bytes.
+// First -C, C being the matrix that solves the chunk's delta rule, as its strictly lower 16 x
+// 16 tiles, each in three BF16 pieces of 16 rows of 16; then arrays of 32 floats over the
+// tokens i, with G the running sum of the log-decays in the chunk: e^{Gi} and e^{Gn - Gi}, the
+// decays from the chunk's start and to its end, beta, one over k's and q's lengths, products
+// of these, G in base 2 as the sum of two floats; and the chunk's whole decay as the sum of
+// two floats.
+constexpr int REC_TILE = 512, REC_C11 = 0, REC_C22 = 3 * REC_TILE, REC_C21 = 6 * REC_TILE, REC_N = 9 * REC_TILE,
+              REC_FROM = REC_N, REC_FROM_K = REC_N + 128, REC_FROM_KB = REC_N + 256, REC_TO_K = REC_N + 384,
+              REC_TO_KB = REC_N + 512, REC_K = REC_N + 640, REC_KB = REC_N + 768, REC_BETA = REC_N + 896,
+              REC_Q = REC_N + 1024, REC_GH = REC_N + 1152, REC_GL = REC_N + 1280, REC_DECAY = REC_N + 1408,
+              REC = REC_N + 1536;
 constexpr int DB = 64;          // tokens of a block: two chunks, whose records are adjacent
+
+// What the backward's scans leave for the gradients, in FP16: per block the state before it
+// (or the adjoint behind it), [blocks][Hv][128 v][128 k], and per chunk its solution rows,
+// [blocks][Hv][2 chunks][128 v][32 tokens]; the values are those stored times the scale of
+// their 32 channels v, a power of two that brings the largest to [2^14, 2^15): [..][4].
+struct DeltaPlanes {
+    _Float16 *state, *rows;
+    float *state_scale, *row_scale;
+};
 
 struct DeltaArgs {
     ItemMap map;                // the scan's items: sequences, or segments of them
@@ -28,18 +41,14 @@ struct DeltaArgs {
     const bf16_t *g, *beta;     // [tokens][Hv]
     int unit;                   // q and k are taken at unit length
     float scale;
-    float* rec;                 // [blocks][Hv][2][REC]
-    float* fac;                 // [blocks][Hv][2][2]: the chunk's decay as the sum of two floats
+    char* rec;                  // [blocks][Hv][2][REC]
+    int rq;                     // the preparation forms one over q's length too (else the scan that reads q)
     bf16_t* o;                  // [tokens][Hv][128]
     const float* s_in;          // states [.][Hv][128 v][128 k], by slot; null: zero
     float* s_out;               // null: none
     const int32_t* slot;        // state slot of sequence n; null: n
     int64_t slots;
-    // for the backward: per block the state before it (or the adjoint behind it) in planes of
-    // high and low BF16 parts [blocks][Hv][2][128 v][128 k], and per chunk its solution rows
-    // [blocks][Hv][2 chunks][2 planes][128 v][32 tokens]
-    bf16_t* state_planes;
-    bf16_t* row_planes;
+    DeltaPlanes planes;         // what a scan leaves for the gradients
     const bf16_t* d_o;          // [tokens][Hv][128]
 };
 
@@ -52,10 +61,9 @@ struct DeltaGradArgs {
     int G;
     int unit;
     float scale;
-    const float* rec;
+    const char* rec;
     const bf16_t* d_o;
-    const bf16_t *s_planes, *z_planes;    // [blocks][Hv][2][128 v][128 k]
-    const bf16_t *w_planes, *y_planes;    // [blocks][Hv][2 chunks][2][128 v][32 tokens]
+    DeltaPlanes forward, backward;        // S and W, Z and Y
     void *dq, *dk;                        // [tokens][Hv][128]: BF16, or packed partials
     int pack;
     bf16_t *dv, *dg, *dbeta;
@@ -80,8 +88,10 @@ struct DeltaTokenArgs {
 
 hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s);
 enum DeltaMode { kDeltaOut = 0, kDeltaRecord = 1 };
-hipError_t launch_delta_scan(const DeltaArgs& a, DeltaMode mode, hipStream_t s);
-hipError_t launch_delta_adjoint(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);   // o and the final states
+// The backward's two scans at once: `forward` leaves its planes, `backward` its own and the
+// adjoint of the initial states.
+hipError_t launch_delta_both(const DeltaArgs& forward, const DeltaArgs& backward, hipStream_t s);
 hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s);
 hipError_t launch_delta_token(const DeltaTokenArgs& a, hipStream_t s);
 

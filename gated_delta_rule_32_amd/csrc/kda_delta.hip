@@ -16,7 +16,7 @@
 // C serves both, and does not depend on the state: a kernel of its own forms it for all
 // chunks at once.  q and k at unit length enter as they are, with one over their length as
 // a factor of their token.
-#include "kda_delta.hpp"
+#include "kda_delta_scan.hpp"
 
 namespace kda {
 
@@ -91,12 +91,14 @@ __global__ __launch_bounds__(64 * PREP_WAVES) void delta_prepare_kernel(DeltaArg
     float rk = 1.0f, rq = 1.0f;
     if (A.unit) {
         diagonal(k, tok);
-        bf16x8 q[4][4];
-        rows((const bf16*)A.q, A.sq, q);
-        diagonal(q, tok + 64);
+        if (A.rq) {
+            bf16x8 q[4][4];
+            rows((const bf16*)A.q, A.sq, q);
+            diagonal(q, tok + 64);
+        }
         __builtin_amdgcn_wave_barrier();
         rk = rsqrtf(tok[lane] + NORM_EPS);
-        rq = rsqrtf(tok[64 + lane] + NORM_EPS);
+        if (A.rq) rq = rsqrtf(tok[64 + lane] + NORM_EPS);
         __builtin_amdgcn_wave_barrier();
     }
     if (!valid) rk = rq = 0.0f;
@@ -110,23 +112,25 @@ __global__ __launch_bounds__(64 * PREP_WAVES) void delta_prepare_kernel(DeltaArg
     beta_[lane] = beta;
     __builtin_amdgcn_wave_barrier();
 
-    float* rec = A.rec + at * (2 * REC);
+    char* rec = A.rec + at * (2 * REC);
     {
-        float* r = rec + (lane >> 5) * REC + (lane & 31);
-        const float from = (float)exp2(G);
-        r[REC_CX] = from * rk;
-        r[REC_CE] = (float)exp2(last - G) * rk;
-        r[REC_CO] = A.scale * (from * rq);
-        r[REC_BETA] = beta;
-        r[REC_GH] = gh;
-        r[REC_GL] = gl;
-        r[REC_A] = A.scale * rq;
-        r[REC_RK] = rk;
+        char* r = rec + (lane >> 5) * REC + (lane & 31) * 4;
+        const float from = (float)exp2(G), to = (float)exp2(last - G);
+        *(float*)(r + REC_FROM) = from;
+        *(float*)(r + REC_FROM_K) = from * rk;
+        *(float*)(r + REC_FROM_KB) = from * rk * beta;
+        *(float*)(r + REC_TO_K) = to * rk;
+        *(float*)(r + REC_TO_KB) = to * rk * beta;
+        *(float*)(r + REC_K) = rk;
+        *(float*)(r + REC_KB) = rk * beta;
+        *(float*)(r + REC_BETA) = beta;
+        *(float*)(r + REC_Q) = rq;
+        *(float*)(r + REC_GH) = gh;
+        *(float*)(r + REC_GL) = gl;
         if ((lane & 31) == 0) {
             const Factor f(exp2(last));
-            float* fac = A.fac + at * 4 + (lane >> 5) * 2;
-            fac[0] = f.f;
-            fac[1] = f.low;
+            *(float*)(r + REC_DECAY) = f.f;
+            *(float*)(r + REC_DECAY + 4) = f.low;
         }
     }
     // A's tiles.  Diagonal: lane (gq, n) holds rows 4gq + e of column n.  Below: lane (gq, n)
@@ -175,14 +179,21 @@ __global__ __launch_bounds__(64 * PREP_WAVES) void delta_prepare_kernel(DeltaArg
             bc[i] = bt[i] * c[i];
         }
         __builtin_amdgcn_wave_barrier();
-        float* out = rec + (gq >> 1) * REC + (gq & 1 ? REC_C22 : REC_C11) + n16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            out[i * 16] = c[i];
-            tile[gq * TS + i * 16 + n16] = c[i];
-        }
+        for (int i = 0; i < 16; ++i) tile[gq * TS + i * 16 + n16] = c[i];
         __builtin_amdgcn_wave_barrier();
     }
+    // 4 columns of a row of -C's tile, in pieces
+    const Pieces pieces(lane);
+    auto put = [&](char* to, f32x4 x) __attribute__((always_inline)) {
+        bf16x4 p[3];
+        pieces.split(-x, p[0], p[1], p[2]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *(bf16x4*)(to + i * REC_TILE + n16 * 32 + gq * 8) = p[i];
+    };
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        put(rec + (b >> 1) * REC + (b & 1 ? REC_C22 : REC_C11), *(const f32x4*)(tile + b * TS + n16 * 16 + 4 * gq));
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const float* c11 = tile + 2 * s * TS;
@@ -199,9 +210,13 @@ __global__ __launch_bounds__(64 * PREP_WAVES) void delta_prepare_kernel(DeltaArg
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             r = __builtin_amdgcn_mfma_f32_16x16x4f32(-row[e] * beta_[32 * s + 16 + 4 * gq + e], h[e], r, 0, 0, 0);
-        float* out = rec + s * REC + REC_C21 + n16;
+        // rows 4gq + e of column n16: through LDS (over tile 2s, which is read) to the rows' order
+        __builtin_amdgcn_wave_barrier();
+        float* t = tile + 2 * s * TS;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[(4 * gq + e) * 16] = r[e];
+        for (int e = 0; e < 4; ++e) t[(4 * gq + e) * 16 + n16] = r[e];
+        __builtin_amdgcn_wave_barrier();
+        put(rec + s * REC + REC_C21, *(const f32x4*)(t + n16 * 16 + 4 * gq));
     }
 }
 
@@ -212,320 +227,26 @@ hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One workgroup per item (kParts = 2: two, each with half of the state's output channels), a
-// wave for every NU tiles of 16 channels v.  A wave keeps its columns of the state as MFMA
-// accumulators: tile (t, u) is S^T[k][v] with
-//     k = 32(t/2) + 8gq + 4(t%2) + e,   v = 32wv + 8(n/4) + 4u + n%4
-// (NU = 1: v = 16wv + n; lane 16gq + n, element e).  The same registers are the operand of
-// S K^T from either side, so that X = V - S K^T comes out with tokens along the elements,
-// where W = X - C B X and S^T += K^T U take it without leaving the lane, and o^T = S Q^T +
-// W^T P^T with 8 neighbouring channels of a token for its store.  Only P = Q K^T passes
-// between waves.
-// Products are exact to FP32: S and B X go in as three BF16 pieces of 8 bits, C as three, U
-// as three; P and W as two where they only meet o.  The rows of the next chunk and its record travel
-// to the other of two LDS buffers while this one is computed.
+// With enough workgroups to share compute units, four waves with two tiles each spend the
+// least on reading the rows out of LDS.  With one workgroup per unit at most, eight waves shorten a
+// chunk, and with one for every second unit, two workgroups of half the columns each.
 template <int NU, int kParts, int kMode>
 __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_scan_kernel(DeltaArgs A) {
-    constexpr bool kOut = kMode == kDeltaOut, kRecord = kMode == kDeltaRecord;
-    constexpr int NW = 8 / NU / kParts;
-    constexpr int SETS = kOut ? 3 : 2, SET = SC * D * 2, LK = 0, LV = 2 * SET, LQ = 4 * SET, LPT = 1024;
-    constexpr int ROWS16 = 16 * D * 2;
-    __shared__ __align__(16) char lds[2 * SETS * SET];
-    __shared__ __align__(16) float lds_r[2][REC];
-    __shared__ __align__(16) char lds_p[kOut ? 3 * LPT : 16];
-
-    const int tid = threadIdx.x;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lane = tid & 63, gq = lane >> 4, n16 = lane & 15;
-    int idx = xcd_order(blockIdx.x, (int)gridDim.x, A.G * kParts);
-    const int part = idx % kParts;
-    idx /= kParts;
-    const int wv = w + NW * part;   // this wave among the columns
-    const Item it = find_item(A.map, idx);
-    const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
-    if (slot < 0 || slot >= A.slots) return;
-    const int Hv = A.map.Hv;
-    const int64_t soff = (slot * Hv + it.h) * (int64_t)STATE;
-    // the item's first block among all blocks
-    const int64_t block0 = (A.blocks.task != nullptr ? A.blocks.tape_off[it.n] + it.n
-                                                     : (int64_t)it.n * ((A.blocks.len + DB - 1) / DB)) + it.off / DB;
-
-    // Loads: one instruction of a wave moves 4 rows of 256 bytes (16 lanes a row) to 1 KiB of
-    // LDS in lane order; a lane fetches the block that belongs there.
-    const int lrow = 4 * w + gq;
-    constexpr int STEP = 4 * NW;
-    const bf16* src[3] = {(const bf16*)A.k, (const bf16*)A.v, (const bf16*)A.q};
-    const int64_t stride[3] = {A.sk, A.sv, A.sq};
-    const char* pr[SETS];
-    unsigned off[SETS];
-#pragma unroll
-    for (int i = 0; i < SETS; ++i) {
-        pr[i] = (const char*)(src[i] + it.tok0 * stride[i] + (i == 1 ? it.h : it.h / A.G) * D);
-        off[i] = (unsigned)lrow * (unsigned)(stride[i] * 2) + ((n16 ^ swz(lrow)) << 4);
-    }
-    static_assert(STEP % 16 == 0, "rows of one lane share their place in a row's order");
-    const char* prec = (const char*)(A.rec + (block0 * Hv + it.h) * (2 * REC));
-    const float* pfac = A.fac + (block0 * Hv + it.h) * 4;
-    auto fetch = [&](char* rows_to, float* rec_to, int t0) __attribute__((always_inline)) {
-        const int rem = it.len - t0;
-#pragma unroll
-        for (int j = 0; j < SC / STEP; ++j) {
-            if (rem >= SC || lrow + STEP * j < rem) {
-#pragma unroll
-                for (int i = 0; i < SETS; ++i)
-                    to_lds<false>(pr[i] + j * STEP * 2 * stride[i], off[i], rows_to + 2 * i * SET + (STEP * j + 4 * w) * D * 2);
-            } else {   // rows behind the last token are not read and count as zero
-#pragma unroll
-                for (int i = 0; i < SETS; ++i)
-                    *(u32x4*)(rows_to + 2 * i * SET + (STEP * j + 4 * w) * D * 2 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
-            }
-        }
-        if (w < 4) {
-            // (a block's second record is behind the first, the next block's Hv blocks on)
-            const int c = t0 / SC;
-            const char* p = prec + ((int64_t)(c >> 1) * Hv * 2 + (c & 1)) * (REC * 4) + w * 1024;
-            to_lds<false>(p, lane * 16, (char*)rec_to + w * 1024);
-        }
-#pragma unroll
-        for (int i = 0; i < SETS; ++i) pr[i] += SC * 2 * stride[i];
-    };
-    static_assert(NW >= 4, "a record is moved by four waves");
-    fetch(lds, lds_r[0], 0);
-
-    f32x4 S[8][NU];
-    const int vrow = NU == 2 ? 32 * wv + 8 * (n16 >> 2) + (n16 & 3) : 16 * wv + n16;   // + 4u
-    auto krow = [&](int t) __attribute__((always_inline)) { return 32 * (t >> 1) + 8 * gq + 4 * (t & 1); };
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-            S[t][u] = A.s_in != nullptr ? *(const f32x4*)(A.s_in + soff + (vrow + 4 * u) * D + krow(t)) : zero4();
-
-    // LDS offsets (bytes): as in the constant-decay scan
-    const int r8 = (n16 * D + ((gq ^ swz(n16)) << 3)) * 2;
-    const int trow = 4 * gq + (n16 >> 2), piece = n16 & 3;
-    const int tr = (trow * D + ((piece ^ swz(trow)) << 3)) * 2;
-    const int trv = NU == 2 ? (trow * D + (((4 * wv + piece) ^ swz(trow)) << 3)) * 2
-                            : (trow * D + (((2 * wv + (piece >> 1)) ^ swz(trow)) << 3) + 4 * (piece & 1)) * 2;
-    const int64_t sy = (int64_t)Hv * D * 2;
-    char* po = (char*)(A.o + (it.tok0 * Hv + it.h) * D);
-    const unsigned oy = (unsigned)n16 * (unsigned)sy + (16 * NU * wv + 4 * NU * gq) * 2;
-
-    // One chunk from `buf` and `rec`, the next one on its way into `rows_to` and `rec_to`.
-    // (Both pairs are halves of the same arrays; as restrict pointers they show the compiler
-    // that what is read through the one need not wait for what is on its way into the other.)
-    auto chunk = [&](int t0, const char* __restrict__ buf, const float* __restrict__ rec, char* __restrict__ rows_to,
-                     float* __restrict__ rec_to) __attribute__((always_inline)) {
-        const int rem = it.len - t0, c = t0 / SC;
-        const bool more = rem > SC;
-        if (more) fetch(rows_to, rec_to, t0 + SC);
-        const float* fac = pfac + (int64_t)(c >> 1) * Hv * 4 + (c & 1) * 2;
-        const float f = fac[0], f_low = fac[1];
-        if (kOut) {   // P^T tiles: (i, j) = (0, 0), (1, 1), (1, 0)
-#pragma unroll
-            for (int tile = 0; tile < 3; ++tile) {
-                if (w != tile) continue;
-                const int bi = tile == 0 ? 0 : 1, bj = tile == 1 ? 1 : 0;
-                f32x4 acc = zero4();
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    acc = mma32(*(const bf16x8*)(buf + LK + ((r8 + bj * ROWS16) ^ (64 * p))),
-                                *(const bf16x8*)(buf + LQ + ((r8 + bi * ROWS16) ^ (64 * p))), acc);
-                const int i = 16 * bi + n16, j = 16 * bj + 4 * gq;
-                const float ai = rec[REC_A + i], hi = rec[REC_GH + i], li = rec[REC_GL + i];
-                const f32x4 rj = *(const f32x4*)(rec + REC_RK + j), bt = *(const f32x4*)(rec + REC_BETA + j),
-                            hj = *(const f32x4*)(rec + REC_GH + j), lj = *(const f32x4*)(rec + REC_GL + j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = acc[e] * (ai * rj[e] * bt[e]) * decay2(hi, li, hj[e], lj[e]);
-                    acc[e] = i >= j + e ? x : 0.0f;
-                }
-                bf16x4 hi4, lo4;
-                split4_rne(acc, hi4, lo4);
-                *(bf16x8*)(lds_p + tile * LPT + lane * 16) = cat8(hi4, lo4);
-            }
-        }
-        // S K^T and S Q^T
-        f32x4 x[2][NU], y[2][NU];
-#pragma unroll
-        for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) x[ti][u] = y[ti][u] = zero4();
-        const bool keep = kRecord && (c & 1) == 0;
-        char* planes = kRecord ? (char*)(A.state_planes + ((block0 + (c >> 1)) * Hv + it.h) * (int64_t)(2 * STATE)) : nullptr;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            bf16x8 ak[2], aq[2];
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti) {
-                ak[ti] = *(const bf16x8*)(buf + LK + ((r8 + ti * ROWS16) ^ (64 * p)));
-                if (kOut) aq[ti] = *(const bf16x8*)(buf + LQ + ((r8 + ti * ROWS16) ^ (64 * p)));
-            }
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                bf16x4 pc[3][2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) split3(S[2 * p + i][u], pc[0][i], pc[1][i], pc[2][i]);
-#pragma unroll
-                for (int d = 0; d < 3; ++d) {
-                    const bf16x8 s = cat8(pc[d][0], pc[d][1]);
-#pragma unroll
-                    for (int ti = 0; ti < 2; ++ti) x[ti][u] = mma32(ak[ti], s, x[ti][u]);
-                    if (kOut && d < 2) {
-#pragma unroll
-                        for (int ti = 0; ti < 2; ++ti) y[ti][u] = mma32(s, aq[ti], y[ti][u]);
-                    }
-                    if (kRecord && d < 2 && keep)
-                        *(bf16x8*)(planes + d * (STATE * 2) + ((vrow + 4 * u) * D + krow(2 * p)) * 2) = s;
-                }
-            }
-        }
-        // X = V - e^G S K^T, W = X - C B X
-        f32x4 wr[2][NU];
-#pragma unroll
-        for (int ti = 0; ti < 2; ++ti) {
-            const f32x4 cx = *(const f32x4*)(rec + REC_CX + 16 * ti + 4 * gq);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const f32x4 v = from_bf4(tr_read(buf + LV + trv + 8 * u + ROWS16 * ti));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) wr[ti][u][e] = fmaf(-cx[e], x[ti][u][e], v[e]);
-            }
-        }
-        {
-            bf16x4 c11[3], c22[3], c21[3];
-            const int rm = n16 * 16 + 4 * gq;
-            split3(-*(const f32x4*)(rec + REC_C11 + rm), c11[0], c11[1], c11[2]);
-            split3(-*(const f32x4*)(rec + REC_C22 + rm), c22[0], c22[1], c22[2]);
-            split3(-*(const f32x4*)(rec + REC_C21 + rm), c21[0], c21[1], c21[2]);
-            const f32x4 b0 = *(const f32x4*)(rec + REC_BETA + 4 * gq), b1 = *(const f32x4*)(rec + REC_BETA + 16 + 4 * gq);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                bf16x4 x0[3], x1[3];
-                split3(wr[0][u] * b0, x0[0], x0[1], x0[2]);
-                split3(wr[1][u] * b1, x1[0], x1[1], x1[2]);
-                // pieces (a, b) with a + b <= 2; row block 0 takes two products at once
-                wr[0][u] = mma32(cat8(c11[0], c11[0]), cat8(x0[0], x0[1]), wr[0][u]);
-                wr[0][u] = mma32(cat8(c11[1], c11[1]), cat8(x0[0], x0[1]), wr[0][u]);
-                wr[0][u] = mma32(cat8(c11[0], c11[2]), cat8(x0[2], x0[0]), wr[0][u]);
-#pragma unroll
-                for (int a = 0; a < 3; ++a)
-#pragma unroll
-                    for (int b = 0; a + b < 3; ++b)
-                        wr[1][u] = mma32(cat8(c21[a], c22[a]), cat8(x0[b], x1[b]), wr[1][u]);
-            }
-        }
-        if (kRecord) {   // the rows W, as planes [v][token]
-            char* rp = (char*)(A.row_planes + (((block0 + (c >> 1)) * Hv + it.h) * 2 + (c & 1)) * (int64_t)(2 * D * SC));
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    bf16x4 hi, lo;
-                    split4_rne(wr[ti][u], hi, lo);
-                    char* d = rp + ((vrow + 4 * u) * SC + 16 * ti + 4 * gq) * 2;
-                    *(bf16x4*)d = hi;
-                    *(bf16x4*)(d + D * SC * 2) = lo;
-                }
-        }
-        if (kOut) {
-            barrier_lds();
-            const bf16x8 p00 = *(const bf16x8*)(lds_p + lane * 16), p11 = *(const bf16x8*)(lds_p + LPT + lane * 16),
-                         p10 = *(const bf16x8*)(lds_p + 2 * LPT + lane * 16);
-            const bf16x8 p1h = __builtin_shufflevector(p10, p11, 0, 1, 2, 3, 8, 9, 10, 11),
-                         p1l = __builtin_shufflevector(p10, p11, 4, 5, 6, 7, 12, 13, 14, 15);
-            const float co[2] = {rec[REC_CO + n16], rec[REC_CO + 16 + n16]};
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                bf16x4 h0, l0, h1, l1;
-                split4_rne(wr[0][u], h0, l0);
-                split4_rne(wr[1][u], h1, l1);
-#pragma unroll
-                for (int ti = 0; ti < 2; ++ti) y[ti][u] *= co[ti];
-                y[0][u] = mma32(cat8(h0, h0), p00, y[0][u]);
-                y[0][u] = mma32(cat8(l0, l0), p00, y[0][u]);
-                y[1][u] = mma32(cat8(h0, h1), p1h, y[1][u]);
-                y[1][u] = mma32(cat8(h0, h1), p1l, y[1][u]);
-                y[1][u] = mma32(cat8(l0, l1), p1h, y[1][u]);
-            }
-#pragma unroll
-            for (int ti = 0; ti < 2; ++ti) {
-                u32x2 r[NU];
-#pragma unroll
-                for (int u = 0; u < NU; ++u) r[u] = __builtin_bit_cast(u32x2, to_bf4(y[ti][u]));
-                if (16 * ti + n16 < rem) {
-                    if constexpr (NU == 2)
-                        *row_ptr<u32x4>(po + 16 * ti * sy, oy) = u32x4{r[0][0], r[0][1], r[1][0], r[1][1]};
-                    else
-                        *row_ptr<u32x2>(po + 16 * ti * sy, oy) = r[0];
-                }
-            }
-            po += SC * sy;
-        }
-        // S <- e^{G_n} S + K^T U
-        bf16x8 u3[3][NU];
-        {
-            const f32x4 e0 = *(const f32x4*)(rec + REC_CE + 4 * gq) * *(const f32x4*)(rec + REC_BETA + 4 * gq);
-            const f32x4 e1 = *(const f32x4*)(rec + REC_CE + 16 + 4 * gq) * *(const f32x4*)(rec + REC_BETA + 16 + 4 * gq);
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                bf16x4 a0[3], a1[3];
-                split3(wr[0][u] * e0, a0[0], a0[1], a0[2]);
-                split3(wr[1][u] * e1, a1[0], a1[1], a1[2]);
-#pragma unroll
-                for (int d = 0; d < 3; ++d) u3[d][u] = cat8(a0[d], a1[d]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const char* row = buf + LK + (tr ^ (64 * (t >> 1))) + 8 * (t & 1);
-            const bf16x8 kt = cat8(tr_read(row), tr_read(row + ROWS16));
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[t][u][e] = fmaf(S[t][u][e], f, S[t][u][e] * f_low);
-#pragma unroll
-                for (int d = 0; d < 3; ++d) S[t][u] = mma32(kt, u3[d][u], S[t][u]);
-            }
-        }
-        if (more) {
-            // the next chunk's rows have arrived when at most this chunk's stores, issued
-            // after them, are outstanding (they complete in order)
-            wait_vm<kOut ? 2 : 4 * NU>();
-            barrier_lds();
-        }
-    };
-    wait_vm<0>();
-    barrier_lds();
-    for (int t0 = 0, at = 0; t0 < it.len; t0 += SC, at ^= 1)
-        chunk(t0, lds + at * SET, lds_r[at], lds + (at ^ 1) * SET, lds_r[at ^ 1]);
-
-    if (A.s_out != nullptr) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) *(f32x4*)(A.s_out + soff + (vrow + 4 * u) * D + krow(t)) = S[t][u];
-    }
+    __shared__ __align__(16) char lds[DeltaScanLds<kMode>::TOTAL];
+    delta_scan<NU, kParts, kMode>(A, blockIdx.x, gridDim.x, lds);
 }
 
-template <int NU, int kParts>
-static void launch_scan(const DeltaArgs& a, DeltaMode mode, hipStream_t s) {
-    const dim3 grid((unsigned)(a.map.items * kParts)), block(512 / NU / kParts);
-    if (mode == kDeltaOut)
-        hipLaunchKernelGGL((delta_scan_kernel<NU, kParts, kDeltaOut>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((delta_scan_kernel<NU, kParts, kDeltaRecord>), grid, block, 0, s, a);
-}
-
-hipError_t launch_delta_scan(const DeltaArgs& a, DeltaMode mode, hipStream_t s) {
+template <int kMode>
+static hipError_t launch_scan(const DeltaArgs& a, hipStream_t s) {
     if (a.map.items <= 128)
-        launch_scan<1, 2>(a, mode, s);
+        hipLaunchKernelGGL((delta_scan_kernel<1, 2, kMode>), dim3((unsigned)(a.map.items * 2)), dim3(256), 0, s, a);
     else if (a.map.items <= 256)
-        launch_scan<1, 1>(a, mode, s);
+        hipLaunchKernelGGL((delta_scan_kernel<1, 1, kMode>), dim3((unsigned)a.map.items), dim3(512), 0, s, a);
     else
-        launch_scan<2, 1>(a, mode, s);
+        hipLaunchKernelGGL((delta_scan_kernel<2, 1, kMode>), dim3((unsigned)a.map.items), dim3(256), 0, s, a);
     return hipGetLastError();
 }
+hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) { return launch_scan<kDeltaOut>(a, s); }
 
 // Token-serial form on the FP32 state pool (decode, drafted tokens, and sequences of a few
 // tokens).  A workgroup takes 32 of the 128 state rows of one (sequence, value head): a half

@@ -56,24 +56,26 @@ int64_t total_blocks(const Delta& d) {
     return n;
 }
 
-// The chunks' records and decays.
+// The chunks' records.
 struct RecordWs {
-    size_t rec = 0, fac = 0, total = 0;
+    size_t rec = 0, total = 0;
 };
 RecordWs record_ws(const Delta& d, int64_t blocks, size_t off = 0) {
     RecordWs w;
     w.rec = off;
-    off = align256(off + (size_t)blocks * d.s.Hv * 2 * kda::REC * sizeof(float));
-    w.fac = off;
-    w.total = align256(off + (size_t)blocks * d.s.Hv * 4 * sizeof(float));
+    w.total = align256(off + (size_t)blocks * d.s.Hv * 2 * kda::REC);
     return w;
 }
 
-// The backward's workspace: records, planes of the states before and the adjoints behind the
-// blocks, planes of the rows W and Y, and partials of dq and dk where value heads share them.
+// The backward's workspace: records, what the two scans leave, and partials of dq and dk
+// where value heads share them.
+struct PlanesWs {
+    size_t state = 0, rows = 0, state_scale = 0, row_scale = 0;
+};
 struct GradWs {
     RecordWs r;
-    size_t s = 0, z = 0, w = 0, y = 0, part_q = 0, part_k = 0, total = 0;
+    PlanesWs forward, backward;
+    size_t part_q = 0, part_k = 0, total = 0;
 };
 GradWs grad_ws(const Delta& d) {
     GradWs g;
@@ -86,15 +88,20 @@ GradWs grad_ws(const Delta& d) {
         return at;
     };
     const size_t items = (size_t)blocks * d.s.Hv;
-    g.s = take(items * 2 * kState * 2);
-    g.z = take(items * 2 * kState * 2);
-    g.w = take(items * 2 * kda::DB * D * 2);
-    g.y = take(items * 2 * kda::DB * D * 2);
+    for (PlanesWs* p : {&g.forward, &g.backward}) {
+        p->state = take(items * kState * 2);
+        p->rows = take(items * kda::DB * D * 2);
+        p->state_scale = take(items * 4 * sizeof(float));
+        p->row_scale = take(items * 8 * sizeof(float));
+    }
     const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
     g.part_q = take(part);
     g.part_k = take(part);
     g.total = off;
     return g;
+}
+kda::DeltaPlanes planes_at(char* ws, const PlanesWs& p) {
+    return {(_Float16*)(ws + p.state), (_Float16*)(ws + p.rows), (float*)(ws + p.state_scale), (float*)(ws + p.row_scale)};
 }
 
 // The item maps of a call (whole sequences, and blocks of 64 tokens) and its hold on the
@@ -208,15 +215,14 @@ kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void*
         if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
         if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
         set_inputs(d, q, k, v, g, beta, a);
-        a.rec = (float*)((char*)workspace + w.rec);
-        a.fac = (float*)((char*)workspace + w.fac);
+        a.rec = (char*)workspace + w.rec;
         a.o = (kda::bf16_t*)o;
         a.s_in = initial_state;
         a.s_out = final_state;
         a.slots = d.s.N;
         hipError_t e = kda::launch_delta_prepare(a, stream);
         if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-        e = kda::launch_delta_scan(a, kda::kDeltaOut, stream);
+        e = kda::launch_delta_scan(a, stream);
         if (e != hipSuccess) return hip_fail(e, "delta scan launch");
         return KDA_OK;
     });
@@ -264,27 +270,24 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
         SeqPlan plan;
         kda::DeltaArgs a{};
         if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
-        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
+        if ((s = check_grid(a.map.items * 4)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
         if (d.s.G > 1 && (s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
         char* ws = (char*)workspace;
         set_inputs(d, q, k, v, g, beta, a);
-        a.rec = (float*)(ws + wl.r.rec);
-        a.fac = (float*)(ws + wl.r.fac);
+        a.rec = ws + wl.r.rec;
+        a.rq = 1;
         a.slots = d.s.N;
         a.d_o = (const kda::bf16_t*)d_o;
         hipError_t e = kda::launch_delta_prepare(a, stream);
         if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-        a.s_in = initial_state;
-        a.state_planes = (kda::bf16_t*)(ws + wl.s);
-        a.row_planes = (kda::bf16_t*)(ws + wl.w);
-        e = kda::launch_delta_scan(a, kda::kDeltaRecord, stream);
-        if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+        kda::DeltaArgs f = a;
+        f.s_in = initial_state;
+        f.planes = planes_at(ws, wl.forward);
         a.s_in = dfinal_state;
         a.s_out = dinitial_state;
-        a.state_planes = (kda::bf16_t*)(ws + wl.z);
-        a.row_planes = (kda::bf16_t*)(ws + wl.y);
-        e = kda::launch_delta_adjoint(a, stream);
-        if (e != hipSuccess) return hip_fail(e, "delta adjoint launch");
+        a.planes = planes_at(ws, wl.backward);
+        e = kda::launch_delta_both(f, a, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta scans launch");
         const bool pack = d.s.G > 1;
         kda::DeltaGradArgs b{};
         b.blocks = a.blocks;
@@ -297,10 +300,8 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
         b.scale = a.scale;
         b.rec = a.rec;
         b.d_o = a.d_o;
-        b.s_planes = (const kda::bf16_t*)(ws + wl.s);
-        b.z_planes = (const kda::bf16_t*)(ws + wl.z);
-        b.w_planes = (const kda::bf16_t*)(ws + wl.w);
-        b.y_planes = (const kda::bf16_t*)(ws + wl.y);
+        b.forward = f.planes;
+        b.backward = a.planes;
         b.dq = pack ? (void*)(ws + wl.part_q) : dq;
         b.dk = pack ? (void*)(ws + wl.part_k) : dk;
         b.pack = pack;
@@ -396,15 +397,14 @@ kda_status kda_delta_infer(const kda_delta_problem* pp, const void* q, const voi
         hipError_t e;
         if (ip.chunked != 0) {
             set_inputs(d, q, k, v, g, beta, a);
-            a.rec = (float*)((char*)workspace + ip.ws.rec);
-            a.fac = (float*)((char*)workspace + ip.ws.fac);
+            a.rec = (char*)workspace + ip.ws.rec;
             a.o = (kda::bf16_t*)o;
             a.s_in = a.s_out = state_pool;
             a.slot = state_indices;
             a.slots = pool_slots;
             e = kda::launch_delta_prepare(a, stream);
             if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-            e = kda::launch_delta_scan(a, kda::kDeltaOut, stream);
+            e = kda::launch_delta_scan(a, stream);
             if (e != hipSuccess) return hip_fail(e, "delta scan launch");
             if (serial == 0) return KDA_OK;
         }

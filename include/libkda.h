@@ -530,7 +530,7 @@ kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* 
  * respect to the inputs as they were given (with use_qk_l2norm through the
  * norm).  dfinal_state NULL counts as zero; dinitial_state may be NULL.  dq and dk
  * sum over the value heads that share a q/k head, in head order; dg and dbeta are BF16
- * [B][T][Hv].  The workspace holds every block's states: about 200 KiB per 64 tokens and value
+ * [B][T][Hv].  The workspace holds every block's states: about 107 KiB per 64 tokens and value
  * head. */
 kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, size_t* bytes);
 kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,

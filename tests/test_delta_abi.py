@@ -153,12 +153,12 @@ def test_workspace_sizes():
         assert getattr(kda._lib, f"kda_delta_{name}_workspace_bytes")(ctypes.byref(p), *a, ctypes.byref(n)) == OK
         return n.value
     p = delta(T=65, B=2, N=2)                                  # two blocks a sequence
-    records = up(4 * 4 * 8192) + up(4 * 4 * 16)
+    records = up(4 * 4 * 2 * 6144)
     assert need("fwd", p) >= records
     assert need("infer", p, 0) >= records
     assert need("infer", delta(T=8), 0) == 0                   # token by token
     assert need("infer", delta(T=40), 39) == 0
-    assert need("bwd", p) >= records + 2 * 4 * 4 * (65536 + 32768)
+    assert need("bwd", p) >= records + 2 * 4 * 4 * (32768 + 16384)
     n = ctypes.c_size_t()
     for name in ("fwd", "bwd"):
         assert getattr(kda._lib, f"kda_delta_{name}_workspace_bytes")(ctypes.byref(p), None) == NULL
