@@ -67,8 +67,8 @@ RecordWs record_ws(const Delta& d, int64_t blocks, size_t off = 0) {
     return w;
 }
 
-// The backward's workspace: records, what the two scans leave, and partials of dq and dk
-// where value heads share them.
+// The backward's workspace: records unless they are given, what the two scans leave, and
+// partials of dq and dk where value heads share them.
 struct PlanesWs {
     size_t state = 0, rows = 0, state_scale = 0, row_scale = 0;
 };
@@ -77,10 +77,10 @@ struct GradWs {
     PlanesWs forward, backward;
     size_t part_q = 0, part_k = 0, total = 0;
 };
-GradWs grad_ws(const Delta& d) {
+GradWs grad_ws(const Delta& d, bool records) {
     GradWs g;
     const int64_t blocks = total_blocks(d);
-    g.r = record_ws(d, blocks);
+    if (!records) g.r = record_ws(d, blocks);
     size_t off = g.r.total;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -228,21 +228,21 @@ kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void*
     });
 }
 
-kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* pp, size_t* bytes) {
+kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* pp, int32_t records_given, size_t* bytes) {
     return guarded([&]() -> kda_status {
         Delta d;
         kda_status s = check_delta(pp, d);
         if (s != KDA_OK) return s;
         if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
-        *bytes = grad_ws(d).total;
+        *bytes = grad_ws(d, records_given != 0).total;
         return KDA_OK;
     });
 }
 
 kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void* k, const void* v, const void* g,
-                         const void* beta, const float* initial_state, const void* d_o, const float* dfinal_state,
-                         void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dinitial_state, void* workspace,
-                         size_t workspace_bytes, void* stream_) {
+                         const void* beta, const float* initial_state, const void* records, size_t records_bytes,
+                         const void* d_o, const float* dfinal_state, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                         float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream_) {
     return guarded([&]() -> kda_status {
         Delta d;
         kda_status s = check_delta(pp, d);
@@ -253,13 +253,19 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
                          {dfinal_state, "dfinal_state"}, {dq, "dq"}, {dk, "dk"}, {dv, "dv"},
                          {dinitial_state, "dinitial_state"}});
         if (s != KDA_OK) return s;
-        const GradWs wl = grad_ws(d);
+        const size_t rec = record_ws(d, total_blocks(d)).total;
+        if (records != nullptr) {
+            if (records_bytes < rec) return fail(KDA_ERR_CTX_SIZE, "records have %zu bytes, need %zu", records_bytes, rec);
+            if ((s = check_align(records, "records")) != KDA_OK) return s;
+        }
+        const GradWs wl = grad_ws(d, records != nullptr);
         if ((s = check_ws(workspace, workspace_bytes, wl.total)) != KDA_OK) return s;
         const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
         const size_t tq = (size_t)d.s.tokens * d.s.Hqk * D * 2, tv = (size_t)d.s.tokens * d.s.Hv * D * 2,
                      tg = (size_t)d.s.tokens * d.s.Hv * 2;
         std::vector<Span> ins = input_spans(pp, d, q, k, v, g, beta);
         ins.push_back({initial_state, initial_state ? st : 0, "initial_state"});
+        ins.push_back({records, records ? rec : 0, "records"});
         ins.push_back({d_o, tv, "do"});
         ins.push_back({dfinal_state, dfinal_state ? st : 0, "dfinal_state"});
         s = check_overlap({{dq, tq, "dq"}, {dk, tq, "dk"}, {dv, tv, "dv"}, {dg, tg, "dg"}, {dbeta, tg, "dbeta"},
@@ -274,12 +280,15 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
         if (d.s.G > 1 && (s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
         char* ws = (char*)workspace;
         set_inputs(d, q, k, v, g, beta, a);
-        a.rec = ws + wl.r.rec;
+        a.rec = records != nullptr ? (char*)records : ws + wl.r.rec;
         a.rq = 1;
         a.slots = d.s.N;
         a.d_o = (const kda::bf16_t*)d_o;
-        hipError_t e = kda::launch_delta_prepare(a, stream);
-        if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+        hipError_t e;
+        if (records == nullptr) {
+            e = kda::launch_delta_prepare(a, stream);
+            if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+        }
         kda::DeltaArgs f = a;
         f.s_in = initial_state;
         f.planes = planes_at(ws, wl.forward);

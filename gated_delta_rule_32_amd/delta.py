@@ -31,8 +31,8 @@ class KdaDeltaProblem(ctypes.Structure):
 
 _declare("kda_delta_fwd_workspace_bytes", KdaDeltaProblem, ctypes.POINTER(_size))
 _declare("kda_delta_fwd", KdaDeltaProblem, *[_vp] * 9, _size, _vp)
-_declare("kda_delta_bwd_workspace_bytes", KdaDeltaProblem, ctypes.POINTER(_size))
-_declare("kda_delta_bwd", KdaDeltaProblem, *[_vp] * 15, _size, _vp)
+_declare("kda_delta_bwd_workspace_bytes", KdaDeltaProblem, ctypes.c_int32, ctypes.POINTER(_size))
+_declare("kda_delta_bwd", KdaDeltaProblem, *[_vp] * 7, _size, *[_vp] * 9, _size, _vp)
 _declare("kda_delta_infer_workspace_bytes", KdaDeltaProblem, ctypes.c_int32, ctypes.POINTER(_size))
 _declare("kda_delta_infer", KdaDeltaProblem, *[_vp] * 6, ctypes.c_int64, *[_vp] * 2, ctypes.c_int32, *[_vp] * 3, _size,
          _vp)
@@ -52,15 +52,17 @@ def kda_delta_fwd(p: KdaDeltaProblem, q, k, v, g, beta, initial_state, o, final_
           _ptr(initial_state), _ptr(o), _ptr(final_state), *_ws(workspace))
 
 
-def kda_delta_bwd_workspace_bytes(p: KdaDeltaProblem) -> int:
-    return _bytes("kda_delta_bwd_workspace_bytes", p)
+def kda_delta_bwd_workspace_bytes(p: KdaDeltaProblem, records_given: bool = False) -> int:
+    n = _size(0)
+    _check(_lib.kda_delta_bwd_workspace_bytes(_byref(p), bool(records_given), _byref(n)))
+    return int(n.value)
 
 
-def kda_delta_bwd(p: KdaDeltaProblem, q, k, v, g, beta, initial_state, d_o, dfinal_state, dq, dk, dv, dg, dbeta,
+def kda_delta_bwd(p: KdaDeltaProblem, q, k, v, g, beta, initial_state, records, d_o, dfinal_state, dq, dk, dv, dg, dbeta,
                   dinitial_state, workspace: torch.Tensor, stream: Optional[int] = None) -> None:
-    """C kda_delta_bwd on torch tensors."""
+    """C kda_delta_bwd on torch tensors (records: kda_delta_fwd's workspace, or None)."""
     _call(_lib.kda_delta_bwd, stream, q, _byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-          _ptr(initial_state), _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
+          _ptr(initial_state), *_ws(records), _ptr(d_o), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
           _ptr(dinitial_state), *_ws(workspace))
 
 
@@ -116,12 +118,14 @@ def _problem(q, k, v, g, beta, scale, use_qk_l2norm, cu_seqlens, cu_seqlens_cpu,
 
 @dataclass
 class GatedDeltaRuleTrainingContext:
-    """What the backward needs of the forward: its problem and its inputs
-    (cu_seqlens and its CPU mirror among them) with their versions (no device
-    memory of its own)."""
+    """What the backward needs of the forward: its problem, its inputs (cu_seqlens
+    and its CPU mirror among them) with their versions, and its chunks' records
+    (about 200 bytes a token and value head; None where the forward was given a
+    workspace, which the caller may have used again since)."""
     problem: KdaDeltaProblem
     inputs: tuple
     versions: tuple
+    records: Optional[torch.Tensor] = None
 
 
 def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, scale=None, out=None,
@@ -151,7 +155,7 @@ def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_s
     kda_delta_fwd(p, q, k, v, g, beta, initial_state, o, fs, ws)
     inputs = (q, k, v, g, beta, initial_state, cu_seqlens, cu_seqlens_cpu)
     versions = tuple(None if t is None else t._version for t in inputs)
-    return o, fs, GatedDeltaRuleTrainingContext(p, inputs, versions)
+    return o, fs, GatedDeltaRuleTrainingContext(p, inputs, versions, ws if workspace is None else None)
 
 
 def gated_delta_rule_training_backward(context: GatedDeltaRuleTrainingContext, do, dfinal_state=None,
@@ -177,8 +181,9 @@ def gated_delta_rule_training_backward(context: GatedDeltaRuleTrainingContext, d
                                          (_BF, _BF, _BF, _BF, _BF, _F32),
                                          (q.shape, k.shape, v.shape, g.shape, beta.shape, states)):
             _dense(name, t, dtype, shape, dev)
-    ws = _workspace(kda_delta_bwd_workspace_bytes(p), workspace, dev)
-    kda_delta_bwd(p, q, k, v, g, beta, s0, do, dfinal_state, *out, ws)
+    records = context.records
+    ws = _workspace(kda_delta_bwd_workspace_bytes(p, records is not None), workspace, dev)
+    kda_delta_bwd(p, q, k, v, g, beta, s0, records, do, dfinal_state, *out, ws)
     return tuple(out)
 
 

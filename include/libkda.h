@@ -520,23 +520,26 @@ kda_status kda_delta_fwd_workspace_bytes(const kda_delta_problem* p, size_t* byt
 
 /* Training forward.  q, k BF16 [B][T][Hqk][128], v, o BF16 [B][T][Hv][128],
  * states FP32 [N][Hv][128][128].  initial_state NULL starts from zero;
- * final_state may be NULL.  Nothing is saved for the backward, which reads
- * the inputs again. */
+ * final_state may be NULL.  The workspace is always needed; it then holds the
+ * chunks' records (12 KiB per 64 tokens and value head), which a backward of the same
+ * problem and inputs may be given. */
 kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
                          const void* beta, const float* initial_state, void* o, float* final_state,
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Training backward: the gradients of <do, o> + <dfinal_state, S_final> with
  * respect to the inputs as they were given (with use_qk_l2norm through the
- * norm).  dfinal_state NULL counts as zero; dinitial_state may be NULL.  dq and dk
- * sum over the value heads that share a q/k head, in head order; dg and dbeta are BF16
- * [B][T][Hv].  The workspace holds every block's states: about 107 KiB per 64 tokens and value
- * head. */
-kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, size_t* bytes);
+ * norm).  records: the workspace of the kda_delta_fwd with the same problem and inputs,
+ * untouched since, or NULL, and they are formed again.  dfinal_state NULL counts as
+ * zero; dinitial_state may be NULL.  dq and dk sum over the value heads that share a
+ * q/k head, in head order; dg and dbeta are BF16 [B][T][Hv].  The workspace holds every
+ * block's states: about 96 KiB per 64 tokens and value head, and the records when they
+ * are not given. */
+kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, int32_t records_given, size_t* bytes);
 kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
-                         const void* beta, const float* initial_state, const void* d_o, const float* dfinal_state,
-                         void* dq, void* dk, void* dv, void* dg, void* dbeta, float* dinitial_state,
-                         void* workspace, size_t workspace_bytes, void* stream);
+                         const void* beta, const float* initial_state, const void* records, size_t records_bytes,
+                         const void* d_o, const float* dfinal_state, void* dq, void* dk, void* dv, void* dg,
+                         void* dbeta, float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Decode (sequences of up to 8 tokens, token by token) and prefill (longer
  * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated

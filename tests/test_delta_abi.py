@@ -12,7 +12,7 @@ import torch
 import gated_delta_rule_32_amd as kda
 from oracle import delta_oracle as do_
 
-OK, NULL, SHAPE, GROUPING, SEQLENS, SCALE, OVERLAP, WS, ROUTE = 0, 1, 2, 3, 4, 5, 7, 10, 11
+OK, NULL, SHAPE, GROUPING, SEQLENS, SCALE, OVERLAP, CTX_SIZE, WS, ROUTE = 0, 1, 2, 3, 4, 5, 7, 8, 10, 11
 GAP = 1 << 36
 BIG = 1 << 35
 
@@ -34,10 +34,11 @@ def fwd(p, ws=90 * GAP, ws_bytes=BIG, **replace):
     return kda._lib.kda_delta_fwd(ctypes.byref(p), *a.values(), ws, ws_bytes, None)
 
 
-def bwd(p, ws=90 * GAP, ws_bytes=BIG, **replace):
+def bwd(p, ws=90 * GAP, ws_bytes=BIG, rec=None, rec_bytes=BIG, **replace):
     a = ptrs("q k v g beta s0 do ds dq dk dv dg db di")
     a.update(replace)
-    return kda._lib.kda_delta_bwd(ctypes.byref(p), *a.values(), ws, ws_bytes, None)
+    a = list(a.values())
+    return kda._lib.kda_delta_bwd(ctypes.byref(p), *a[:6], rec, rec_bytes, *a[6:], ws, ws_bytes, None)
 
 
 def infer(p, slots=40, idx=None, spec=0, acc=None, ws=90 * GAP, ws_bytes=BIG, **replace):
@@ -51,10 +52,9 @@ def infer(p, slots=40, idx=None, spec=0, acc=None, ws=90 * GAP, ws_bytes=BIG, **
 
 
 def sizes(p):
-    out = []
-    for name in ("fwd", "bwd"):
-        n = ctypes.c_size_t()
-        out.append(getattr(kda._lib, f"kda_delta_{name}_workspace_bytes")(ctypes.byref(p), ctypes.byref(n)))
+    n = ctypes.c_size_t()
+    out = [kda._lib.kda_delta_fwd_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           kda._lib.kda_delta_bwd_workspace_bytes(ctypes.byref(p), 0, ctypes.byref(n))]
     out.append(kda._lib.kda_delta_infer_workspace_bytes(ctypes.byref(p), 0, ctypes.byref(n)))
     return out
 
@@ -94,10 +94,14 @@ def test_refuses_arguments():
         assert infer(p, **{name: 20 * GAP + 8}) == SHAPE
     assert fwd(p, ws=None) == NULL and bwd(p, ws=None) == NULL and infer(p, ws=None) == NULL
     assert fwd(p, ws=90 * GAP + 4) == SHAPE
-    for call, name in ((fwd, "fwd"), (bwd, "bwd")):
-        n = ctypes.c_size_t()
-        assert getattr(kda._lib, f"kda_delta_{name}_workspace_bytes")(ctypes.byref(p), ctypes.byref(n)) == OK
-        assert call(p, ws_bytes=n.value - 1) == WS
+    n = ctypes.c_size_t()
+    assert kda._lib.kda_delta_fwd_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == OK
+    assert fwd(p, ws_bytes=n.value - 1) == WS
+    for rec in (None, 80 * GAP):
+        assert kda._lib.kda_delta_bwd_workspace_bytes(ctypes.byref(p), rec is not None, ctypes.byref(n)) == OK
+        assert bwd(p, ws_bytes=n.value - 1, rec=rec) == WS
+    assert bwd(p, rec=80 * GAP, rec_bytes=4 * 2 * 6144 - 1) == CTX_SIZE
+    assert bwd(p, rec=80 * GAP + 8) == SHAPE
 
 
 def test_refuses_overlaps():
@@ -111,6 +115,8 @@ def test_refuses_overlaps():
     assert bwd(p, dq=7 * GAP) == OVERLAP                       # dq over do
     assert bwd(p, dg=13 * GAP) == OVERLAP                      # dg over dbeta
     assert bwd(p, di=8 * GAP) == OVERLAP                       # dinitial over dfinal
+    assert bwd(p, rec=12 * GAP - 64) == OVERLAP                # records into dv's space
+    assert bwd(p, rec=90 * GAP) == OVERLAP                     # records in the workspace
     assert infer(p, o=6 * GAP) == OVERLAP
     assert infer(delta(B=2, T=1, N=2), idx=[0, 1], o=8 * GAP) == OVERLAP
 
@@ -158,10 +164,10 @@ def test_workspace_sizes():
     assert need("infer", p, 0) >= records
     assert need("infer", delta(T=8), 0) == 0                   # token by token
     assert need("infer", delta(T=40), 39) == 0
-    assert need("bwd", p) >= records + 2 * 4 * 4 * (32768 + 16384)
+    assert need("bwd", p, 0) == records + need("bwd", p, 1) >= records + 2 * 4 * 4 * (32768 + 16384)
     n = ctypes.c_size_t()
-    for name in ("fwd", "bwd"):
-        assert getattr(kda._lib, f"kda_delta_{name}_workspace_bytes")(ctypes.byref(p), None) == NULL
+    assert kda._lib.kda_delta_fwd_workspace_bytes(ctypes.byref(p), None) == NULL
+    assert kda._lib.kda_delta_bwd_workspace_bytes(ctypes.byref(p), 0, None) == NULL
     assert kda._lib.kda_delta_infer_workspace_bytes(None, 0, ctypes.byref(n)) == NULL
 
 

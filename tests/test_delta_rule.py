@@ -133,6 +133,24 @@ def test_training_step(case):
     du.check_gradients(inp, got[2:])
 
 
+@pytest.mark.parametrize("unit", [True, False])
+def test_gradients_with_records_formed_again(unit):
+    """A forward with a given workspace keeps no records: the backward forms them."""
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([70, 33, 100], True, 1, 2, seed=21, unit=unit, gates="mixed")
+    want = train(inp)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")   # (5 blocks of 2 heads need 120 KiB)
+    _, _, ctx = call_forward(inp, workspace=ws)
+    assert ctx.records is None
+    ws.fill_(255)
+    grads = kda.gated_delta_rule_training_backward(ctx, inp.dev(inp.do), inp.dev(inp.ds))
+    torch.cuda.synchronize()
+    du.check_gradients(inp, grads)
+    # (one over q's length is summed in another order there: equal to an FP32 rounding or two, and to the gradients' own)
+    for a, b in zip(want[4:7], grads[2:5]):
+        assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
+
+
 def test_training_step_without_states():
     """initial_state and dfinal_state None count as zero."""
     inp = Inp([5, 150, 64], True, 1, 2, seed=3, state=False)
@@ -227,18 +245,19 @@ def test_captured_training_step(packed):
     if packed:
         p.cu_seqlens, p.cu_seqlens_host = d["cu"].data_ptr(), inp.cu.data_ptr()
     outs = [torch.empty_like(d[n]) for n in ("v", "s0", "q", "k", "v", "g", "beta", "s0")]
-    need = max(kda.kda_delta_fwd_workspace_bytes(p), kda.kda_delta_bwd_workspace_bytes(p))
-    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    rec = torch.empty(kda.kda_delta_fwd_workspace_bytes(p), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda.kda_delta_bwd_workspace_bytes(p, True), dtype=torch.uint8, device="cuda")
     ins = [d[n] for n in ("q", "k", "v", "g", "beta", "s0")]
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        kda.kda_delta_fwd(p, *ins, outs[0], outs[1], ws)
-        kda.kda_delta_bwd(p, *ins, d["do"], d["ds"], *outs[2:], ws)
+        kda.kda_delta_fwd(p, *ins, outs[0], outs[1], rec)
+        kda.kda_delta_bwd(p, *ins, rec, d["do"], d["ds"], *outs[2:], ws)
     for _ in range(3):
         for x in outs:
             x.zero_()
         ws.fill_(255)    # (NaN: nothing of an earlier pass may be read)
+        rec.fill_(255)
         graph.replay()
         torch.cuda.synchronize()
         want = train(inp)
