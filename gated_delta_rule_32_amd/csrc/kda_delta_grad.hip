@@ -61,6 +61,7 @@ __device__ __forceinline__ float row16_before(float x) {
 // which large parts may cancel, go in as two BF16 pieces.
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 constexpr int GS_O = 0, GS_R = 4096, GS_S = GS_R + 8192, GS = GS_S + 16384;    // stage: do, rows, states
+constexpr int GS2 = 32768;                                                     // the second stage
 constexpr int GM = 32768, GN = GM + 16384, GTOTAL = GN + 16384;                // q, k rows; e; f
 __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     constexpr int TILES = 10;
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     __shared__ float dots[5][4][DB];        // per wave: q.(state part of dq), k.(its two parts of dk), then q.dq and k.dk
     __shared__ float sums[2][4][DB];        // of the tiles e q.k - f k.k: of a row, by column tile; of the rows i >= t before column t, by row tile
     __shared__ float diag[DB], whole[4];
-    static_assert(GTOTAL >= 2 * GS, "the products' areas lie over the two stages");
+    static_assert(GS <= GS2 && GTOTAL >= GS2 + GS, "the products' areas lie over the two stages");
 
     const int tid = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -112,27 +113,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
 
     auto finish = [&](float zs, int lane) __attribute__((always_inline)) {
     const int gq = lane >> 4, n16 = lane & 15, prow = 8 * gq + (n16 >> 2), pa = n16 & 3;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
     if (lane == 0) whole[w] = zs;
-    // the stages are read; q's and k's rows go over them
-    {
-        const bf16* src[2] = {(const bf16*)A.q, (const bf16*)A.k};
-        const int64_t stride[2] = {A.sq, A.sk};
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 16 * w + 4 * j;
-                char* d = lds + i * 16384 + r * 256;
-                if (r + gq < it.len)
-                    to_lds<false>((const char*)(src[i] + (it.tok0 + r) * stride[i] + (it.h / A.G) * D),
-                                  (unsigned)gq * (unsigned)(stride[i] * 2) + ((n16 ^ swz(4 * j + gq)) << 4), d);
-                else
-                    *(u32x4*)(d + lane * 16) = zero;
-            }
-    }
-    wait_vm<0>();
-    barrier_lds();
     constexpr int LQ = 0, LK = 16384;
     const int r8 = n16 * 256 + ((gq ^ swz(n16)) << 4);   // 8 channels 32p + 8gq of row n (xor 64p)
     // matrices of 64 rows of 128 bytes: block b of row r at b ^ r % 8; hi at 0, lo at 8192
@@ -388,6 +369,22 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         for (int j = 0; j < 4; ++j)
             to_lds<false>(pstate + (32 * vb + 4 * j) * 256, fresh(off_s) ^ (((2 * j & 2) | j >> 1) << 4), to + GS_S + w * 4096 + j * 1024);
     };
+    auto load_rows = [&]() __attribute__((always_inline)) {
+        const bf16* src[2] = {(const bf16*)A.q, (const bf16*)A.k};
+        const int64_t stride[2] = {A.sq, A.sk};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 16 * w + 4 * j;
+                char* d = lds + i * 16384 + r * 256;
+                if (r + gq < it.len)
+                    to_lds<false>((const char*)(src[i] + (it.tok0 + r) * stride[i] + (it.h / A.G) * D),
+                                  (unsigned)gq * (unsigned)(stride[i] * 2) + ((n16 ^ swz(4 * j + gq)) << 4), d);
+                else
+                    *(u32x4*)(d + lane * 16) = zero;
+            }
+    };
     // operands of 8 channels v = 32vb + 8gq ..: do, rows (0: W, 1: Y) and states (0: S, 1: Z)
     const int prow = 8 * gq + (n16 >> 2), pa = n16 & 3;   // this lane's row of a transposing read, and its piece there
     const int at_row = prow * 64 + ((gq & 1) << 5) + 8 * pa;
@@ -408,7 +405,10 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     const float* w_scale = A.forward.row_scale + blk * 8;
     const float* y_scale = A.backward.row_scale + blk * 8;
     auto part = [&](int vb, const char* __restrict__ from, char* __restrict__ to) __attribute__((always_inline)) {
-        if (vb < 3) load_stage(to, vb + 1);
+        if (vb < 3)
+            load_stage(to, vb + 1);
+        else   // q's and k's rows, over the first stage
+            load_rows();
         const float fs = s_scale[vb], fz = z_scale[vb];
         const float fw[2] = {w_scale[vb], second ? w_scale[4 + vb] : 0.0f}, fy[2] = {y_scale[vb], second ? y_scale[4 + vb] : 0.0f};
         const f16x8 yr = get_row(from, 1, w);
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     load_stage(lds, 0);
     wait_vm<0>();
     barrier_lds();
-    for (int vb = 0; vb < 4; ++vb) part(vb, lds + (vb & 1) * GS, lds + (~vb & 1) * GS);
+    for (int vb = 0; vb < 4; ++vb) part(vb, lds + (vb & 1) * GS2, lds + (~vb & 1) * GS2);
     zs = group_sum<64>(zs);
     finish(zs, fresh(tid & 63));
 }
