@@ -50,6 +50,12 @@ struct DeltaArgs {
     int64_t slots;
     DeltaPlanes planes;         // what a scan leaves for the gradients
     const bf16_t* d_o;          // [tokens][Hv][128]
+    // of sequences cut into segments (map), per segment and value head: what the segment adds
+    // to a state, in whose place the chain puts the state before it, [128 v][128 k], and what it
+    // makes of one, M transposed, [128 k][128 k']: S <- S M + Q.  Null: not cut.
+    float* seg;                 // [segments][Hv][2][128][128]
+    float* behind;              // of the adjoint likewise the first: [segments][Hv][128][128]
+    ItemMap seqs;               // the whole sequences
 };
 
 // The gradients of a block of tokens from what the two scans left: the state before the
@@ -87,8 +93,11 @@ struct DeltaTokenArgs {
 };
 
 hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s);
-enum DeltaMode { kDeltaOut = 0, kDeltaRecord = 1 };
+enum DeltaMode { kDeltaOut = 0, kDeltaRecord = 1, kDeltaState = 2 };
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);   // o and the final states
+hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s);   // M and Q, and the states chained
+hipError_t launch_delta_chain(const DeltaArgs& a, bool reverse, hipStream_t s);
+hipError_t launch_delta_behind(const DeltaArgs& a, hipStream_t s);     // the same of the adjoint, M being there
 // The backward's two scans at once: `forward` leaves its planes, `backward` its own and the
 // adjoint of the initial states.
 hipError_t launch_delta_both(const DeltaArgs& forward, const DeltaArgs& backward, hipStream_t s);

@@ -238,15 +238,120 @@ __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_scan_kernel(DeltaA
 
 template <int kMode>
 static hipError_t launch_scan(const DeltaArgs& a, hipStream_t s) {
-    if (a.map.items <= 128)
-        hipLaunchKernelGGL((delta_scan_kernel<1, 2, kMode>), dim3((unsigned)(a.map.items * 2)), dim3(256), 0, s, a);
-    else if (a.map.items <= 256)
-        hipLaunchKernelGGL((delta_scan_kernel<1, 1, kMode>), dim3((unsigned)a.map.items), dim3(512), 0, s, a);
+    const int64_t items = a.map.items * (kMode == kDeltaState ? 2 : 1);
+    if (items <= 128)
+        hipLaunchKernelGGL((delta_scan_kernel<1, 2, kMode>), dim3((unsigned)(items * 2)), dim3(256), 0, s, a);
+    else if (items <= 256)
+        hipLaunchKernelGGL((delta_scan_kernel<1, 1, kMode>), dim3((unsigned)items), dim3(512), 0, s, a);
     else
-        hipLaunchKernelGGL((delta_scan_kernel<2, 1, kMode>), dim3((unsigned)a.map.items), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((delta_scan_kernel<2, 1, kMode>), dim3((unsigned)items), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) { return launch_scan<kDeltaOut>(a, s); }
+
+// The states before the segments, S <- S M + Q from one to the next; kReverse: the adjoints behind
+// them, Z <- Z M^T + R from the last to the first.  A workgroup per sequence, value head and 16 channels v,
+// wave t with their tile of the state as in the scan.  The product is exact to FP32, both
+// factors in three BF16 pieces.  Bound by the way of the M's: those of the next two segments
+// are on theirs.
+template <bool kReverse>
+__global__ __launch_bounds__(512) void delta_chain_kernel(DeltaArgs A) {
+    __shared__ __align__(16) char lds[2][3 * 4 * 1024];   // the state in pieces: [piece][32 channels k][lane][8]
+    const Item it = find_item(A.seqs, blockIdx.x >> 3);
+    const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
+    if (slot < 0 || slot >= A.slots) return;
+    const int Hv = A.map.Hv;
+    const int t = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, gq = lane >> 4, n16 = lane & 15;
+    const int64_t per = A.map.seg_len;
+    const int segs = (int)((it.len + per - 1) / per);
+    const int64_t first = A.map.task != nullptr ? A.map.tape_off[it.n] + it.n : it.n * (int64_t)segs;
+    // (a place i counts from the chain's start)
+    const int64_t item = (first + (kReverse ? segs - 1 : 0)) * Hv + it.h;
+    const int64_t step = kReverse ? -Hv : Hv;
+    const int64_t size = kReverse ? STATE : 2 * STATE;
+    const int at = (16 * (blockIdx.x & 7) + n16) * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1);
+    float* own = (kReverse ? A.behind : A.seg) + item * size + at;
+    // of M transposed, [k][k']: 8 values k' of the row k that belongs to lane n, or (reverse) 8 rows k of column k'
+    const int row = 32 * (t >> 1) + 8 * (n16 >> 2) + 4 * (t & 1) + (n16 & 3);
+    const float* map = A.seg + item * (2 * STATE) + STATE + (kReverse ? 8 * gq * D + row : row * D + 8 * gq);
+    auto get_map = [&](int i, f32x4 (&m)[4][2]) __attribute__((always_inline)) {
+        const float* from = map + i * step * (2 * STATE);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (kReverse) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[p][j][e] = from[(32 * p + 4 * j + e) * D];
+                } else {
+                    m[p][j] = *(const f32x4*)(from + 32 * p + 4 * j);
+                }
+            }
+    };
+    auto get_own = [&](int i) __attribute__((always_inline)) { return *(const f32x4*)(own + i * step * size); };
+
+    const Pieces pieces(lane);
+    f32x4 x = A.s_in != nullptr ? *(const f32x4*)(A.s_in + (slot * Hv + it.h) * (int64_t)STATE + at) : zero4();
+    f32x4 m1[4][2], m2[4][2], q0 = zero4(), q1 = zero4(), q2 = zero4();
+    if (segs > 1) q0 = get_own(0);
+    if (segs > 2) {
+        q1 = get_own(1);
+        get_map(1, m1);
+    }
+    if (segs > 3) {
+        q2 = get_own(2);
+        get_map(2, m2);
+    }
+    *(f32x4*)own = x;
+    if (segs == 1) return;
+    x = q0;   // (the first place's own sum starts from s_in)
+    auto place = [&](int i, f32x4 (&m)[4][2], f32x4& q, char* to) __attribute__((always_inline)) {
+        *(f32x4*)(own + i * step * size) = x;
+        if (i + 1 == segs) return false;
+        bf16x4 a[3];
+        pieces.split(x, a[0], a[1], a[2]);
+#pragma unroll
+        for (int d = 0; d < 3; ++d) *(bf16x4*)(to + ((d * 4 + (t >> 1)) * 64 + lane) * 16 + 8 * (t & 1)) = a[d];
+        barrier_lds();
+        x = q;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            bf16x4 m0[3], m1[3];
+            pieces.split(m[p][0], m0[0], m0[1], m0[2]);
+            pieces.split(m[p][1], m1[0], m1[1], m1[2]);
+            bf16x8 b[3];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) b[d] = *(const bf16x8*)(to + ((d * 4 + p) * 64 + lane) * 16);
+#pragma unroll
+            for (int i = 2; i >= 0; --i)
+#pragma unroll
+                for (int d = 0; d <= i; ++d) x = mma32(cat8(m0[d], m1[d]), b[i - d], x);
+        }
+        if (i + 3 < segs) {
+            q = get_own(i + 2);
+            get_map(i + 2, m);
+        }
+        return true;
+    };
+    for (int i = 1;; i += 2) {
+        if (!place(i, m1, q1, lds[0])) break;
+        if (!place(i + 1, m2, q2, lds[1])) break;
+    }
+}
+
+hipError_t launch_delta_chain(const DeltaArgs& a, bool reverse, hipStream_t s) {
+    const dim3 grid((unsigned)(a.seqs.items * 8));
+    if (reverse)
+        hipLaunchKernelGGL((delta_chain_kernel<true>), grid, dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((delta_chain_kernel<false>), grid, dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s) {
+    const hipError_t e = launch_scan<kDeltaState>(a, s);
+    return e == hipSuccess ? launch_delta_chain(a, false, s) : e;
+}
 
 // Token-serial form on the FP32 state pool (decode, drafted tokens, and sequences of a few
 // tokens).  A workgroup takes 32 of the 128 state rows of one (sequence, value head): a half

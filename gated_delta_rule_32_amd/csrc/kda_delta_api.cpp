@@ -14,6 +14,8 @@ namespace {
 
 using namespace kda_host;
 
+constexpr int kDeltaChunk = 32;
+
 struct Delta {
     Seqs s;
     int B = 0, T = 0;
@@ -56,14 +58,58 @@ int64_t total_blocks(const Delta& d) {
     return n;
 }
 
-// The chunks' records.
+int64_t total_segs(const Delta& d, int seg) {
+    int64_t n = 0;
+    for (int64_t len : d.s.len) n += (len + seg - 1) / seg;
+    return n;
+}
+
+// Tokens of the segments that the scans walk side by side, or 0 for whole sequences:
+// whichever an estimate says is faster.  A scan over whole sequences takes the longest one's
+// latency, 2.4 to 2.9 us a chunk of 32 tokens, or the total's throughput, 15 ns a chunk and
+// head.  Segments shorten the first, for a scan that forms each one's M and Q, and 2.4 us for
+// every segment of the chain that joins them.  Both scans' chunk together takes 4.1 us with 64
+// segments and heads, 4.8 with 128, 7.9 with 256 and 32 ns each with more.
+// In us, forward and backward, whole sequences against the segments of this rule:
+// 16 heads x 1024 tokens 92, 130 / 68, 91; 32 x 2048 170, 264 / 117, 190; 16 x 4096 320, 451 / 128,
+// 203; 8 x 8192 618, 831 / 148, 217; 32 x 8192 634, 1006 / 296, 602; 16 x 32768 2490, 3539 / 601, 1194;
+// 64 x 16384 1325, 2441 / 1041, 2296; 4 x 65536 4866, 6321 / 422, 749; 2 sequences x 32 x 4096
+// 348, 637 / 289, 595; and against segments that it does not take, forward: 4 x 32 x 4096 389 / 484 (of
+// 1024 tokens), 96 x 32768 2778 / 2969 (of 8192).  Other lengths than its own: 16 x 32768 730, 593, 682
+// in segments of 512, 1024 and 4096, 32 x 8192 320, 355 of 512 and 2048, 16 x 4096 181, 138, 158 of 128,
+// 256 and 1024.
+int auto_segment(const Delta& d) {
+    if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
+    double chunks = 0;
+    for (int64_t len : d.s.len) chunks += (double)((len + kDeltaChunk - 1) / kDeltaChunk);
+    const double items = (double)d.s.N * d.s.Hv;
+    const double whole = std::max((2.4 + 0.002 * std::min(items, 256.0)) * (double)((d.s.max_len + kDeltaChunk - 1) / kDeltaChunk),
+                                  0.0151 * chunks * d.s.Hv);
+    double best = 0.95 * whole;
+    int seg = 0;
+    for (int wanted = 64; wanted <= 512; wanted *= 2) {
+        const int64_t len = (d.s.tokens * d.s.Hv / wanted + 63) / 64 * 64;
+        if (len < 64 || len >= d.s.max_len) continue;
+        const double n = (double)total_segs(d, (int)len) * d.s.Hv;
+        const double pair = n <= 128 ? 3.4 + 0.011 * n : n <= 256 ? 7.9 : 0.032 * n;
+        const double cut = pair * (double)(len / kDeltaChunk) + 2.4 * (double)((d.s.max_len + len - 1) / len) + 12.0;
+        if (cut < best) {
+            best = cut;
+            seg = (int)len;
+        }
+    }
+    return seg;
+}
+
+// The chunks' records, and with segments their states.  (The records first: a backward is
+// given them.)
 struct RecordWs {
-    size_t rec = 0, total = 0;
+    size_t rec = 0, seg = 0, total = 0;
 };
-RecordWs record_ws(const Delta& d, int64_t blocks, size_t off = 0) {
+RecordWs record_ws(const Delta& d, int seg) {
     RecordWs w;
-    w.rec = off;
-    w.total = align256(off + (size_t)blocks * d.s.Hv * 2 * kda::REC);
+    w.seg = align256((size_t)total_blocks(d) * d.s.Hv * 2 * kda::REC);
+    w.total = align256(w.seg + (seg ? (size_t)total_segs(d, seg) * d.s.Hv * 2 * kState * sizeof(float) : 0));
     return w;
 }
 
@@ -75,12 +121,12 @@ struct PlanesWs {
 struct GradWs {
     RecordWs r;
     PlanesWs forward, backward;
-    size_t part_q = 0, part_k = 0, total = 0;
+    size_t part_q = 0, part_k = 0, behind = 0, total = 0;
 };
-GradWs grad_ws(const Delta& d, bool records) {
+GradWs grad_ws(const Delta& d, int seg, bool records) {
     GradWs g;
     const int64_t blocks = total_blocks(d);
-    if (!records) g.r = record_ws(d, blocks);
+    if (!records) g.r = record_ws(d, seg);
     size_t off = g.r.total;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -97,6 +143,7 @@ GradWs grad_ws(const Delta& d, bool records) {
     const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
     g.part_q = take(part);
     g.part_k = take(part);
+    g.behind = take(seg ? (size_t)total_segs(d, seg) * d.s.Hv * kState * sizeof(float) : 0);
     g.total = off;
     return g;
 }
@@ -104,28 +151,61 @@ kda::DeltaPlanes planes_at(char* ws, const PlanesWs& p) {
     return {(_Float16*)(ws + p.state), (_Float16*)(ws + p.rows), (float*)(ws + p.state_scale), (float*)(ws + p.row_scale)};
 }
 
-// The item maps of a call (whole sequences, and blocks of 64 tokens) and its hold on the
-// device schedule (packed calls).
-kda_status make_maps(const Delta& d, hipStream_t stream, SeqPlan& plan, kda::DeltaArgs& a) {
-    kda::ItemMap m{};
-    m.N = d.s.N;
-    m.Hv = d.s.Hv;
-    m.len = d.T;
-    if (d.packed) {
-        kda_status s = get_seq_plan(d.s, d.B, d.T, d.packed, kda::DB, stream, plan);
+// The item maps of a call (whole sequences, blocks of 64 tokens, and the scan's: the
+// former or segments of `seg` tokens) and its hold on the device schedules (packed calls).
+struct Plans {
+    SeqPlan blocks, segs;
+};
+kda_status make_maps(const Delta& d, int seg, hipStream_t stream, Plans& plans, kda::DeltaArgs& a) {
+    auto map = [&](int len, SeqPlan& plan, kda::ItemMap& m) -> kda_status {
+        m = {};
+        m.N = d.s.N;
+        m.Hv = d.s.Hv;
+        m.len = d.T;
+        m.seg_len = len;
+        m.items = total_segs(d, len) * d.s.Hv;
+        if (!d.packed) return KDA_OK;
+        kda_status s = get_seq_plan(d.s, d.B, d.T, d.packed, len, stream, plan);
         if (s != KDA_OK) return s;
         m.task = plan.dev.task;
         m.seg = plan.seg;
         m.seq_start = plan.dev.seq_start;
         m.seq_len = plan.dev.seq_len;
         m.tape_off = plan.dev.tape_off;
+        return KDA_OK;
+    };
+    kda_status s = map(kda::DB, plans.blocks, a.blocks);
+    if (s != KDA_OK) return s;
+    a.seqs = a.blocks;
+    a.seqs.seg_len = 0;
+    a.seqs.items = (int64_t)d.s.N * d.s.Hv;
+    a.map = a.seqs;
+    return seg != 0 ? map(seg, plans.segs, a.map) : KDA_OK;
+}
+
+// The chunks' records and the segments' states.
+kda_status run_records(const kda::DeltaArgs& a, hipStream_t stream) {
+    hipError_t e = kda::launch_delta_prepare(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
+    if (a.seg != nullptr) {
+        e = kda::launch_delta_segments(a, stream);
+        if (e != hipSuccess) return hip_fail(e, "delta segment launch");
     }
-    a.map = m;
-    a.map.items = (int64_t)d.s.N * d.s.Hv;
-    a.blocks = m;
-    a.blocks.seg_len = kda::DB;
-    a.blocks.items = total_blocks(d) * d.s.Hv;
     return KDA_OK;
+}
+kda_status run_forward(const kda::DeltaArgs& a, hipStream_t stream) {
+    kda_status s = run_records(a, stream);
+    if (s != KDA_OK) return s;
+    hipError_t e = kda::launch_delta_scan(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "delta scan launch");
+    return KDA_OK;
+}
+// The grids of these launches.
+kda_status check_forward_grid(const kda::DeltaArgs& a) {
+    kda_status s = check_grid(a.map.items * 4);
+    if (s == KDA_OK) s = check_grid(a.blocks.items);
+    if (s == KDA_OK) s = check_grid(a.seqs.items * 8);
+    return s;
 }
 
 void set_inputs(const Delta& d, const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -155,21 +235,31 @@ std::vector<Span> input_spans(const kda_delta_problem* pp, const Delta& d, const
 // length, so that a user's tokens are computed the same way whoever else is in the batch.
 constexpr int64_t kTokenSerialMax = 8;
 
-// Whether some sequence runs in chunks, and how many do (a packed call's schedule has them
-// first), with how many blocks.
+// How many sequences run in chunks (a packed call's schedule has them first), with how many
+// blocks and segments of `seg` tokens (0: whole).
 struct InferPlan {
-    int64_t chunked = 0, blocks = 0;
+    int64_t chunked = 0, blocks = 0, segs = 0;
+    int seg = 0;
     RecordWs ws;
 };
 InferPlan infer_plan(const Delta& d, int spec) {
     InferPlan r;
     if (spec > 0 || d.s.max_len <= kTokenSerialMax) return r;
+    Delta c;
+    c.segment = d.segment;
+    c.unit = d.unit;
+    c.s.Hv = d.s.Hv;
+    c.s.max_len = d.s.max_len;
     for (int64_t len : d.s.len)
         if (len > kTokenSerialMax) {
-            ++r.chunked;
-            r.blocks += (len + kda::DB - 1) / kda::DB;
+            c.s.len.push_back(len);
+            c.s.tokens += len;
         }
-    r.ws = record_ws(d, total_blocks(d));   // (blocks are numbered among all sequences)
+    r.chunked = c.s.N = (int)c.s.len.size();
+    r.blocks = total_blocks(c);
+    r.seg = auto_segment(c);
+    if (r.seg != 0) r.segs = total_segs(c, r.seg);
+    r.ws = record_ws(d, r.seg);   // (blocks and segments are numbered among all sequences)
     return r;
 }
 
@@ -183,7 +273,7 @@ kda_status kda_delta_fwd_workspace_bytes(const kda_delta_problem* pp, size_t* by
         kda_status s = check_delta(pp, d);
         if (s != KDA_OK) return s;
         if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
-        *bytes = record_ws(d, total_blocks(d)).total;
+        *bytes = record_ws(d, auto_segment(d)).total;
         return KDA_OK;
     });
 }
@@ -200,7 +290,8 @@ kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void*
         s = check_align({{q, "q"}, {k, "k"}, {v, "v"}, {initial_state, "initial_state"}, {o, "o"},
                          {final_state, "final_state"}});
         if (s != KDA_OK) return s;
-        const RecordWs w = record_ws(d, total_blocks(d));
+        const int seg = auto_segment(d);
+        const RecordWs w = record_ws(d, seg);
         if ((s = check_ws(workspace, workspace_bytes, w.total)) != KDA_OK) return s;
         const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
         std::vector<Span> ins = input_spans(pp, d, q, k, v, g, beta);
@@ -210,21 +301,17 @@ kda_status kda_delta_fwd(const kda_delta_problem* pp, const void* q, const void*
                            {workspace, w.total, "workspace"}}, ins);
         if (s != KDA_OK) return s;
         hipStream_t stream = (hipStream_t)stream_;
-        SeqPlan plan;
+        Plans plans;
         kda::DeltaArgs a{};
-        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
-        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
+        if ((s = make_maps(d, seg, stream, plans, a)) != KDA_OK || (s = check_forward_grid(a)) != KDA_OK) return s;
         set_inputs(d, q, k, v, g, beta, a);
         a.rec = (char*)workspace + w.rec;
+        if (seg != 0) a.seg = (float*)((char*)workspace + w.seg);
         a.o = (kda::bf16_t*)o;
         a.s_in = initial_state;
         a.s_out = final_state;
         a.slots = d.s.N;
-        hipError_t e = kda::launch_delta_prepare(a, stream);
-        if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-        e = kda::launch_delta_scan(a, stream);
-        if (e != hipSuccess) return hip_fail(e, "delta scan launch");
-        return KDA_OK;
+        return run_forward(a, stream);
     });
 }
 
@@ -234,7 +321,7 @@ kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* pp, int32_t re
         kda_status s = check_delta(pp, d);
         if (s != KDA_OK) return s;
         if (bytes == nullptr) return fail(KDA_ERR_NULL_ARG, "bytes is NULL");
-        *bytes = grad_ws(d, records_given != 0).total;
+        *bytes = grad_ws(d, auto_segment(d), records_given != 0).total;
         return KDA_OK;
     });
 }
@@ -253,12 +340,14 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
                          {dfinal_state, "dfinal_state"}, {dq, "dq"}, {dk, "dk"}, {dv, "dv"},
                          {dinitial_state, "dinitial_state"}});
         if (s != KDA_OK) return s;
-        const size_t rec = record_ws(d, total_blocks(d)).total;
+        const int seg = auto_segment(d);
+        const RecordWs given = record_ws(d, seg);
+        const size_t rec = given.total;
         if (records != nullptr) {
             if (records_bytes < rec) return fail(KDA_ERR_CTX_SIZE, "records have %zu bytes, need %zu", records_bytes, rec);
             if ((s = check_align(records, "records")) != KDA_OK) return s;
         }
-        const GradWs wl = grad_ws(d, records != nullptr);
+        const GradWs wl = grad_ws(d, seg, records != nullptr);
         if ((s = check_ws(workspace, workspace_bytes, wl.total)) != KDA_OK) return s;
         const size_t st = (size_t)d.s.N * d.s.Hv * kState * 4;
         const size_t tq = (size_t)d.s.tokens * d.s.Hqk * D * 2, tv = (size_t)d.s.tokens * d.s.Hv * D * 2,
@@ -273,28 +362,30 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
                            {workspace, wl.total, "workspace"}}, ins);
         if (s != KDA_OK) return s;
         hipStream_t stream = (hipStream_t)stream_;
-        SeqPlan plan;
+        Plans plans;
         kda::DeltaArgs a{};
-        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
-        if ((s = check_grid(a.map.items * 4)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK) return s;
+        if ((s = make_maps(d, seg, stream, plans, a)) != KDA_OK || (s = check_forward_grid(a)) != KDA_OK) return s;
         if (d.s.G > 1 && (s = check_grid((d.s.tokens * d.s.Hqk * (D / 8) + 255) / 256)) != KDA_OK) return s;
         char* ws = (char*)workspace;
         set_inputs(d, q, k, v, g, beta, a);
         a.rec = records != nullptr ? (char*)records : ws + wl.r.rec;
+        if (seg != 0) a.seg = (float*)(records != nullptr ? (char*)records + given.seg : ws + wl.r.seg);
         a.rq = 1;
         a.slots = d.s.N;
         a.d_o = (const kda::bf16_t*)d_o;
-        hipError_t e;
-        if (records == nullptr) {
-            e = kda::launch_delta_prepare(a, stream);
-            if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-        }
         kda::DeltaArgs f = a;
         f.s_in = initial_state;
         f.planes = planes_at(ws, wl.forward);
+        hipError_t e;
+        if (records == nullptr && (s = run_records(f, stream)) != KDA_OK) return s;
         a.s_in = dfinal_state;
         a.s_out = dinitial_state;
         a.planes = planes_at(ws, wl.backward);
+        if (seg != 0) {
+            a.behind = (float*)(ws + wl.behind);
+            e = kda::launch_delta_behind(a, stream);
+            if (e != hipSuccess) return hip_fail(e, "delta adjoint launch");
+        }
         e = kda::launch_delta_both(f, a, stream);
         if (e != hipSuccess) return hip_fail(e, "delta scans launch");
         const bool pack = d.s.G > 1;
@@ -394,16 +485,14 @@ kda_status kda_delta_infer(const kda_delta_problem* pp, const void* q, const voi
                            {workspace, ip.ws.total, "workspace"}}, ins);
         if (s != KDA_OK) return s;
         hipStream_t stream = (hipStream_t)stream_;
-        SeqPlan plan;
+        Plans plans;
         kda::DeltaArgs a{};
-        if ((s = make_maps(d, stream, plan, a)) != KDA_OK) return s;
+        if ((s = make_maps(d, ip.seg, stream, plans, a)) != KDA_OK) return s;
         const int64_t serial = d.s.N - ip.chunked;
-        a.map.items = ip.chunked * d.s.Hv;
+        a.seqs.items = ip.chunked * d.s.Hv;
+        a.map.items = ip.seg != 0 ? ip.segs * d.s.Hv : a.seqs.items;
         a.blocks.items = ip.blocks * d.s.Hv;
-        if ((s = check_grid(a.map.items * 2)) != KDA_OK || (s = check_grid(a.blocks.items)) != KDA_OK ||
-            (s = check_grid(serial * d.s.Hv * 4)) != KDA_OK)
-            return s;
-        hipError_t e;
+        if ((s = check_forward_grid(a)) != KDA_OK || (s = check_grid(serial * d.s.Hv * 4)) != KDA_OK) return s;
         if (ip.chunked != 0) {
             set_inputs(d, q, k, v, g, beta, a);
             a.rec = (char*)workspace + ip.ws.rec;
@@ -411,16 +500,13 @@ kda_status kda_delta_infer(const kda_delta_problem* pp, const void* q, const voi
             a.s_in = a.s_out = state_pool;
             a.slot = state_indices;
             a.slots = pool_slots;
-            e = kda::launch_delta_prepare(a, stream);
-            if (e != hipSuccess) return hip_fail(e, "delta prepare launch");
-            e = kda::launch_delta_scan(a, stream);
-            if (e != hipSuccess) return hip_fail(e, "delta scan launch");
-            if (serial == 0) return KDA_OK;
+            if (ip.seg != 0) a.seg = (float*)((char*)workspace + ip.ws.seg);
+            if ((s = run_forward(a, stream)) != KDA_OK || serial == 0) return s;
         }
         kda::DeltaTokenArgs t{};
-        t.map = a.map;
+        t.map = a.seqs;
         t.map.items = serial * d.s.Hv;
-        if (d.packed) t.map.task = a.map.task + ip.chunked * d.s.Hv;
+        if (d.packed) t.map.task = a.seqs.task + ip.chunked * d.s.Hv;
         t.q = (const kda::bf16_t*)q; t.sq = d.sq;
         t.k = (const kda::bf16_t*)k; t.sk = d.sk;
         t.v = (const kda::bf16_t*)v; t.sv = d.sv;
@@ -435,7 +521,7 @@ kda_status kda_delta_infer(const kda_delta_problem* pp, const void* q, const voi
         t.slots = pool_slots;
         t.each = 1 + spec;
         t.accepted = num_accepted_tokens;
-        e = kda::launch_delta_token(t, stream);
+        const hipError_t e = kda::launch_delta_token(t, stream);
         if (e != hipSuccess) return hip_fail(e, "delta decode launch");
         return KDA_OK;
     });

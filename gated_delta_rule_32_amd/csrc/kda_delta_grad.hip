@@ -13,7 +13,7 @@ __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_both_kernel(DeltaA
     // (the longer chunks of the backward first)
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
-        delta_adjoint<NU, kParts>(backward, blockIdx.x, half, lds);
+        delta_adjoint<NU, kParts, false>(backward, blockIdx.x, half, lds);
     else
         delta_scan<NU, kParts, kDeltaRecord>(forward, blockIdx.x - half, half, lds);
 }
@@ -27,6 +27,24 @@ hipError_t launch_delta_both(const DeltaArgs& f, const DeltaArgs& b, hipStream_t
     else
         hipLaunchKernelGGL((delta_both_kernel<2, 1>), dim3(items * 2), dim3(256), 0, s, f, b);
     return hipGetLastError();
+}
+
+template <int NU, int kParts>
+__global__ __launch_bounds__(512 / NU / kParts, 2) void delta_behind_kernel(DeltaArgs A) {
+    __shared__ __align__(16) char lds[DeltaAdjointLds::TOTAL];
+    delta_adjoint<NU, kParts, true>(A, blockIdx.x, gridDim.x, lds);
+}
+
+hipError_t launch_delta_behind(const DeltaArgs& a, hipStream_t s) {
+    const unsigned items = (unsigned)a.map.items;
+    if (items <= 128)
+        hipLaunchKernelGGL((delta_behind_kernel<1, 2>), dim3(items * 2), dim3(256), 0, s, a);
+    else if (items <= 256)
+        hipLaunchKernelGGL((delta_behind_kernel<1, 1>), dim3(items), dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((delta_behind_kernel<2, 1>), dim3(items), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? launch_delta_chain(a, true, s) : e;
 }
 
 // Sum over the lanes before this one in its row of 16.

@@ -155,20 +155,30 @@ struct PlaneWriter {
 
 template <int NU, int kParts, int kMode>
 __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int grid, char* lds) {
-    constexpr bool kOut = kMode == kDeltaOut, kRecord = kMode == kDeltaRecord;
+    constexpr bool kOut = kMode == kDeltaOut, kRecord = kMode == kDeltaRecord, kState = kMode == kDeltaState;
+    constexpr int kJobs = kState ? 2 : 1;
     typedef DeltaScanLds<kMode> M;
     constexpr int NW = 8 / NU / kParts;
 
-    int idx = xcd_order(block, grid, A.G * kParts);
+    int idx = xcd_order(block, grid, A.G * kParts * kJobs);
     const int part = idx % kParts;
     idx /= kParts;
+    const bool map_job = kState && (idx & 1) != 0;   // what the segment makes of a state: V zero, from the identity
+    idx /= kJobs;
     const DeltaLane<NU, kParts> L(part);
     const int w = L.w, lane = L.lane, gq = L.gq, n16 = L.n16;
     const Item it = find_item(A.map, idx);
+    // of a sequence's segments, the last one's state is not needed, nor the first one's map
+    const bool last = it.off + it.len >= (A.map.task != nullptr ? A.map.seq_len[it.n] : A.map.len);
+    if (kState && (last || (map_job && it.off == 0))) return;
     const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
     if (slot < 0 || slot >= A.slots) return;
     const int Hv = A.map.Hv;
     const int64_t soff = (slot * Hv + it.h) * (int64_t)STATE;
+    float* seg = A.seg == nullptr ? nullptr : A.seg + (it.seg * Hv + it.h) * (int64_t)(2 * STATE);
+    const float* s_in = !kState && seg != nullptr ? seg
+                        : A.s_in != nullptr && !(kState && (map_job || it.off != 0)) ? A.s_in + soff
+                                                                                     : nullptr;
     // the item's first block among all blocks
     const int64_t block0 = (A.blocks.task != nullptr ? A.blocks.tape_off[it.n] + it.n
                                                      : (int64_t)it.n * ((A.blocks.len + DB - 1) / DB)) + it.off / DB;
@@ -205,7 +215,15 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int u = 0; u < NU; ++u)
-            S[t][u] = A.s_in != nullptr ? *(const f32x4*)(A.s_in + soff + (L.vrow + 4 * u) * D + L.krow(t)) : zero4();
+            S[t][u] = s_in != nullptr ? *(const f32x4*)(s_in + (L.vrow + 4 * u) * D + L.krow(t)) : zero4();
+    if (map_job)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[t][u][e] = L.krow(t) + e == L.vrow + 4 * u ? 1.0f : 0.0f;
+    const unsigned v_mask = map_job ? 0u : ~0u;
 
     const PlaneWriter<NU, kParts> planes{L, (float (*)[8][2])(lds + M::X)};
     auto state_max = [&]() __attribute__((always_inline)) {
@@ -306,7 +324,9 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
             const f32x4 cx = num4(REC_FROM_K, 16 * ti + 4 * gq) * before;
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                const f32x4 vf = from_bf4(tr_read(v + L.trv + 8 * u + DROWS16 * ti));
+                bf16x4 vb = tr_read(v + L.trv + 8 * u + DROWS16 * ti);
+                if (kState) vb = __builtin_bit_cast(bf16x4, __builtin_bit_cast(u32x2, vb) & v_mask);
+                const f32x4 vf = from_bf4(vb);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) wr[ti][u][e] = fmaf(-cx[e], x[ti][u][e], vf[e]);
             }
@@ -396,6 +416,10 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
             po += SC * sy;
             if (lengths != nullptr && lane < SC) lengths[lane] = lds_q[lane];   // (for a backward that is given the records)
         }
+        if (kState) {
+            if (more) wait_vm<0>();
+            barrier_lds();
+        }
         if (kRecord) {
             // the planes of this chunk's rows, and of the state when it is the next block's
             const bool edge = (c & 1) != 0 && more;
@@ -426,7 +450,7 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
     for (; c < steady; ++c) at(c, std::true_type{});
     for (; c < chunks; ++c) at(c, std::false_type{});
 
-    if (A.s_out != nullptr) {
+    if (kState || (A.s_out != nullptr && last)) {
         const Factor decay(held);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -435,7 +459,12 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
                 f32x4 r;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) r[e] = decay.apply(S[t][u][e]);
-                *(f32x4*)(A.s_out + soff + (L.vrow + 4 * u) * D + L.krow(t)) = r;
+                if (map_job) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) seg[STATE + (L.krow(t) + e) * D + L.vrow + 4 * u] = r[e];
+                    continue;
+                }
+                *(f32x4*)((kState ? seg : A.s_out + soff) + (L.vrow + 4 * u) * D + L.krow(t)) = r;
             }
     }
 }
@@ -444,7 +473,8 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
 //     dU = P^T do + e^{G_n - G} K Z,   Y = dU - C^T B dU,
 //     Z <- e^{G_n} Z + Q^T (s e^G do) - K^T (e^G B Y),
 // the pieces of P, C^T, B dU, do and Y as exact as above.
-template <int NU, int kParts>
+// kState: only what a segment adds to an adjoint.
+template <int NU, int kParts, bool kState>
 __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int grid, char* lds) {
     typedef DeltaAdjointLds M;
     constexpr int NW = 8 / NU / kParts;
@@ -454,8 +484,12 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
     const DeltaLane<NU, kParts> L(part);
     const int w = L.w, lane = L.lane, gq = L.gq, n16 = L.n16;
     const Item it = find_item(A.map, idx);
+    if (kState && it.off == 0) return;
+    const bool last = it.off + it.len >= (A.map.task != nullptr ? A.map.seq_len[it.n] : A.map.len);
     const int Hv = A.map.Hv;
     const int64_t soff = ((int64_t)it.n * Hv + it.h) * (int64_t)STATE;
+    float* behind = A.behind == nullptr ? nullptr : A.behind + (it.seg * Hv + it.h) * (int64_t)STATE;
+    const float* s_in = !kState && behind != nullptr ? behind : A.s_in != nullptr && !(kState && !last) ? A.s_in + soff : nullptr;
     const int64_t block0 = (A.blocks.task != nullptr ? A.blocks.tape_off[it.n] + it.n
                                                      : (int64_t)it.n * ((A.blocks.len + DB - 1) / DB)) + it.off / DB;
     const int chunks = (it.len + SC - 1) / SC;
@@ -496,7 +530,7 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int u = 0; u < NU; ++u)
-            Z[t][u] = A.s_in != nullptr ? *(const f32x4*)(A.s_in + soff + (L.vrow + 4 * u) * D + L.krow(t)) : zero4();
+            Z[t][u] = s_in != nullptr ? *(const f32x4*)(s_in + (L.vrow + 4 * u) * D + L.krow(t)) : zero4();
 
     const PlaneWriter<NU, kParts> planes{L, (float (*)[8][2])(lds + M::X)};
     auto state_max = [&]() __attribute__((always_inline)) {
@@ -642,6 +676,11 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
                 for (int d = 0; d < 3; ++d) Z[t][u] = mma32(qt, o3[d], Z[t][u]);
             }
         }
+        if (kState) {
+            if (more) wait_vm<0>();
+            barrier_lds();
+            return;
+        }
         // the planes of this chunk's rows, and of the adjoint when it is behind the next block
         const bool edge = (c & 1) == 0 && more;
         planes.put(c & 1, edge ? state_max() : 0.0f, top);
@@ -654,10 +693,10 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
             planes.state(Z, (float)held, planes.get(c & 1, 0), A.planes.state + (blk - Hv) * (int64_t)STATE,
                          A.planes.state_scale + (blk - Hv) * 4);
     };
-    planes.put(chunks & 1, state_max(), 0.0f);
+    if (!kState) planes.put(chunks & 1, state_max(), 0.0f);
     wait_vm<0>();
     barrier_lds();
-    {
+    if (!kState) {
         const int64_t blk = (block0 + ((chunks - 1) >> 1)) * Hv + it.h;
         planes.state(Z, 1.0f, planes.get(chunks & 1, 0), A.planes.state + blk * (int64_t)STATE, A.planes.state_scale + blk * 4);
     }
@@ -669,7 +708,7 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
     for (int c = chunks - 1; c > 0; --c) at(c, std::true_type{});
     at(0, std::false_type{});
 
-    if (A.s_out != nullptr) {
+    if (kState || (A.s_out != nullptr && it.off == 0)) {
         const Factor decay(held);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -678,7 +717,7 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
                 f32x4 r;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) r[e] = decay.apply(Z[t][u][e]);
-                *(f32x4*)(A.s_out + soff + (L.vrow + 4 * u) * D + L.krow(t)) = r;
+                *(f32x4*)((kState ? behind : A.s_out + soff) + (L.vrow + 4 * u) * D + L.krow(t)) = r;
             }
     }
 }

@@ -521,8 +521,9 @@ kda_status kda_delta_fwd_workspace_bytes(const kda_delta_problem* p, size_t* byt
 /* Training forward.  q, k BF16 [B][T][Hqk][128], v, o BF16 [B][T][Hv][128],
  * states FP32 [N][Hv][128][128].  initial_state NULL starts from zero;
  * final_state may be NULL.  The workspace is always needed; it then holds the
- * chunks' records (12 KiB per 64 tokens and value head), which a backward of the same
- * problem and inputs may be given. */
+ * chunks' records (12 KiB per 64 tokens and value head) and the states of the segments that
+ * long sequences on few heads are cut into (128 KiB per segment and value head), which a
+ * backward of the same problem and inputs may be given. */
 kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
                          const void* beta, const float* initial_state, void* o, float* final_state,
                          void* workspace, size_t workspace_bytes, void* stream);
@@ -533,8 +534,8 @@ kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* 
  * untouched since, or NULL, and they are formed again.  dfinal_state NULL counts as
  * zero; dinitial_state may be NULL.  dq and dk sum over the value heads that share a
  * q/k head, in head order; dg and dbeta are BF16 [B][T][Hv].  The workspace holds every
- * block's states: about 96 KiB per 64 tokens and value head, and the records when they
- * are not given. */
+ * block's states: about 96 KiB per 64 tokens and value head, 64 KiB per segment, and the
+ * records when they are not given. */
 kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, int32_t records_given, size_t* bytes);
 kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,
                          const void* beta, const float* initial_state, const void* records, size_t records_bytes,

@@ -165,6 +165,12 @@ def test_workspace_sizes():
     assert need("infer", delta(T=8), 0) == 0                   # token by token
     assert need("infer", delta(T=40), 39) == 0
     assert need("bwd", p, 0) == records + need("bwd", p, 1) >= records + 2 * 4 * 4 * (32768 + 16384)
+    cut = delta(T=65, B=2, N=2, segment=64)                    # two segments a sequence, two matrices each
+    states = 4 * 4 * 65536
+    assert need("fwd", cut) == need("infer", cut, 0) == need("fwd", p) + 2 * states
+    assert need("bwd", cut, 1) == need("bwd", p, 1) + states
+    assert need("bwd", cut, 0) == need("bwd", p, 0) + 3 * states
+    assert need("fwd", delta(T=64, B=2, N=2, segment=64)) == need("fwd", delta(T=64, B=2, N=2))
     n = ctypes.c_size_t()
     assert kda._lib.kda_delta_fwd_workspace_bytes(ctypes.byref(p), None) == NULL
     assert kda._lib.kda_delta_bwd_workspace_bytes(ctypes.byref(p), 0, None) == NULL

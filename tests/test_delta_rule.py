@@ -151,6 +151,54 @@ def test_gradients_with_records_formed_again(unit):
         assert (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
 
 
+SEGMENTS = {  # lengths, packed, Hqk, Hv, unit, gates, segment
+    "two": ([128], False, 1, 1, True, "layer", 64),
+    "one_and_a_token": ([65], False, 1, 2, True, "none", 64),
+    "many": ([64 * 9 + 31], False, 1, 1, True, "none", 64),
+    "batch": ([260] * 3, False, 2, 4, True, "layer", 64),
+    "ragged": ([1, 64, 65, 200, 3, 129, 400], True, 1, 3, False, "mixed", 64),
+    "longer": ([500, 128, 129, 7, 384], True, 2, 2, True, "none", 128),
+    "strong": ([300, 190], True, 1, 2, True, "strong", 64),
+    "eight_waves": ([130] * 20, False, 4, 4, True, "layer", 64),       # 240 segments and heads
+    "four_waves": ([190, 70, 64] * 14, True, 4, 8, True, "mixed", 64),  # 672 of them
+}
+
+
+@pytest.mark.parametrize("case", list(SEGMENTS))
+def test_training_step_in_segments(case):
+    lengths, packed, Hqk, Hv, unit, gates, segment = SEGMENTS[case]
+    print(f"[delta] segments {case}", flush=True)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=200 + len(case), unit=unit, gates=gates)
+    got = train(inp, segment=segment)
+    check_forward(inp, got)
+    du.check_gradients(inp, got[2:])
+
+
+def test_training_step_in_segments_without_states_and_records():
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([150, 7, 333], True, 1, 2, seed=23, state=False)
+    du.check_gradients(inp, train(inp, segment=64)[2:])
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")   # (10 segments of 2 heads need 2.5 MiB, 10 blocks 240 KiB)
+    _, _, ctx = call_forward(inp, workspace=ws, segment=64)
+    ws.fill_(255)
+    grads = kda.gated_delta_rule_training_backward(ctx, inp.dev(inp.do), None)
+    torch.cuda.synchronize()
+    du.check_gradients(inp, grads)
+
+
+def test_a_long_sequence_on_few_heads_goes_in_segments():
+    """The library's own choice of segments, and its workspace for them."""
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([2500], False, 1, 2, seed=24, gates="none")
+    p = kda.KdaDeltaProblem(1, 2500, 1, 2, 1)
+    own = kda.kda_delta_fwd_workspace_bytes(p)
+    p.segment = 4096
+    assert own > kda.kda_delta_fwd_workspace_bytes(p)
+    got = train(inp)
+    check_forward(inp, got)
+    du.check_gradients(inp, got[2:])
+
+
 def test_training_step_without_states():
     """initial_state and dfinal_state None count as zero."""
     inp = Inp([5, 150, 64], True, 1, 2, seed=3, state=False)
@@ -229,8 +277,8 @@ def test_training_step_on_another_stream_and_the_same_bits_again():
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("packed", [False, True])
-def test_captured_training_step(packed):
+@pytest.mark.parametrize("segment,packed", [(0, False), (0, True), (64, False), (64, True)])
+def test_captured_training_step(segment, packed):
     """Forward and backward in one graph, replayed with eager calls between; every replay
     gives the eager bits, on changed inputs too.  A fixed-layout call needs no call before
     the capture."""
@@ -238,10 +286,11 @@ def test_captured_training_step(packed):
     inp = Inp([150, 7, 143] if packed else [150, 150], packed, 1, 2, seed=14)
     d = {n: inp.dev(getattr(inp, n)) for n in ("q", "k", "v", "g", "beta", "do", "s0", "ds", "cu")}
     if packed:  # the schedule: made by one call, seen on the device by a second
-        train(inp)
-        train(inp)
+        train(inp, segment=segment)
+        train(inp, segment=segment)
     p = kda.KdaDeltaProblem(inp.B, inp.T, 1, 2, inp.N)
     p.use_qk_l2norm = 1
+    p.segment = segment
     if packed:
         p.cu_seqlens, p.cu_seqlens_host = d["cu"].data_ptr(), inp.cu.data_ptr()
     outs = [torch.empty_like(d[n]) for n in ("v", "s0", "q", "k", "v", "g", "beta", "s0")]
@@ -260,7 +309,7 @@ def test_captured_training_step(packed):
         rec.fill_(255)
         graph.replay()
         torch.cuda.synchronize()
-        want = train(inp)
+        want = train(inp, segment=segment)
         for a, b in zip(want, outs):
             assert torch.equal(a, b)
         inp.v = inp.v.flip(1).contiguous()
@@ -315,6 +364,8 @@ BATCHES = {  # lengths, packed, Hqk, Hv
     "prefill_packed": ([129, 9, 64], True, 3, 3),
     "mixed": ([8, 9, 1, 300, 5, 2], True, 2, 4),
     "last_is_long": ([4, 3, 2, 64], True, 1, 3),
+    "segments": ([3, 1500, 1, 200, 9], True, 1, 2),                   # (the long one's, and the others beside them)
+    "segments_of_a_batch": ([1100] * 2, False, 1, 1),
 }
 
 
