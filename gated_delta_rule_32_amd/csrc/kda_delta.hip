@@ -227,9 +227,10 @@ hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// With enough workgroups to share compute units, four waves with two tiles each spend the
-// least on reading the rows out of LDS.  With one workgroup per unit at most, eight waves shorten a
-// chunk, and with one for every second unit, two workgroups of half the columns each.
+// Four waves with two tiles each spend the least on reading the rows out of LDS.  With one
+// workgroup for every second compute unit at most, two of half the columns each shorten a chunk.
+// (2048 tokens of 96, 128, 160, 256 heads, in us: 254, 261, 262, 282 in four waves, 195, 204 in two
+// workgroups; in eight waves with a tile each 274, 305 at 160 and 256 heads.)
 template <int NU, int kParts, int kMode>
 __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_scan_kernel(DeltaArgs A) {
     __shared__ __align__(16) char lds[DeltaScanLds<kMode>::TOTAL];
@@ -241,8 +242,6 @@ static hipError_t launch_scan(const DeltaArgs& a, hipStream_t s) {
     const int64_t items = a.map.items * (kMode == kDeltaState ? 2 : 1);
     if (items <= 128)
         hipLaunchKernelGGL((delta_scan_kernel<1, 2, kMode>), dim3((unsigned)(items * 2)), dim3(256), 0, s, a);
-    else if (items <= 256)
-        hipLaunchKernelGGL((delta_scan_kernel<1, 1, kMode>), dim3((unsigned)items), dim3(512), 0, s, a);
     else
         hipLaunchKernelGGL((delta_scan_kernel<2, 1, kMode>), dim3((unsigned)items), dim3(256), 0, s, a);
     return hipGetLastError();

@@ -18,12 +18,13 @@ __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_both_kernel(DeltaA
         delta_scan<NU, kParts, kDeltaRecord>(forward, blockIdx.x - half, half, lds);
 }
 
+// (As the forward's scan: while two workgroups a compute unit hold both scans' halves.  A backward
+// of 2048 tokens of 48, 64, 96, 128 heads, in us: 292, 326, 414, 481 in halves; 415, 449, 506, 565 in four
+// waves with two tiles each; 461, 523 at 96 and 128 heads in eight with a tile each.)
 hipError_t launch_delta_both(const DeltaArgs& f, const DeltaArgs& b, hipStream_t s) {
     const unsigned items = (unsigned)f.map.items;
-    if (items <= 64)
+    if (items <= 128)
         hipLaunchKernelGGL((delta_both_kernel<1, 2>), dim3(items * 4), dim3(256), 0, s, f, b);
-    else if (items <= 128)
-        hipLaunchKernelGGL((delta_both_kernel<1, 1>), dim3(items * 2), dim3(512), 0, s, f, b);
     else
         hipLaunchKernelGGL((delta_both_kernel<2, 1>), dim3(items * 2), dim3(256), 0, s, f, b);
     return hipGetLastError();
@@ -37,10 +38,8 @@ __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_behind_kernel(Delt
 
 hipError_t launch_delta_behind(const DeltaArgs& a, hipStream_t s) {
     const unsigned items = (unsigned)a.map.items;
-    if (items <= 128)
+    if (items <= 256)   // (8 heads x 8192 tokens in 128 segments and heads: the backward 206 us against 228)
         hipLaunchKernelGGL((delta_behind_kernel<1, 2>), dim3(items * 2), dim3(256), 0, s, a);
-    else if (items <= 256)
-        hipLaunchKernelGGL((delta_behind_kernel<1, 1>), dim3(items), dim3(512), 0, s, a);
     else
         hipLaunchKernelGGL((delta_behind_kernel<2, 1>), dim3(items), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
