@@ -58,6 +58,50 @@ __device__ __forceinline__ float row16_before(float x) {
     return x;
 }
 
+// Sum over this lane and those behind it in its row of 16.
+__device__ __forceinline__ float row16_from(float x) {
+#define KDA_SHIFTED(n) __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x100 + (n), 0xF, 0xF, true))
+    x += KDA_SHIFTED(1);   // (row_shl: zero where there is no lane)
+    x += KDA_SHIFTED(2);
+    x += KDA_SHIFTED(4);
+    x += KDA_SHIFTED(8);
+#undef KDA_SHIFTED
+    return x;
+}
+
+// Sums of x over the four rows of lanes.  Of four values: value i's in row i.
+__device__ __forceinline__ float rows_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ float rows_sum(const float (&x)[4]) {
+    // (a swap of 32 gives lower halves in its first result and upper halves in its second, one of 16
+    // even and odd rows)
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[0]), __float_as_uint(x[2]), false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[1]), __float_as_uint(x[3]), false, false);
+    const float y0 = __uint_as_float(a[0]) + __uint_as_float(a[1]), y1 = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    const auto c = __builtin_amdgcn_permlane16_swap(__float_as_uint(y0), __float_as_uint(y1), false, false);
+    return __uint_as_float(c[0]) + __uint_as_float(c[1]);
+}
+
+// pack_quad's format for less: halves are rounded away from zero, and a value below 2^-14 of the
+// quad's scale is cut to a multiple of 2^-23 (at most 2^-22 of the quad's largest).
+__device__ __forceinline__ u32x2 pack_quad_fast(f32x4 x) {
+    const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    const unsigned q = __float_as_uint(top) >> 27;
+    const float scale = __uint_as_float((253u - 16u * q) << 23);
+    const bool bad = !(x[0] * 0.0f + x[1] * 0.0f + x[2] * 0.0f + x[3] * 0.0f == 0.0f);
+    f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __uint_as_float((__float_as_uint(x[i] * scale) + 0x2000u) & ~0x3fffu);
+    const u32x2 h = __builtin_bit_cast(u32x2, to_f16x4(r));
+    const u32x2 w = {(h[0] >> 1 & 0x7fffu) | (h[0] >> 2 & 0x3fff8000u) | q << 30,
+                     (h[1] >> 1 & 0x7fffu) | (h[1] >> 2 & 0x3fff8000u) | (q >> 2) << 30};
+    return u32x2{bad ? ~0u : w[0], bad ? ~0u : w[1]};
+}
+
 // Gradients of a block of 64 tokens of one value head, all blocks at once.  With S the
 // state before the block, Z the adjoint behind it, G the running sums from the block's
 // start, and q, k at unit length:
@@ -97,7 +141,11 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     const int64_t blk = it.seg * Hv + it.h;
     const char* rec = A.rec + blk * (2 * REC);
 
-    if (w == 0) {
+    const float* s_scale = A.forward.state_scale + blk * 4;
+    const float* z_scale = A.backward.state_scale + blk * 4;
+    const float* w_scale = A.forward.row_scale + blk * 8;
+    const float* y_scale = A.backward.row_scale + blk * 8;
+    auto put_tokens = [&]() __attribute__((always_inline)) {
         const char* r = rec + (lane >> 5) * REC + (lane & 31) * 4;
         float hi = *(const float*)(r + REC_GH), lo = *(const float*)(r + REC_GL);
         if (lane >= 32) {   // behind the first chunk's decay: the exact sum of the high parts and the rest
@@ -111,7 +159,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         tok[2][lane] = lo;
         tok[3][lane] = *(const float*)(r + REC_K);
         tok[4][lane] = *(const float*)(r + REC_Q);
-    }
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) sums[i][w][lane] = 0.0f;
 
@@ -134,6 +182,8 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     constexpr int LQ = 0, LK = 16384;
     const int r8 = n16 * 256 + ((gq ^ swz(n16)) << 4);   // 8 channels 32p + 8gq of row n (xor 64p)
     // matrices of 64 rows of 128 bytes: block b of row r at b ^ r % 8; hi at 0, lo at 8192
+    const bf16x4 none = __builtin_bit_cast(bf16x4, u32x2{0u, 0u});
+    const bf16x8 id8 = cat8(identity_frag(lane), none);
     auto mat = [&](int base, int row, int block) __attribute__((always_inline)) {
         return lds + base + row * 128 + ((block ^ (row & 7)) << 4);
     };
@@ -159,7 +209,10 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
             m[e] = i >= j ? x : 0.0f;
             n[e] = i > j ? -y : 0.0f;
             h[e] = i > j ? m[e] * qk[e] + n[e] * kk[e] : 0.0f;
-            if (i == j) diag[j] = F[s][e];
+        }
+        if (bi == bj) {   // F's diagonal
+            const float d01 = n16 & 1 ? F[s][1] : F[s][0], d23 = n16 & 1 ? F[s][3] : F[s][2];
+            if (gq == n16 >> 2) diag[j] = n16 & 2 ? d23 : d01;
         }
         // along a row to its columns before t; the rows from t on of that, down column t
         f32x4 along;
@@ -170,43 +223,27 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
             const float x = row16_before(h[e]);
             down += bi != bj || 4 * gq + e >= n16 ? x : 0.0f;
         }
-        down += __shfl_xor(down, 16, 64);
-        down += __shfl_xor(down, 32, 64);
+        down = rows_sum(down);
         if (n16 == 0) *(f32x4*)&sums[0][bj][i0] = along;
         if (gq == 0) sums[1][bi][j] = down;
         bf16x4 mh, ml, nh, nl;
         split4_rne(m, mh, ml);
         split4_rne(n, nh, nl);
-        {   // e as [j][i], zeros above the diagonal
-            char* at = mat(GM, j, 2 * bi + (gq >> 1)) + 8 * (gq & 1);
-            *(bf16x4*)at = mh;
-            *(bf16x4*)(at + 8192) = ml;
-            if (bi != bj) {
-                at = mat(GM, 16 * bi + n16, 2 * bj + (gq >> 1)) + 8 * (gq & 1);
-                *(u32x2*)at = u32x2{0u, 0u};
-                *(u32x2*)(at + 8192) = u32x2{0u, 0u};
-            }
+        char* at = mat(GM, j, 2 * bi + (gq >> 1)) + 8 * (gq & 1);   // e as [j][i], zeros where its pair of tiles goes on above the diagonal
+        *(bf16x4*)at = mh;
+        *(bf16x4*)(at + 8192) = ml;
+        if ((bi & 1) != 0 && bj == bi - 1) {
+            at = mat(GM, 16 * bi + n16, 2 * bj + (gq >> 1)) + 8 * (gq & 1);
+            *(u32x2*)at = u32x2{0u, 0u};
+            *(u32x2*)(at + 8192) = u32x2{0u, 0u};
         }
-        // -f, both ways
-        if (bi != bj) {
-            char* at = mat(GN, j, 2 * bi + (gq >> 1)) + 8 * (gq & 1);
-            *(bf16x4*)at = nh;
-            *(bf16x4*)(at + 8192) = nl;
+        if (bi == bj) {   // the sum with its transpose (which the matrix unit forms, exactly)
+            nh = to_bf4(mma32(cat8(nh, none), id8, from_bf4(nh)));
+            nl = to_bf4(mma32(cat8(nl, none), id8, from_bf4(nl)));
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + e;
-            char* at = mat(GN, i, j >> 3) + 2 * (j & 7);
-            if (i >= j) {
-                *(bf16*)at = nh[e];
-                *(bf16*)(at + 8192) = nl[e];
-            }
-            if (bi == bj && i > j) {
-                at = mat(GN, j, i >> 3) + 2 * (i & 7);
-                *(bf16*)at = nh[e];
-                *(bf16*)(at + 8192) = nl[e];
-            }
-        }
+        at = mat(GN, j, 2 * bi + (gq >> 1)) + 8 * (gq & 1);         // -f likewise
+        *(bf16x4*)at = nh;
+        *(bf16x4*)(at + 8192) = nl;
     }
     // the parts that come from the states, and what they say of the decays
     const float hn = tok[1][DB - 1], ln = tok[2][DB - 1];
@@ -215,9 +252,9 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) s += (float)x[e] * y[0][e] + (float)x[4 + e] * y[1][e];
-        s += __shfl_xor(s, 16, 64);
-        return s + __shfl_xor(s, 32, 64);
+        return s;
     };
+    float part[3][4];
 #pragma unroll
     for (int ti = 0; ti < 4; ++ti) {
         const int t = 16 * ti + n16;
@@ -232,15 +269,14 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
             dks[ti][u] *= cs;
             dke[ti][u] *= ce;
         }
-        const float s0 = dot8(q8, dq[ti]), s1 = dot8(k8, dks[ti]), s2 = dot8(k8, dke[ti]);
-        if (gq == 0) {
-            dots[0][w][t] = s0;
-            dots[1][w][t] = s1;
-            dots[2][w][t] = s2;
-        }
+        part[0][ti] = dot8(q8, dq[ti]);
+        part[1][ti] = dot8(k8, dks[ti]);
+        part[2][ti] = dot8(k8, dke[ti]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) dks[ti][u] += dke[ti][u];
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) dots[i][w][lane] = rows_sum(part[i]);
     barrier_lds();
     // the products inside the block
 #pragma unroll
@@ -268,7 +304,11 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) dks[ti][u] = mma32(qt[u], m, dks[ti][u]);
                 }
-                const bf16x8 n = *(const bf16x8*)(mat(GN, 16 * ti + n16, 4 * pair + gq) + piece * 8192);
+                // -sum over i > j of f_ij k_i (tiles from ti on), -sum over i < j of f_ji k_i (those up to ti)
+                const bf16x8 n = 2 * pair >= ti
+                                     ? *(const bf16x8*)(mat(GN, 16 * ti + n16, 4 * pair + gq) + piece * 8192)
+                                     : cat8(tr_read(mat(GN, r0, 2 * ti + (pa >> 1)) + 8 * (pa & 1) + piece * 8192),
+                                            tr_read(mat(GN, r1, 2 * ti + (pa >> 1)) + 8 * (pa & 1) + piece * 8192));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) dks[ti][u] = mma32(kt[u], n, dks[ti][u]);
             }
@@ -278,15 +318,13 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     bf16x8 q8[4], k8[4];
 #pragma unroll
     for (int ti = 0; ti < 4; ++ti) {
-        const int t = 16 * ti + n16;
         q8[ti] = *(const bf16x8*)(lds + LQ + ti * 4096 + n16 * 256 + rch);
         k8[ti] = *(const bf16x8*)(lds + LK + ti * 4096 + n16 * 256 + rch);
-        const float s0 = dot8(q8[ti], dq[ti]), s1 = dot8(k8[ti], dks[ti]);
-        if (gq == 0) {
-            dots[3][w][t] = s0;
-            dots[4][w][t] = s1;
-        }
+        part[0][ti] = dot8(q8[ti], dq[ti]);
+        part[1][ti] = dot8(k8[ti], dks[ti]);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dots[3 + i][w][lane] = rows_sum(part[i]);
     barrier_lds();
 #pragma unroll
     for (int ti = 0; ti < 4; ++ti) {
@@ -308,44 +346,36 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         u32x2 x[4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            x[u] = A.pack ? pack_quad(dq[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dq[ti][u]));
-            x[2 + u] = A.pack ? pack_quad(dks[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dks[ti][u]));
+            x[u] = A.pack ? pack_quad_fast(dq[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dq[ti][u]));
+            x[2 + u] = A.pack ? pack_quad_fast(dks[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dks[ti][u]));
         }
         *(u32x4*)((char*)A.dq + at) = u32x4{x[0][0], x[0][1], x[1][0], x[1][1]};
         *(u32x4*)((char*)A.dk + at) = u32x4{x[2][0], x[2][1], x[3][0], x[3][1]};
     }
-    if (w == 0) {   // lane t: token t
+    if (w == 3) {   // lane t: token t
         const int b = lane >> 4;
+        auto at_lane = [&](float x, int i) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i)); };
         auto four = [&](int i) { return (dots[i][0][lane] + dots[i][1][lane]) + (dots[i][2][lane] + dots[i][3][lane]); };
-        float x = __shfl_up(four(2), 1, 64), y = four(0) + four(1);
-        if (lane == 0) x = 0.0f;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const float a = __shfl_up(x, d, 64), c = __shfl_down(y, d, 64);
-            if (lane >= d) x += a;
-            if (lane + d < 64) y += c;
+        // of x the tokens before this one, of y this one and those behind it
+        const float x = four(2), y = four(0) + four(1);
+        float before = row16_before(x), from = row16_from(y);
+        const float x16 = before + x, y16 = from;
+        float dg = before + from;
+        {
+            const float x0 = at_lane(x16, 15), x1 = at_lane(x16, 31), x2 = at_lane(x16, 47);
+            const float y1 = at_lane(y16, 16), y2 = at_lane(y16, 32), y3 = at_lane(y16, 48);
+            dg += b == 0 ? y1 + y2 + y3 : b == 1 ? x0 + (y2 + y3) : b == 2 ? x0 + x1 + y3 : x0 + x1 + x2;
         }
-        float dg = decay2(hn, ln, 0.0f, 0.0f) * ((whole[0] + whole[1]) + (whole[2] + whole[3])) + x + y;
+        dg += decay2(hn, ln, 0.0f, 0.0f) * ((whole[0] + whole[1]) + (whole[2] + whole[3]));
         // sum over i >= t > j: of column tile b, and of the column tiles before it
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i >= b) dg += sums[1][i][lane];
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-            const float r = sums[0][c][lane];
-            float from = r;   // this row and the tile's rows behind it
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) {
-                const float z = __shfl_down(from, d, 16);
-                if ((lane & 15) + d < 16) from += z;
-            }
-            float below = 0.0f;
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                const float all = __shfl(from, 16 * i, 64);
-                if (i > b) below += all;
-            }
-            if (c < b) dg += from + below;
+            const float r = row16_from(sums[0][c][lane]);   // this row and the tile's rows behind it
+            const float r2 = at_lane(r, 32), r3 = at_lane(r, 48);
+            if (c < b) dg += b == 1 ? r + (r2 + r3) : b == 2 ? r + r3 : r;
         }
         if (lane < it.len) {
             const int64_t at = (it.tok0 + lane) * Hv + it.h;
@@ -417,17 +447,23 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         return __builtin_bit_cast(f16x8, cat8(tr_read(r + at), tr_read(r + ((at + 4 * 256) ^ 32))));
     };
     bf16* pdv = (bf16*)A.dv + ((it.tok0 + 16 * w + n16) * Hv + it.h) * D + 8 * gq;
-    const float* s_scale = A.forward.state_scale + blk * 4;
-    const float* z_scale = A.backward.state_scale + blk * 4;
-    const float* w_scale = A.forward.row_scale + blk * 8;
-    const float* y_scale = A.backward.row_scale + blk * 8;
+    // the planes' scales, in one register's lanes: S, Z, then W and Y of either chunk
+    float scales = 0.0f;
+    {
+        const int i = lane & 3, set = lane >> 2;
+        const float* from = set == 0 ? s_scale : set == 1 ? z_scale : set < 4 ? w_scale + 4 * (set - 2) : y_scale + 4 * (set - 4);
+        if (set < 6 && (second || set < 2 || (set & 1) == 0)) scales = from[i];
+    }
+    auto scale_of = [&](int set, int vb) __attribute__((always_inline)) {
+        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scales), 4 * set + vb));
+    };
     auto part = [&](int vb, const char* __restrict__ from, char* __restrict__ to) __attribute__((always_inline)) {
         if (vb < 3)
             load_stage(to, vb + 1);
         else   // q's and k's rows, over the first stage
             load_rows();
-        const float fs = s_scale[vb], fz = z_scale[vb];
-        const float fw[2] = {w_scale[vb], second ? w_scale[4 + vb] : 0.0f}, fy[2] = {y_scale[vb], second ? y_scale[4 + vb] : 0.0f};
+        const float fs = scale_of(0, vb), fz = scale_of(1, vb);
+        const float fw[2] = {scale_of(2, vb), scale_of(3, vb)}, fy[2] = {scale_of(4, vb), scale_of(5, vb)};
         const f16x8 yr = get_row(from, 1, w);
         if (16 * w + n16 < it.len) {   // dv of the wave's 16 tokens: 8 channels a lane.  (No branch
             // stands behind the sums below: the compiler would move them all past it.)
@@ -503,6 +539,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         barrier_lds();
     };
     load_stage(lds, 0);
+    if (w == 3) put_tokens();
     wait_vm<0>();
     barrier_lds();
     for (int vb = 0; vb < 4; ++vb) part(vb, lds + (vb & 1) * GS2, lds + (~vb & 1) * GS2);
