@@ -69,13 +69,7 @@ __device__ __forceinline__ float row16_from(float x) {
     return x;
 }
 
-// Sums of x over the four rows of lanes.  Of four values: value i's in row i.
-__device__ __forceinline__ float rows_sum(float x) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
+// Sums over the four rows of lanes of four values: value i's in row i.
 __device__ __forceinline__ float rows_sum(const float (&x)[4]) {
     // (a swap of 32 gives lower halves in its first result and upper halves in its second, one of 16
     // even and odd rows)
