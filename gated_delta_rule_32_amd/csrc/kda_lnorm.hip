@@ -133,12 +133,10 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void lnorm_fwd_ker
         for (int c = 0; c < kVecs; ++c) {
             const int at = (c * kThreads + t) * 8;
             if (at >= a.C) continue;
-            f32x8 y = x[c] * r * (kHold ? w[c] : load8(a.w + at));
-            if (kHold)
-                y += b[c];
-            else if (a.b != nullptr)
-                y += load8(a.b + at);
-            store_row<kStream>(py + at, y);
+            const f32x8 wc = kHold ? w[c] : load8(a.w + at);
+            const f32x8 bc = kHold ? b[c] : a.b != nullptr ? load8(a.b + at) : f32x8{};
+            // (one rounding, so that a row's bits do not depend on how many there are)
+            store_row<kStream>(py + at, __builtin_elementwise_fma(x[c] * r, wc, bc));
         }
         row += step;
         if (!kHold || row >= a.rows) break;

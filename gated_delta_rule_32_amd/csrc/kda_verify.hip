@@ -5,9 +5,9 @@
 //
 // Products and sums are formed in 64 bits, where the product of two FP32 values is exact, so
 // that a token depends neither on how the row is split nor on the order of its sums (beyond
-// 2^-50 of the total).  Only one row of p and q of each sequence is read, once: first the
-// tiles' sums, by as many workgroups as there are tiles, then the tile that the draw falls
-// into again.
+// 2^-50 of the total).  Only one row of p and q of each sequence is read.  A row that one workgroup
+// holds in registers is read once, by one kernel; of longer ones first the tiles' sums are formed, by
+// as many workgroups as there are tiles, then the tile that the draw falls into is read again.
 #include "kda_common.hpp"
 #include "kda_delta.h"
 
@@ -64,19 +64,26 @@ __device__ __forceinline__ void weights(const Row& r, int i, float p, float q, d
     more = d > 0.0 ? d : 0.0;
     whole = p > 0.0f ? (double)p : 0.0;
 }
-// 16 values from `at` on, zero behind the row.
-__device__ __forceinline__ void load16(const float* row, int at, int V, float (&x)[VPER]) {
-    if (at + VPER <= V) {
+// Values from `at` on, zero behind the row.
+template <int kPer>
+__device__ __forceinline__ void load_values(const float* row, int at, int V, float (&x)[kPer]) {
+    if (at + kPer <= V) {
 #pragma unroll
-        for (int c = 0; c < VPER / 4; ++c) {
+        for (int c = 0; c < kPer / 4; ++c) {
             const f32x4u y = *(const f32x4u*)(row + at + 4 * c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[4 * c + e] = y[e];
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < VPER; ++c) x[c] = at + c < V ? row[at + c] : 0.0f;
+        for (int c = 0; c < kPer; ++c) x[c] = at + c < V ? row[at + c] : 0.0f;
     }
+}
+
+__device__ __forceinline__ void put_tokens(const VerifyArgs& A, int64_t n, int stand, int token, int threads) {
+    for (int i = threadIdx.x; i <= A.S; i += threads)
+        A.tokens[n * (A.S + 1) + i] = i < stand ? A.drafts[n * A.S + i] : i == stand ? token : -1;
+    if (threadIdx.x == 0) A.accepted[n] = stand + 1;
 }
 
 // Inclusive sum over the wave's lanes.
@@ -101,8 +108,8 @@ __global__ __launch_bounds__(VTHREADS) void verify_sums_kernel(VerifyArgs A) {
     const Row r = draw_row(A, n, stand, lens);
     const int at = tile * VT + threadIdx.x * VPER;
     float p[VPER], q[VPER];
-    load16(r.p, at, A.V, p);
-    if (r.q != nullptr) load16(r.q, at, A.V, q);
+    load_values(r.p, at, A.V, p);
+    if (r.q != nullptr) load_values(r.q, at, A.V, q);
     double more = 0.0, whole = 0.0;
 #pragma unroll
     for (int c = 0; c < VPER; ++c) {
@@ -183,8 +190,8 @@ __global__ __launch_bounds__(VTHREADS) void verify_draw_kernel(VerifyArgs A) {
         if (threadIdx.x < 2) found[threadIdx.x] = threadIdx.x == 0 ? 0x7fffffff : -1;
         const int at = tile * VT + threadIdx.x * VPER;
         float p[VPER], q[VPER];
-        load16(r.p, at, A.V, p);
-        if (r.q != nullptr) load16(r.q, at, A.V, q);
+        load_values(r.p, at, A.V, p);
+        if (r.q != nullptr) load_values(r.q, at, A.V, q);
         double x[VPER], own = 0.0;
         int mine = -1;   // this thread's last index with a weight
 #pragma unroll
@@ -210,14 +217,96 @@ __global__ __launch_bounds__(VTHREADS) void verify_draw_kernel(VerifyArgs A) {
         __syncthreads();
         token = found[0] != 0x7fffffff ? found[0] : found[1];
     }
-    for (int i = threadIdx.x; i <= A.S; i += VTHREADS)
-        A.tokens[n * (A.S + 1) + i] = i < stand ? A.drafts[n * A.S + i] : i == stand ? token : -1;
-    if (threadIdx.x == 0) A.accepted[n] = stand + 1;
+    put_tokens(A, n, stand, token, VTHREADS);
 }
 
-int verify_tiles(int64_t V) { return (int)((V + VT - 1) / VT); }
+// The same for a row of up to 1024 kPer values, in one go.
+template <int kPer>
+__global__ __launch_bounds__(1024) void verify_row_kernel(VerifyArgs A) {
+    __shared__ double part[16][2];
+    __shared__ int found[2];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t n = blockIdx.x;
+    const int lens = lengths(A, n), stand = standing(A, n, lens, lane);
+    const Row r = draw_row(A, n, stand, lens);
+    const int at = threadIdx.x * kPer;
+    constexpr int GROUP = kPer < 16 ? kPer : 16;
+    double own[2] = {0.0, 0.0}, scan[2];
+    int last[2] = {-1, -1};    // this thread's last indices with a weight
+#pragma unroll
+    for (int g = 0; g < kPer; g += GROUP) {
+        float p[GROUP], q[GROUP];
+        load_values(r.p, at + g, A.V, p);
+        if (r.q != nullptr) load_values(r.q, at + g, A.V, q);
+#pragma unroll
+        for (int c = 0; c < GROUP; ++c) {
+            double a, b;
+            weights(r, at + g + c, p[c], q[c], a, b);
+            own[0] += a;
+            own[1] += b;
+            if (a > 0.0) last[0] = at + g + c;
+            if (b > 0.0) last[1] = at + g + c;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        scan[i] = wave_scan(own[i], lane);
+        if (lane == 63) part[w][i] = scan[i];
+    }
+    if (threadIdx.x < 2) found[threadIdx.x] = threadIdx.x == 0 ? 0x7fffffff : -1;
+    __syncthreads();
+    double total[2] = {0.0, 0.0}, before[2] = {0.0, 0.0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (j == w) before[i] = total[i];
+            total[i] += part[j][i];
+        }
+    const bool all = !(total[0] > 0.0);   // p exceeds q nowhere
+    const double u = (double)A.uniform[n * (A.S + 1) + A.S];
+    const double mark = (u > 0.0 ? u : 0.0) * (all ? total[1] : total[0]);
+    double sum = all ? before[1] + (scan[1] - own[1]) : before[0] + (scan[0] - own[0]);
+    const double end = sum + (all ? own[1] : own[0]);
+    int first = 0x7fffffff;
+    const int mine = all ? last[1] : last[0];
+    // only where the sum passes the mark the values are walked again (by more than the sums' rounding
+    // around it, so that one of two neighbours finds it)
+    if (mine >= 0 && sum <= mark * (1.0 + 0x1p-40) && end >= mark * (1.0 - 0x1p-40)) {
+        for (int g = 0; g < kPer; g += GROUP) {
+            float p[GROUP], q[GROUP];
+            load_values(r.p, at + g, A.V, p);
+            if (r.q != nullptr) load_values(r.q, at + g, A.V, q);
+#pragma unroll
+            for (int c = 0; c < GROUP; ++c) {
+                double a, b;
+                weights(r, at + g + c, p[c], q[c], a, b);
+                const double x = all ? b : a;
+                sum += x;
+                if (x > 0.0 && sum > mark) first = min(first, at + g + c);
+            }
+        }
+    }
+    if (first != 0x7fffffff) atomicMin(&found[0], first);
+    if (mine >= 0) atomicMax(&found[1], mine);
+    __syncthreads();
+    put_tokens(A, n, stand, found[0] != 0x7fffffff ? found[0] : found[1], 1024);
+}
+
+// Rows of up to VROW values go in one kernel.  (In us, captured, against two: 1 row of 4000 7.6 / 13.4,
+// of 16000 10.1 / 13.4, 128 of 16000 11.2 / 14.7; a row of 32000 17.8 / 10.6: a thread's values then
+// pass through the first cache more than once.)
+constexpr int64_t VROW = 16384;
+int verify_tiles(int64_t V) { return V <= VROW ? 0 : (int)((V + VT - 1) / VT); }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
+    if (a.tiles == 0) {
+        if (a.V <= 4096)
+            hipLaunchKernelGGL((verify_row_kernel<4>), dim3((unsigned)a.N), dim3(1024), 0, s, a);
+        else
+            hipLaunchKernelGGL((verify_row_kernel<16>), dim3((unsigned)a.N), dim3(1024), 0, s, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(verify_sums_kernel, dim3((unsigned)((int64_t)a.N * a.tiles)), dim3(VTHREADS), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

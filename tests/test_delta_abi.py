@@ -200,14 +200,18 @@ def test_verify_refuses_arguments():
     p = kda.KdaVerifyProblem(3, 2, 100)
     for name in "drafts target uniform tokens accepted".split():
         assert verify(p, **{name: None}) == NULL
-    assert verify(p, ws=None) == NULL
-    assert verify(p, ws_bytes=3 * 16 - 1) == WS
-    assert verify(p, ws=90 * GAP + 8) == SHAPE
+    long = kda.KdaVerifyProblem(3, 2, 40000)                   # (the sums of ten tiles of each row)
+    n = ctypes.c_size_t()
+    for q, need in ((p, 0), (kda.KdaVerifyProblem(3, 2, 16384), 0), (long, 3 * 10 * 16)):
+        assert kda._lib.kda_verify_workspace_bytes(ctypes.byref(q), ctypes.byref(n)) == OK and n.value == need
+    assert verify(long, ws=None) == NULL
+    assert verify(long, ws_bytes=3 * 10 * 16 - 1) == WS
+    assert verify(long, ws=90 * GAP + 8) == SHAPE
+    assert verify(long, ws=4 * GAP) == OVERLAP
     assert verify(p, tokens=GAP) == OVERLAP                    # tokens over the drafts
     assert verify(p, accepted=2 * GAP) == OVERLAP              # over draft_lens
     assert verify(p, tokens=3 * GAP + 8 * 400) == OVERLAP      # over target's last row
     assert verify(p, accepted=6 * GAP + 4) == OVERLAP          # over the tokens
-    assert verify(p, ws=4 * GAP) == OVERLAP
     assert kda._lib.kda_verify_workspace_bytes(ctypes.byref(p), None) == NULL
 
 

@@ -16,7 +16,9 @@ from tests import layer_util as lu
 pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 8), (3, 16), (5, 504), (70, 512), (9, 520), (13, 1024), (6, 1032), (700, 2048), (33, 4096), (7, 6144 + 8),
-          (5, 8192), (3, 12288), (4, 12296), (3, 16384), (2, 16392), (3, 32760), (2, 32768)]
+          (5, 8192), (3, 12288), (4, 12296), (3, 16384), (2, 16392), (3, 32760), (2, 32768),
+          (20001, 96), (9000, 128), (2500, 136), (2100, 1000), (1300, 4096), (700, 12288), (300, 16384), (270, 24000),
+          (260, 32768)]    # (more rows than workgroups take at once)
 
 
 def make(T, C, seed, shift=0.5):
@@ -59,6 +61,33 @@ def test_parity(T, C):
     torch.cuda.synchronize()
     check_forward(y, x, w, b, 1e-5)
     check_backward(got, dy, x, w, 1e-5)
+
+
+@pytest.mark.parametrize("T,C", [(66000, 1024), (5500, 12288)])
+def test_more_than_a_cache_holds(T, C):
+    """Rows that go past the caches: the same bits as of the rows by themselves, and the sums over
+    all of them."""
+    import gated_delta_rule_32_amd as kda
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, dy = (torch.randn((T, C), generator=g, device="cuda").bfloat16() for _ in range(2))
+    w, b = (torch.randn(C, generator=g, device="cuda") for _ in range(2))
+    y, (dx, dw, db) = kda.layer_norm_forward(x, w, b), kda.layer_norm_backward(dy, x, w)
+    for r in (slice(0, 40), slice(T // 2, T // 2 + 40), slice(T - 40, T)):
+        assert torch.equal(kda.layer_norm_forward(x[r], w, b), y[r])
+        assert torch.equal(kda.layer_norm_backward(dy[r], x[r], w)[0], dx[r])
+    sum_w, sum_b, terms_w, terms_b = (torch.zeros(C, dtype=torch.float64, device="cuda") for _ in range(4))
+    for i in range(0, T, 4096):
+        x64, d64 = x[i:i + 4096].double(), dy[i:i + 4096].double()
+        c = x64 - x64.mean(-1, keepdim=True)
+        h = c / torch.sqrt((c * c).mean(-1, keepdim=True) + 1e-5)
+        sum_w += (d64 * h).sum(0)
+        sum_b += d64.sum(0)
+        terms_w += (d64 * h).abs().sum(0)
+        terms_b += d64.abs().sum(0)
+    # a thread adds T / 256 rows in turn at most, the second kernel 8 and 16 partial sums: 2^-24 each; h 2^-20
+    bar = 2.0 ** -24 * (T / 256 + 24)
+    assert ((dw - sum_w).abs() <= (bar + 2.0 ** -20) * terms_w).all()
+    assert ((db - sum_b).abs() <= bar * terms_b).all()
 
 
 def test_without_a_bias_and_with_another_eps():

@@ -45,7 +45,8 @@ class Drafts:
 
 @pytest.mark.parametrize("point", [False, True])
 @pytest.mark.parametrize("N,S,V", [(1, 1, 1), (3, 2, 2), (9, 4, 17), (5, 3, 4095), (5, 3, 4096), (5, 3, 4097), (4, 5, 9000),
-                                   (2, 1, 40001), (2, 70, 33), (3, 0, 5000)])
+                                   (2, 1, 40001), (2, 70, 33), (3, 0, 5000), (3, 2, 16384), (3, 2, 16385), (4, 3, 32767),
+                                   (4, 3, 32768), (4, 3, 32769), (2, 2, 300007)])
 def test_parity(N, S, V, point):
     print(f"[verify] {N} {S} {V} {point}", flush=True)
     for seed in range(3):
@@ -76,46 +77,50 @@ def test_drafts_outside_the_vocabulary_never_stand():
         d.check()
 
 
-def test_equal_probabilities_fall_back_to_the_targets():
+@pytest.mark.parametrize("V", [5000, 50000])
+def test_equal_probabilities_fall_back_to_the_targets(V):
     """Where p exceeds q nowhere, the token is drawn from p."""
-    d = Drafts(3, 2, 5000, 9)
+    d = Drafts(3, 2, V, 9)
     d.target[:, :2] = 0.5 * d.draft
     d.uniform[:, 0] = 0.75
     assert (d.call()[1] == 1).all()
     d.check()
 
 
-def test_rows_without_a_probability():
-    d = Drafts(3, 1, 100, 10)
+@pytest.mark.parametrize("V", [100, 40000])
+def test_rows_without_a_probability(V):
+    d = Drafts(3, 1, V, 10)
     d.target[1] = 0.0
     tokens, accepted = d.call()
     assert accepted[1] == 1 and tokens[1].tolist() == [-1, -1]
     d.check()
 
 
-def test_draws_at_the_ends():
+@pytest.mark.parametrize("V", [9000, 39000])
+def test_draws_at_the_ends(V):
     """A random number of 0 (or below, or NaN) draws the first index with a weight, one of
     1 and above the last."""
-    d = Drafts(5, 0, 9000, 11)
+    d = Drafts(5, 0, V, 11)
     d.target[:, :, :5] = 0.0
-    d.target[:, :, 8990:] = 0.0
+    d.target[:, :, V - 10:] = 0.0
     d.uniform[:, 0] = torch.tensor([0.0, -1.0, float("nan"), 1.0, 7.0])
     tokens, _ = d.call()
-    assert tokens[:, 0].tolist() == [5, 5, 5, 8989, 8989]
+    assert tokens[:, 0].tolist() == [5, 5, 5, V - 11, V - 11]
     d.check()
 
 
-def test_ties_go_to_the_lowest_index():
+@pytest.mark.parametrize("V", [8192, 65536])
+def test_ties_go_to_the_lowest_index(V):
     """Equal weights: u V falls on a border, which belongs to the index above it."""
-    V = 8192
     d = Drafts(4, 0, V, 12)
     d.target[:] = 1.0 / V
     d.uniform[:, 0] = torch.tensor([0.0, 0.5, 0.25, 4095 / V])
-    assert d.call()[0][:, 0].tolist() == [0, 4096, 2048, 4095]
+    assert d.call()[0][:, 0].tolist() == [0, V // 2, V // 4, 4095]
 
 
-def test_nan_counts_as_nothing():
-    d = Drafts(2, 1, 600, 13)
+@pytest.mark.parametrize("V", [600, 40000])
+def test_nan_counts_as_nothing(V):
+    d = Drafts(2, 1, V, 13)
     d.uniform[:, 0] = 0.9999999
     d.target[0, 0, 7] = float("nan")
     d.draft[1, 0, 5] = float("nan")
@@ -132,23 +137,25 @@ def test_slices_of_wider_rows(V):
     Drafts(5, 3, V, 14).check(wrap=wrap)
 
 
-def test_given_outputs_and_workspace():
+@pytest.mark.parametrize("V", [700, 40000])
+def test_given_outputs_and_workspace(V):
     import gated_delta_rule_32_amd as kda
-    d = Drafts(5, 3, 700, 15)
+    d = Drafts(5, 3, V, 15)
     out = (torch.empty((5, 4), dtype=torch.int32, device="cuda"), torch.empty(5, dtype=torch.int32, device="cuda"))
-    ws = torch.empty(kda.kda_verify_workspace_bytes(kda.KdaVerifyProblem(5, 3, 700)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda.kda_verify_workspace_bytes(kda.KdaVerifyProblem(5, 3, V)), dtype=torch.uint8, device="cuda")
     got = d.call(out=out, workspace=ws)
     assert got[0] is out[0] and got[1] is out[1]
     d.check()
 
 
-def test_captured():
+@pytest.mark.parametrize("V", [5000, 40000])
+def test_captured(V):
     """One graph, replayed on changed inputs with eager calls between."""
     import gated_delta_rule_32_amd as kda
-    a, b = Drafts(6, 3, 5000, 16), Drafts(6, 3, 5000, 17)
+    a, b = Drafts(6, 3, V, 16), Drafts(6, 3, V, 17)
     dev = [x.cuda() for x in (a.drafts, a.target, a.uniform, a.draft)]
     out = (torch.empty((6, 4), dtype=torch.int32, device="cuda"), torch.empty(6, dtype=torch.int32, device="cuda"))
-    ws = torch.empty(kda.kda_verify_workspace_bytes(kda.KdaVerifyProblem(6, 3, 5000)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(kda.kda_verify_workspace_bytes(kda.KdaVerifyProblem(6, 3, V)), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
