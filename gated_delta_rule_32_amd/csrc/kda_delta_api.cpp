@@ -233,7 +233,10 @@ std::vector<Span> input_spans(const kda_delta_problem* pp, const Delta& d, const
 
 // kda_delta_infer takes sequences of up to this many tokens token by token, each by its own
 // length, so that a user's tokens are computed the same way whoever else is in the batch.
-constexpr int64_t kTokenSerialMax = 8;
+// In us of 2, 4, 6, 8, 12 tokens of 32 heads, against 32 in chunks: 1 sequence 5.3, 7.8, 10.1, 12.7,
+// 17.5 against 13.7; 8 of them 10.3, 14.2, 18.0, 21.8, 28.4 against 19.6; 32 of them 27, 39, 50, 62, 87
+// against 41; 128 of them 97, 140, 187, 227, 315 against 132 to 142.
+constexpr int64_t kTokenSerialMax = 4;
 
 // How many sequences run in chunks (a packed call's schedule has them first), with how many
 // blocks and segments of `seg` tokens (0: whole).

@@ -194,7 +194,7 @@ def gated_delta_rule(q, k, v, g, beta, initial_state=None, scale=None, cu_seqlen
     (output, pool).  initial_state is the pool [P, Hv, 128, 128], updated in
     place: sequence n reads and writes slot ssm_state_indices[n] (int32, with
     its CPU mirror), or slot n.  None starts every sequence from zero in a new
-    pool of N slots.  Sequences of up to 8 tokens run token by token, longer ones
+    pool of N slots.  Sequences of up to 4 tokens run token by token, longer ones
     in chunks, whatever else is in the call.  Drafted tokens (num_spec_tokens =
     S): every sequence has 1+S tokens, ssm_state_indices is [N, 1+S]; the state
     starts from slot [n, a-1] with a = num_accepted_tokens[n] (int32; verify_drafts

@@ -542,10 +542,10 @@ kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* 
                          const void* d_o, const float* dfinal_state, void* dq, void* dk, void* dv, void* dg,
                          void* dbeta, float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Decode (sequences of up to 8 tokens, token by token) and prefill (longer
+/* Decode (sequences of up to 4 tokens, token by token) and prefill (longer
  * ones, in chunks) on an FP32 state pool [pool_slots][Hv][128][128], updated
  * in place.  One call may hold both: each sequence runs by its own length, and
- * one of up to 8 tokens gives the same bits whatever else is in the call.
+ * one of up to 4 tokens gives the same bits whatever else is in the call.
  * Sequence n reads and writes slot state_indices[n] (slot n when NULL); other
  * slots are not touched.  The indices must be distinct and in range, checked on
  * the host mirror (given iff state_indices is).  A slot that the device copy

@@ -162,7 +162,7 @@ def test_workspace_sizes():
     records = up(4 * 4 * 2 * 6144)
     assert need("fwd", p) >= records
     assert need("infer", p, 0) >= records
-    assert need("infer", delta(T=8), 0) == 0                   # token by token
+    assert need("infer", delta(T=4), 0) == 0                   # token by token
     assert need("infer", delta(T=40), 39) == 0
     assert need("bwd", p, 0) == records + need("bwd", p, 1) >= records + 2 * 4 * 4 * (32768 + 16384)
     cut = delta(T=65, B=2, N=2, segment=64)                    # two segments a sequence, two matrices each
