@@ -565,3 +565,80 @@ def test_captured_decode_and_prefill():
         assert torch.equal(pool, eager)
         for a, b in zip(outs, eager_outs):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# far rows and far apart values
+# ---------------------------------------------------------------------------
+def test_rows_behind_2_31_elements():
+    """Token rows as far apart as a call takes: q's, k's and v's last ones lie behind 2^31 elements."""
+    import gated_delta_rule_32_amd as kda
+    T, stride = 70, 1 << 25
+    inp = Inp([T], False, 1, 2, seed=61)
+    wide = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda").view(1, T, stride)
+    d = []
+    for at, x in ((0, inp.q), (256, inp.k), (stride - 256, inp.v)):
+        n = x.shape[2] * 128
+        wide[:, :, at:at + n] = x.view(1, T, n).cuda()
+        d.append(wide[:, :, at:at + n].unflatten(-1, (-1, 128)))
+    rest = [inp.dev(x) for x in (inp.g, inp.beta, inp.s0)]
+    o, fs, ctx = kda.gated_delta_rule_training_forward(*d, *rest, use_qk_l2norm=True)
+    grads = kda.gated_delta_rule_training_backward(ctx, inp.dev(inp.do), inp.dev(inp.ds))
+    pool = inp.dev(inp.s0)
+    served, _ = kda.gated_delta_rule(*d, *rest[:2], pool, use_qk_l2norm=True)
+    torch.cuda.synchronize()
+    for a, b in zip(train(inp), (o, fs) + grads):
+        assert torch.equal(a, b)
+    assert torch.equal(served, o) and torch.equal(pool, fs)
+
+
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_slots_behind_2_31_elements(T):
+    Hv, slots = 64, [2099, 7]
+    inp = Inp([T] * 2, False, 16, Hv, seed=62)
+    pool = torch.empty((2100, Hv, 128, 128), device="cuda")     # 2.2e9 values
+    pool[slots] = inp.s0.cuda()
+    out = pool_call(inp, pool, slots)
+    near = inp.s0.cuda()
+    assert torch.equal(out, pool_call(inp, near, [0, 1]))
+    assert torch.equal(pool[slots], near)
+
+
+@pytest.mark.parametrize("segment", [0, 64])
+def test_values_far_apart(segment):
+    """Tokens, output channels and states of sizes from 2^-12 to 2^12 side by side: every result is
+    held to the sizes of its own terms.  (The backward keeps 32 channels' states and rows to a part
+    of their largest value in FP16: 2^-39 of it, far below the bars at a ratio of 2^24.)"""
+    inp = Inp([190, 70], True, 1, 2, seed=63, gates="layer")
+    g = torch.Generator().manual_seed(64)
+
+    def spread(x, *dims):
+        shape = [n if i in dims else 1 for i, n in enumerate(x.shape)]
+        return (x.float() * 2.0 ** torch.randint(-6, 7, shape, generator=g)).to(x.dtype)
+    inp.v, inp.do = spread(spread(inp.v, 1), 2, 3), spread(spread(inp.do, 1), 2, 3)
+    inp.s0, inp.ds = spread(spread(inp.s0, 1, 2), 0), spread(spread(inp.ds, 1, 2), 0)
+    got = train(inp, segment=segment)
+    check_forward(inp, got)
+    du.check_gradients(inp, got[2:])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -40, 2.0 ** 40])
+def test_small_and_large_values(scale):
+    """The rule is linear in v and the states, its gradients in do: a power of two goes through all of
+    it exactly, while the numbers stay normal.  At 2^-60 the gradients of q and k are of the size of 2^-120 and the
+    pieces of their factors end at 2^-126, BF16's least normal number: of each of a token's 64 elements
+    of the three matrices e, f and f^T less than 2^-126 is lost twice, times a key's or query's channel, at
+    most 1; and as much of each of 128 products with a state.  That is below 2^-116; a gate's gradient sums
+    128 channels of those, at most 1 in all, over up to 100 tokens of two gradients: 2^-108."""
+    inp = Inp([100], False, 1, 2, seed=65)
+    want = train(inp)
+    for n in ("v", "s0", "do", "ds"):
+        x = getattr(inp, n)
+        setattr(inp, n, (x.float() * scale).to(x.dtype))
+    got = train(inp)
+    for name, a, b, power in zip("o final dq dk dv dg dbeta ds0".split(), want, got, (1, 1, 2, 2, 1, 2, 2, 1)):
+        if power == 2 and scale < 2.0 ** -50:
+            bar = 2.0 ** -108 if name in ("dg", "dbeta") else 2.0 ** -116
+            assert (a.double() * scale ** power - b.double()).abs().max() <= bar, name
+        else:
+            assert torch.equal((a.double() * scale ** power).to(a.dtype), b), name

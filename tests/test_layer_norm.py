@@ -175,3 +175,16 @@ def test_the_same_bits_again_and_captured():
         for a, c in zip(outs, want):
             assert torch.equal(a, c)
         x.copy_(x.flip(0))
+
+
+@pytest.mark.parametrize("C", [64, 2000])
+def test_rows_behind_2_31_elements(C):
+    import gated_delta_rule_32_amd as kda
+    T, stride = 70, 1 << 25
+    x, w, b, dy = make(T, C, 31)
+    wide = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda").view(T, stride)[:, 8:8 + C]
+    wide.copy_(x)
+    args = [t.cuda() for t in (w, b, dy)]
+    y, grads = kda.layer_norm_forward(wide, *args[:2]), kda.layer_norm_backward(args[2], wide, args[0])
+    assert torch.equal(y, kda.layer_norm_forward(x.cuda(), *args[:2]))
+    assert all(torch.equal(a, e) for a, e in zip(grads, kda.layer_norm_backward(args[2], x.cuda(), args[0])))

@@ -179,3 +179,21 @@ def test_one_sequence_does_not_see_the_others():
         one.drafts, one.target, one.draft, one.uniform = (x[n:n + 1].contiguous() for x in (d.drafts, d.target, d.draft, d.uniform))
         t, a = one.call()
         assert torch.equal(t[0], tokens[n]) and a[0] == accepted[n]
+
+
+@pytest.mark.parametrize("V", [3000, 20000])
+def test_rows_behind_2_31_values(V):
+    stride = 1 << 29                       # five rows of 2 GiB: the last begins behind 2^31 values
+    space = torch.empty(5 * stride, device="cuda")
+
+    def wrap(x):
+        w = space[:x.shape[0] * x.shape[1] * stride].view(*x.shape[:2], stride)[..., :V]
+        w.copy_(x)
+        return w
+    d = Drafts(1, 4, V, 21)
+    d.uniform[:, :4] = 0.0                 # (all stand: the draw is from the last row)
+    d.draft = d.draft.clamp_min(1e-9)
+    import gated_delta_rule_32_amd as kda
+    tokens, accepted = kda.verify_drafts(d.drafts.cuda(), wrap(d.target.cuda()), d.uniform.cuda(), d.draft.cuda())
+    want, count = d.reference()
+    assert np.array_equal(accepted.cpu().numpy(), count) and np.array_equal(tokens.cpu().numpy(), want)
