@@ -13,9 +13,10 @@ rounding is off.
     products and written rows in two (2^-17 each): 2^-14 of the weights, and its own rounding, u |o|.
   - The norm of a BF16 result's error: one rounding's errors are spread evenly, u/sqrt(3) of the value in
     the mean square at most; 3/4 u leaves 30% for the parts above.
-  - A gradient's sums take the states before and behind a block as two BF16 pieces (off by
-    2^-16), the rows W and Y and the block's matrices as two (2^-17): four products of such
-    pairs add up in dk, and 2^-13 of the weights covers them.  dq and dk of shared heads are
+  - A gradient's sums take the states before and behind a block and the rows W and Y in FP16, off by
+    2^-11 at most and 2^-12.3 in the mean square; over 128 terms that is 2^-12.3 sqrt(2) / sqrt(128)
+    of the weights, 2^-14 with terms of uneven sizes, in the mean square.  The block's matrices go as two BF16 pieces
+    (2^-17).  2^-13 of the weights covers twice that, and u |ref| beside it leaves room for more.  dq and dk of shared heads are
     sums of partials that are rounded to 10 bits: 2^-10 of the partials' sizes.  dinitial_state is as exact
     as a final state.
 """
