@@ -88,14 +88,26 @@ __device__ __forceinline__ void put_tokens(const VerifyArgs& A, int64_t n, int s
     if (threadIdx.x == 0) A.accepted[n] = stand + 1;
 }
 
+__device__ __forceinline__ double lane_of(double x, int i) {
+    const u32x2 b = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_readlane((int)b[0], i),
+                                            (unsigned)__builtin_amdgcn_readlane((int)b[1], i)});
+}
+// The value `kDown` lanes before this one in its row of 16, or zero.
+template <int kDown>
+__device__ __forceinline__ double shifted(double x) {
+    const u32x2 b = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_update_dpp(0, (int)b[0], 0x110 + kDown, 0xF, 0xF, true),
+                                            (unsigned)__builtin_amdgcn_update_dpp(0, (int)b[1], 0x110 + kDown, 0xF, 0xF, true)});
+}
 // Inclusive sum over the wave's lanes.
 __device__ __forceinline__ double wave_scan(double x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d, 64);
-        if (lane >= d) x += y;
-    }
-    return x;
+    x += shifted<1>(x);
+    x += shifted<2>(x);
+    x += shifted<4>(x);
+    x += shifted<8>(x);
+    const double a = lane_of(x, 15), b = a + lane_of(x, 31), c = b + lane_of(x, 47);
+    return lane < 16 ? x : x + (lane < 32 ? a : lane < 48 ? b : c);
 }
 
 }  // namespace
@@ -120,8 +132,8 @@ __global__ __launch_bounds__(VTHREADS) void verify_sums_kernel(VerifyArgs A) {
         more += a;
         whole += b;
     }
-    more = __shfl(wave_scan(more, lane), 63, 64);
-    whole = __shfl(wave_scan(whole, lane), 63, 64);
+    more = lane_of(wave_scan(more, lane), 63);
+    whole = lane_of(wave_scan(whole, lane), 63);
     if (lane == 0) {
         part[w][0] = more;
         part[w][1] = whole;
@@ -151,7 +163,7 @@ __global__ __launch_bounds__(VTHREADS) void verify_draw_kernel(VerifyArgs A) {
         total = 0.0;
         for (int base = 0; base < A.tiles; base += 64) {
             const int i = base + lane;
-            total += __shfl(wave_scan(i < A.tiles ? sums[2 * i + which] : 0.0, lane), 63, 64);
+            total += lane_of(wave_scan(i < A.tiles ? sums[2 * i + which] : 0.0, lane), 63);
         }
         if (total > 0.0) break;
     }
@@ -177,13 +189,13 @@ __global__ __launch_bounds__(VTHREADS) void verify_draw_kernel(VerifyArgs A) {
             if (past != 0) {
                 const int f = __ffsll(past) - 1;
                 tile = base + f;
-                start = __shfl(from, f, 64);
+                start = lane_of(from, f);
             } else if (some != 0) {
                 const int l = 63 - __clzll(some);
                 last = base + l;
-                last_start = __shfl(from, l, 64);
+                last_start = lane_of(from, l);
             }
-            before = __shfl(sum, 63, 64);
+            before = lane_of(sum, 63);
         }
         if (tile < 0) {
             tile = last;
@@ -222,82 +234,98 @@ __global__ __launch_bounds__(VTHREADS) void verify_draw_kernel(VerifyArgs A) {
     put_tokens(A, n, stand, token, VTHREADS);
 }
 
-// The same for a row of up to 1024 kPer values, in one go.
+// The same for a row of up to 1024 kPer values, in one go.  A wave sums its 64 kPer values as
+// they lie in memory; the one that the draw falls into, and the last one with a weight, take them
+// again (out of a cache), kPer in a row to a lane.
 template <int kPer>
 __global__ __launch_bounds__(1024) void verify_row_kernel(VerifyArgs A) {
     __shared__ double part[16][2];
-    __shared__ int found[2];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    __shared__ int found[2];   // first index whose running sum passes; last index with a weight
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n = blockIdx.x;
     const int lens = lengths(A, n), stand = standing(A, n, lens, lane);
-    const Row r = draw_row(A, n, stand, lens);
-    const int at = threadIdx.x * kPer;
-    constexpr int GROUP = kPer < 16 ? kPer : 16;
-    double own[2] = {0.0, 0.0}, scan[2];
-    int last[2] = {-1, -1};    // this thread's last indices with a weight
+    Row r = draw_row(A, n, stand, lens);
+    double more = 0.0, whole = 0.0;
+    {
+        float p[kPer / 4][4], q[kPer / 4][4];
 #pragma unroll
-    for (int g = 0; g < kPer; g += GROUP) {
-        float p[GROUP], q[GROUP];
-        load_values(r.p, at + g, A.V, p);
-        if (r.q != nullptr) load_values(r.q, at + g, A.V, q);
-#pragma unroll
-        for (int c = 0; c < GROUP; ++c) {
-            double a, b;
-            weights(r, at + g + c, p[c], q[c], a, b);
-            own[0] += a;
-            own[1] += b;
-            if (a > 0.0) last[0] = at + g + c;
-            if (b > 0.0) last[1] = at + g + c;
+        for (int g = 0; g < kPer / 4; ++g) {
+            const int at = w * 64 * kPer + 256 * g + 4 * lane;
+            load_values(r.p, at, A.V, p[g]);
+            if (r.q != nullptr) load_values(r.q, at, A.V, q[g]);
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        scan[i] = wave_scan(own[i], lane);
-        if (lane == 63) part[w][i] = scan[i];
+        for (int g = 0; g < kPer / 4; ++g)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                double a, b;
+                weights(r, w * 64 * kPer + 256 * g + 4 * lane + c, p[g][c], q[g][c], a, b);
+                more += a;
+                whole += b;
+            }
+    }
+    more = wave_scan(more, lane);
+    whole = wave_scan(whole, lane);
+    if (lane == 63) {
+        part[w][0] = more;
+        part[w][1] = whole;
     }
     if (threadIdx.x < 2) found[threadIdx.x] = threadIdx.x == 0 ? 0x7fffffff : -1;
     __syncthreads();
-    double total[2] = {0.0, 0.0}, before[2] = {0.0, 0.0};
+    double total = 0.0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (j == w) before[i] = total[i];
-            total[i] += part[j][i];
-        }
-    const bool all = !(total[0] > 0.0);   // p exceeds q nowhere
-    const double u = (double)A.uniform[n * (A.S + 1) + A.S];
-    const double mark = (u > 0.0 ? u : 0.0) * (all ? total[1] : total[0]);
-    double sum = all ? before[1] + (scan[1] - own[1]) : before[0] + (scan[0] - own[0]);
-    const double end = sum + (all ? own[1] : own[0]);
-    int first = 0x7fffffff;
-    const int mine = all ? last[1] : last[0];
-    // only where the sum passes the mark the values are walked again (by more than the sums' rounding
-    // around it, so that one of two neighbours finds it)
-    if (mine >= 0 && sum <= mark * (1.0 + 0x1p-40) && end >= mark * (1.0 - 0x1p-40)) {
-        for (int g = 0; g < kPer; g += GROUP) {
-            float p[GROUP], q[GROUP];
-            load_values(r.p, at + g, A.V, p);
-            if (r.q != nullptr) load_values(r.q, at + g, A.V, q);
-#pragma unroll
-            for (int c = 0; c < GROUP; ++c) {
-                double a, b;
-                weights(r, at + g + c, p[c], q[c], a, b);
-                const double x = all ? b : a;
-                sum += x;
-                if (x > 0.0 && sum > mark) first = min(first, at + g + c);
-            }
-        }
+    for (int j = 0; j < 16; ++j) total += part[j][0];
+    const int which = total > 0.0 ? 0 : 1;   // 1: p exceeds q nowhere
+    if (which == 1) {
+        r.q = nullptr;
+        r.point = -1;
     }
-    if (first != 0x7fffffff) atomicMin(&found[0], first);
-    if (mine >= 0) atomicMax(&found[1], mine);
+    double before = 0.0;
+    int last = -1;
+    total = 0.0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (j == w) before = total;
+        const double x = part[j][which];
+        if (x > 0.0) last = j;
+        total += x;
+    }
+    const double u = (double)A.uniform[n * (A.S + 1) + A.S];
+    const double mark = (u > 0.0 ? u : 0.0) * total;
+    // (by more than the sums' rounding around the mark, so that one of two neighbours finds it)
+    const double end = before + part[w][which];
+    if (w == last || (w < last && before <= mark * (1.0 + 0x1p-40) && end >= mark * (1.0 - 0x1p-40))) {
+        const int at = (w * 64 + lane) * kPer;
+        float p[kPer], q[kPer];
+        load_values(r.p, at, A.V, p);
+        if (r.q != nullptr) load_values(r.q, at, A.V, q);
+        double own = 0.0;
+        int mine = -1, first = 0x7fffffff;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            double a, b;
+            weights(r, at + c, p[c], q[c], a, b);
+            own += a;
+            if (a > 0.0) mine = at + c;
+        }
+        double sum = before + (wave_scan(own, lane) - own);
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+            double a, b;
+            weights(r, at + c, p[c], q[c], a, b);
+            sum += a;
+            if (a > 0.0 && sum > mark) first = min(first, at + c);
+        }
+        if (first != 0x7fffffff) atomicMin(&found[0], first);
+        if (mine >= 0) atomicMax(&found[1], mine);
+    }
     __syncthreads();
     put_tokens(A, n, stand, found[0] != 0x7fffffff ? found[0] : found[1], 1024);
 }
 
-// Rows of up to VROW values go in one kernel.  (In us, captured, against two: 1 row of 4000 7.6 / 13.4,
-// of 16000 10.1 / 13.4, 128 of 16000 11.2 / 14.7; a row of 32000 17.8 / 10.6: a thread's values then
-// pass through the first cache more than once.)
+// Rows of up to VROW values go in one kernel.  (In us, captured, against two: 1 row of 4000 7.3 / 10.1,
+// of 16000 10.3 / 12.2, 128 of 16000 11.1 / 14.1; with 32 values a thread a row of 32000 15.5 / 11.9, 128 of
+// them 18.4 / 16.0: one unit takes as long to read it as the two kernels.)
 constexpr int64_t VROW = 16384;
 int verify_tiles(int64_t V) { return V <= VROW ? 0 : (int)((V + VT - 1) / VT); }
 
