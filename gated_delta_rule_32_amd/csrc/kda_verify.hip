@@ -8,8 +8,8 @@
 // 2^-50 of the total).  Only one row of p and q of each sequence is read.  A row that one workgroup
 // holds in registers is read once, by one kernel; of longer ones first the tiles' sums are formed, by
 // as many workgroups as there are tiles, then the tile that the draw falls into is read again.
-// Bound by HBM with many rows (128 of 131072: 17.8 us, 5.2 TB/s, and 9.4 us for the draws), by latency with
-// few (one of 32000: 4.8 and 6.7 us).
+// Bound by HBM with many rows (128 of 131072: 17.3 us, 5.4 TB/s, and 8.8 us for the draws), by latency with
+// few (one of 32000: 4.4 and 6.1 us).
 #include "kda_common.hpp"
 #include "kda_delta.h"
 
