@@ -43,9 +43,10 @@ def kda_verify(p: KdaVerifyProblem, draft_tokens, draft_lens, target_probs, draf
 def _prob_rows(name, t, shape, device) -> int:
     """The row stride of FP32 [N, rows, V] probabilities: dense, or a slice of
     wider rows."""
-    _require(isinstance(t, torch.Tensor) and t.dtype is _F32, f"{name} must be a float32 tensor")
-    _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _require(t.device == device, f"{name} must be on {device}, got {t.device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.shape == shape and t.device == device):
+        _require(isinstance(t, torch.Tensor) and t.dtype is _F32, f"{name} must be a float32 tensor")
+        _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        _require(False, f"{name} must be on {device}, got {t.device}")
     N, R, V = shape
     if t.is_contiguous():
         return V
@@ -77,7 +78,8 @@ def verify_drafts(draft_tokens, target_probs, uniform, draft_probs=None, draft_l
         _require(isinstance(target_probs, torch.Tensor) and target_probs.dim() == 3, "target_probs must be [N, 1+S, V]")
         _require(False, f"tensors must be on a GPU, got {target_probs.device}")
     dev = target_probs.device
-    N, S, V = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    N, S, V = target_probs.shape
+    S -= 1
     _require(N >= 1 and S >= 0 and V >= 1, "target_probs must not be empty")
     p = KdaVerifyProblem(N, S, V, _prob_rows("target_probs", target_probs, (N, S + 1, V), dev), 0)
     _dense("draft_tokens", draft_tokens, _I32, (N, S), dev)
@@ -87,7 +89,7 @@ def verify_drafts(draft_tokens, target_probs, uniform, draft_probs=None, draft_l
     if draft_lens is not None:
         _dense("draft_lens", draft_lens, _I32, (N,), dev)
     if out is None:
-        out = (torch.empty((N, S + 1), dtype=_I32, device=dev), torch.empty((N,), dtype=_I32, device=dev))
+        out = (draft_tokens.new_empty((N, S + 1)), draft_tokens.new_empty((N,)))
     else:
         _require(len(out) == 2, "out must hold two tensors")
         _dense("tokens", out[0], _I32, (N, S + 1), dev)
