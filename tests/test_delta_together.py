@@ -130,3 +130,38 @@ def test_serving_loop():
             stood.add(a)
             so_far[n] = [torch.cat([t, c[:, :a]], 1) for t, c in zip(so_far[n], new)]
     assert len(stood) > 1     # (drafts stood and did not)
+
+
+def test_calls_on_two_streams_at_once():
+    """Training steps, prompts and drafted tokens on two streams, each with its own tensors and both
+    with the same cached schedules: the bits of the calls by themselves, again and again."""
+    import gated_delta_rule_32_amd as kda
+    inps = [Inp([200, 64, 1, 130], True, 1, 2, seed=s) for s in (101, 102)]
+    dev = [{n: i.dev(getattr(i, n)) for n in ("q", "k", "v", "g", "beta", "s0", "do", "ds", "cu")} for i in inps]
+    rows_ = [ln.make(300, 1024, s) for s in (103, 104)]
+    rows_ = [[t.cuda() for t in r] for r in rows_]
+
+    def work(j):
+        d, (x, w, b, dy) = dev[j], rows_[j]
+        ins = [d[n] for n in ("q", "k", "v", "g", "beta")]
+        more = dict(use_qk_l2norm=True, cu_seqlens_cpu=inps[j].cu)
+        out = []
+        for segment in (0, 64):
+            o, final, ctx = kda.gated_delta_rule_training_forward(*ins, d["s0"], d["cu"], segment=segment, **more)
+            out += [o, final, *kda.gated_delta_rule_training_backward(ctx, d["do"], d["ds"])]
+        pool = d["s0"].clone()
+        out += [kda.gated_delta_rule(*ins, pool, cu_seqlens=d["cu"], **more)[0], pool]
+        out += [kda.layer_norm_forward(x, w, b), *kda.layer_norm_backward(dy, x, w)]
+        return out
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for j in (0, 1):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(work(j))
+    torch.cuda.synchronize()
+    for j in (0, 1):
+        for again in got[j]:
+            assert all(torch.equal(a, e) for a, e in zip(again, want[j]))
