@@ -252,12 +252,14 @@ hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) { return launch_
 // The states before the segments, S <- S M + Q from one to the next; kReverse: the adjoints behind
 // them, Z <- Z M^T + R from the last to the first.  A workgroup per sequence, value head and 16 channels v,
 // wave t with their tile of the state as in the scan.  The product is exact to FP32, both
-// factors in three BF16 pieces.  Bound by the way of the M's: those of the next two segments
-// are on theirs.
+// factors in three BF16 pieces.  Bound by the steps of one segment, 2.6 us: M's pieces, S's way through
+// LDS, the products in four sums (in one sum, M taken apart behind the barrier, 3.2 us).  The M's of the
+// next two segments are on their way meanwhile.
 template <bool kReverse>
 __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaArgs A) {
     __shared__ __align__(16) char lds[2][3 * 4 * 1024];   // the state in pieces: [piece][32 channels k][lane][8]
-    const Item it = find_item(A.seqs, blockIdx.x >> 3);
+    const int block = xcd_order(blockIdx.x, gridDim.x, 8);   // (the eight that read an M share a cache)
+    const Item it = find_item(A.seqs, block >> 3);
     const int64_t slot = A.slot != nullptr ? A.slot[it.n] : it.n;
     if (slot < 0 || slot >= A.slots) return;
     const int Hv = A.map.Hv;
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaArgs A) {
     const int64_t item = (first + (kReverse ? segs - 1 : 0)) * Hv + it.h;
     const int64_t step = kReverse ? -Hv : Hv;
     const int64_t size = kReverse ? STATE : 2 * STATE;
-    const int at = (16 * (blockIdx.x & 7) + n16) * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1);
+    const int at = (16 * (block & 7) + n16) * D + 32 * (t >> 1) + 8 * gq + 4 * (t & 1);
     float* own = (kReverse ? A.behind : A.seg) + item * size + at;
     // of M transposed, [k][k']: 8 values k' of the row k that belongs to lane n, or (reverse) 8 rows k of column k'
     const int row = 32 * (t >> 1) + 8 * (n16 >> 2) + 4 * (t & 1) + (n16 & 3);
@@ -309,29 +311,38 @@ __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaArgs A) {
     auto place = [&](int i, f32x4 (&m)[4][2], f32x4& q, char* to) __attribute__((always_inline)) {
         *(f32x4*)(own + i * step * size) = x;
         if (i + 1 == segs) return false;
-        bf16x4 a[3];
-        pieces.split(x, a[0], a[1], a[2]);
-#pragma unroll
-        for (int d = 0; d < 3; ++d) *(bf16x4*)(to + ((d * 4 + (t >> 1)) * 64 + lane) * 16 + 8 * (t & 1)) = a[d];
-        barrier_lds();
-        x = q;
+        bf16x8 mp[4][3];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             bf16x4 m0[3], m1[3];
             pieces.split(m[p][0], m0[0], m0[1], m0[2]);
             pieces.split(m[p][1], m1[0], m1[1], m1[2]);
-            bf16x8 b[3];
 #pragma unroll
-            for (int d = 0; d < 3; ++d) b[d] = *(const bf16x8*)(to + ((d * 4 + p) * 64 + lane) * 16);
-#pragma unroll
-            for (int i = 2; i >= 0; --i)
-#pragma unroll
-                for (int d = 0; d <= i; ++d) x = mma32(cat8(m0[d], m1[d]), b[i - d], x);
+            for (int d = 0; d < 3; ++d) mp[p][d] = cat8(m0[d], m1[d]);
         }
+        bf16x4 a[3];
+        pieces.split(x, a[0], a[1], a[2]);
+#pragma unroll
+        for (int d = 0; d < 3; ++d) *(bf16x4*)(to + ((d * 4 + (t >> 1)) * 64 + lane) * 16 + 8 * (t & 1)) = a[d];
+        const f32x4 add = q;
         if (i + 3 < segs) {
             q = get_own(i + 2);
             get_map(i + 2, m);
         }
+        barrier_lds();
+        f32x4 sum[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            bf16x8 b[3];
+#pragma unroll
+            for (int d = 0; d < 3; ++d) b[d] = *(const bf16x8*)(to + ((d * 4 + p) * 64 + lane) * 16);
+            sum[p] = zero4();
+#pragma unroll
+            for (int i = 2; i >= 0; --i)
+#pragma unroll
+                for (int d = 0; d <= i; ++d) sum[p] = mma32(mp[p][d], b[i - d], sum[p]);
+        }
+        x = add + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         return true;
     };
     for (int i = 1;; i += 2) {

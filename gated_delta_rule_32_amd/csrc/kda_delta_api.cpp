@@ -67,7 +67,7 @@ int64_t total_segs(const Delta& d, int seg) {
 // Tokens of the segments that the scans walk side by side, or 0 for whole sequences:
 // whichever an estimate says is faster.  A scan over whole sequences takes the longest one's
 // latency, 2.4 to 2.9 us a chunk of 32 tokens, or the total's throughput, 15 ns a chunk and
-// head.  Segments shorten the first, for a scan that forms each one's M and Q, and 2.4 us for
+// head.  Segments shorten the first, for a scan that forms each one's M and Q, and 2 to 2.4 us for
 // every segment of the chain that joins them.  Both scans' chunk together takes 4.1 us with 64
 // segments and heads, 4.8 with 128, 7.9 with 256 and 32 ns each with more.
 // In us, forward and backward, whole sequences against the segments of this rule:
