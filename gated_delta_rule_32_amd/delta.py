@@ -120,7 +120,8 @@ def _problem(q, k, v, g, beta, scale, use_qk_l2norm, cu_seqlens, cu_seqlens_cpu,
 class GatedDeltaRuleTrainingContext:
     """What the backward needs of the forward: its problem, its inputs (cu_seqlens
     and its CPU mirror among them) with their versions, and its chunks' records
-    (about 200 bytes a token and value head; None where the forward was given a
+    (about 200 bytes a token and value head, and 128 KiB for each segment of a long
+    sequence on few heads; None where the forward was given a
     workspace, which the caller may have used again since)."""
     problem: KdaDeltaProblem
     inputs: tuple
@@ -139,7 +140,9 @@ def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_s
     v: [B, T, Hv, 128], dense or slices of wider token rows; value head h uses
     q/k head h // (Hv // Hqk); with use_qk_l2norm q and k are taken at unit
     length.  g (the decay's logarithm, at most 0) and beta: BF16 [B, T, Hv].
-    Packed calls pass cu_seqlens (int64 [N+1]) with its CPU mirror and B = 1."""
+    Packed calls pass cu_seqlens (int64 [N+1]) with its CPU mirror and B = 1.
+    segment: tokens of the segments that a sequence is walked in (a multiple of 64;
+    0: the library's choice)."""
     dev = _cuda(q)
     p = _problem(q, k, v, g, beta, scale, use_qk_l2norm, cu_seqlens, cu_seqlens_cpu, segment)
     states = (p.N, p.Hv, HEAD_DIM, HEAD_DIM)
