@@ -75,6 +75,7 @@ __device__ __forceinline__ void plane_scale(float m, float& up, float& down) {
 template <int NU, int kParts>
 struct DeltaLane {
     static constexpr int NW = 8 / NU / kParts, STEP = 4 * NW;
+    static_assert(NW == 4, "four waves: three tiles of P and one to spare, 8 lanes a row for q's length");
     static_assert(STEP % 16 == 0, "rows of one lane share their place in a row's order");
     int w, lane, gq, n16, wv, lrow, vrow, r8, trow, piece, tr, trv;
     __device__ __forceinline__ DeltaLane(int part) {
@@ -293,14 +294,14 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
             }
             bf16x4 hi4, lo4;
             pieces.split(acc, hi4, lo4);
-            *(bf16x8*)(lds_p + min(w, 3) * 1024 + lane * 16) = cat8(hi4, lo4);
+            *(bf16x8*)(lds_p + w * 1024 + lane * 16) = cat8(hi4, lo4);
             // one over q's length: 2 NW lanes a row
             constexpr int PER = 64 / NW;   // channels a lane
             const bf16x2* row = (const bf16x2*)(q + (32 / NW * w + lane / (2 * NW)) * 256 + lane % (2 * NW) * (2 * PER));
             float s = 0.0f;
 #pragma unroll
             for (int e = 0; e < PER / 2; ++e) s = __builtin_amdgcn_fdot2_f32_bf16(row[e], row[e], s, false);
-            s = NW == 8 ? row16_sum(s) : row8_sum(s);
+            s = row8_sum(s);
             lds_q[32 / NW * w + lane / (2 * NW)] = A.unit ? rsqrtf(s + NORM_EPS) : 1.0f;
         }
         // S K^T and S Q^T
@@ -587,7 +588,7 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
             }
             bf16x4 a, b, d;
             pieces.split(acc, a, b, d);
-            char* to = lds_p + min(w, 3) * 1536 + lane * 8;
+            char* to = lds_p + w * 1536 + lane * 8;
             *(bf16x4*)to = a;
             *(bf16x4*)(to + 512) = b;
             *(bf16x4*)(to + 1024) = d;
