@@ -23,13 +23,16 @@ constexpr int REC_TILE = 512, REC_C11 = 0, REC_C22 = 3 * REC_TILE, REC_C21 = 6 *
               REC = REC_N + 1536;
 constexpr int DB = 64;          // tokens of a block: two chunks, whose records are adjacent
 
-// What the backward's scans leave for the gradients, in FP16: per block the state before it
-// (or the adjoint behind it), [blocks][Hv][128 v][128 k], and per chunk its solution rows,
-// [blocks][Hv][2 chunks][128 v][32 tokens]; the values are those stored times the scale of
-// their 32 channels v, a power of two that brings the largest to [2^14, 2^15): [..][4].
+// What the backward's scans leave for the gradients.  Per block the state before it (or the adjoint
+// behind it), transposed, as an operand of 8 channels v a lane needs it: what is stored times scale,
+// [blocks][Hv], FP32 values rounded to their upper 24 bits (off by 2^-17 at most), the upper 16 of those as
+// [blocks][Hv][v/16][128 k][16 v], and STATE_LOW bytes behind them the lower 8 likewise.  Per chunk its solution
+// rows as two BF16 pieces (off by 2^-18), [blocks][Hv][2 chunks][v/32][2 pieces][32 v][32 tokens],
+// tokens 16t + 4p + e at 8p + 4(t ^ (v/8)%2) + e.
+constexpr int STATE_LOW = 128 * 128 * 2, PLANE_STATE = 128 * 128 * 3, PLANE_ROWS = 2 * 128 * 32 * 2;   // bytes
 struct DeltaPlanes {
-    _Float16 *state, *rows;
-    float *state_scale, *row_scale;
+    char *state, *rows;
+    float* scale;
 };
 
 struct DeltaArgs {

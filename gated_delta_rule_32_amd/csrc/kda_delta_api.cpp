@@ -116,7 +116,7 @@ RecordWs record_ws(const Delta& d, int seg) {
 // The backward's workspace: records unless they are given, what the two scans leave, and
 // partials of dq and dk where value heads share them.
 struct PlanesWs {
-    size_t state = 0, rows = 0, state_scale = 0, row_scale = 0;
+    size_t state = 0, rows = 0, scale = 0;
 };
 struct GradWs {
     RecordWs r;
@@ -135,10 +135,9 @@ GradWs grad_ws(const Delta& d, int seg, bool records) {
     };
     const size_t items = (size_t)blocks * d.s.Hv;
     for (PlanesWs* p : {&g.forward, &g.backward}) {
-        p->state = take(items * kState * 2);
-        p->rows = take(items * kda::DB * D * 2);
-        p->state_scale = take(items * 4 * sizeof(float));
-        p->row_scale = take(items * 8 * sizeof(float));
+        p->state = take(items * kda::PLANE_STATE);
+        p->rows = take(items * 2 * kda::PLANE_ROWS);
+        p->scale = take(items * sizeof(float));
     }
     const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
     g.part_q = take(part);
@@ -148,7 +147,7 @@ GradWs grad_ws(const Delta& d, int seg, bool records) {
     return g;
 }
 kda::DeltaPlanes planes_at(char* ws, const PlanesWs& p) {
-    return {(_Float16*)(ws + p.state), (_Float16*)(ws + p.rows), (float*)(ws + p.state_scale), (float*)(ws + p.row_scale)};
+    return {ws + p.state, ws + p.rows, (float*)(ws + p.scale)};
 }
 
 // The item maps of a call (whole sequences, blocks of 64 tokens, and the scan's: the

@@ -111,13 +111,15 @@ __device__ __forceinline__ u32x2 pack_quad_fast(f32x4 x) {
 // whose terms all hold the decay of token t, so that none has to cancel behind a strong one.
 // Four waves; each forms its 32 channels of dq and dk (as D^T: lane (gq, n) holds channels
 // 32w + 8gq + 4u + e of token n) and up to three of the ten lower tiles of E and F.  What the scans
-// left comes in FP16 (11 bits: an eighth of a BF16 rounding), 32 channels v of the sums at a time,
-// for which do is brought to FP16 too; every such part is added up with its scale in FP32.  The matrices e and f, of
-// which large parts may cancel, go in as two BF16 pieces.
-// Bound by its waves' own steps and HBM beside them: 64 KB of stages let two workgroups share a unit,
-// whose vector instructions take 57% of the time at 3.7 TB/s (8 x 1024 tokens, 96 heads: 679 us, 2.5 GB).
-typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-constexpr int GS_O = 0, GS_R = 4096, GS_S = GS_R + 8192, GS = GS_S + 16384;    // stage: do, rows, states
+// left comes 32 channels v of the sums at a time: of the states each wave reads its own columns k, straight
+// into the registers where they are operands, ahead by one such part; W, Y and do go through LDS.  A state's value
+// becomes two BF16 pieces, as W and Y are, and the products of two pairs take three of the four; so do
+// the matrices e and f.
+// Bound by HBM: two workgroups share a unit, each with 44 KB on its way (20 of rows and do, 24 of
+// states): 8 x 1024 tokens, 96 heads 742 us, 3.3 GB, 4.5 TB/s.  (States through LDS like the rows, as two BF16
+// pieces each and 16 channels at a time, 26 KB on their way: 962 us.  States and rows in FP16 took 677 us, and
+// results were off by 0.8% more than one rounding of the exact ones.)
+constexpr int GS_O = 0, GS_R = 4096, GS = GS_R + 16384;                        // stage: do, rows
 constexpr int GS2 = 32768;                                                     // the second stage
 constexpr int GM = 32768, GN = GM + 16384, GTOTAL = GN + 16384;                // q, k rows; e; f
 __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
@@ -137,10 +139,6 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
     const int64_t blk = it.seg * Hv + it.h;
     const char* rec = A.rec + blk * (2 * REC);
 
-    const float* s_scale = A.forward.state_scale + blk * 4;
-    const float* z_scale = A.backward.state_scale + blk * 4;
-    const float* w_scale = A.forward.row_scale + blk * 8;
-    const float* y_scale = A.backward.row_scale + blk * 8;
     auto put_tokens = [&]() __attribute__((always_inline)) {
         const char* r = rec + (lane >> 5) * REC + (lane & 31) * 4;
         float hi = *(const float*)(r + REC_GH), lo = *(const float*)(r + REC_GL);
@@ -170,11 +168,12 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         for (int u = 0; u < 2; ++u) dq[ti][u] = dks[ti][u] = dke[ti][u] = zero4();
 #pragma unroll
     for (int s = 0; s < 3; ++s) E[s] = F[s] = zero4();
-    float zs = 0.0f;
+    f32x4 zs = zero4();   // of S^T Z, the sum of whose diagonals is <Z, S>
 
     auto finish = [&](float zs, int lane) __attribute__((always_inline)) {
     const int gq = lane >> 4, n16 = lane & 15, prow = 8 * gq + (n16 >> 2), pa = n16 & 3;
-    if (lane == 0) whole[w] = zs;
+    const float fs = A.forward.scale[blk], fz = A.backward.scale[blk];
+    if (lane == 0) whole[w] = zs * (fs * fz);
     constexpr int LQ = 0, LK = 16384;
     const int r8 = n16 * 256 + ((gq ^ swz(n16)) << 4);   // 8 channels 32p + 8gq of row n (xor 64p)
     // matrices of 64 rows of 128 bytes: block b of row r at b ^ r % 8; hi at 0, lo at 8192
@@ -256,7 +255,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         const int t = 16 * ti + n16;
         const float b = tok[0][t], hi = tok[1][t], lo = tok[2][t], rk = tok[3][t], rq = tok[4][t];
         const float from = decay2(hi, lo, 0.0f, 0.0f), to = decay2(hn, ln, hi, lo);
-        const float cq = A.scale * from * rq, cs = -from * b * rk, ce = to * b * rk;
+        const float cq = A.scale * from * rq * fs, cs = -from * b * rk * fs, ce = to * b * rk * fz;
         const bf16x8 q8 = *(const bf16x8*)(lds + LQ + ti * 4096 + n16 * 256 + rch);
         const bf16x8 k8 = *(const bf16x8*)(lds + LK + ti * 4096 + n16 * 256 + rch);
 #pragma unroll
@@ -380,20 +379,17 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         }
     }
     };
-    // Loads: 16 rows of 64 bytes or 4 of 256 an instruction, a lane fetching the 16 bytes that
-    // belong in its place.  Rows of 64 bytes: block b of do's row r at b ^ (r/4)%4, of a plane's row
-    // at b ^ 2 (r/8)%2; of 256 bytes as in the scans.
+    // Loads to LDS: 16 rows of 64 bytes or 4 of 256 an instruction, a lane fetching the 16 bytes that
+    // belong in its place.  Rows of 64 bytes: block b of do's row r at b ^ (r/4)%4, of W and Y as they are in
+    // the planes; of 256 bytes as in the scans.
     const u32x4 zero = {0u, 0u, 0u, 0u};
     const int r16 = lane >> 2, b4 = lane & 3;
     const int64_t so = (int64_t)Hv * D;
     const bf16* pdo = (const bf16*)A.d_o + ((it.tok0 + 16 * w) * Hv + it.h) * D;
     const unsigned off_o = (unsigned)r16 * (unsigned)(so * 2) + ((b4 ^ ((r16 >> 2) & 3)) << 4);
-    const unsigned off_r = r16 * 64 + ((b4 ^ (((r16 >> 3) & 1) << 1)) << 4);
-    const unsigned off_s = gq * 256 + ((n16 ^ (gq << 2)) << 4);   // (xor the block bits of the rows 4j)
     const bool second = it.len > SC;   // (a block may end in its first chunk)
-    // rows W (waves 0, 1) and Y of chunk w % 2; channels 16 (w % 2) .. of the 32 of S (waves 0, 1) and Z
-    const char* prows = (const char*)((w < 2 ? A.forward.rows : A.backward.rows) + (blk * 2 + (w & 1)) * (int64_t)(D * SC));
-    const char* pstate = (const char*)((w < 2 ? A.forward.state : A.backward.state) + blk * (int64_t)STATE) + (w & 1) * 16 * 256;
+    // rows W (waves 0, 1) and Y of chunk w % 2
+    const char* prows = (w < 2 ? A.forward.rows : A.backward.rows) + (blk * 2 + (w & 1)) * PLANE_ROWS;
     auto load_stage = [&](char* to, int vb) __attribute__((always_inline)) {
         char* o = to + GS_O + w * 1024;
         if (16 * w + r16 < it.len)
@@ -401,16 +397,28 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
         else
             *(u32x4*)(o + lane * 16) = zero;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            char* d = to + GS_R + w * 2048 + half * 1024;
+        for (int i = 0; i < 4; ++i) {
+            char* d = to + GS_R + w * 4096 + i * 1024;
             if ((w & 1) == 0 || second)
-                to_lds<false>(prows + (32 * vb + 16 * half) * 64, fresh(off_r), d);
+                to_lds<false>(prows + vb * 4096 + i * 1024, lane * 16, d);
             else
                 *(u32x4*)(d + lane * 16) = zero;
         }
+    };
+    // S and Z: 8 channels v = 32vb + 8gq .. of column k = 32w + 8(n/4) + 4u + n%4
+    const char* pstate[2] = {A.forward.state + blk * PLANE_STATE, A.backward.state + blk * PLANE_STATE};
+    const int off_k = (gq >> 1) * (D * 16) + (32 * w + 8 * (n16 >> 2) + (n16 & 3)) * 16 + 8 * (gq & 1);
+    u32x4 high[2][2];
+    u32x2 low[2][2];
+    auto load_states = [&](int vb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            to_lds<false>(pstate + (32 * vb + 4 * j) * 256, fresh(off_s) ^ (((2 * j & 2) | j >> 1) << 4), to + GS_S + w * 4096 + j * 1024);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = off_k + u * 64;
+                high[i][u] = *row_ptr<const u32x4>(pstate[i] + vb * 8192, 2 * at);
+                low[i][u] = *row_ptr<const u32x2>(pstate[i] + STATE_LOW + vb * 4096, at);
+            }
     };
     auto load_rows = [&]() __attribute__((always_inline)) {
         const bf16* src[2] = {(const bf16*)A.q, (const bf16*)A.k};
@@ -428,119 +436,114 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
                     *(u32x4*)(d + lane * 16) = zero;
             }
     };
-    // operands of 8 channels v = 32vb + 8gq ..: do, rows (0: W, 1: Y) and states (0: S, 1: Z)
-    const int prow = 8 * gq + (n16 >> 2), pa = n16 & 3;   // this lane's row of a transposing read, and its piece there
-    const int at_row = prow * 64 + ((gq & 1) << 5) + 8 * pa;
-    const int at_state = prow * 256 + (((4 * w + pa) ^ swz(prow)) << 4);          // (the row 4 below: block bit 1 flipped)
+    // operands of 8 channels v = 32vb + 8gq ..: rows (0: W, 1: Y), do
+    const int pa = n16 & 3;   // this lane's piece of a transposing read
+    const int at_row = (8 * gq + (n16 >> 2)) * 64 + pa * 16 + (gq & 1) * 8;
     const int at_o = n16 * 64 + ((gq ^ (n16 >> 2)) << 4);
-    auto get_row = [&](const char* from, int set, int ti) __attribute__((always_inline)) {
-        const char* r = from + GS_R + (set * 2 + (ti >> 1)) * 2048 + (fresh(at_row) ^ ((ti & 1) << 5));
-        return __builtin_bit_cast(f16x8, cat8(tr_read(r), tr_read(r + 4 * 64)));
+    auto get_row = [&](const char* from, int set, int ti, int piece) __attribute__((always_inline)) {
+        const char* r = from + GS_R + (set * 2 + (ti >> 1)) * 4096 + piece * 2048 + (fresh(at_row) ^ ((ti & 1) * 8));
+        return cat8(tr_read(r), tr_read(r + 4 * 64));
     };
-    auto get_state = [&](const char* from, int set, int u) __attribute__((always_inline)) {
-        const char* r = from + GS_S + set * 8192 + 8 * u;
-        const int at = fresh(at_state);
-        return __builtin_bit_cast(f16x8, cat8(tr_read(r + at), tr_read(r + ((at + 4 * 256) ^ 32))));
+    auto get_o = [&](const char* from, int ti) __attribute__((always_inline)) {
+        return *(const bf16x8*)(from + GS_O + ti * 1024 + fresh(at_o));
     };
     bf16* pdv = (bf16*)A.dv + ((it.tok0 + 16 * w + n16) * Hv + it.h) * D + 8 * gq;
-    // the planes' scales, in one register's lanes: S, Z, then W and Y of either chunk
-    float scales = 0.0f;
-    {
-        const int i = lane & 3, set = lane >> 2;
-        const float* from = set == 0 ? s_scale : set == 1 ? z_scale : set < 4 ? w_scale + 4 * (set - 2) : y_scale + 4 * (set - 4);
-        if (set < 6 && (second || set < 2 || (set & 1) == 0)) scales = from[i];
-    }
-    auto scale_of = [&](int set, int vb) __attribute__((always_inline)) {
-        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scales), 4 * set + vb));
-    };
     auto part = [&](int vb, const char* __restrict__ from, char* __restrict__ to) __attribute__((always_inline)) {
-        if (vb < 3)
-            load_stage(to, vb + 1);
-        else   // q's and k's rows, over the first stage
-            load_rows();
-        const float fs = scale_of(0, vb), fz = scale_of(1, vb);
-        const float fw[2] = {scale_of(2, vb), scale_of(3, vb)}, fy[2] = {scale_of(4, vb), scale_of(5, vb)};
-        const f16x8 yr = get_row(from, 1, w);
-        if (16 * w + n16 < it.len) {   // dv of the wave's 16 tokens: 8 channels a lane.  (No branch
-            // stands behind the sums below: the compiler would move them all past it.)
-            const float b = tok[0][16 * w + n16] * (w < 2 ? fy[0] : fy[1]);
-            f32x4 y0, y1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y0[e] = b * (float)yr[e];
-                y1[e] = b * (float)yr[4 + e];
-            }
-            *(bf16x8*)(pdv + 32 * vb) = cat8(to_bf4(y0), to_bf4(y1));
-        }
-        // do in FP16, its largest at [2^14, 2^15)
-        auto get_o = [&](int ti) __attribute__((always_inline)) {
-            return *(const bf16x8*)(from + GS_O + ti * 1024 + fresh(at_o));
-        };
-        u16x8 high = {};
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            const u16x8 x = __builtin_bit_cast(u16x8, get_o(ti)) & (unsigned short)0x7fff;
-            high = __builtin_elementwise_max(high, x);
-        }
-        unsigned short h1 = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h1 = high[e] > h1 ? high[e] : h1;
-        float up, fo;
-        plane_scale(wave_max(__uint_as_float((unsigned)h1 << 16)), up, fo);
-        f16x8 o[4];
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            const bf16x8 x = get_o(ti);
-            o[ti] = cat8h(to_f16x4(from_bf4(__builtin_shufflevector(x, x, 0, 1, 2, 3)) * up),
-                          to_f16x4(from_bf4(__builtin_shufflevector(x, x, 4, 5, 6, 7)) * up));
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        f16x8 st[2][2];
+        bf16x8 st[2][2][2];   // S, Z; u; piece
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) st[i][u] = get_state(from, i, u);
-        float z = 0.0f;
+            for (int u = 0; u < 2; ++u) {
+                st[i][u][0] = __builtin_bit_cast(bf16x8, high[i][u]);
+                u32x4 rest;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+                for (int j = 0; j < 4; ++j) {   // the upper half's value off the whole one is exact, and 8 bits
+                    const unsigned h = high[i][u][j], l = low[i][u][j >> 1];
+                    const unsigned x0 = __builtin_amdgcn_perm(h, l, j & 1 ? 0x0504020cu : 0x0504000cu),
+                                   x1 = __builtin_amdgcn_perm(h, l, j & 1 ? 0x0706030cu : 0x0706010cu);
+                    rest[j] = cvt_pk_bf16(__uint_as_float(x0) - __uint_as_float(h << 16),
+                                          __uint_as_float(x1) - __uint_as_float(h & 0xffff0000u));
+                }
+                st[i][u][1] = __builtin_bit_cast(bf16x8, rest);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if (vb < 3) {
+            load_states(vb + 1);
+            load_stage(to, vb + 1);
+        } else {   // q's and k's rows, over the first stage
+            load_rows();
+        }
+        {   // dv of the wave's 16 tokens, 8 channels a lane.  (No branch stands behind the sums below: the
+            // compiler would move them all past it.)
+            const bf16x8 a = get_row(from, 1, w, 0), b = get_row(from, 1, w, 1);
+            if (16 * w + n16 < it.len) {
+                const float beta = tok[0][16 * w + n16];
+                f32x4 y0, y1;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z = fmaf((float)st[0][u][e], (float)st[1][u][e], z);
-        zs = fmaf(z, fs * fz, zs);
+                for (int e = 0; e < 4; ++e) {
+                    y0[e] = beta * ((float)a[e] + (float)b[e]);
+                    y1[e] = beta * ((float)a[4 + e] + (float)b[4 + e]);
+                }
+                *(bf16x8*)(pdv + 32 * vb) = cat8(to_bf4(y0), to_bf4(y1));
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            zs = mma32(st[0][u][0], st[1][u][0], zs);
+            zs = mma32(st[0][u][0], st[1][u][1], zs);
+            zs = mma32(st[0][u][1], st[1][u][0], zs);
+        }
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) {
             __builtin_amdgcn_sched_barrier(0);   // (the parts of one tile of tokens at a time)
-            const f16x8 wr = get_row(from, 0, ti), yr = get_row(from, 1, ti);
-            const float cq = fs * fo, cs = fs * fy[ti >> 1], ce = fz * fw[ti >> 1];
+            const bf16x8 o = get_o(from, ti);
+            bf16x8 wr[2], yr[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                dq[ti][u] += mma32h(st[0][u], o[ti], zero4()) * cq;
-                dks[ti][u] += mma32h(st[0][u], yr, zero4()) * cs;
-                dke[ti][u] += mma32h(st[1][u], wr, zero4()) * ce;
+            for (int d = 0; d < 2; ++d) {
+                wr[d] = get_row(from, 0, ti, d);
+                yr[d] = get_row(from, 1, ti, d);
             }
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) dq[ti][u] = mma32(st[0][u][d], o, dq[ti][u]);
+#pragma unroll
+            for (int d = 0; d < 3; ++d)   // (pieces 0 0, 0 1 and 1 0)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    dks[ti][u] = mma32(st[0][u][d >> 1], yr[d & 1], dks[ti][u]);
+                    dke[ti][u] = mma32(st[1][u][d >> 1], wr[d & 1], dke[ti][u]);
+                }
         }
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             __builtin_amdgcn_sched_barrier(0);
             const int t = min(w + 4 * s, TILES - 1);   // (the last tile again where there is none: its sums are not used)
             const int bi = tile_i(t), bj = tile_j(t);
-            const f16x8 wr = get_row(from, 0, bj), yr = get_row(from, 1, bi);
-            const bf16x8 x = get_o(bi);
-            const f16x8 oi = cat8h(to_f16x4(from_bf4(__builtin_shufflevector(x, x, 0, 1, 2, 3)) * up),
-                                   to_f16x4(from_bf4(__builtin_shufflevector(x, x, 4, 5, 6, 7)) * up));
-            const float cw = bj < 2 ? fw[0] : fw[1], cy = bi < 2 ? fy[0] : fy[1];
-            E[s] += mma32h(oi, wr, zero4()) * (fo * cw);
-            F[s] += mma32h(yr, wr, zero4()) * (cy * cw);
+            const bf16x8 o = get_o(from, bi);
+            bf16x8 wr[2], yr[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                wr[d] = get_row(from, 0, bj, d);
+                yr[d] = get_row(from, 1, bi, d);
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d) E[s] = mma32(o, wr[d], E[s]);
+#pragma unroll
+            for (int d = 0; d < 3; ++d) F[s] = mma32(yr[d >> 1], wr[d & 1], F[s]);
         }
         wait_vm<0>();
         barrier_lds();
     };
+    load_states(0);
     load_stage(lds, 0);
     if (w == 3) put_tokens();
     wait_vm<0>();
     barrier_lds();
     for (int vb = 0; vb < 4; ++vb) part(vb, lds + (vb & 1) * GS2, lds + (~vb & 1) * GS2);
-    zs = group_sum<64>(zs);
-    finish(zs, fresh(tid & 63));
+    const float z01 = n16 & 1 ? zs[1] : zs[0], z23 = n16 & 1 ? zs[3] : zs[2];
+    finish(group_sum<64>(gq == n16 >> 2 ? (n16 & 2 ? z23 : z01) : 0.0f), fresh(tid & 63));
 }
 
 hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s) {

@@ -17,7 +17,7 @@
 // memory to LDS while this one is computed.
 // Bound by the steps of a chunk, each of which needs the one before: 2.4 us with up to one workgroup a
 // unit; with two, matrix and vector instructions take 47% and 53% of the time (8 x 1024 tokens, 96 heads:
-// forward 327 us, 3.3 TB/s; both scans of the backward with their planes 660 us, 4.1 TB/s).  The exact
+// forward 327 us, 3.3 TB/s; both scans of the backward with their planes 722 us, 4.8 TB/s).  The exact
 // products are most of it: some 790 matrix instructions a chunk and head, 1.5 us of a unit's four.
 // Sequences may be cut into segments, which a launch walks side by side: what a segment adds to a
 // state, Q, and what it makes of one, M (the same scan with V = 0 from the identity), are formed first
@@ -32,7 +32,7 @@ constexpr int DSET = SC * D * 2;        // LDS bytes of a chunk's rows
 constexpr int DROWS16 = 16 * D * 2;     // of 16 rows
 
 // LDS (bytes): a chunk's rows and its record in two buffers each; P's tiles (two of two pieces in the
-// scan, one of three in the adjoint, with a fourth tile that is not used), q's lengths or the planes' maxima.
+// scan, one of three in the adjoint, with a fourth tile that is not used), q's lengths.
 template <bool kThree, int kTiles>
 struct DeltaLds {
     static constexpr int K = 0, V = 2 * DSET, Q = 4 * DSET, R = kThree ? 6 * DSET : 4 * DSET, P = R + 2 * REC,
@@ -49,28 +49,6 @@ __device__ __forceinline__ float row8_sum(float x) {
     x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xF, 0xF, true));
     return x;
 }
-// The largest of a wave's |x|, in every lane.
-__device__ __forceinline__ float wave_max(float x) {
-    x = fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0xB1, 0xF, 0xF, true)));
-    x = fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4E, 0xF, 0xF, true)));
-    x = fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xF, 0xF, true)));
-    x = fmaxf(x, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x140, 0xF, 0xF, true)));
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float max4(f32x4 x, float m) {
-    m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), m);
-    return fmaxf(fmaxf(fabsf(x[2]), fabsf(x[3])), m);
-}
-// The power of two that brings m to [2^14, 2^15), and its inverse.
-__device__ __forceinline__ void plane_scale(float m, float& up, float& down) {
-    const int e = max((int)(__float_as_uint(m) >> 23), 15);
-    up = __uint_as_float((unsigned)(268 - e) << 23);
-    down = __uint_as_float((unsigned)(e - 14) << 23);
-}
-
 // Where a wave's lanes lie, among the rows and in LDS.
 template <int NU, int kParts>
 struct DeltaLane {
@@ -125,44 +103,73 @@ struct DeltaLane {
     }
 };
 
-// The planes of a state and of a chunk's rows.  The waves that share 32 channels v agree on a
-// scale through LDS (`x`: two rounds of 8 pairs of maxima; a barrier between put and get).
+// The planes of a state, which is `held` times S, and of a chunk's rows.  A store of a wave covers whole 512
+// or 256 bytes.  (Both scans of 4 x 4096 tokens of 32 heads, in halves: 488 us; 570 with 32 channels v side by
+// side, of which a half's wave has 16.)
 template <int NU, int kParts>
 struct PlaneWriter {
     const DeltaLane<NU, kParts>& L;
-    float (*x)[8][2];
-    __device__ __forceinline__ void put(int round, float state, float rows) const {
-        state = wave_max(state);
-        rows = wave_max(rows);
-        if (L.lane == 0) {
-            x[round][L.w][0] = state;
-            x[round][L.w][1] = rows;
+    const Pieces& pieces;
+    // The matrix units turn the state around: its pieces times an identity, added up, are 4 channels v of
+    // column k = n.
+    __device__ __forceinline__ void state(const f32x4 (&S)[8][NU], float held, const DeltaPlanes& to, int64_t blk) const {
+        char* p = to.state + blk * PLANE_STATE;
+        bf16x8 id[2];   // columns 16i + n of 32
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f32x4 x[2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j >> 2][j & 3] = 8 * L.gq + j == 16 * i + L.n16 ? 1.0f : 0.0f;
+            id[i] = cat8(to_bf4(x[0]), to_bf4(x[1]));
         }
+        const int at = NU == 2 ? (2 * L.wv + (L.gq >> 1)) * (D * 16) + L.n16 * 16 + 8 * (L.gq & 1)
+                               : L.wv * (D * 16) + L.n16 * 16 + 4 * L.gq;
+#pragma unroll
+        for (int t = 0; t < 8; t += 2) {
+            bf16x8 piece[NU][2];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                f32x4 x = S[t][u], y = S[t + 1][u];
+                piece[u][0] = pieces.take(x, y);
+                piece[u][1] = cat8(to_bf4(x), to_bf4(y));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int off = at + 16 * (t + i) * 16;
+                unsigned high[2 * NU], low[NU];
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    const f32x4 x = mma32(piece[u][1], id[i], mma32(piece[u][0], id[i], zero4()));
+                    const u32x4 y = __builtin_bit_cast(u32x4, x) + 0x80u;   // (a NaN's lower half is zero)
+                    high[2 * u] = __builtin_amdgcn_perm(y[1], y[0], 0x07060302u);
+                    high[2 * u + 1] = __builtin_amdgcn_perm(y[3], y[2], 0x07060302u);
+                    low[u] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(y[3], y[2], 0x0c0c0501u),
+                                                   __builtin_amdgcn_perm(y[1], y[0], 0x0c0c0501u), 0x05040100u);
+                }
+                if constexpr (NU == 2) {
+                    *(u32x4*)(p + 2 * off) = u32x4{high[0], high[1], high[2], high[3]};
+                    *(u32x2*)(p + STATE_LOW + off) = u32x2{low[0], low[1]};
+                } else {
+                    *(u32x2*)(p + 2 * off) = u32x2{high[0], high[1]};
+                    *(unsigned*)(p + STATE_LOW + off) = low[0];
+                }
+            }
+        }
+        if (threadIdx.x == 0) to.scale[blk] = held;   // (both parts the same)
     }
-    __device__ __forceinline__ float get(int round, int which) const {
-        if (NU == 2) return x[round][L.w][which];
-        return fmaxf(x[round][L.w & ~1][which], x[round][L.w | 1][which]);
-    }
-    __device__ __forceinline__ void state(const f32x4 (&S)[8][NU], float held, float top, _Float16* to, float* scale) const {
-        float up, down;
-        plane_scale(top * held, up, down);
-        up *= held;
+    __device__ __forceinline__ void rows(const f32x4 (&w)[2][NU], const DeltaPlanes& to, int64_t chunk) const {
+        char* p = to.rows + chunk * PLANE_ROWS;
 #pragma unroll
-        for (int u = 0; u < NU; ++u)
+        for (int u = 0; u < NU; ++u) {
+            const int v = L.vrow + 4 * u;
+            const bool odd = (v & 8) != 0;
+            bf16x4 a[2], b[2];
+            split4_rne(w[0][u], a[0], a[1]);
+            split4_rne(w[1][u], b[0], b[1]);
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                *(f16x8*)(to + (L.vrow + 4 * u) * D + L.krow(2 * p)) =
-                    cat8h(to_f16x4(S[2 * p][u] * up), to_f16x4(S[2 * p + 1][u] * up));
-        if (L.lane == 0) scale[NU == 2 ? L.wv : L.wv >> 1] = down;
-    }
-    __device__ __forceinline__ void rows(const f32x4 (&w)[2][NU], float top, _Float16* to, float* scale) const {
-        float up, down;
-        plane_scale(top, up, down);
-#pragma unroll
-        for (int ti = 0; ti < 2; ++ti)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) *(f16x4*)(to + (L.vrow + 4 * u) * SC + 16 * ti + 4 * L.gq) = to_f16x4(w[ti][u] * up);
-        if (L.lane == 0) scale[NU == 2 ? L.wv : L.wv >> 1] = down;
+            for (int d = 0; d < 2; ++d)
+                *(bf16x8*)(p + (v >> 5) * 4096 + d * 2048 + (v & 31) * 64 + 16 * L.gq) = odd ? cat8(b[d], a[d]) : cat8(a[d], b[d]);
+        }
     }
 };
 
@@ -238,19 +245,11 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
                 for (int e = 0; e < 4; ++e) S[t][u][e] = L.krow(t) + e == L.vrow + 4 * u ? 1.0f : 0.0f;
     const unsigned v_mask = map_job ? 0u : ~0u;
 
-    const PlaneWriter<NU, kParts> planes{L, (float (*)[8][2])(lds + M::X)};
-    auto state_max = [&]() __attribute__((always_inline)) {
-        float m = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) m = max4(S[t][u], m);
-        return m;
-    };
+    const Pieces pieces(lane);
+    const PlaneWriter<NU, kParts> planes{L, pieces};
     const int64_t sy = (int64_t)Hv * D * 2;
     char* po = kOut ? (char*)(A.o + (it.tok0 * Hv + it.h) * D) : nullptr;
     const unsigned oy = (unsigned)n16 * (unsigned)sy + (16 * NU * L.wv + 4 * NU * gq) * 2;
-    const Pieces pieces(lane);
     double held = 1.0;   // the state is `held` times S
 
     // One chunk from `rows` and `rec`, the next one on its way into `rows_to` and `rec_to`.
@@ -352,7 +351,6 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
                 for (int u = 0; u < NU; ++u) S[t][u] *= down;
         }
         // W = X - C B X; S <- e^{G_n} S + K^T U
-        float top = 0.0f;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             f32x4 &w0 = wr[0][u], &w1 = wr[1][u];
@@ -377,7 +375,6 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
 #pragma unroll
                     for (int b = 0; a + b < 3; ++b) w1 = mma32(cat8(c21[a], c22[a]), cat8(x0[b], x1[b]), w1);
             }
-            if (kRecord) top = max4(w1, max4(w0, top));
             bf16x8 u3[3];
             {
                 const f32x4 e0 = num4(REC_TO_KB, 4 * gq) * up, e1 = num4(REC_TO_KB, 16 + 4 * gq) * up;
@@ -436,24 +433,16 @@ __device__ __forceinline__ void delta_scan(const DeltaArgs& A, int block, int gr
         if (kRecord) {
             // the planes of this chunk's rows, and of the state when it is the next block's
             const bool edge = (c & 1) != 0 && more;
-            planes.put(c & 1, edge ? state_max() : 0.0f, top);
             if (more) wait_vm<0>();
             barrier_lds();
             const int64_t blk = (block0 + (c >> 1)) * Hv + it.h;
-            planes.rows(wr, planes.get(c & 1, 1), A.planes.rows + (blk * 2 + (c & 1)) * (int64_t)(D * SC),
-                        A.planes.row_scale + (blk * 2 + (c & 1)) * 4);
-            if (edge)
-                planes.state(S, (float)held, planes.get(c & 1, 0), A.planes.state + (blk + Hv) * (int64_t)STATE,
-                             A.planes.state_scale + (blk + Hv) * 4);
+            planes.rows(wr, A.planes, blk * 2 + (c & 1));
+            if (edge) planes.state(S, (float)held, A.planes, blk + Hv);
         }
     };
-    if (kRecord) planes.put(1, state_max(), 0.0f);
     wait_vm<0>();
     barrier_lds();
-    if (kRecord) {
-        const int64_t blk = block0 * Hv + it.h;
-        planes.state(S, 1.0f, planes.get(1, 0), A.planes.state + blk * (int64_t)STATE, A.planes.state_scale + blk * 4);
-    }
+    if (kRecord) planes.state(S, 1.0f, A.planes, block0 * Hv + it.h);
     auto at = [&](int c, auto steady) __attribute__((always_inline)) {
         const int x = c & 1;
         chunk(c, lds + x * DSET, lds + M::R + x * REC, lds + (x ^ 1) * DSET, lds + M::R + (x ^ 1) * REC, steady);
@@ -545,16 +534,8 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
         for (int u = 0; u < NU; ++u)
             Z[t][u] = s_in != nullptr ? *(const f32x4*)(s_in + (L.vrow + 4 * u) * D + L.krow(t)) : zero4();
 
-    const PlaneWriter<NU, kParts> planes{L, (float (*)[8][2])(lds + M::X)};
-    auto state_max = [&]() __attribute__((always_inline)) {
-        float m = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int u = 0; u < NU; ++u) m = max4(Z[t][u], m);
-        return m;
-    };
     const Pieces pieces(lane);
+    const PlaneWriter<NU, kParts> planes{L, pieces};
     double held = 1.0;   // the adjoint is `held` times Z
     auto chunk = [&](int c, const char* __restrict__ rows, const char* __restrict__ rec, char* __restrict__ rows_to,
                      char* __restrict__ rec_to, auto before) __attribute__((always_inline)) {
@@ -625,7 +606,6 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
         }
         const bf16x4 none = __builtin_bit_cast(bf16x4, u32x2{0u, 0u});
         f32x4 yr[2][NU];
-        float top = 0.0f;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             if (NU == 2) __builtin_amdgcn_sched_barrier(0);   // (as many pieces at a time as registers hold)
@@ -664,7 +644,6 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
             }
             yr[0][u] = y0;
             yr[1][u] = y1;
-            top = max4(y1, max4(y0, top));
             bf16x8 y3[3], o3[3];   // what the state takes up, in pieces
             {
                 bf16x4 a0[3], a1[3];
@@ -696,23 +675,15 @@ __device__ __forceinline__ void delta_adjoint(const DeltaArgs& A, int block, int
         }
         // the planes of this chunk's rows, and of the adjoint when it is behind the next block
         const bool edge = (c & 1) == 0 && more;
-        planes.put(c & 1, edge ? state_max() : 0.0f, top);
         if (more) wait_vm<0>();
         barrier_lds();
         const int64_t blk = (block0 + (c >> 1)) * Hv + it.h;
-        planes.rows(yr, planes.get(c & 1, 1), A.planes.rows + (blk * 2 + (c & 1)) * (int64_t)(D * SC),
-                    A.planes.row_scale + (blk * 2 + (c & 1)) * 4);
-        if (edge)
-            planes.state(Z, (float)held, planes.get(c & 1, 0), A.planes.state + (blk - Hv) * (int64_t)STATE,
-                         A.planes.state_scale + (blk - Hv) * 4);
+        planes.rows(yr, A.planes, blk * 2 + (c & 1));
+        if (edge) planes.state(Z, (float)held, A.planes, blk - Hv);
     };
-    if (!kState) planes.put(chunks & 1, state_max(), 0.0f);
     wait_vm<0>();
     barrier_lds();
-    if (!kState) {
-        const int64_t blk = (block0 + ((chunks - 1) >> 1)) * Hv + it.h;
-        planes.state(Z, 1.0f, planes.get(chunks & 1, 0), A.planes.state + blk * (int64_t)STATE, A.planes.state_scale + blk * 4);
-    }
+    if (!kState) planes.state(Z, 1.0f, A.planes, (block0 + ((chunks - 1) >> 1)) * Hv + it.h);
     int x = 0;
     auto at = [&](int c, auto before) __attribute__((always_inline)) {
         chunk(c, lds + x * DSET, lds + M::R + x * REC, lds + (x ^ 1) * DSET, lds + M::R + (x ^ 1) * REC, before);

@@ -534,7 +534,7 @@ kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* 
  * untouched since, or NULL, and they are formed again.  dfinal_state NULL counts as
  * zero; dinitial_state may be NULL.  dq and dk sum over the value heads that share a
  * q/k head, in head order; dg and dbeta are BF16 [B][T][Hv].  The workspace holds every
- * block's states: about 96 KiB per 64 tokens and value head, 64 KiB per segment, and the
+ * block's states: about 160 KiB per 64 tokens and value head, 64 KiB per segment, and the
  * records when they are not given. */
 kda_status kda_delta_bwd_workspace_bytes(const kda_delta_problem* p, int32_t records_given, size_t* bytes);
 kda_status kda_delta_bwd(const kda_delta_problem* p, const void* q, const void* k, const void* v, const void* g,

@@ -1,0 +1,63 @@
+"""GPU tests of how far the gated delta rule's results may be off: each BF16 result by one rounding
+of what 32-bit arithmetic gives.
+
+Bars.  u = 2^-8 is half a BF16 step relative to the value.
+  - One element: u |ref| (and u of that, where the value crosses into the next binade), and what came
+    before the rounding.  Written rows and states are off by 2^-18 of their terms' sizes (delta_util), and as two BF16
+    pieces by 2^-18 more (a piece is off by 2^-9 of itself at most, the second by that of the first's
+    rest); where two of them are multiplied that is 2^-16, the block's matrices as pieces and the sums of 128
+    + 64 products in FP32 add 2^-18 each: below 2^-15 of the oracle's weights.
+  - The norm: that of the exact values' own roundings, r.  Errors d before the rounding, independent of it,
+    make it sqrt(r^2 + d^2).  Of random sign they are about 2^-17 of the result, and 2^-13 with
+    terms 16 times as large as their sums; r is 2^-9.2 of it, so that this adds 2^-8.6 of r at most: bar
+    (1 + 2^-8) r.  (A part of 11 bits, 2^-12.8 in the mean square, would add 2^-8.2 of r for
+    each factor that it enters in.)
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import delta_util as du
+from tests import layer_util as lu
+from tests.delta_util import Inp
+from tests.test_delta_rule import train
+
+pytestmark = pytest.mark.gpu
+
+FINE = 2.0 ** -15
+
+
+def check_one_rounding(name, got, ref, weights):
+    got = lu.f64(got)
+    assert np.isfinite(got).all(), f"{name}: not finite"
+    err = np.abs(got - ref)
+    worst = (err / np.maximum(lu.U * np.abs(ref) * (1 + lu.U) + FINE * weights, 1e-30)).max()
+    once = np.linalg.norm(lu.f64(torch.from_numpy(ref).bfloat16()) - ref)
+    ratio = np.linalg.norm(err) / once
+    print(f"{name:5s} norm {ratio:.5f} of one rounding's (bar {1 + lu.U:.5f})  elementwise {worst:.3f} of the bar", flush=True)
+    assert worst <= 1.0 and ratio <= 1 + lu.U, name
+
+
+CASES = {  # lengths, packed, Hqk, Hv, unit, gates, segment: every launch variant, whole and cut
+    "few_workgroups": ([70, 200, 33], True, 3, 3, True, "layer", 0),
+    "many_workgroups": ([96, 65] * 13, True, 6, 6, True, "layer", 0),
+    "given_lengths": ([150, 190], True, 2, 2, False, "layer", 0),
+    "no_decay": ([300], False, 2, 2, True, "none", 0),
+    "segments": ([300, 130], True, 2, 2, True, "layer", 64),
+    "many_segments": ([500, 700], True, 8, 8, True, "layer", 64),
+    "grouped": ([150, 31], True, 2, 8, True, "layer", 0),
+}
+
+
+@pytest.mark.parametrize("case", list(CASES))
+def test_results_are_rounded_once(case):
+    lengths, packed, Hqk, Hv, unit, gates, segment = CASES[case]
+    print(f"[delta precision] {case}", flush=True)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=300 + len(case), unit=unit, gates=gates)
+    got = train(inp, segment=segment)
+    o, _, (wo, _), _ = inp.reference()
+    refs, weights, _ = inp.gradients()
+    check_one_rounding("o", got[0], o, wo)
+    for i, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        if i > 1 or Hqk == Hv:
+            check_one_rounding(name, got[2 + i], refs[i], weights[i])
