@@ -73,8 +73,8 @@ struct DeltaGradArgs {
     const char* rec;
     const bf16_t* d_o;
     DeltaPlanes forward, backward;        // S and W, Z and Y
-    void *dq, *dk;                        // [tokens][Hv][128]: BF16, or packed partials
-    int pack;
+    void *dq, *dk;                        // [tokens][Hv][128]: BF16, or partials' upper 16 bits
+    int64_t low;                          // bytes from those to their lower 8; 0: no partials
     bf16_t *dv, *dg, *dbeta;
 };
 
@@ -105,6 +105,8 @@ hipError_t launch_delta_behind(const DeltaArgs& a, hipStream_t s);     // the sa
 // adjoint of the initial states.
 hipError_t launch_delta_both(const DeltaArgs& forward, const DeltaArgs& backward, hipStream_t s);
 hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s);
+hipError_t launch_delta_group_sum(const void* src0, const void* src1, int64_t low, bf16_t* dst0, bf16_t* dst1, int64_t tokens,
+                                  int Hqk, int G, hipStream_t s);
 hipError_t launch_delta_token(const DeltaTokenArgs& a, hipStream_t s);
 
 struct VerifyArgs {

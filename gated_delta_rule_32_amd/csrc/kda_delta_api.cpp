@@ -139,7 +139,7 @@ GradWs grad_ws(const Delta& d, int seg, bool records) {
         p->rows = take(items * 2 * kda::PLANE_ROWS);
         p->scale = take(items * sizeof(float));
     }
-    const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 2 : 0;
+    const size_t part = d.s.G > 1 ? (size_t)d.s.tokens * d.s.Hv * D * 3 : 0;
     g.part_q = take(part);
     g.part_k = take(part);
     g.behind = take(seg ? (size_t)total_segs(d, seg) * d.s.Hv * kState * sizeof(float) : 0);
@@ -406,15 +406,15 @@ kda_status kda_delta_bwd(const kda_delta_problem* pp, const void* q, const void*
         b.backward = a.planes;
         b.dq = pack ? (void*)(ws + wl.part_q) : dq;
         b.dk = pack ? (void*)(ws + wl.part_k) : dk;
-        b.pack = pack;
+        b.low = pack ? d.s.tokens * d.s.Hv * D * 2 : 0;
         b.dv = (kda::bf16_t*)dv;
         b.dg = (kda::bf16_t*)dg;
         b.dbeta = (kda::bf16_t*)dbeta;
         e = kda::launch_delta_grad(b, stream);
         if (e != hipSuccess) return hip_fail(e, "delta gradient launch");
         if (pack) {
-            e = kda::launch_decay_group_sum(ws + wl.part_q, ws + wl.part_k, (kda::bf16_t*)dq, (kda::bf16_t*)dk, d.s.tokens,
-                                            d.s.Hqk, d.s.G, stream);
+            e = kda::launch_delta_group_sum(ws + wl.part_q, ws + wl.part_k, b.low, (kda::bf16_t*)dq, (kda::bf16_t*)dk,
+                                            d.s.tokens, d.s.Hqk, d.s.G, stream);
             if (e != hipSuccess) return hip_fail(e, "group sum launch");
         }
         return KDA_OK;

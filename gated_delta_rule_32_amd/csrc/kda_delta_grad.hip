@@ -80,20 +80,26 @@ __device__ __forceinline__ float rows_sum(const float (&x)[4]) {
     return __uint_as_float(c[0]) + __uint_as_float(c[1]);
 }
 
-// pack_quad's format for less: halves are rounded away from zero, and a value below 2^-14 of the
-// quad's scale is cut to a multiple of 2^-23 (at most 2^-22 of the quad's largest).
-__device__ __forceinline__ u32x2 pack_quad_fast(f32x4 x) {
-    const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    const unsigned q = __float_as_uint(top) >> 27;
-    const float scale = __uint_as_float((253u - 16u * q) << 23);
-    const bool bad = !(x[0] * 0.0f + x[1] * 0.0f + x[2] * 0.0f + x[3] * 0.0f == 0.0f);
-    f32x4 r;
+// A partial of dq or dk (value heads that share a q/k head each form one) keeps the upper 24 bits of its FP32
+// value, rounded to nearest: off by 2^-17 at most, the upper 16 of them in one array and the lower 8
+// in another.  (With 15 bits and a scale for four, 2 bytes in place of 3, dq and dk were off by 4% more than
+// one rounding of the exact values.)
+__device__ __forceinline__ unsigned round24(float x) {
+    const unsigned u = __float_as_uint(x);
+    return x != x ? 0x7fc00000u : u + 0x7fu + (u >> 8 & 1u);
+}
+__device__ __forceinline__ void put_partials(const f32x4 (&x)[2], char* high, char* low) {
+    unsigned u[8], h[4], l[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = __uint_as_float((__float_as_uint(x[i] * scale) + 0x2000u) & ~0x3fffu);
-    const u32x2 h = __builtin_bit_cast(u32x2, to_f16x4(r));
-    const u32x2 w = {(h[0] >> 1 & 0x7fffu) | (h[0] >> 2 & 0x3fff8000u) | q << 30,
-                     (h[1] >> 1 & 0x7fffu) | (h[1] >> 2 & 0x3fff8000u) | (q >> 2) << 30};
-    return u32x2{bad ? ~0u : w[0], bad ? ~0u : w[1]};
+    for (int i = 0; i < 8; ++i) u[i] = round24(x[i >> 2][i & 3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __builtin_amdgcn_perm(u[2 * i + 1], u[2 * i], 0x07060302u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        l[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[4 * i + 3], u[4 * i + 2], 0x0c0c0501u),
+                                     __builtin_amdgcn_perm(u[4 * i + 1], u[4 * i], 0x0c0c0501u), 0x05040100u);
+    *(u32x4*)high = u32x4{h[0], h[1], h[2], h[3]};
+    *(u32x2*)low = u32x2{l[0], l[1]};
 }
 
 // Gradients of a block of 64 tokens of one value head, all blocks at once.  With S the
@@ -337,15 +343,14 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
                     dks[ti][u][e] -= sk * (float)k8[ti][4 * u + e];
                 }
         }
-        const int64_t at = (((it.tok0 + t) * Hv + it.h) * D + 32 * w + 8 * gq) * 2;
-        u32x2 x[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            x[u] = A.pack ? pack_quad_fast(dq[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dq[ti][u]));
-            x[2 + u] = A.pack ? pack_quad_fast(dks[ti][u]) : __builtin_bit_cast(u32x2, to_bf4(dks[ti][u]));
+        const int64_t at = ((it.tok0 + t) * Hv + it.h) * D + 32 * w + 8 * gq;
+        if (A.low != 0) {
+            put_partials(dq[ti], (char*)A.dq + 2 * at, (char*)A.dq + A.low + at);
+            put_partials(dks[ti], (char*)A.dk + 2 * at, (char*)A.dk + A.low + at);
+        } else {
+            *(bf16x8*)((bf16*)A.dq + at) = cat8(to_bf4(dq[ti][0]), to_bf4(dq[ti][1]));
+            *(bf16x8*)((bf16*)A.dk + at) = cat8(to_bf4(dks[ti][0]), to_bf4(dks[ti][1]));
         }
-        *(u32x4*)((char*)A.dq + at) = u32x4{x[0][0], x[0][1], x[1][0], x[1][1]};
-        *(u32x4*)((char*)A.dk + at) = u32x4{x[2][0], x[2][1], x[3][0], x[3][1]};
     }
     if (w == 3) {   // lane t: token t
         const int b = lane >> 4;
@@ -548,6 +553,38 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaGradArgs A) {
 
 hipError_t launch_delta_grad(const DeltaGradArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(delta_grad_kernel, dim3((unsigned)a.blocks.items), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// Sum over the G value heads of a q/k head, in head order, of partials to BF16: 8 channels per thread.
+__global__ __launch_bounds__(256) void delta_group_sum_kernel(const char* src0, const char* src1, int64_t low, bf16* dst0,
+                                                              bf16* dst1, int64_t vecs, int G) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (token, q/k head, 8 channels)
+    if (i >= vecs) return;
+    const int64_t row = i >> 4;
+    const int c = (int)(i & 15) * 8;
+    const char* src = blockIdx.y ? src1 : src0;
+    f32x4 a = zero4(), b = zero4();
+    for (int g = 0; g < G; ++g) {
+        const int64_t at = (row * G + g) * D + c;
+        const u32x4 h = *(const u32x4*)(src + 2 * at);
+        const u32x2 l = *(const u32x2*)(src + low + at);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // channels 2j, 2j + 1 of either half
+            a[2 * j] += __uint_as_float(__builtin_amdgcn_perm(h[j], l[0], j ? 0x0504020cu : 0x0504000cu));
+            a[2 * j + 1] += __uint_as_float(__builtin_amdgcn_perm(h[j], l[0], j ? 0x0706030cu : 0x0706010cu));
+            b[2 * j] += __uint_as_float(__builtin_amdgcn_perm(h[2 + j], l[1], j ? 0x0504020cu : 0x0504000cu));
+            b[2 * j + 1] += __uint_as_float(__builtin_amdgcn_perm(h[2 + j], l[1], j ? 0x0706030cu : 0x0706010cu));
+        }
+    }
+    *(bf16x8*)((blockIdx.y ? dst1 : dst0) + row * D + c) = cat8(to_bf4(a), to_bf4(b));
+}
+
+hipError_t launch_delta_group_sum(const void* src0, const void* src1, int64_t low, bf16_t* dst0, bf16_t* dst1, int64_t tokens,
+                                  int Hqk, int G, hipStream_t s) {
+    const int64_t vecs = tokens * Hqk * (D / 8);
+    hipLaunchKernelGGL(delta_group_sum_kernel, dim3((unsigned)((vecs + 255) / 256), 2), dim3(256), 0, s, (const char*)src0,
+                       (const char*)src1, low, (bf16*)dst0, (bf16*)dst1, vecs, G);
     return hipGetLastError();
 }
 

@@ -61,3 +61,36 @@ def test_results_are_rounded_once(case):
     for i, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
         if i > 1 or Hqk == Hv:
             check_one_rounding(name, got[2 + i], refs[i], weights[i])
+
+
+SHARED = {  # lengths, packed, Hqk, Hv, unit, segment
+    "two": ([150, 31], True, 2, 4, True, 0),
+    "four": ([200], False, 2, 8, True, 0),
+    "three_of_given_length": ([70, 3, 130], True, 1, 3, False, 0),
+    "segments": ([260] * 2, False, 2, 4, True, 64),
+}
+
+
+@pytest.mark.parametrize("case", list(SHARED))
+def test_gradients_of_shared_heads_are_rounded_once(case):
+    """dq and dk that sum over value heads: a head's partial is off by 2^-17 of itself, which the bars
+    above leave room for (2^-17 of the partials' sizes for one element)."""
+    lengths, packed, Hqk, Hv, unit, segment = SHARED[case]
+    print(f"[delta precision] shared {case}", flush=True)
+    inp = Inp(lengths, packed, Hqk, Hv, seed=320 + len(case), unit=unit)
+    got = train(inp, segment=segment)
+    refs, weights, parts = inp.gradients()
+    for i, name in enumerate(("dq", "dk")):
+        check_one_rounding(name, got[2 + i], refs[i], weights[i] + 2.0 ** -17 / FINE * parts[i])
+
+
+def test_a_shared_heads_nan_and_infinity_stay_in_their_sequence():
+    """A NaN of any bits in one value head's adjoint: its sequence's dq and dk are NaN where the heads
+    are summed, the other sequence's what they are without."""
+    inp = Inp([70, 40], True, 1, 2, seed=340)
+    want = train(inp)
+    inp.do[:, 10, 1] = torch.tensor([0x7fff], dtype=torch.int16).view(torch.bfloat16)
+    got = train(inp)
+    assert got[2][:, 10].isnan().all()
+    for a, b in zip(got[2:7], want[2:7]):
+        assert torch.equal(a[:, 70:], b[:, 70:])
