@@ -14,7 +14,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import HEAD_DIM, _check, _lib, _ptr, _require
-from .layers import _bytes, _byref, _call, _cuda, _declare, _dense, _new, _rows, _size, _vp, _workspace, _ws
+from .layers import (_bytes, _byref, _call, _cuda, _declare, _dense, _new, _raw_stream, _rows, _size, _vp, _workspace,
+                     _ws)
 
 _BF, _F32 = torch.bfloat16, torch.float32
 
@@ -122,11 +123,14 @@ class GatedDeltaRuleTrainingContext:
     and its CPU mirror among them) with their versions, and its chunks' records
     (about 200 bytes a token and value head, and 128 KiB for each segment of a long
     sequence on few heads; None where the forward was given a
-    workspace, which the caller may have used again since)."""
+    workspace, which the caller may have used again since).  A backward on another stream than
+    the forward's is the caller's to order behind it; the context may be dropped as soon as it is
+    called."""
     problem: KdaDeltaProblem
     inputs: tuple
     versions: tuple
     records: Optional[torch.Tensor] = None
+    stream: Optional[int] = None   # of the forward
 
 
 def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, scale=None, out=None,
@@ -158,7 +162,8 @@ def gated_delta_rule_training_forward(q, k, v, g, beta, initial_state=None, cu_s
     kda_delta_fwd(p, q, k, v, g, beta, initial_state, o, fs, ws)
     inputs = (q, k, v, g, beta, initial_state, cu_seqlens, cu_seqlens_cpu)
     versions = tuple(None if t is None else t._version for t in inputs)
-    return o, fs, GatedDeltaRuleTrainingContext(p, inputs, versions, ws if workspace is None else None)
+    return o, fs, GatedDeltaRuleTrainingContext(p, inputs, versions, ws if workspace is None else None,
+                                                _raw_stream(q.get_device()))
 
 
 def gated_delta_rule_training_backward(context: GatedDeltaRuleTrainingContext, do, dfinal_state=None,
@@ -187,6 +192,12 @@ def gated_delta_rule_training_backward(context: GatedDeltaRuleTrainingContext, d
     records = context.records
     ws = _workspace(kda_delta_bwd_workspace_bytes(p, records is not None), workspace, dev)
     kda_delta_bwd(p, q, k, v, g, beta, s0, records, do, dfinal_state, *out, ws)
+    if _raw_stream(q.get_device()) != context.stream:
+        # once the context is dropped, its memory waits for this stream too
+        other = torch.cuda.current_stream(dev)
+        for t in (*inputs[:7], records):
+            if t is not None:
+                t.record_stream(other)
     return tuple(out)
 
 

@@ -531,7 +531,8 @@ kda_status kda_delta_fwd(const kda_delta_problem* p, const void* q, const void* 
 /* Training backward: the gradients of <do, o> + <dfinal_state, S_final> with
  * respect to the inputs as they were given (with use_qk_l2norm through the
  * norm).  records: the workspace of the kda_delta_fwd with the same problem and inputs,
- * untouched since, or NULL, and they are formed again.  dfinal_state NULL counts as
+ * untouched since (only its size can be checked), or NULL, and they are formed again; on another
+ * stream than the forward's the caller orders the backward behind it.  dfinal_state NULL counts as
  * zero; dinitial_state may be NULL.  dq and dk sum over the value heads that share a
  * q/k head, in head order; dg and dbeta are BF16 [B][T][Hv].  The workspace holds every
  * block's states: about 160 KiB per 64 tokens and value head, 64 KiB per segment, and the
