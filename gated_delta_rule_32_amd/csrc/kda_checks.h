@@ -64,9 +64,9 @@ inline size_t strided_bytes(int64_t tokens, int64_t stride, int heads) {
     return (size_t)((tokens - 1) * stride + (int64_t)heads * D) * 2;
 }
 
-// A launch holds less than 2^32 threads; workgroups of 256 here.
-inline kda_status check_grid(int64_t blocks) {
-    if (blocks >= (int64_t)1 << 24) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks or tokens");
+// A launch holds less than 2^32 threads.
+inline kda_status check_grid(int64_t blocks, int threads = 256) {
+    if (blocks >= ((int64_t)1 << 32) / threads) return fail(KDA_ERR_SHAPE, "too many (sequence, head) tasks or tokens");
     return KDA_OK;
 }
 inline kda_status check_ws(const void* ws, size_t bytes, size_t need) {

@@ -203,7 +203,7 @@ kda_status run_forward(const kda::DeltaArgs& a, hipStream_t stream) {
 kda_status check_forward_grid(const kda::DeltaArgs& a) {
     kda_status s = check_grid(a.map.items * 4);
     if (s == KDA_OK) s = check_grid(a.blocks.items);
-    if (s == KDA_OK) s = check_grid(a.seqs.items * 8);
+    if (s == KDA_OK) s = check_grid(a.seqs.items * 8, a.map.seg_len != 0 ? 512 : 256);   // (the chain's of segments)
     return s;
 }
 

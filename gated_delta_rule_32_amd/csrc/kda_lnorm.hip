@@ -139,7 +139,8 @@ __global__ __launch_bounds__(kThreads < 256 ? 256 : kThreads) void lnorm_fwd_ker
             store_row<kStream>(py + at, __builtin_elementwise_fma(x[c] * r, wc, bc));
         }
         row += step;
-        if (!kHold || row >= a.rows) break;
+        if (row >= a.rows) break;
+        if (!kHold) load(row);
     }
 }
 
@@ -320,6 +321,7 @@ hipError_t launch_stream(const LNormArgs& a, bool bwd, hipStream_t s) {
     if (!bwd) {
         int64_t blocks = (a.rows + ROWS - 1) / ROWS;
         if (kStream && kThreads < 1024) blocks = walk_blocks(a.rows, a.C);
+        if (kThreads == 1024) blocks = std::min<int64_t>(blocks, 1 << 16);   // (a launch holds less than 2^32 threads)
         hipLaunchKernelGGL((lnorm_fwd_kernel<kThreads, kVecs, kStream>), dim3((unsigned)blocks), dim3(BLOCK), 0, s, a);
         return hipGetLastError();
     }

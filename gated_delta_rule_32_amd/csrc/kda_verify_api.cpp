@@ -2,8 +2,6 @@
 // launch.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-
 #include "../../include/libkda.h"
 #include "kda_checks.h"
 #include "kda_delta.h"
@@ -26,7 +24,7 @@ kda_status check_verify(const kda_verify_problem* p, kda::VerifyArgs& a) {
             return fail(KDA_ERR_SHAPE, "a row stride must be in [V=%d, 2^31] (got %lld)", p->V, (long long)st);
     if ((int64_t)p->N * (p->S + 1) >= (int64_t)1 << 31) return fail(KDA_ERR_SHAPE, "too many rows (N x (S+1))");
     a.tiles = kda::verify_tiles(p->V);
-    return check_grid((int64_t)p->N * std::max(a.tiles, 1));
+    return a.tiles == 0 ? check_grid(p->N, 1024) : check_grid((int64_t)p->N * a.tiles);
 }
 size_t verify_ws(const kda::VerifyArgs& a) { return (size_t)a.N * a.tiles * 2 * sizeof(double); }
 
