@@ -4,8 +4,9 @@
 // draft, or where p exceeds q nowhere): the first index whose running sum passes u times the total.
 //
 // Products and sums are formed in 64 bits, where the product of two FP32 values is exact, so
-// that a token depends neither on how the row is split nor on the order of its sums (beyond
-// 2^-50 of the total).  Only one row of p and q of each sequence is read.  A row that one workgroup
+// that a token depends neither on how the row is split nor on the order of its sums, beyond 2^-53 of the
+// total for each addition that a sum takes in turn: 30 of them and one for every 64 tiles, 2^-40 in all for
+// the longest rows.  Only one row of p and q of each sequence is read.  A row that one workgroup
 // holds in registers is read once, by one kernel; of longer ones first the tiles' sums are formed, by
 // as many workgroups as there are tiles, then the tile that the draw falls into is read again.
 // Bound by HBM with many rows (128 of 131072: 17.3 us, 5.4 TB/s, and 8.8 us for the draws), by latency with

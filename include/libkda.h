@@ -581,7 +581,8 @@ kda_status kda_delta_infer(const kda_delta_problem* p, const void* q, const void
  * uniform[n][S] (taken as 0 when negative or NaN) times the total, or the last index with a
  * weight when none is.  tokens (INT32 [N][1+S]) becomes x_0 .. x_{j-1}, the drawn
  * token (-1 when no probability is positive), then -1; num_accepted (INT32 [N])
- * becomes 1 + j.  Comparisons and sums are formed in 64 bits; a NaN counts as 0.  Rows may be of any
+ * becomes 1 + j.  Comparisons and sums are formed in 64 bits.  A draft that is compared by a NaN does
+ * not stand; an index whose weight would be a NaN has none.  Rows may be of any
  * alignment to 4 bytes, `*_stride` elements apart (0: V).  Only row j is read whole.
  * May be captured into a graph at once.
  * ------------------------------------------------------------------------- */
