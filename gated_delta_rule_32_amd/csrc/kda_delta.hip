@@ -230,8 +230,8 @@ hipError_t launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
 
 // Four waves with two tiles each spend the least on reading the rows out of LDS.  With one
 // workgroup for every second compute unit at most, two of half the columns each shorten a chunk.
-// (2048 tokens of 96, 128, 160, 256 heads, in us: 254, 261, 262, 282 in four waves, 195, 204 in two
-// workgroups; in eight waves with a tile each 274, 305 at 160 and 256 heads.)
+// (1024 tokens of 48, 64, 96, 128 sequences and heads, in us: 113, 111, 114, 117 in four waves, 83, 84, 87, 94 in two
+// workgroups; of 160, 192, 256: 123, 124, 129 and 128, 130, 142.)
 template <int NU, int kParts, int kMode>
 __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_scan_kernel(DeltaArgs A) {
     __shared__ __align__(16) char lds[DeltaScanLds<kMode>::TOTAL];

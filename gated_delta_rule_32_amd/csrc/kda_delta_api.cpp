@@ -71,13 +71,13 @@ int64_t total_segs(const Delta& d, int seg) {
 // every segment of the chain that joins them.  Both scans' chunk together takes 4.1 us with 64
 // segments and heads, 4.8 with 128, 7.9 with 256 and 32 ns each with more.
 // In us, forward and backward, whole sequences against the segments of this rule:
-// 16 heads x 1024 tokens 92, 130 / 68, 91; 32 x 2048 170, 264 / 117, 190; 16 x 4096 320, 451 / 128,
-// 203; 8 x 8192 618, 831 / 148, 217; 32 x 8192 634, 1006 / 296, 602; 16 x 32768 2490, 3539 / 601, 1194;
-// 64 x 16384 1325, 2441 / 1041, 2296; 4 x 65536 4866, 6321 / 422, 749; 2 sequences x 32 x 4096
-// 348, 637 / 289, 595; and against segments that it does not take, forward: 4 x 32 x 4096 389 / 484 (of
-// 1024 tokens), 96 x 32768 2778 / 2969 (of 8192).  Other lengths than its own: 16 x 32768 730, 593, 682
-// in segments of 512, 1024 and 4096, 32 x 8192 320, 355 of 512 and 2048, 16 x 4096 181, 138, 158 of 128,
-// 256 and 1024.
+// 16 heads x 1024 tokens 93, 118 / 66, 82; 32 x 2048 171, 243 / 113, 188; 16 x 4096 322, 414 / 128,
+// 198; 8 x 8192 625, 754 / 146, 211; 32 x 8192 638, 929 / 305, 620; 16 x 32768 2501, 3237 / 593, 1201;
+// 64 x 16384 1413, 2353 / 1107, 2338; 4 x 65536 4866, 5699 / 437, 741; 2 sequences x 32 x 4096
+// 337, 606 / 298, 622; and against segments that it does not take: 4 x 32 x 4096 397, 967 / 505, 1181 (of
+// 1024 tokens), 96 x 32768 2881, 6557 / 3197, 7610 (of 8192).  Other lengths than its own, forward and backward: 16 x
+// 32768 667, 1317; 577, 1227; 718, 1301 in segments of 512, 1024 and 4096 (its own 2048), 32 x 8192 307, 639; 360,
+// 662 of 512 and 2048 (1024), 16 x 4096 167, 242; 130, 200; 163, 252 of 128, 256 and 1024 (512: 125, 192).
 int auto_segment(const Delta& d) {
     if (d.segment != 0) return d.s.max_len > d.segment ? d.segment : 0;
     double chunks = 0;

@@ -18,9 +18,9 @@ __global__ __launch_bounds__(512 / NU / kParts, 2) void delta_both_kernel(DeltaA
         delta_scan<NU, kParts, kDeltaRecord>(forward, blockIdx.x - half, half, lds);
 }
 
-// (As the forward's scan: while two workgroups a compute unit hold both scans' halves.  A backward
-// of 2048 tokens of 48, 64, 96, 128 heads, in us: 292, 326, 414, 481 in halves; 415, 449, 506, 565 in four
-// waves with two tiles each; 461, 523 at 96 and 128 heads in eight with a tile each.)
+// (As the forward's scan: while two workgroups a compute unit hold both scans' halves.  1024 tokens
+// of 48, 64, 96, 128 sequences and heads, in us: 97, 99, 121, 131 in halves, 154, 155, 160, 166 in four waves with two
+// tiles each; of 160, 192, 256: 222, 231, 277 and 194, 196, 223.)
 hipError_t launch_delta_both(const DeltaArgs& f, const DeltaArgs& b, hipStream_t s) {
     const unsigned items = (unsigned)f.map.items;
     if (items <= 128)

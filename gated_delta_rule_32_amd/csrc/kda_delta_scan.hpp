@@ -16,8 +16,8 @@
 // as two where they only meet o.  The rows of the next chunk and its record travel from
 // memory to LDS while this one is computed.
 // Bound by the steps of a chunk, each of which needs the one before: 2.4 us with up to one workgroup a
-// unit; with two, matrix and vector instructions take 47% and 53% of the time (8 x 1024 tokens, 96 heads:
-// forward 327 us, 3.3 TB/s; both scans of the backward with their planes 722 us, 4.8 TB/s).  The exact
+// unit; with two, matrix and vector instructions take 47% and 52% of the time (8 x 1024 tokens, 96 heads:
+// forward 327 to 342 us, 3.1 TB/s; both scans of the backward with their planes 720 us, 4.8 TB/s).  The exact
 // products are most of it: some 790 matrix instructions a chunk and head, 1.5 us of a unit's four.
 // Sequences may be cut into segments, which a launch walks side by side: what a segment adds to a
 // state, Q, and what it makes of one, M (the same scan with V = 0 from the identity), are formed first

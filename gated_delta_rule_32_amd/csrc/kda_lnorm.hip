@@ -9,8 +9,8 @@
 // summed per thread over the rows of a workgroup, and over the workgroups by a second kernel, all in a
 // fixed order.
 // Bound by HBM.  So that it never waits for a row's sums, the next row is on its way meanwhile:
-// 8192 x 12288 took 218 us backward with a row at a time (2.8 TB/s) and takes 112 (5.4 TB/s, as a copy of
-// that size), forward 103 and 71 (5.7 TB/s).
+// 8192 x 12288 took 218 us backward with a row at a time and takes 111 (105 at 6.0 TB/s, and 5 for the sums
+// over workgroups), forward 103 and 67 (6.0 TB/s).
 #include <algorithm>
 
 #include "kda_common.hpp"

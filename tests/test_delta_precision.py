@@ -1,5 +1,6 @@
 """GPU tests of how far the gated delta rule's results may be off: each BF16 result by one rounding
-of what 32-bit arithmetic gives.
+of what 32-bit arithmetic gives.  (The bars of delta_util leave room for what the gradients are formed from in
+11 bits, and for partials of 10; it has 16 to 18, and the partials 16.)
 
 Bars.  u = 2^-8 is half a BF16 step relative to the value.
   - One element: u |ref| (and u of that, where the value crosses into the next binade), and what came
