@@ -114,9 +114,9 @@ struct VerifyArgs {
     const int32_t* drafts;      // [N][S]
     const int32_t* lens;        // [N] drafts of each sequence; null: S
     const float* target;        // rows [N][S+1]
-    int64_t target_stride;      // of rows (elements)
+    int64_t target_stride, target_seq;   // of rows and of sequences (elements)
     const float* draft;         // rows [N][S]; null: the drafts are certain
-    int64_t draft_stride;
+    int64_t draft_stride, draft_seq;
     const float* uniform;       // [N][S+1]
     int32_t* tokens;            // [N][S+1]
     int32_t* accepted;          // [N]

@@ -39,8 +39,8 @@ __device__ __forceinline__ int standing(const VerifyArgs& A, int64_t n, int lens
             const int x = A.drafts[n * A.S + i];
             ok = false;
             if (x >= 0 && x < A.V) {
-                const float p = A.target[(n * (A.S + 1) + i) * A.target_stride + x];
-                const float q = A.draft != nullptr ? A.draft[(n * A.S + i) * A.draft_stride + x] : 1.0f;
+                const float p = A.target[n * A.target_seq + i * A.target_stride + x];
+                const float q = A.draft != nullptr ? A.draft[n * A.draft_seq + i * A.draft_stride + x] : 1.0f;
                 ok = (double)A.uniform[n * (A.S + 1) + i] * (double)q < (double)p;
             }
         }
@@ -54,9 +54,9 @@ __device__ __forceinline__ int lengths(const VerifyArgs& A, int64_t n) {
 }
 __device__ __forceinline__ Row draw_row(const VerifyArgs& A, int64_t n, int stand, int lens) {
     Row r;
-    r.p = A.target + (n * (A.S + 1) + stand) * A.target_stride;
+    r.p = A.target + n * A.target_seq + stand * A.target_stride;
     const bool refused = stand < lens;
-    r.q = refused && A.draft != nullptr ? A.draft + (n * A.S + stand) * A.draft_stride : nullptr;
+    r.q = refused && A.draft != nullptr ? A.draft + n * A.draft_seq + stand * A.draft_stride : nullptr;
     r.point = refused && A.draft == nullptr ? A.drafts[n * A.S + stand] : -1;
     return r;
 }

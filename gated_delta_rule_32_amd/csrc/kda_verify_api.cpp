@@ -23,6 +23,15 @@ kda_status check_verify(const kda_verify_problem* p, kda::VerifyArgs& a) {
         if (st < p->V || st > (int64_t)1 << 31)
             return fail(KDA_ERR_SHAPE, "a row stride must be in [V=%d, 2^31] (got %lld)", p->V, (long long)st);
     if ((int64_t)p->N * (p->S + 1) >= (int64_t)1 << 31) return fail(KDA_ERR_SHAPE, "too many rows (N x (S+1))");
+    auto seq = [&](int64_t given, int rows, int64_t stride, int64_t& out) -> kda_status {
+        out = given == 0 ? rows * stride : given;
+        if (given != 0 && (given < (rows - 1) * stride + p->V || given > ((int64_t)1 << 60) / p->N))
+            return fail(KDA_ERR_SHAPE, "a sequence stride must reach over its %d rows (got %lld)", rows, (long long)given);
+        return KDA_OK;
+    };
+    kda_status s = seq(p->target_seq_stride, p->S + 1, a.target_stride, a.target_seq);
+    if (s == KDA_OK) s = seq(p->draft_seq_stride, p->S, a.draft_stride, a.draft_seq);
+    if (s != KDA_OK) return s;
     a.tiles = kda::verify_tiles(p->V);
     return a.tiles == 0 ? check_grid(p->N, 1024) : check_grid((int64_t)p->N * a.tiles);
 }
@@ -55,15 +64,15 @@ kda_status kda_verify(const kda_verify_problem* pp, const int32_t* draft_tokens,
         const size_t need = verify_ws(a);
         if ((s = check_ws(workspace, workspace_bytes, need)) != KDA_OK) return s;
         const size_t n = (size_t)a.N, rows = n * (a.S + 1), drafts = n * a.S;
-        auto row_bytes = [&](size_t count, int64_t stride) {
-            return count == 0 ? 0 : ((count - 1) * (size_t)stride + a.V) * sizeof(float);
+        auto row_bytes = [&](int of, int64_t seq, int64_t stride) {
+            return of == 0 ? 0 : (size_t)((a.N - 1) * seq + (of - 1) * stride + a.V) * sizeof(float);
         };
         s = check_overlap({{tokens, rows * 4, "tokens"}, {num_accepted, n * 4, "num_accepted"},
                            {workspace, need, "workspace"}},
                           {{draft_tokens, draft_tokens ? drafts * 4 : 0, "draft_tokens"},
                            {draft_lens, draft_lens ? n * 4 : 0, "draft_lens"},
-                           {target_probs, row_bytes(rows, a.target_stride), "target_probs"},
-                           {draft_probs, draft_probs ? row_bytes(drafts, a.draft_stride) : 0, "draft_probs"},
+                           {target_probs, row_bytes(a.S + 1, a.target_seq, a.target_stride), "target_probs"},
+                           {draft_probs, draft_probs ? row_bytes(a.S, a.draft_seq, a.draft_stride) : 0, "draft_probs"},
                            {uniform, rows * 4, "uniform"}});
         if (s != KDA_OK) return s;
         a.drafts = draft_tokens;

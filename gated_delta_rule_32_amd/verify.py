@@ -20,6 +20,7 @@ class KdaVerifyProblem(ctypes.Structure):
     _fields_ = [
         ("N", ctypes.c_int32), ("S", ctypes.c_int32), ("V", ctypes.c_int32),
         ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64),
+        ("target_seq_stride", ctypes.c_int64), ("draft_seq_stride", ctypes.c_int64),
     ]
 
 
@@ -40,23 +41,22 @@ def kda_verify(p: KdaVerifyProblem, draft_tokens, draft_lens, target_probs, draf
           _ptr(draft_probs), _ptr(uniform), _ptr(tokens), _ptr(num_accepted), *_ws(workspace))
 
 
-def _prob_rows(name, t, shape, device) -> int:
-    """The row stride of FP32 [N, rows, V] probabilities: dense, or a slice of
-    wider rows."""
+def _prob_rows(name, t, shape, device):
+    """The strides of rows and of sequences of FP32 [N, rows, V] probabilities (the latter 0: as
+    many rows): dense, or a slice of wider rows, or of more of them."""
     if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.shape == shape and t.device == device):
         _require(isinstance(t, torch.Tensor) and t.dtype is _F32, f"{name} must be a float32 tensor")
         _require(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         _require(False, f"{name} must be on {device}, got {t.device}")
     N, R, V = shape
     if t.is_contiguous():
-        return V
+        return V, 0
     sn, sr, sv = t.stride()
     _require(sv == 1 or V == 1, f"{name} must have dense rows")
     if R <= 1:
-        sr = sn if N > 1 else V
-    _require(N == 1 or sn == R * sr, f"{name}'s rows must be a fixed distance apart")
-    _require(sr >= V, f"{name}'s rows must not overlap")
-    return sr
+        sr = V
+    _require(sr >= V and (N == 1 or sn >= (R - 1) * sr + V), f"{name}'s rows must not overlap")
+    return sr, sn if N > 1 else 0
 
 
 def verify_drafts(draft_tokens, target_probs, uniform, draft_probs=None, draft_lens=None, *,
@@ -68,7 +68,8 @@ def verify_drafts(draft_tokens, target_probs, uniform, draft_probs=None, draft_l
     [N], how many of them there are; None: S each).  target_probs: float32 [N, 1+S,
     V], the target's probabilities p at each draft's place and behind the last one.
     draft_probs: float32 [N, S, V], those q that the drafts were drawn from; None
-    for drafts that are certain.  uniform: float32 [N, 1+S], random numbers in [0, 1).
+    for drafts that are certain.  Both may be slices of wider rows, or the first rows of buffers with
+    more of them.  uniform: float32 [N, 1+S], random numbers in [0, 1).
     Draft i stands while those before it do and uniform[:, i] q(x) < p(x); then one
     token is drawn from the positive part of p - q (behind the last draft from p) by
     uniform[:, S].  tokens holds the drafts that stand, the drawn token, then -1;
@@ -81,11 +82,12 @@ def verify_drafts(draft_tokens, target_probs, uniform, draft_probs=None, draft_l
     N, S, V = target_probs.shape
     S -= 1
     _require(N >= 1 and S >= 0 and V >= 1, "target_probs must not be empty")
-    p = KdaVerifyProblem(N, S, V, _prob_rows("target_probs", target_probs, (N, S + 1, V), dev), 0)
+    p = KdaVerifyProblem(N, S, V)
+    p.target_stride, p.target_seq_stride = _prob_rows("target_probs", target_probs, (N, S + 1, V), dev)
     _dense("draft_tokens", draft_tokens, _I32, (N, S), dev)
     _dense("uniform", uniform, _F32, (N, S + 1), dev)
     if draft_probs is not None:
-        p.draft_stride = _prob_rows("draft_probs", draft_probs, (N, S, V), dev)
+        p.draft_stride, p.draft_seq_stride = _prob_rows("draft_probs", draft_probs, (N, S, V), dev)
     if draft_lens is not None:
         _dense("draft_lens", draft_lens, _I32, (N,), dev)
     if out is None:

@@ -583,12 +583,14 @@ kda_status kda_delta_infer(const kda_delta_problem* p, const void* q, const void
  * token (-1 when no probability is positive), then -1; num_accepted (INT32 [N])
  * becomes 1 + j.  Comparisons and sums are formed in 64 bits.  A draft that is compared by a NaN does
  * not stand; an index whose weight would be a NaN has none.  Rows may be of any
- * alignment to 4 bytes, `*_stride` elements apart (0: V).  Only row j is read whole.
+ * alignment to 4 bytes, `*_stride` elements apart (0: V), and those of a sequence begin `*_seq_stride`
+ * elements behind those of the one before (0: as many rows on).  Only row j is read whole.
  * May be captured into a graph at once.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int32_t N, S, V;
     int64_t target_stride, draft_stride;
+    int64_t target_seq_stride, draft_seq_stride;
 } kda_verify_problem;
 
 kda_status kda_verify_workspace_bytes(const kda_verify_problem* p, size_t* bytes);

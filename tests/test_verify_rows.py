@@ -63,3 +63,18 @@ def test_a_draft_compared_by_nan_does_not_stand(V):
     d.draft[2, 0, x[2]] = float("nan")
     assert d.call()[1].tolist() == [1, 1, 1, 3]
     d.check()
+
+
+@pytest.mark.parametrize("V", [1, 700, 20000])
+def test_first_rows_of_buffers_with_more(V):
+    """Drafts' and target's probabilities as the first rows of one shape of buffer, of sequences that lie
+    apart, of wider rows too; what lies between is NaN."""
+    for n, S, pad in ((5, 3, 0), (4, 1, 3), (1, 4, 0), (3, 0, 0)):
+        def wrap(x):
+            w = torch.full((2 * n, S + 3, V + pad), float("nan"), device="cuda")[::2, :x.shape[1], :V]
+            w.copy_(x)
+            return w
+        d = Drafts(n, S, V, 25 + S)
+        tokens, accepted = d.call(wrap=wrap)
+        want, count = d.reference()
+        assert np.array_equal(tokens.cpu().numpy(), want) and np.array_equal(accepted.cpu().numpy(), count)
