@@ -140,7 +140,7 @@ struct PlaneWriter {
 #pragma unroll
                 for (int u = 0; u < NU; ++u) {
                     const f32x4 x = mma32(piece[u][1], id[i], mma32(piece[u][0], id[i], zero4()));
-                    const u32x4 y = __builtin_bit_cast(u32x4, x) + 0x80u;   // (a NaN's lower half is zero)
+                    const u32x4 y = __builtin_bit_cast(u32x4, x) + 0x80u;   // (the matrix units' NaN is 0xffc00000)
                     high[2 * u] = __builtin_amdgcn_perm(y[1], y[0], 0x07060302u);
                     high[2 * u + 1] = __builtin_amdgcn_perm(y[3], y[2], 0x07060302u);
                     low[u] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(y[3], y[2], 0x0c0c0501u),

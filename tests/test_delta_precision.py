@@ -95,3 +95,43 @@ def test_a_shared_heads_nan_and_infinity_stay_in_their_sequence():
     assert got[2][:, 10].isnan().all()
     for a, b in zip(got[2:7], want[2:7]):
         assert torch.equal(a[:, 70:], b[:, 70:])
+
+
+@pytest.mark.parametrize("bits", [0x7fc00000, 0x7fffffff, -1, 0x7f800001, 0x7f800000])
+@pytest.mark.parametrize("Hqk", [1, 2])
+def test_a_states_nan_is_not_lost(bits, Hqk):
+    """A NaN of any bits, or an infinity, in an initial state's or final adjoint's element [v, k]: the gradients that
+    take it up are NaN or infinite (dq's channel k of every token that sees the state; every token's dk)."""
+    inp = Inp([70, 40], True, Hqk, 2, seed=341, unit=False)
+    bad = torch.tensor([bits], dtype=torch.int32).view(torch.float32)
+    inp.s0[0, 1, 5, 7] = bad
+    got = train(inp)
+    assert not got[2][:, :64, Hqk - 1, 7].isfinite().any()
+    assert all(t[:, 70:].isfinite().all() for t in got[2:7])
+    inp = Inp([70, 40], True, Hqk, 2, seed=341, unit=False)
+    inp.ds[0, 1, 5, 7] = bad
+    got = train(inp)
+    assert not got[3][:, :70, Hqk - 1, 7].isfinite().any()
+    assert all(t[:, 70:].isfinite().all() for t in got[2:7])
+
+
+def test_tokens_of_sizes_far_apart_in_one_block():
+    """do and v of neighbouring tokens 2^30 apart: a small token's gradients are as exact as a large
+    one's wherever its own terms make them up (its dq of the state before the block, by the state alone; its dv
+    behind which nothing comes)."""
+    inp = Inp([64], False, 1, 1, seed=342, unit=False)
+    inp.ds.zero_()
+    size = 2.0 ** -30 * torch.ones(64)
+    size[::2] = 1.0
+    size[63] = 2.0 ** -30
+    inp.do = (inp.do.float() * size[None, :, None, None]).bfloat16()
+    got = train(inp)
+    refs, _, _ = inp.gradients()
+    # dq_i is do_i times the state behind token i: all of a token's terms have do_i's size
+    small = size < 1.0
+    for name, x, ref in (("dq", got[2][:, small], refs[0][:, small]), ("dv", got[4][:, 63:], refs[2][:, 63:])):
+        x = lu.f64(x)
+        once = np.linalg.norm(lu.f64(torch.from_numpy(ref).bfloat16()) - ref)
+        ratio = np.linalg.norm(x - ref) / once
+        print(f"{name} norm {ratio:.5f} of one rounding's", flush=True)
+        assert ratio <= 1 + lu.U, name

@@ -51,3 +51,27 @@ def test_backward_on_the_forwards_stream_gives_its_memory_back():
         del ctx
         used.append(torch.cuda.memory_allocated())
     assert used[1] == used[3]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_captured_backward_of_an_eager_forward(packed):
+    """A graph of the backward alone, replayed with eager steps between: the eager bits."""
+    import gated_delta_rule_32_amd as kda
+    inp = Inp([130, 70] if packed else [130, 130], packed, 1, 2, seed=353)
+    do, ds = inp.dev(inp.do), inp.dev(inp.ds)
+    call_forward(inp)
+    _, _, ctx = call_forward(inp)
+    want = kda.gated_delta_rule_training_backward(ctx, do, ds)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kda.gated_delta_rule_training_backward(ctx, do, ds)
+    for _ in range(3):
+        for x in got:
+            x.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        again = kda.gated_delta_rule_training_backward(ctx, do, ds)
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, again):
+            assert torch.equal(a, b) and torch.equal(c, b)
